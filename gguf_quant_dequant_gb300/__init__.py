@@ -62,6 +62,15 @@ SIGNATURES = {
     "qk_gemv_swiglu": (_int, [_int, _p, _p, _i64, _i64, _p, _p, _p]),
     "qk_gemm_workspace": (_sz, [_int, _i64, _i64, _i64]),
     "qk_gemm": (_int, [_int, _p, _i64, _i64, _p, _i64, _p, _p, _sz, _p]),
+    "qk_kv_page_bytes": (_sz, [_int, _int, _int, _int]),
+    "qk_kv_plan": (_int, [_p, _p, _p, _i64, _int, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p]),
+    "qk_kv_append": (_int, [_int, _p, _p, _int, _i64, _i64, _i64, _int, _int, _p, _p, _p, _i64, _int, _p]),
+    "qk_kv_compact": (_int, [_int, _p, _p, _i64, _int, _int, _int, _p, _i64, _p, _p, _i64, _p, _i64, _p]),
+    "qk_attn_tree_workspace": (_sz, [_int, _i64, _int, _i64, _int, _int, _int]),
+    "qk_attn_tree": (_int, [_int, _p, _i64, _i64, _p, _p, _i64, _int, _p, _i64, _p, _p, _p, _i64, _int, _int, _int, _int,
+                            ctypes.c_float, _p, _i64, _p, _sz, _p]),
+    "qk_logits_process": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _i64,
+                                 _p, _p, _i64, _p, _i64, _p]),
     "qk_unpack": (_int, [_int, _p, _i64, _p, _p, _p, _p, _p, _p]),
     "qk_device_status": (_int, [_p]),
     "qk_test_stalled_wait": (_int, [ctypes.c_uint32, _p]),
@@ -267,6 +276,159 @@ def gemm(t: int, W, rows: int, cols: int, X, Y=None, ws=None, stream=None):
     _check(load().qk_gemm(t, _ptr(W), rows, cols, _ptr(X), M, _ptr(Y), _ptr(ws), nbytes, _stream(stream)),
            "qk_gemm")
     return Y
+
+
+# ------------------------------------- paged KV cache, tree attention, logits --
+
+TREE_MAX = 64
+
+
+def _dtype(x, what: str) -> int:
+    import torch
+    if x.dtype is torch.float32:
+        return OUT_F32
+    if x.dtype is torch.bfloat16:
+        return OUT_BF16
+    raise QKError(8, what, f"dtype {x.dtype}: float32 or bfloat16 expected")
+
+
+def _rows(x, what: str) -> int:
+    """Elements from row to row of a tensor whose rows are contiguous."""
+    want = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size != 1 and stride != want:
+            raise QKError(8, what, f"strides {x.stride()} of shape {tuple(x.shape)}: contiguous rows expected")
+        want *= size
+    return x.stride(0) if x.shape[0] > 1 else want
+
+
+def _of(x, dtype, what: str, shape=None):
+    """A contiguous array of the type (and shape) the C call reads, or None."""
+    if x is not None:
+        if x.dtype is not dtype or not x.is_contiguous():
+            raise QKError(8, what, f"contiguous {dtype} expected, got {x.dtype} with strides {x.stride()}")
+        if shape is not None and tuple(x.shape) != shape:
+            raise QKError(2, what, f"shape {tuple(x.shape)}, expected {shape}")
+    return _ptr(x)
+
+
+def _pool_pages(t: int, K, V, n_kv: int, d: int, page: int, what: str) -> int:
+    import torch
+    pb = load().qk_kv_page_bytes(t, n_kv, d, page)
+    if pb == 0:
+        raise QKError(2, what, f"no paged cache of type {t} with n_kv={n_kv}, d={d}, page={page}")
+    if _of(K, torch.uint8, what) is None or _of(V, torch.uint8, what) is None or K.numel() != V.numel() or K.numel() % pb:
+        raise QKError(2, what, f"K and V must be uint8 pools of the same whole number of {pb}-byte pages")
+    return K.numel() // pb
+
+
+def kv_page_bytes(t: int, n_kv: int, d: int, page: int) -> int:
+    return load().qk_kv_page_bytes(t, n_kv, d, page)
+
+
+def kv_plan(have, start, want, table, free_pages, n_free, page: int, cap: int, out=None, stream=None) -> dict:
+    """Page bookkeeping of a step (qk_kv_plan): int32 CUDA have, start, want
+    [n_req], table [n_req, P] and free_pages [F] (both updated in place), n_free
+    [1] -> {"n_free" [1], "granted" [n_req], "cu" [n_req + 1], "slots" int64,
+    "pos", "req" [cap]}.  out: a dict of such tensors to be written instead of
+    new ones."""
+    import torch
+    n, dev = have.shape[0], have.device
+    if out is None:
+        e = torch.empty(2 + 2 * n + 2 * cap, dtype=torch.int32, device=dev)
+        out = {"n_free": e[:1], "granted": e[1:1 + n], "cu": e[1 + n:2 + 2 * n], "pos": e[2 + 2 * n:2 + 2 * n + cap],
+               "req": e[2 + 2 * n + cap:], "slots": torch.empty(cap, dtype=torch.int64, device=dev)}
+    i32, w = torch.int32, "kv_plan"
+    _check(load().qk_kv_plan(
+        _of(have, i32, w), _of(start, i32, w, (n,)), _of(want, i32, w, (n,)), n, page,
+        _of(table, i32, w, (n, table.shape[1])), table.shape[1], _of(free_pages, i32, w), free_pages.numel(),
+        _of(n_free, i32, w), _of(out["n_free"], i32, w, (1,)), _of(out["granted"], i32, w, (n,)),
+        _of(out["cu"], i32, w, (n + 1,)), _of(out["slots"], torch.int64, w, (cap,)), _of(out["pos"], i32, w, (cap,)),
+        _of(out["req"], i32, w, (cap,)), cap, _stream(stream)), "qk_kv_plan")
+    return out
+
+
+def kv_append(t: int, k, v, slots, K, V, page: int, stream=None) -> None:
+    """Quantize k, v (fp32 or bf16 CUDA [n_tok, n_kv, d], rows contiguous) into
+    the uint8 pools K, V at slots int64 [n_tok] (qk_kv_append)."""
+    import torch
+    n, n_kv, d = k.shape
+    w = "kv_append"
+    if v.shape != k.shape or v.dtype is not k.dtype:
+        raise QKError(2, w, "k and v differ in shape or type")
+    pages = _pool_pages(t, K, V, n_kv, d, page, w)
+    _check(load().qk_kv_append(t, _ptr(k), _ptr(v), _dtype(k, w), n, _rows(k, w), _rows(v, w), n_kv, d,
+                               _of(slots, torch.int64, w, (n,)), _ptr(K), _ptr(V), pages, page, _stream(stream)),
+           "qk_kv_append")
+
+
+def kv_compact(t: int, K, V, page: int, n_kv: int, d: int, table, base, path, n_path, stream=None) -> None:
+    """Move the accepted rows base + path[:, j] to base + j (qk_kv_compact):
+    int32 CUDA table [n_req, P], base, n_path [n_req], path [n_req, m]."""
+    import torch
+    w, i32, n = "kv_compact", torch.int32, base.shape[0]
+    pages = _pool_pages(t, K, V, n_kv, d, page, w)
+    _check(load().qk_kv_compact(t, _ptr(K), _ptr(V), pages, page, n_kv, d, _of(table, i32, w, (n, table.shape[1])),
+                                table.shape[1], _of(base, i32, w), _of(path, i32, w, (n, path.shape[1])), path.shape[1],
+                                _of(n_path, i32, w, (n,)), n, _stream(stream)), "qk_kv_compact")
+
+
+def attn_tree_workspace(t: int, n_req: int, max_q: int, max_pos: int, n_heads: int, n_kv: int, d: int) -> int:
+    return load().qk_attn_tree_workspace(t, n_req, max_q, max_pos, n_heads, n_kv, d)
+
+
+def attn_tree(t: int, q, K, V, page: int, n_kv: int, table, ctx, cu, mask, max_q: int, scale: float, out=None, ws=None,
+              stream=None):
+    """Attention of drafted-token trees over the paged cache (qk_attn_tree):
+    q bf16 CUDA [n_tok, n_heads, d] (rows contiguous); table int32 [n_req, P],
+    ctx int32 [n_req], cu int32 [n_req + 1], mask int64 [n_tok] (64 bits) or
+    None -> out bf16 [n_tok, n_heads, d]."""
+    import torch
+    w, i32 = "attn_tree", torch.int32
+    n, n_heads, d = q.shape
+    r = ctx.shape[0]
+    if _dtype(q, w) != OUT_BF16:
+        raise QKError(8, w, "q must be bfloat16")
+    if out is None:
+        out = torch.empty((n, n_heads, d), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype is not torch.bfloat16 or out.shape != q.shape:
+        raise QKError(2, w, "out must be bfloat16 of q's shape")
+    pages = _pool_pages(t, K, V, n_kv, d, page, w)
+    P = table.shape[1]
+    if ws is None:
+        ws = torch.empty(max(load().qk_attn_tree_workspace(t, r, max_q, P * page, n_heads, n_kv, d), 16),
+                         dtype=torch.uint8, device=q.device)
+    _check(load().qk_attn_tree(t, _ptr(q), n, _rows(q, w), _ptr(K), _ptr(V), pages, page, _of(table, i32, w, (r, P)), P,
+                               _of(ctx, i32, w), _of(cu, i32, w, (r + 1,)), _of(mask, torch.int64, w, (n,)), r, max_q,
+                               n_heads, n_kv, d, scale, _ptr(out), _rows(out, w), _ptr(ws),
+                               ws.numel() * ws.element_size(), _stream(stream)), "qk_attn_tree")
+    return out
+
+
+def logits_process(logits, cu, hist, hist_len, rep, pres, freq, draft=None, mask=None, bias_tok=None, bias_val=None,
+                   bias_len=None, grammar=None, out=None, stream=None):
+    """Penalties, biases and grammar masks on logits (qk_logits_process):
+    logits fp32 or bf16 CUDA [n_rows, vocab]; cu int32 [n_req + 1]; hist int32
+    [n_req, H], hist_len int32, rep, pres, freq fp32 [n_req]; draft int32,
+    mask int64 [n_rows]; bias_tok int32, bias_val fp32 [n_req, B], bias_len
+    int32 [n_req]; grammar int32 [n_rows, words] -> out (may be logits)."""
+    import torch
+    w, i32, f32 = "logits_process", torch.int32, torch.float32
+    n, V = logits.shape
+    r = cu.shape[0] - 1
+    if out is None:
+        out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+    elif out.dtype is not logits.dtype or out.shape != logits.shape:
+        raise QKError(2, w, "out must have the logits' type and shape")
+    B = 0 if bias_tok is None else bias_tok.shape[1]
+    _check(load().qk_logits_process(
+        _ptr(logits), _dtype(logits, w), n, V, _rows(logits, w), _of(cu, i32, w), r, _of(hist, i32, w, (r, hist.shape[1])),
+        hist.shape[1], _of(hist_len, i32, w, (r,)), _of(rep, f32, w, (r,)), _of(pres, f32, w, (r,)), _of(freq, f32, w, (r,)),
+        _of(draft, i32, w, (n,)), _of(mask, torch.int64, w, (n,)), _of(bias_tok, i32, w, (r, B)),
+        _of(bias_val, f32, w, (r, B)) if B else None, B, _of(bias_len, i32, w, (r,)) if B else None,
+        _of(grammar, i32, w, None if grammar is None else (n, grammar.shape[1])), 0 if grammar is None else grammar.shape[1], _ptr(out), _rows(out, w), _stream(stream)),
+        "qk_logits_process")
+    return out
 
 
 def unpack(t: int, W, nblocks: int, stream=None):

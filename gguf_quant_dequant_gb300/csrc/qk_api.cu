@@ -106,6 +106,32 @@ qk_status check_matrix(int type, const void* W, int64_t rows, int64_t cols) {
     return QK_OK;
 }
 
+bool kv_type(int t) { return t == QK_Q8_0 || t == QK_Q5_0 || t == QK_Q4_0; }
+
+// log2 of a page size the paged cache takes, else -1.
+int page_log2(int page) {
+    for (int l = 4; l <= 8; ++l)
+        if (page == 1 << l) return l;
+    return -1;
+}
+
+// The most any count or stride of the paged calls may be (products of two of
+// them, and of one with a row's bytes, stay inside 63 bits).
+constexpr int64_t kCountMax = 0x7fffffff;
+bool count_ok(int64_t n) { return n >= 0 && n <= kCountMax; }
+
+// Shared validation of a paged pool's geometry and pointers.
+qk_status check_pool(int type, int n_kv, int d, int page, int64_t n_pages, const void* K, const void* V) {
+    if (!kv_type(type)) return fail(QK_ERR_TYPE, "KV cache type %d: Q8_0, Q5_0 or Q4_0 expected", type);
+    if (n_kv < 1 || n_kv > 4096 || (d != 32 && d != 64 && d != 128 && d != 256))
+        return fail(QK_ERR_SHAPE, "bad KV rows n_kv=%d d=%d", n_kv, d);
+    if (page_log2(page) < 0) return fail(QK_ERR_SHAPE, "page=%d: 16, 32, 64, 128 or 256 expected", page);
+    if (!count_ok(n_pages)) return fail(QK_ERR_SHAPE, "bad n_pages=%lld", (long long)n_pages);
+    if (!K || !V) return fail(QK_ERR_NULL, "a KV pool is NULL");
+    if (!aligned(K, 16) || !aligned(V, 16)) return fail(QK_ERR_ALIGN, "the KV pools must be 16-byte aligned");
+    return QK_OK;
+}
+
 }  // namespace
 
 namespace qk {
@@ -396,6 +422,182 @@ qk_status qk_test_stalled_wait(uint32_t limit_us, void* stream) {
     return QK_OK;
 }
 
+// --- the paged KV cache, tree attention over it, logits ---
+
+size_t qk_kv_page_bytes(int type, int n_kv, int d, int page) {
+    if (!kv_type(type) || n_kv < 1 || n_kv > 4096 || (d != 32 && d != 64 && d != 128 && d != 256) || page_log2(page) < 0)
+        return 0;
+    return (size_t)n_kv * page * (d / 32) * block_bytes(type);
+}
+
+qk_status qk_kv_plan(const int32_t* have, const int32_t* start, const int32_t* want, int64_t n_req, int page,
+                     int32_t* table, int64_t table_stride, int32_t* free_pages, int64_t free_cap, const int32_t* n_free,
+                     int32_t* n_free_out, int32_t* granted, int32_t* cu, int64_t* slots, int32_t* pos, int32_t* req,
+                     int64_t cap, void* stream) {
+    if (n_req < 0 || n_req > QK_PLAN_MAX_REQ)
+        return fail(QK_ERR_SHAPE, "n_req=%lld outside 0..%d", (long long)n_req, QK_PLAN_MAX_REQ);
+    if (page_log2(page) < 0) return fail(QK_ERR_SHAPE, "page=%d: 16, 32, 64, 128 or 256 expected", page);
+    if (!count_ok(table_stride) || !count_ok(free_cap) || !count_ok(cap))
+        return fail(QK_ERR_SHAPE, "bad table_stride=%lld, free_cap=%lld or cap=%lld", (long long)table_stride,
+                    (long long)free_cap, (long long)cap);
+    if (!n_free || !n_free_out || !cu || (n_req > 0 && (!have || !start || !want || !granted)) ||
+        (n_req > 0 && table_stride > 0 && !table) || (free_cap > 0 && !free_pages) || (cap > 0 && !slots))
+        return fail(QK_ERR_NULL, "NULL pointer argument");
+    for (const void* p : {(const void*)have, (const void*)start, (const void*)want, (const void*)table,
+                          (const void*)free_pages, (const void*)n_free, (const void*)n_free_out, (const void*)granted,
+                          (const void*)cu, (const void*)pos, (const void*)req})
+        if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "the int32 arrays must be 4-byte aligned");
+    if (!aligned(slots, 8)) return fail(QK_ERR_ALIGN, "slots must be 8-byte aligned");
+    if (n_free == n_free_out) return fail(QK_ERR_ARG, "n_free_out must not be n_free");
+    int sms = 0;
+    const qk_status st = device_state(nullptr, &sms);
+    if (st != QK_OK) return st;
+    cudaError_t e = qk::launch_kv_plan(have, start, want, (int)n_req, page_log2(page), table, table_stride, free_pages,
+                                       free_cap, n_free, n_free_out, granted, cu, slots, pos, req, cap, sms,
+                                       static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_kv_plan launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
+qk_status qk_kv_append(int type, const void* k, const void* v, int dtype, int64_t n_tok, int64_t k_stride, int64_t v_stride,
+                       int n_kv, int d, const int64_t* slots, void* K, void* V, int64_t n_pages, int page, void* stream) {
+    qk_status st = check_pool(type, n_kv, d, page, n_pages, K, V);
+    if (st != QK_OK) return st;
+    if (dtype != QK_OUT_F32 && dtype != QK_OUT_BF16) return fail(QK_ERR_ARG, "bad dtype %d", dtype);
+    const int64_t row = (int64_t)n_kv * d;
+    // the launch's grid: 64 blocks of 32 elements a CTA
+    if (n_tok < 0 || n_tok > (int64_t(1) << 31) * 32 / row)
+        return fail(QK_ERR_SHAPE, "bad n_tok=%lld", (long long)n_tok);
+    if (n_tok == 0) return QK_OK;
+    if (k_stride < row || v_stride < row || !count_ok(k_stride) || !count_ok(v_stride))
+        return fail(QK_ERR_SHAPE, "bad strides k_stride=%lld v_stride=%lld", (long long)k_stride, (long long)v_stride);
+    if (!k || !v || !slots) return fail(QK_ERR_NULL, "k, v or slots is NULL");
+    const size_t es = dtype == QK_OUT_BF16 ? 2 : 4;
+    if (!aligned(k, es) || !aligned(v, es) || !aligned(slots, 8))
+        return fail(QK_ERR_ALIGN, "k and v must be aligned to their element, slots to 8 bytes");
+    unsigned* status = nullptr;
+    st = device_state(&status, nullptr);
+    if (st != QK_OK) return st;
+    cudaError_t e = qk::launch_kv_append(type, k, v, dtype == QK_OUT_BF16, n_tok, k_stride, v_stride, n_kv, d, slots,
+                                         static_cast<uint8_t*>(K), static_cast<uint8_t*>(V), n_pages, page_log2(page),
+                                         (int)qk_row_bytes(type, d), status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_kv_append launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
+qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, int n_kv, int d, const int32_t* table,
+                        int64_t table_stride, const int32_t* base, const int32_t* path, int64_t path_stride,
+                        const int32_t* n_path, int64_t n_req, void* stream) {
+    qk_status st = check_pool(type, n_kv, d, page, n_pages, K, V);
+    if (st != QK_OK) return st;
+    if (!count_ok(n_req) || !count_ok(table_stride) || !count_ok(path_stride))
+        return fail(QK_ERR_SHAPE, "bad n_req=%lld, table_stride=%lld or path_stride=%lld", (long long)n_req,
+                    (long long)table_stride, (long long)path_stride);
+    if (n_req == 0 || path_stride == 0) return QK_OK;
+    if (!table || !base || !path || !n_path) return fail(QK_ERR_NULL, "NULL pointer argument");
+    if (!aligned(table, 4) || !aligned(base, 4) || !aligned(path, 4) || !aligned(n_path, 4))
+        return fail(QK_ERR_ALIGN, "the int32 arrays must be 4-byte aligned");
+    unsigned* status = nullptr;
+    st = device_state(&status, nullptr);
+    if (st != QK_OK) return st;
+    cudaError_t e = qk::launch_kv_compact(static_cast<uint8_t*>(K), static_cast<uint8_t*>(V), n_pages, page_log2(page),
+                                          n_kv, (int)qk_row_bytes(type, d), table, table_stride, base, path, path_stride,
+                                          n_path, n_req, status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_kv_compact launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
+static bool attn_tree_shape_ok(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d) {
+    return n_req >= 0 && n_req <= 65535 && max_q >= 1 && max_q <= QK_TREE_MAX && max_pos >= 0 &&
+           max_pos <= kCountMax * 256 && n_kv >= 1 && n_kv <= 4096 && n_heads >= n_kv && n_heads % n_kv == 0 &&
+           n_heads / n_kv <= 64 && (d == 32 || d == 64 || d == 128 || d == 256);
+}
+
+size_t qk_attn_tree_workspace(int type, int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d) {
+    if (!kv_type(type) || !attn_tree_shape_ok(n_req, max_q, max_pos, n_heads, n_kv, d)) return 0;
+    return (size_t)qk::attn_tree_ws_bytes(n_req, max_q, max_pos, n_heads, d);
+}
+
+qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const void* K, const void* V,
+                       int64_t n_pages, int page, const int32_t* table, int64_t table_stride, const int32_t* ctx,
+                       const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q, int n_heads, int n_kv, int d,
+                       float scale, void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream) {
+    qk_status st = check_pool(type, n_kv, d, page, n_pages, K, V);
+    if (st != QK_OK) return st;
+    if (!count_ok(table_stride) || !count_ok(n_tok) ||
+        !attn_tree_shape_ok(n_req, max_q, table_stride * page, n_heads, n_kv, d))
+        return fail(QK_ERR_SHAPE, "bad attention shape n_req=%lld n_tok=%lld max_q=%d table_stride=%lld n_heads=%d n_kv=%d d=%d",
+                    (long long)n_req, (long long)n_tok, max_q, (long long)table_stride, n_heads, n_kv, d);
+    if (n_tok == 0 || n_req == 0) return QK_OK;
+    const int64_t row = (int64_t)n_heads * d;
+    if (q_stride < row || out_stride < row || !count_ok(q_stride) || !count_ok(out_stride))
+        return fail(QK_ERR_SHAPE, "bad strides q_stride=%lld out_stride=%lld", (long long)q_stride, (long long)out_stride);
+    if (!q || !out || !ctx || !cu || (table_stride > 0 && !table) || !ws) return fail(QK_ERR_NULL, "NULL pointer argument");
+    if (!aligned(q, 16) || q_stride % 8 != 0)
+        return fail(QK_ERR_ALIGN, "q must be 16-byte aligned and q_stride a multiple of 8");
+    if (!aligned(out, 2) || !aligned(ws, 16) || !aligned(table, 4) || !aligned(ctx, 4) || !aligned(cu, 4) || !aligned(mask, 8))
+        return fail(QK_ERR_ALIGN, "out must be 2-byte aligned, ws 16, the int32 arrays 4 and mask 8");
+    const int64_t need = qk::attn_tree_ws_bytes(n_req, max_q, table_stride * page, n_heads, d);
+    if (ws_bytes < (size_t)need) return fail(QK_ERR_WORKSPACE, "workspace %zu bytes < %lld needed", ws_bytes, (long long)need);
+    unsigned* status = nullptr;
+    int sms = 0;
+    st = device_state(&status, &sms);
+    if (st != QK_OK) return st;
+    cudaError_t e = qk::launch_attn_tree(type, q, n_tok, q_stride, static_cast<const uint8_t*>(K),
+                                         static_cast<const uint8_t*>(V), n_pages, page_log2(page),
+                                         (int)qk_row_bytes(type, d), table, table_stride, ctx, cu, mask, n_req, max_q,
+                                         n_heads, n_kv, d, scale, out, out_stride, ws, status, sms,
+                                         static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_attn_tree launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
+qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* cu, int64_t n_req, const int32_t* hist, int64_t hist_stride,
+                            const int32_t* hist_len, const float* rep, const float* pres, const float* freq,
+                            const int32_t* draft, const uint64_t* mask, const int32_t* bias_tok, const float* bias_val,
+                            int64_t bias_stride, const int32_t* bias_len, const uint32_t* grammar, int64_t grammar_stride,
+                            void* out, int64_t out_stride, void* stream) {
+    if (dtype != QK_OUT_F32 && dtype != QK_OUT_BF16) return fail(QK_ERR_ARG, "bad dtype %d", dtype);
+    if (!count_ok(n_rows) || !count_ok(vocab) || !count_ok(n_req))
+        return fail(QK_ERR_SHAPE, "bad n_rows=%lld, vocab=%lld or n_req=%lld", (long long)n_rows, (long long)vocab,
+                    (long long)n_req);
+    if (n_rows == 0 || vocab == 0) return QK_OK;
+    if (row_stride < vocab || out_stride < vocab || !count_ok(row_stride) || !count_ok(out_stride))
+        return fail(QK_ERR_SHAPE, "bad strides row_stride=%lld out_stride=%lld", (long long)row_stride, (long long)out_stride);
+    if (hist_stride < 0 || hist_stride >= (1 << 20) - 64)
+        return fail(QK_ERR_SHAPE, "hist_stride=%lld outside 0..2^20-65", (long long)hist_stride);
+    if (bias_tok && (bias_stride < 0 || bias_stride > 4095))
+        return fail(QK_ERR_SHAPE, "bias_stride=%lld outside 0..4095", (long long)bias_stride);
+    if (grammar && (grammar_stride < (vocab + 31) / 32 || !count_ok(grammar_stride)))
+        return fail(QK_ERR_SHAPE, "grammar_stride=%lld below vocab / 32", (long long)grammar_stride);
+    if (!logits || !out || !cu || (n_req > 0 && (!hist_len || !rep || !pres || !freq || (hist_stride > 0 && !hist))) ||
+        (bias_tok && (!bias_val || !bias_len)))
+        return fail(QK_ERR_NULL, "NULL pointer argument");
+    const size_t es = dtype == QK_OUT_BF16 ? 2 : 4;
+    if (!aligned(logits, es) || !aligned(out, es)) return fail(QK_ERR_ALIGN, "logits and out must be aligned to their element");
+    for (const void* p : {(const void*)cu, (const void*)hist, (const void*)hist_len, (const void*)rep, (const void*)pres,
+                          (const void*)freq, (const void*)draft, (const void*)bias_tok, (const void*)bias_val,
+                          (const void*)bias_len, (const void*)grammar})
+        if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "the lists must be 4-byte aligned");
+    if (!aligned(mask, 8)) return fail(QK_ERR_ALIGN, "mask must be 8-byte aligned");
+    if (out == logits && out_stride != row_stride) return fail(QK_ERR_ARG, "in place needs out_stride == row_stride");
+    int sms = 0;
+    const qk_status st = device_state(nullptr, &sms);
+    if (st != QK_OK) return st;
+    const qk::LogitsArgs a{logits, dtype == QK_OUT_BF16, n_rows, vocab, row_stride, cu, n_req, hist, hist_stride, hist_len,
+                           rep, pres, freq, draft, mask, bias_tok, bias_val, bias_stride, bias_len, grammar,
+                           grammar_stride, out, out_stride};
+    cudaError_t e = qk::launch_logits_process(a, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_logits_process launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
 qk_status qk_device_status(void* stream) {
     unsigned* status = nullptr;
     qk_status st = device_state(&status, nullptr);
@@ -407,6 +609,7 @@ qk_status qk_device_status(void* stream) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "qk_device_status");
     if (v & 1u) return fail(QK_ERR_TIMEOUT, "a bounded wait inside a kernel ran out (status 0x%x)", v);
+    if (v & 2u) return fail(QK_ERR_ARG, "a page id or slot outside its KV pool (status 0x%x)", v);
     return QK_OK;
 }
 

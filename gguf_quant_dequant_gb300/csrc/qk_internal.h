@@ -59,6 +59,50 @@ cudaError_t launch_hgemv_tokens(int type, const uint8_t* W, int64_t rows, int64_
 cudaError_t launch_gemv(int type, const GemvPlan& plan, const uint8_t* W, int64_t rows, int64_t cols,
                         const float* x, int64_t M, float* y, unsigned* status, cudaStream_t s);
 
+// The paged KV cache (qk_kv.cu) and attention over it (qk_tree.cu).
+cudaError_t launch_kv_plan(const int32_t* have, const int32_t* start, const int32_t* want, int n_req, int page_log2,
+                           int32_t* table, int64_t table_stride, int32_t* free_pages, int64_t free_cap,
+                           const int32_t* n_free, int32_t* n_free_out, int32_t* granted, int32_t* cu, int64_t* slots,
+                           int32_t* pos, int32_t* req, int64_t cap, int sms, cudaStream_t s);
+cudaError_t launch_kv_append(int type, const void* k, const void* v, bool bf16, int64_t n_tok, int64_t k_stride,
+                             int64_t v_stride, int n_kv, int d, const int64_t* slots, uint8_t* K, uint8_t* V,
+                             int64_t n_pages, int page_log2, int row_bytes, unsigned* status, cudaStream_t s);
+cudaError_t launch_kv_compact(uint8_t* K, uint8_t* V, int64_t n_pages, int page_log2, int n_kv, int row_bytes,
+                              const int32_t* table, int64_t table_stride, const int32_t* base, const int32_t* path,
+                              int64_t path_stride, const int32_t* n_path, int64_t n_req, unsigned* status,
+                              cudaStream_t s);
+int64_t attn_tree_ws_bytes(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int d);
+cudaError_t launch_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const uint8_t* K, const uint8_t* V,
+                             int64_t n_pages, int page_log2, int row_bytes, const int32_t* table, int64_t table_stride,
+                             const int32_t* ctx, const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q,
+                             int n_heads, int n_kv, int d, float scale, void* out, int64_t out_stride, void* ws,
+                             unsigned* status, int sms, cudaStream_t s);
+
+// Penalties, biases and grammar masks on logits (qk_logits.cu); the members
+// are qk_logits_process's arguments.
+struct LogitsArgs {
+    const void* logits;
+    bool bf16;
+    int64_t n_rows, vocab, row_stride;
+    const int32_t* cu;
+    int64_t n_req;
+    const int32_t* hist;
+    int64_t hist_stride;
+    const int32_t* hist_len;
+    const float *rep, *pres, *freq;
+    const int32_t* draft;
+    const uint64_t* mask;
+    const int32_t* bias_tok;
+    const float* bias_val;
+    int64_t bias_stride;
+    const int32_t* bias_len;
+    const uint32_t* grammar;
+    int64_t grammar_stride;
+    void* out;
+    int64_t out_stride;
+};
+cudaError_t launch_logits_process(const LogitsArgs& a, int sms, cudaStream_t s);
+
 // One thread waiting on an mbarrier nothing arrives on (bounded by limit_ns).
 cudaError_t launch_stalled_wait(unsigned* status, uint64_t limit_ns, cudaStream_t s);
 

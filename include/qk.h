@@ -322,6 +322,172 @@ qk_status qk_gemm(int type, const void* W, int64_t rows, int64_t cols,
                   const void* X_bf16, int64_t M, float* Y,
                   void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A paged, block-quantized KV cache of many requests, and one verification
+ * step of speculative decoding over it.
+ *
+ * The cache is two pools (K and V) of n_pages pages.  A page holds `page`
+ * consecutive positions of one request for every kv head, head by head:
+ *   pool [n_pages][n_kv][page][d], each (page, head, position) row d / 32
+ *   blocks of a 32-weight type (Q8_0, Q5_0 or Q4_0),
+ * so one head's part of a page is contiguous and a multiple of 16 bytes (it
+ * is what attention fetches with one copy).  page is 16, 32, 64, 128 or 256;
+ * d is 32, 64, 128 or 256.  Position p of request r lives in page
+ * table[r * table_stride + p / page] at p % page; its slot is
+ * (page id) * page + p % page.  A pool needs n_pages * qk_kv_page_bytes
+ * bytes, 16-byte aligned.  Requests, lengths and tables are int32 arrays in
+ * device memory, so a step's launches need nothing from the host and can be
+ * captured into a graph.
+ *
+ * A page id or slot outside the pool is never followed: the row concerned is
+ * skipped (attention: not visible) and qk_device_status() then reports
+ * QK_ERR_ARG.  A slot of -1 is a token without a place and is skipped
+ * silently. */
+
+/* Most drafted tokens of one request (the width of a tree mask). */
+#define QK_TREE_MAX 64
+/* Most requests one qk_kv_plan call takes. */
+#define QK_PLAN_MAX_REQ 8192
+
+/* Bytes of one page of one pool; 0 when the type, n_kv, d or page is not one
+ * of the above. */
+size_t qk_kv_page_bytes(int type, int n_kv, int d, int page);
+
+/* Page bookkeeping of a step: requests whose lengths change give pages back
+ * and take pages, and every token to be written gets its slot.  One launch.
+ *   have   int32 [n_req]: positions the request holds pages for (before).
+ *   want   int32 [n_req]: positions it shall hold pages for (after); 0 frees
+ *          all of them.
+ *   start  int32 [n_req]: the first position to be written; the tokens of
+ *          request r are positions start[r] .. want[r] - 1 (none when
+ *          start[r] >= want[r]).
+ *   table  int32 [n_req, table_stride], updated in place: with P_old =
+ *          ceil(have / page) and P_new = ceil(want / page), entries P_old ..
+ *          P_new - 1 are written; no other entry changes (entries past a
+ *          request's pages are stale, not cleared).
+ *   free_pages int32 [free_cap]: a stack of free page ids, *n_free of them
+ *          (device int32).  The pages given back (in request order, each
+ *          request's by rising index) are pushed first; then each growing
+ *          request, in order, takes its pages from the top.  Only entries at
+ *          *n_free and above are written, and the count after the call goes
+ *          to *n_free_out, which must not be n_free itself: the call gives
+ *          the same results when repeated on the same buffers.
+ *   granted int32 [n_req]: 1, or 0 when the running sum of pages taken up to
+ *          and including this request exceeds what is free, or when its
+ *          numbers are not valid (negative, or more pages than table_stride).
+ *          A request that is refused keeps the pages it had.
+ *   cu     int32 [n_req + 1]: running sum of the requests' token counts (a
+ *          refused request's tokens count, an invalid request has none).
+ *   slots  int64 [cap], pos int32 [cap], req int32 [cap]: of token i (in
+ *          request order, positions rising) its slot (-1 when refused), its
+ *          position and its request; entries past the last token are -1.
+ *          Tokens past cap are not written.  pos and req may be NULL.
+ * All integers; the result does not depend on the launch.  n_req == 0 sets
+ * cu[0] = 0, *n_free_out = *n_free and the token arrays to -1.
+ * Errors: QK_ERR_SHAPE (negative sizes, n_req above QK_PLAN_MAX_REQ, a page
+ * size that is not listed), QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG (n_free_out
+ * == n_free). */
+qk_status qk_kv_plan(const int32_t* have, const int32_t* start, const int32_t* want, int64_t n_req, int page,
+                     int32_t* table, int64_t table_stride, int32_t* free_pages, int64_t free_cap, const int32_t* n_free,
+                     int32_t* n_free_out, int32_t* granted, int32_t* cu, int64_t* slots, int32_t* pos, int32_t* req,
+                     int64_t cap, void* stream);
+
+/* Quantize n_tok tokens' K and V rows into the cache (one launch for both).
+ *   k, v   [n_tok, n_kv, d], dtype QK_OUT_F32 or QK_OUT_BF16, aligned to the
+ *          element; k_stride and v_stride elements from token to token (at
+ *          least n_kv * d), so slices of a fused projection's output serve
+ *          as they are.  Rows that start on 16-byte boundaries are read
+ *          faster.
+ *   slots  int64 [n_tok]; -1 is skipped; the others are distinct.
+ * The blocks are byte for byte those qk_quantize writes for the same values.
+ * n_tok == 0 queues nothing.
+ * Errors: QK_ERR_TYPE, QK_ERR_SHAPE, QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG
+ * (dtype). */
+qk_status qk_kv_append(int type, const void* k, const void* v, int dtype, int64_t n_tok, int64_t k_stride, int64_t v_stride,
+                       int n_kv, int d, const int64_t* slots, void* K, void* V, int64_t n_pages, int page, void* stream);
+
+/* Keep the accepted path of each request's drafted tree: the rows at
+ * positions base[r] + path[r * path_stride + j] move to base[r] + j, for j <
+ * n_path[r], in both pools, as if all were read before any is written.
+ *   base, n_path int32 [n_req]; path int32 [n_req, path_stride], entries 0 ..
+ *   QK_TREE_MAX - 1.  n_path above path_stride or QK_TREE_MAX is cut to it;
+ *   a row whose source or target has no page is left as it is.
+ * Errors as qk_kv_append. */
+qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, int n_kv, int d, const int32_t* table,
+                        int64_t table_stride, const int32_t* base, const int32_t* path, int64_t path_stride,
+                        const int32_t* n_path, int64_t n_req, void* stream);
+
+/* Attention of a tree of drafted tokens over the paged cache: the tokens of
+ * all requests in one call.  Request r has tokens cu[r] .. cu[r + 1] - 1 (rows
+ * of q; n of them) and ctx[r] committed positions; the K and V rows of its
+ * token j are in the cache at position ctx[r] + j (qk_kv_append before).
+ * For token i of the request, query head h and kv head g = h / (n_heads /
+ * n_kv):
+ *   s_t = scale * sum_e q[i, h, e] K[t, g, e],   t < ctx[r]: every one,
+ *         t = ctx[r] + j: those with bit j of the token's mask set,
+ *   out[i, h] = sum_t softmax(s)_t V[t, g].
+ * A token that sees no position gives zeros.  What a token does not see
+ * never reaches its result, whatever it holds (NaN and infinities included);
+ * stale bytes past a request's last position are not read.
+ *   q      bf16 [n_tok, n_heads, d], q_stride elements from token to token (a
+ *          multiple of 8), 16-byte aligned.
+ *   ctx    int32 [n_req], cu int32 [n_req + 1] (non-decreasing, within 0 ..
+ *          n_tok).  Requests may have no tokens.
+ *   mask   uint64 [n_tok], bit j = the request's token j is visible (its own
+ *          bit included where it sees itself); NULL = a plain chain: token i
+ *          sees tokens 0 .. i.  n_req requests with one token each and mask
+ *          NULL is ordinary batched decoding.
+ *   max_q  at least the most tokens of one request, at most QK_TREE_MAX;
+ *          tokens past it are not computed.
+ *   out    bf16 [n_tok, n_heads, d], out_stride elements from token to token,
+ *          2-byte aligned; rows of no request are not written.
+ *   ws     at least qk_attn_tree_workspace(..) bytes, 16-byte aligned;
+ *          max_pos = table_stride * page.
+ * fp32 scores, softmax and sums.  Accuracy, with A the largest |scale| sum_e
+ * |q_e K_te| of a visible position: |out - out_exact| <= 2^-8 |out_exact| +
+ * (2^-10 (1 + A) + 2^-13) sum_t p_t |V[t]|, and near the rounding of the
+ * output in practice.  Cached values beyond fp16's range (|w| > 65504) may
+ * give infinities or NaN for the tokens that see them.
+ * n_tok == 0 or n_req == 0 queues nothing.  Errors: QK_ERR_TYPE,
+ * QK_ERR_SHAPE, QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_WORKSPACE. */
+size_t qk_attn_tree_workspace(int type, int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d);
+qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const void* K, const void* V,
+                       int64_t n_pages, int page, const int32_t* table, int64_t table_stride, const int32_t* ctx,
+                       const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q, int n_heads, int n_kv, int d,
+                       float scale, void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* Penalties for repeated tokens, biases and grammar masks on logits, as a
+ * sampler wants them before it picks.  Rows cu[r] .. cu[r + 1] - 1 belong to
+ * request r.  With c the number of times token v stands in the request's
+ * history and among the row's drafted ancestors,
+ *   y = x > 0 ? x / rep[r] : x * rep[r],  then  y - freq[r] * c - pres[r]   (c > 0; else y = x)
+ *   y + bias of token v (if listed),
+ *   -inf where the row's grammar bit of v is 0.
+ *   logits [n_rows, vocab], dtype QK_OUT_F32 or QK_OUT_BF16, aligned to the
+ *          element, row_stride elements from row to row; out likewise (its
+ *          own out_stride; out == logits with equal strides is fine, any
+ *          other overlap is not).  fp32 arithmetic, rounded once.
+ *   hist   int32 [n_req, hist_stride], the first hist_len[r] of them;
+ *          hist_stride below 2^20 - 64.  rep, pres, freq fp32 [n_req].
+ *   draft  int32 [n_rows], the drafted token of each row, and mask uint64
+ *          [n_rows] as in qk_attn_tree: bit j = the request's row j is an
+ *          ancestor (the row itself too, when its own bit is set).  mask NULL:
+ *          rows cu[r] .. the row itself.  draft NULL: no drafted tokens.
+ *   bias_tok int32, bias_val fp32 [n_req, bias_stride], the first
+ *          bias_len[r]; of entries with the same token the last counts;
+ *          bias_stride at most 4095; bias_tok NULL: no biases.
+ *   grammar uint32 [n_rows, grammar_stride], bit v % 32 of word v / 32; NULL:
+ *          no masks.
+ * Token ids outside 0 .. vocab - 1 are ignored.  Rows of no request get the
+ * grammar mask only.  Deterministic.  n_rows == 0 or vocab == 0 queues
+ * nothing.  Errors: QK_ERR_SHAPE, QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG. */
+qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* cu, int64_t n_req, const int32_t* hist, int64_t hist_stride,
+                            const int32_t* hist_len, const float* rep, const float* pres, const float* freq,
+                            const int32_t* draft, const uint64_t* mask, const int32_t* bias_tok, const float* bias_val,
+                            int64_t bias_stride, const int32_t* bias_len, const uint32_t* grammar, int64_t grammar_stride,
+                            void* out, int64_t out_stride, void* stream);
+
 /* Test hook: unpack nblocks consecutive blocks into their integer fields.
  *   codes int16 [nblocks * block_elems]: Q4_K 0..15, Q5_K 0..31, Q6_K 0..63,
  *         Q8_0 -128..127, Q5_0 0..31, Q4_0 0..15, Q2_K 0..3, Q3_K -4..3.
@@ -347,8 +513,9 @@ qk_status qk_unpack(int type, const void* W, int64_t nblocks, int16_t* codes,
 qk_status qk_test_stalled_wait(uint32_t limit_us, void* stream);
 
 /* Synchronize `stream`, then read and clear this device's kernel status
- * word: QK_OK, or QK_ERR_TIMEOUT when a bounded wait ran out since the last
- * call (the affected outputs are then invalid). */
+ * word: QK_OK, QK_ERR_TIMEOUT when a bounded wait ran out since the last
+ * call (the affected outputs are then invalid), or QK_ERR_ARG when a paged
+ * call met a page id or slot outside its pool. */
 qk_status qk_device_status(void* stream);
 
 /* ------------------------------------------------------------------------

@@ -518,7 +518,7 @@ static bool attn_tree_shape_ok(int64_t n_req, int max_q, int64_t max_pos, int n_
 
 size_t qk_attn_tree_workspace(int type, int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d) {
     if (!kv_type(type) || !attn_tree_shape_ok(n_req, max_q, max_pos, n_heads, n_kv, d)) return 0;
-    return (size_t)qk::attn_tree_ws_bytes(n_req, max_q, max_pos, n_heads, d);
+    return (size_t)qk::attn_tree_ws_bytes(n_req, max_q, max_pos, n_heads, n_kv, d, sm_count_or_default());
 }
 
 qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const void* K, const void* V,
@@ -540,8 +540,8 @@ qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride,
         return fail(QK_ERR_ALIGN, "q must be 16-byte aligned and q_stride a multiple of 8");
     if (!aligned(out, 2) || !aligned(ws, 16) || !aligned(table, 4) || !aligned(ctx, 4) || !aligned(cu, 4) || !aligned(mask, 8))
         return fail(QK_ERR_ALIGN, "out must be 2-byte aligned, ws 16, the int32 arrays 4 and mask 8");
-    const int64_t need = qk::attn_tree_ws_bytes(n_req, max_q, table_stride * page, n_heads, d);
-    if (ws_bytes < (size_t)need) return fail(QK_ERR_WORKSPACE, "workspace %zu bytes < %lld needed", ws_bytes, (long long)need);
+    const size_t need = qk_attn_tree_workspace(type, n_req, max_q, table_stride * page, n_heads, n_kv, d);
+    if (ws_bytes < need) return fail(QK_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     unsigned* status = nullptr;
     int sms = 0;
     st = device_state(&status, &sms);

@@ -428,7 +428,7 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
  *   out[i, h] = sum_t softmax(s)_t V[t, g].
  * A token that sees no position gives zeros.  What a token does not see
  * never reaches its result, whatever it holds (NaN and infinities included);
- * stale bytes past a request's last position are not read.
+ * stale bytes past a request's last position are not used.
  *   q      bf16 [n_tok, n_heads, d], q_stride elements from token to token (a
  *          multiple of 8), 16-byte aligned.
  *   ctx    int32 [n_req], cu int32 [n_req + 1] (non-decreasing, within 0 ..
@@ -445,9 +445,9 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
  *          max_pos = table_stride * page.
  * fp32 scores, softmax and sums.  Accuracy, with A the largest |scale| sum_e
  * |q_e K_te| of a visible position: |out - out_exact| <= 2^-8 |out_exact| +
- * (2^-10 (1 + A) + 2^-13) sum_t p_t |V[t]|, and near the rounding of the
- * output in practice.  Cached values beyond fp16's range (|w| > 65504) may
- * give infinities or NaN for the tokens that see them.
+ * (2^-10 (1 + A) + 2^-13) sum_t p_t |V[t]| + 2^-32 sum_t |V[t]|, and near
+ * the rounding of the output in practice.  Cached K values beyond fp16's
+ * range (|w| > 65504) may give NaN for the tokens that see them.
  * n_tok == 0 or n_req == 0 queues nothing.  Errors: QK_ERR_TYPE,
  * QK_ERR_SHAPE, QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_WORKSPACE. */
 size_t qk_attn_tree_workspace(int type, int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d);

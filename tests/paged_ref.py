@@ -64,10 +64,10 @@ def visible(mask, n: int, i: int):
 def attn_tree(name, q, K, V, page, n_kv, table, ctx, cu, mask, max_q, scale):
     """q fp64 [n_tok, heads, d]; K, V byte pools [n_pages, n_kv, page, row
     bytes]; mask uint64 or None.  Returns (out, sum p|V|, max_t |scale| sum
-    |q k|), NaN in rows that no request has."""
+    |q k|, sum |V| of the visible); out is NaN in rows that no request has."""
     n_tok, heads, d = q.shape
     G = heads // n_kv
-    out, Sv = np.full(q.shape, np.nan), np.zeros(q.shape)
+    out, Sv, V1 = np.full(q.shape, np.nan), np.zeros(q.shape), np.zeros(q.shape)
     A = np.zeros((n_tok, heads))
     for r in range(len(ctx)):
         n = min(int(cu[r + 1] - cu[r]), max_q)
@@ -90,7 +90,8 @@ def attn_tree(name, q, K, V, page, n_kv, table, ctx, cu, mask, max_q, scale):
                     w = e / e.sum()
                     out[tok, h] = w @ v[see]
                     Sv[tok, h] = w @ np.abs(v[see])
-    return out, Sv, A
+                    V1[tok, h] = np.abs(v[see]).sum(0)
+    return out, Sv, A, V1
 
 
 def logits(x, cu, hist, hist_len, rep, pres, freq, draft=None, mask=None, bias_tok=None, bias_val=None, bias_len=None,

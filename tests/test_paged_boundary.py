@@ -184,7 +184,7 @@ def test_plain_tree_equals_the_oracles_decode_attention(oracle_mod):
     n_kv, heads, d, page, T = 2, 6, 64, 16, 37
     K, V = (paged_ref.pool("Q5_0", 3, n_kv, page, d, s) for s in (1, 2))
     q = synth.activations(heads, d, 3).reshape(1, heads, d)
-    out, Sv, _ = paged_ref.attn_tree("Q5_0", q.astype(np.float64), K, V, page, n_kv, np.array([[0, 1, 2]]), [T - 1], [0, 1], None, 1,
+    out, Sv, _, _ = paged_ref.attn_tree("Q5_0", q.astype(np.float64), K, V, page, n_kv, np.array([[0, 1, 2]]), [T - 1], [0, 1], None, 1,
                                      0.125)
     flat = lambda p: np.ascontiguousarray(p.transpose(0, 2, 1, 3)).reshape(-1, n_kv, p.shape[-1])[:T].reshape(-1)  # noqa: E731
     ref, Sr = oracle.attn_decode(qk.Q5_0, q[0], flat(K), flat(V), T, heads, n_kv, d, 0.125)
@@ -196,10 +196,10 @@ def test_plain_tree_masks():
     q = synth.activations(3, 32, 6).reshape(3, 1, 32).astype(np.float64)
     table = np.array([[1]])
     args = (q, K, V, 16, 1, table, [0], [0, 3])
-    full, _, _ = paged_ref.attn_tree("Q8_0", *args, np.array([1, 3, 7], np.uint64), 3, 0.3)
-    chain, _, _ = paged_ref.attn_tree("Q8_0", *args, None, 3, 0.3)
+    full, *_ = paged_ref.attn_tree("Q8_0", *args, np.array([1, 3, 7], np.uint64), 3, 0.3)
+    chain, *_ = paged_ref.attn_tree("Q8_0", *args, None, 3, 0.3)
     assert np.array_equal(full, chain)
-    alone, _, _ = paged_ref.attn_tree("Q8_0", *args, np.array([0, 2, 0], np.uint64), 3, 0.3)
+    alone, *_ = paged_ref.attn_tree("Q8_0", *args, np.array([0, 2, 0], np.uint64), 3, 0.3)
     assert not alone[0].any() and not alone[2].any()
     assert np.allclose(alone[1, 0], paged_ref.values("Q8_0", V[1, 0, 1], 32))
 

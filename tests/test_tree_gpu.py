@@ -7,7 +7,9 @@ the output to bf16 (2^-8 of it); each probability and each V element to fp16
 (2^-11 each, together 2^-10 of sum p|V|); each K element to fp16, which moves a
 score by at most 2^-11 A (A the largest scale * sum |q k| of a visible
 position) and a probability by twice that, 2^-10 A of sum p|V|; 2^-13 for the
-fp32 sums and exponentials."""
+fp32 sums and exponentials; and where a probability is too small for fp16 (it
+is held times 2^7 at least, against the row's largest), half a step, 2^-32 of
+its |V|."""
 import numpy as np
 import pytest
 import torch
@@ -53,14 +55,14 @@ def to_dev(c, gpu):
 
 
 def check(c, out, ref=None):
-    ref, Sv, A = ref or paged_ref.attn_tree(c["name"], c["q"].double().numpy(), c["K"], c["V"], c["page"], c["n_kv"], c["table"],
+    ref, Sv, A, V1 = ref or paged_ref.attn_tree(c["name"], c["q"].double().numpy(), c["K"], c["V"], c["page"], c["n_kv"], c["table"],
                                             c["ctx"], c["cu"], c["mask"], c["max_q"], c["scale"])
     got = out.float().cpu().numpy().astype(np.float64)
     rows = ~np.isnan(ref).all(axis=(1, 2))
-    tol = 2.0**-8 * np.abs(ref) + (2.0**-10 * (1 + A[..., None]) + 2.0**-13) * Sv + 1e-30
+    tol = 2.0**-8 * np.abs(ref) + (2.0**-10 * (1 + A[..., None]) + 2.0**-13) * Sv + 2.0**-32 * V1 + 1e-30
     bad = ~(np.abs(got - ref) <= tol)[rows]
     assert not bad.any(), f"{bad.sum()} outputs off, worst {np.nanmax((np.abs(got - ref) / tol)[rows]):.3g} of the tolerance"
-    return ref, Sv, A
+    return ref, Sv, A, V1
 
 
 def run(c, gpu):

@@ -513,7 +513,8 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
 static bool attn_tree_shape_ok(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d) {
     return n_req >= 0 && n_req <= 65535 && max_q >= 1 && max_q <= QK_TREE_MAX && max_pos >= 0 &&
            max_pos <= kCountMax * 256 && n_kv >= 1 && n_kv <= 4096 && n_heads >= n_kv && n_heads % n_kv == 0 &&
-           n_heads / n_kv <= 64 && (d == 32 || d == 64 || d == 128 || d == 256);
+           n_heads / n_kv <= 64 && (d == 32 || d == 64 || d == 128 || d == 256) &&
+           qk::attn_tree_max_tiles(n_req, max_q, max_pos, n_heads, n_kv, d) < 2147000000.0;   // counted in 32 bits
 }
 
 size_t qk_attn_tree_workspace(int type, int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d) {

@@ -72,6 +72,7 @@ cudaError_t launch_kv_compact(uint8_t* K, uint8_t* V, int64_t n_pages, int page_
                               int64_t path_stride, const int32_t* n_path, int64_t n_req, unsigned* status,
                               cudaStream_t s);
 int64_t attn_tree_ws_bytes(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d, int sms);
+double attn_tree_max_tiles(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d);
 cudaError_t launch_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const uint8_t* K, const uint8_t* V,
                              int64_t n_pages, int page_log2, int row_bytes, const int32_t* table, int64_t table_stride,
                              const int32_t* ctx, const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q,

@@ -14,23 +14,27 @@
 //
 // Both products have the positions (or d) as their 128-row side and the rows
 // as N, which costs what the rows need (N = 16 .. 64) instead of 128:
-//   S^T [positions x rows] = K [positions x d] Q^T     A = K, B = Q, K-major
-//   O^T [d x rows]        += V^T [d x positions] P     A = V, B = P, MN-major
-// K and V tiles are decoded once per unit to fp16 (code * d, one rounding) and
-// serve both as they lie, [position][d] in 128-byte swizzled rows; no
-// transposition anywhere.  A softmax thread owns one position and all rows of
-// a tile.  Row maxima are needed only as a reference: a tile keeps the
-// present reference unless some score exceeds it by 2^8 (one vote), and only
-// then the new maxima are found and O and the sums are rescaled, so the
-// ordinary tile has no reduction across threads; the rows' sums of
-// probabilities stay per thread until the unit's end.
+//   S^T [positions x rows] = K [positions x d] Q^T     A = K from tensor memory, B = Q
+//   O^T [d x rows]        += V^T [d x positions] P     A = V, B = P, MN-major in shared memory
+// K and V tiles are decoded once per unit to fp16 (code * d, one rounding): K
+// straight into tensor memory, a lane per position; V as it lies, [position]
+// [d] in 128-byte swizzled rows.  No transposition anywhere.  A softmax thread
+// owns one position and half of the rows of a tile.  Row maxima are needed
+// only as a reference: a tile keeps the present reference unless some score
+// exceeds it by 2^8 (one vote), and only then the new maxima are found and O
+// and the sums are rescaled, so the ordinary tile has no reduction across
+// threads; the rows' sums of probabilities stay per thread until the unit's
+// end.
 //
 // Warps: 0 copies (cp.async.bulk of the pages' contiguous head slabs into a
-// ring), 1 issues the MMAs, 2-3 load the unit's queries, 4-7 softmax and
-// epilogue (TMEM lanes), 8-15 decode.  Every hand-over is an mbarrier with a
-// bounded wait; after a wait has run out (status word) the copies and MMAs
-// stop, the other roles run through without waiting, and the CTA leaves in
-// order.
+// ring), 1 issues Q K, 2 issues P V, 3 looks at the V scales; 4-11 softmax and
+// epilogue (two warpgroups, half of the rows each); 12-19 decode K; 20-27
+// decode V and load the unit's queries.  A tile is a chain of short steps, so
+// it is the number of warps on it that sets the rate: with one warpgroup each
+// for softmax and (K and V) decoding a tile took 5,000 clocks.  Every hand-over
+// is an mbarrier with a bounded wait; after a wait has run out (status word)
+// the copies and MMAs stop, the other roles run through without waiting, and
+// the CTA leaves in order.
 //
 // What is not visible never reaches a result: a masked score is replaced, not
 // added to; rows past the end are decoded as zeros; a V block whose scale is
@@ -52,15 +56,16 @@
 namespace qk {
 namespace tree {
 
-constexpr int kRows = 64;        // rows of a unit, at most (N of the MMAs)
-constexpr int kDq = 8;           // decoding warps
-constexpr int kThreads = (8 + kDq) * 32;
-constexpr int kH = 3;            // fp16 tile buffers (K and V tiles alternate)
-constexpr int kTmem = 512;       // columns: S^T twice 64, O^T 128 (two halves of d = 256), the same for large V tiles
-constexpr int kTmemO = 128, kTmemBig = 256;
+constexpr int kThreads = 28 * 32;
+constexpr int kSm = 4, kKd = 12, kVd = 20;   // first warps of softmax, K and V decoding
+constexpr int kDw = 8;                       // warps of each of these
+constexpr int kV = 2;                        // V tile buffers
+// Tensor memory: S^T twice 64 columns, O^T 64 (or two halves of 32 at d = 256), the large V tiles' O^T, K twice d / 2.
+constexpr int kTmem = 512, kTmemO = 128, kTmemBig = 192, kTmemK = 256;
 constexpr float kBig = 128.0f;   // scale of the large V tiles
 constexpr float kLift = 7.0f;    // probabilities are held times 2^7 (fp16 keeps 2^-21 of the maximum at full precision)
 constexpr float kOver = 15.0f;   // and stay below 2^15
+constexpr int kRows = 64;        // most rows of a unit
 
 struct Args {
     const __nv_bfloat16* q;
@@ -71,7 +76,7 @@ struct Args {
     int64_t table_stride;
     const int32_t *ctx, *cu;
     const uint64_t* mask;
-    int n_req, max_q, G, n_heads;
+    int n_req, max_q, G;
     float scale;
     __nv_bfloat16* out;
     int64_t out_stride;
@@ -80,16 +85,21 @@ struct Args {
     unsigned* status;
 };
 
+// A request: its first token's row, its tokens, its committed positions and
+// the positions walked (those past the table's end do not exist: they are
+// reported, and not walked).
 struct Req {
-    int64_t tok0;
-    int64_t ctx;
-    int n;
+    int tok0, n, ctx, len;
 };
 __device__ __forceinline__ Req req_of(const Args& a, int r) {
     Req q;
-    q.tok0 = min(max((int64_t)a.cu[r], (int64_t)0), a.n_tok);
-    q.n = (int)min(max(min((int64_t)a.cu[r + 1], a.n_tok) - q.tok0, (int64_t)0), (int64_t)a.max_q);
-    q.ctx = max(a.ctx[r], 0);
+    const int n_tok = (int)a.n_tok;
+    q.tok0 = min(max(a.cu[r], 0), n_tok);
+    q.n = min(max(min(a.cu[r + 1], n_tok) - q.tok0, 0), a.max_q);
+    const int64_t ctx = max(a.ctx[r], 0), cap = a.table_stride << a.pool.page_log2;
+    q.ctx = (int)min(ctx, cap);
+    q.len = (int)min(ctx + q.n, cap);
+    if (q.n > 0 && ctx + q.n > cap) atomicOr(a.status, STATUS_BAD_PAGE);
     return q;
 }
 // The drafted tokens that token i of the request sees.
@@ -101,90 +111,90 @@ __device__ __forceinline__ uint64_t seen_of(const Args& a, const Req& q, int i) 
 // Geometry of one instantiation.
 template <int T, int D> struct Geo {
     static constexpr int BN = D == 256 ? 64 : 128;         // positions per tile
+    static constexpr int NR = D == 256 ? 32 : 64;          // rows of a unit, at most
     static constexpr int NB = D / 32;                      // blocks per row
     static constexpr int RB = NB * Fmt<T>::BB;             // bytes per row
     static constexpr int CH = D <= 64 ? 1 : D / 64;        // 64-element chunks of a row
     static constexpr int CHB = BN * 128;                   // bytes of a chunk: BN rows of 128
-    static constexpr int HB = CH * CHB;                    // an fp16 tile
-    static constexpr int QB = CH * kRows * 128;            // the unit's queries
+    static constexpr int VB = CH * CHB;                    // a V tile
+    static constexpr int QB = CH * NR * 128;               // the unit's queries
     static constexpr int PB = BN * 128;                    // one P tile
-    static constexpr int RAW = BN * RB + 16;               // a packed tile
-    static constexpr int SEGS = BN * D / 64;               // 64-element segments of a tile
-    static constexpr int SPW = D <= 64 ? 32 : 2048 / D;    // segments across, per decoding warp
-    static constexpr int PPS = D == 32 ? 2 : 1;            // positions per segment
-    static constexpr int FIXED = kH * HB + QB + 2 * PB;
-    static constexpr int MISC = 8192;
+    static constexpr int RAW = BN * RB + 16;               // a packed tile (word loads may read 2 bytes past it)
+    static constexpr int ITEM = D == 32 ? 32 : 64;         // elements a decoding thread takes at once
+    static constexpr int ITEMS = BN * D / ITEM;            // of them in a tile
+    static constexpr int IPR = D / ITEM;                   // in a row
+    static constexpr int KC = D / 2;                       // tensor-memory columns of a K tile
+    static constexpr int FIXED = kV * VB + QB + 2 * PB;
+    static constexpr int MISC = 10240;
     static constexpr int NS0 = (227 * 1024 - 1024 - MISC - FIXED) / RAW;
-    static constexpr int NS = NS0 > 8 ? 8 : NS0;           // ring stages
+    static constexpr int NS = (NS0 > 8 ? 8 : NS0) & ~1;    // ring stages; even: V tiles always take the odd ones
     static constexpr int SMEM = 1024 + FIXED + NS * RAW + MISC;
-    static_assert(NS >= 2 && RAW % 16 == 0, "tree attention's ring");
-    // A partial result: O [rows][D], reference and sum per row.
-    static constexpr int64_t PART = (int64_t)kRows * (D + 2) * 4;
+    static_assert(NS >= 4 && RAW % 16 == 0, "tree attention's ring");
 };
+// A partial result: O [rows][D], reference and sum per row.
+template <int D> __host__ __device__ constexpr int64_t part_bytes() { return (int64_t)kRows * (D + 2) * 4; }
 
 struct __align__(16) Misc {
     float cmul[kRows];           // scale * log2 e * 2^e of the row's query
     float cref[kRows];           // kLift less the row's reference
-    uint64_t seen[4][kRows];     // by unit mod 4
+    uint64_t seen[4][kRows];     // by unit mod 4, as the next two
     float colc[4][kRows];
+    int64_t rowoff[4][kRows];    // the row's place in out
     uint4 valid[16];             // by tile mod 16: bit per position that exists
     float ref[kRows], factor[kRows];
     float wsum[4][kRows];
-    int wmax[4][kRows];
-    unsigned long long bad_draft[4][8];   // by unit mod 4, 32-block: drafted V rows that are not finite
-    unsigned bad_ctx[4][8];
+    float wmax[4][kRows];
+    unsigned long long bad_draft[8][8];   // by unit mod 8, 32-block: drafted V rows that are not finite
+    unsigned bad_ctx[8][8];
     unsigned big_tile[16];       // by tile mod 16: the V tile is decoded times 2^-7
-    unsigned used[4];            // by unit mod 4: bit 0 the plain sums, bit 1 the large tiles' sums hold something
-    uint64_t raw_full[8], raw_empty[8], h_full[kH], h_empty[kH], s_full[2], s_empty[2], p_full[2], pv_done[2];
-    uint64_t q_full, q_empty, o_empty, drain;
-    long long scan[16];
-    long long start_base;
-    int start_r, abort;
+    unsigned used[8];            // by unit mod 8: bit 0 the plain sums, bit 1 the large tiles' sums hold something
+    uint64_t raw_full[8], raw_empty[8], v_ok[8], k_full[2], k_empty[2], v_full[kV], v_empty[kV], s_full[2], s_empty[2],
+        p_full[2], pv_done[2];
+    uint64_t q_full, q_empty, o_empty, drain[2];
+    int scan[32];
+    Req start_q;
+    int start_base, start_r, abort;
     uint32_t tmem;
 };
-static_assert(sizeof(Misc) <= 8192, "Misc");
+static_assert(sizeof(Misc) <= 10240, "Misc");
 
 // ------------------------------------------------------- the work list ----
+// Counts of tiles stay inside 31 bits (the host refuses more).
 
-__device__ __forceinline__ int tiles_of(const Req& q, int bn) { return (int)((q.ctx + q.n + bn - 1) / bn); }
-__device__ __forceinline__ int groups_of(const Req& q, int G) { return (q.n * G + kRows - 1) / kRows; }
-__device__ __forceinline__ int64_t work_of(const Args& a, const Req& q, int bn) {
-    return q.n ? (int64_t)a.pool.n_kv * groups_of(q, a.G) * tiles_of(q, bn) : 0;
+__device__ __forceinline__ int tiles_of(const Req& q, int bn) { return (q.len + bn - 1) / bn; }
+__device__ __forceinline__ int groups_of(const Req& q, int G, int nr) { return (q.n * G + nr - 1) / nr; }
+template <int BN, int NR> __device__ __forceinline__ int work_of(const Args& a, const Req& q) {
+    return q.n ? a.pool.n_kv * groups_of(q, a.G, NR) * max(tiles_of(q, BN), 1) : 0;
 }
 // Columns (N of the MMAs) a unit of that many rows takes.
 __device__ __forceinline__ int cols_of(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
+// A piece of a unit: request, kv head, rows, tiles [t0, t1) of nt.
 struct Piece {
-    Req q;
-    int r, g, row0, rows;    // the unit: request, kv head, its rows
-    int t0, t1, nt;          // tiles [t0, t1) of its nt
-    int64_t u0;              // place of its tile 0 in the work list
+    int r, g, row0, rows, t0, t1, nt, u0;   // u0: place of its tile 0 in the work list
 };
-// The pieces of the run [x, end) of the list, from request r whose tiles
+// The pieces of the run [x, end) of the list; the present request r's tiles
 // start at base.
-struct Walk {
-    int64_t x, end, base;
-    int r;
-    __device__ __forceinline__ bool next(const Args& a, int bn, Piece& p) {
+template <int BN, int NR> struct Walk {
+    int x, end, base, r;
+    Req q;
+    __device__ __forceinline__ bool next(const Args& a, Piece& p) {
         if (x >= end) return false;
-        Req q = req_of(a, r);
-        int64_t w = work_of(a, q, bn);
+        int w = work_of<BN, NR>(a, q);
         while (x >= base + w) {
             base += w;
             q = req_of(a, ++r);
-            w = work_of(a, q, bn);
+            w = work_of<BN, NR>(a, q);
         }
-        const int nt = tiles_of(q, bn), gr = groups_of(q, a.G);
-        const int64_t rel = x - base;
-        const int unit = (int)(rel / nt);
-        p.q = q;
+        const int nt = max(tiles_of(q, BN), 1), gr = groups_of(q, a.G, NR);
+        const int rel = x - base, unit = rel / nt;
         p.r = r;
         p.g = unit / gr;
-        p.row0 = (unit - p.g * gr) * kRows;
-        p.rows = min(kRows, q.n * a.G - p.row0);
+        p.row0 = (unit - p.g * gr) * NR;
+        p.rows = min(NR, q.n * a.G - p.row0);
         p.nt = nt;
-        p.t0 = (int)(rel - (int64_t)unit * nt);
-        p.t1 = (int)min((int64_t)nt, p.t0 + (end - x));
+        p.t0 = rel - unit * nt;
+        p.t1 = min(nt, p.t0 + (end - x));
         p.u0 = x - p.t0;
         x += p.t1 - p.t0;
         return true;
@@ -196,8 +206,7 @@ struct Walk {
 struct __align__(16) Cut {
     int rows, first, last;   // rows; CTAs of its first and last piece
     int first_slot;          // 2 c + (0: the piece starts at the CTA's run, 1: later)
-    long long tok0;
-    int row0, g;
+    int tok0, row0, g, pad;
 };
 
 // ------------------------------------------------------------- PTX bits ----
@@ -215,6 +224,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The warp's largest (NaN aside).
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
 // Packed fp32 pairs (each half rounded as by itself).
@@ -244,43 +259,53 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// Barrier of the four softmax warps; true where any of their threads asks.
-__device__ __forceinline__ bool vote_softmax(bool any) {
+// Barriers 1 and 2: one softmax warpgroup each.
+__device__ __forceinline__ bool vote_group(int wg, bool any) {   // true where any of its threads asks
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)any)
+        : "r"((uint32_t)any), "r"(1 + wg)
         : "memory");
     return r != 0;
 }
-// The same of the eight decoding warps.
-__device__ __forceinline__ bool vote_decode(bool any) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 2, 256, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)any)
-        : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void sync_softmax() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void sync_group(int wg) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+// This warp's 32 TMEM lanes, N = 8 or 16 consecutive columns each.
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&v)[16]) { tc::tmem_ld16(t, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(t)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(taddr),
+        "%16};" ::"r"(t),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] x B[smem]^T; issued by one thread.
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 
 // Instruction descriptor: fp16 A and B (format 0), fp32 D, M = 128; bits 15
 // and 16 mark A and B as MN-major.
@@ -302,8 +327,10 @@ __device__ __forceinline__ void bulk_g2s_keep(void* dst, const void* src, uint32
         : "memory");
 }
 
-// A wait of the roles that run on after a failure: no waiting once *abort is set.
-__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
+// A wait of the roles that run on after a failure: no waiting once *abort is
+// set.  One lane polls, the warp waits for it.
+__device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1; i < kWaitSpins; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -314,10 +341,9 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, unsign
     atomicOr(status, STATUS_TIMEOUT);
     return false;
 }
-// The same for a whole warp: one lane polls, the others wait for it.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Args& a, volatile int* abort) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
     int ok = 1;
-    if ((threadIdx.x & 31) == 0 && !mbar_try_wait(bar, parity)) ok = wait_long(bar, parity, a.status, abort);
+    if ((threadIdx.x & 31) == 0) ok = wait_lane(bar, parity, status, abort);
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
@@ -337,20 +363,27 @@ __device__ __forceinline__ int element_of(int slot) {
 // Largest code magnitude.
 template <int T> __host__ __device__ constexpr float code_max() { return T == T_Q8_0 ? 128.0f : (T == T_Q5_0 ? 16.0f : 8.0f); }
 
-// A segment is 64 elements, two blocks: 17, 9 or 11 words from a 4-byte
-// aligned shared address (rows are whole segments, except that at d = 32 a
-// segment is two rows).
-template <int T> struct Seg {
-    static constexpr int BYTES = 2 * Fmt<T>::BB, W = BYTES / 4;
+// What a decoding thread takes at once: 64 elements, two blocks (17, 9 or 11
+// words from a 4-byte aligned shared address), or at d = 32 one block, which
+// starts on a word or 2 bytes into one.
+template <int T, int D> struct Item {
+    static constexpr int BB = Fmt<T>::BB, NBLK = D == 32 ? 1 : 2, BYTES = NBLK * BB, W = D == 32 ? (BB + 2) / 4 : BYTES / 4;
     uint32_t w[W];
-    __device__ __forceinline__ explicit Seg(const uint8_t* p) {
+    bool odd;   // d = 32: the block starts 2 bytes into w[0]
+    __device__ __forceinline__ explicit Item(const uint8_t* p) {
+        odd = D == 32 && (reinterpret_cast<uintptr_t>(p) & 2);
+        if (odd) p -= 2;
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = hm::lds32(p + 4 * i);
     }
-    // Scale bits of block b (0, 1); word i past block b's scale.
-    __device__ __forceinline__ uint32_t scale(int b) const { return b ? w[Fmt<T>::BB / 4] >> 16 : w[0] & 0xffffu; }
+    // Scale bits of block b; word i past block b's scale.
+    __device__ __forceinline__ uint32_t scale(int b) const {
+        return b ? w[BB / 4] >> 16 : (odd ? w[0] >> 16 : w[0] & 0xffffu);
+    }
     __device__ __forceinline__ uint32_t word(int b, int i) const {
-        return b ? w[(Fmt<T>::BB + 2) / 4 + i] : __funnelshift_r(w[i], w[i + 1], 16);
+        if (b) return w[(BB + 2) / 4 + i];
+        const uint32_t x = __funnelshift_r(w[i], w[i + 1], 16);
+        return D == 32 && odd ? w[i + 1] : x;
     }
     // Chunk k (0..3) of block b: code (exact) * d; a large tile takes the
     // code times 2^-7, still exact.
@@ -386,249 +419,217 @@ template <int T> struct Seg {
 
 // -------------------------------------------------------------- softmax ----
 
-// Sums over the warp of v[0 .. 16 NC): lane l gets the sums of columns l (and
-// l + 32) in v[0] (and v[1]), by exchanging halves.
-template <int NC>
-__device__ __forceinline__ void warp_sums(float (&v)[16 * NC], int lane) {
-    constexpr int C = 16 * NC;
-    if constexpr (C == 16) {   // a 32-wide exchange starts with the two halves adding up
+// Sums over the warp of v[0 .. C): lane l gets column l mod C in v[0], by
+// exchanging halves.
+template <int C>
+__device__ __forceinline__ void warp_sums(float (&v)[C], int lane) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    for (int o = 16; o >= C; o >>= 1)
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1)
+        for (int i = 0; i < C; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 #pragma unroll
-            for (int i = 0; i < o; ++i) {
-                const bool up = lane & o;
-                const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            }
-    } else {
+    for (int o = C / 2; o >= 1; o >>= 1)
 #pragma unroll
-        for (int h = 0; h < C; h += 32)
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-                for (int i = 0; i < o; ++i) {
-                    const bool up = lane & o;
-                    const float give = up ? v[h + i] : v[h + i + o], keep = up ? v[h + i + o] : v[h + i];
-                    v[h + i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
-        if constexpr (C == 64) v[1] = v[32];
-    }
+        for (int i = 0; i < o; ++i) {
+            const bool up = lane & o;
+            const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
 }
 
-// One piece of a unit by the softmax warps, with 16 NC columns (rows) live.
-// tile: running count of the CTA's tiles; unit: of its pieces.
-template <int T, int D, int NC>
-__device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* sp, uint32_t tmem, const Piece& p, uint32_t& tile,
-                                              uint32_t unit, uint8_t* part) {
+// One piece of a unit by a softmax warpgroup (wg 0, 1), which has C columns
+// (rows): C wg .. C wg + C - 1.  tile: running count of the CTA's tiles; unit:
+// of its pieces.
+template <int T, int D, int C>
+__device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* sp, uint32_t tmem, const Piece& p, int ctx,
+                                              uint32_t& tile, uint32_t unit, uint8_t* part, int wg) {
     using G = Geo<T, D>;
-    constexpr int C = 16 * NC;
-    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, tid = 32 * wq + lane;
+    constexpr int CW = C < 16 ? C : 16;   // columns of a tensor-memory access
+    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, tid = 32 * wq + lane, c0 = C * wg;
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
-    const uint64_t* seen = m.seen[unit & 3];
+    const uint64_t* seen = m.seen[unit & 3] + c0;
     volatile int* abort = &m.abort;
     uint64_t l2[C / 2];   // this thread's sums of probabilities, columns in pairs
 #pragma unroll
     for (int c = 0; c < C / 2; ++c) l2[c] = 0;
 #pragma unroll 1
     for (int t = p.t0; t < p.t1; ++t, ++tile) {
-        const uint32_t b = tile & 1, ph = (tile >> 1) & 1;
-        wait_warp(&m.s_full[b], ph, a, abort);
+        const uint32_t b = tile & 1;
+        wait_warp(&m.s_full[b], (tile >> 1) & 1, a.status, abort);
         tc::fence_after_sync();
-        uint32_t s[C];
+        uint32_t s[C];   // scores, then probabilities
+        auto load = [&] {
 #pragma unroll
-        for (int h = 0; h < C; h += 16) tc::tmem_ld16(lanes + 64 * b + h, *reinterpret_cast<uint32_t(*)[16]>(&s[h]));
-        const int64_t pos0 = (int64_t)t * G::BN, pos = pos0 + tid;
+            for (int h = 0; h < C; h += CW) tmem_ld(lanes + 64 * b + c0 + h, *reinterpret_cast<uint32_t(*)[CW]>(&s[h]));
+        };
+        load();
+        const int pos0 = t * G::BN;
         const uint4 vw = m.valid[tile & 15];
+        const bool all = pos0 + G::BN <= ctx && (vw.x & vw.y) == 0xffffffffu && (G::BN == 64 || (vw.z & vw.w) == 0xffffffffu);
         const uint32_t mine = wq == 0 ? vw.x : wq == 1 ? vw.y : wq == 2 ? vw.z : vw.w;
         const bool here = (mine >> lane) & 1;   // the position exists (false past BN)
-        const bool all = pos0 + G::BN <= p.q.ctx && (vw.x & vw.y) == 0xffffffffu &&
-                         (G::BN == 64 || (vw.z & vw.w) == 0xffffffffu);
-        const int64_t j = pos - p.q.ctx;   // drafted token at this position, if >= 0
+        const int j = pos0 + tid - ctx;         // drafted token at this position, if >= 0
         // Visibility of this position to column c.
         auto vis = [&](int c) { return here && (j < 0 || ((seen[c] >> (j & 63)) & 1)); };
-        tc::tmem_wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m.s_empty[b]);   // S^T has been read
         const bool first = t == p.t0;
-        // log2 of the lifted probabilities of columns c .. c + 3
-        auto logs = [&](int c, float (&x)[4]) {
-            const float4 k = *reinterpret_cast<const float4*>(&m.cmul[c]), r = *reinterpret_cast<const float4*>(&m.cref[c]);
-            const float2 u = unpair(fma2(pair(s[c], s[c + 1]), pair(k.x, k.y), pair(r.x, r.y)));
-            const float2 v = unpair(fma2(pair(s[c + 2], s[c + 3]), pair(k.z, k.w), pair(r.z, r.w)));
-            x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
-        };
-        bool over = first;
-        if (!first) {
+        // Scores to probabilities (lifted) on the present references; the
+        // largest of their logarithms.
+        auto probabilities = [&](auto masked) {
             float mx = -INFINITY;
-            if (all) {
 #pragma unroll
-                for (int c = 0; c < C; c += 4) {
-                    float x[4];
-                    logs(c, x);
-                    mx = fmaxf(fmaxf(mx, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
+            for (int c = 0; c < C; c += 4) {
+                const float4 k = *reinterpret_cast<const float4*>(&m.cmul[c0 + c]), r = *reinterpret_cast<const float4*>(&m.cref[c0 + c]);
+                const float2 u = unpair(fma2(pair(s[c], s[c + 1]), pair(k.x, k.y), pair(r.x, r.y)));
+                const float2 v = unpair(fma2(pair(s[c + 2], s[c + 3]), pair(k.z, k.w), pair(r.z, r.w)));
+                float x[4] = {u.x, u.y, v.x, v.y};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // a hidden position: probability 0, whatever the score (and the reference: none yet is -inf)
+                    if constexpr (decltype(masked)::value) x[i] = vis(c + i) ? x[i] : -INFINITY;
+                    s[c + i] = __float_as_uint(ex2(x[i]));
                 }
-            } else {
-#pragma unroll
-                for (int c = 0; c < C; c += 4) {
-                    float x[4];
-                    logs(c, x);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, vis(c + i) ? x[i] : -INFINITY);
-                }
+                mx = fmaxf(fmaxf(mx, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
             }
-            over = mx > kOver && (G::BN == 128 || tid < G::BN);
-        }
-        if (vote_softmax(over)) {
-            // New references: the rows' maxima over the tile, as ordered integers.
-            const float* mul = m.colc[unit & 3];
-#pragma unroll
-            for (int h = 0; h < C; h += 16) {
-                int keep = 0;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    float y = __uint_as_float(s[h + c]) * mul[h + c];
-                    if (!(vis(h + c) && y == y)) y = -INFINITY;
-                    int k = __float_as_int(y);
-                    k ^= (k >> 31) & 0x7fffffff;
-                    k = __reduce_max_sync(0xffffffffu, k);
-                    if (lane == c) keep = k;
-                }
-                if (lane < 16) m.wmax[wq][h + lane] = keep;
+            return mx;
+        };
+        tc::tmem_wait_ld();
+        bool over = true;
+        if (!first) over = (all ? probabilities(std::false_type{}) : probabilities(std::true_type{})) > kOver;
+        if (vote_group(wg, over && (G::BN == 128 || tid < G::BN))) {
+            // New references: the rows' maxima over the tile.
+            if (!first) {
+                load();
+                tc::tmem_wait_ld();
             }
-            sync_softmax();
+            const float* mul = m.colc[unit & 3] + c0;
+            float keep = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float y = __uint_as_float(s[c]) * mul[c];
+                if (!all) y = vis(c) ? y : -INFINITY;
+                else if (G::BN == 64) y = here ? y : -INFINITY;
+                y = warp_max(y);
+                if (lane == c) keep = y;
+            }
+            if (lane < C) m.wmax[wq][c0 + lane] = keep;
+            sync_group(wg);
             if (tid < C) {
-                int k = max(max(m.wmax[0][tid], m.wmax[1][tid]), max(m.wmax[2][tid], m.wmax[3][tid]));
-                k ^= (k >> 31) & 0x7fffffff;
-                const float old = first ? -INFINITY : m.ref[tid], now = fmaxf(old, __int_as_float(k));
-                m.factor[tid] = old == -INFINITY ? 0.0f : ex2(old - now);
-                m.ref[tid] = now;
-                m.cmul[tid] = mul[tid];
-                m.cref[tid] = kLift - now;
+                const int c = c0 + tid;
+                const float top = fmaxf(fmaxf(m.wmax[0][c], m.wmax[1][c]), fmaxf(m.wmax[2][c], m.wmax[3][c]));
+                const float old = first ? -INFINITY : m.ref[c], now = fmaxf(fmaxf(old, top), -INFINITY);   // never NaN
+                m.factor[c] = old == -INFINITY ? 0.0f : ex2(old - now);
+                m.ref[c] = now;
+                m.cmul[c] = mul[tid];
+                m.cref[c] = kLift - now;
             }
-            sync_softmax();
+            sync_group(wg);
             if (!first) {
 #pragma unroll
-                for (int c = 0; c < C; c += 2) l2[c / 2] = mul2(l2[c / 2], *reinterpret_cast<const uint64_t*>(&m.factor[c]));
-                wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a, abort);   // O^T is at rest
+                for (int c = 0; c < C; c += 2)
+                    l2[c / 2] = mul2(l2[c / 2], *reinterpret_cast<const uint64_t*>(&m.factor[c0 + c]));
+            }
+            if (all) probabilities(std::false_type{});
+            else probabilities(std::true_type{});
+            if (!first) {
+                wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a.status, abort);   // O^T is at rest
                 tc::fence_after_sync();
-                const bool big = *(volatile unsigned*)&m.used[unit & 3] & 2;
+                const int sets = *(volatile unsigned*)&m.used[unit & 7] & 2 ? 2 : 1;   // the plain sums, the large tiles' too
 #pragma unroll 1
-                for (int h = 0; h < (big ? 2 : 1) * (D == 256 ? 2 : 1) * C; h += 16) {
-                    const int set = h / C, c0 = h - set * C;   // D = 256: halves, then the large tiles' halves
-                    const uint32_t at = lanes + (D == 256 ? kTmemO + 64 * set : set ? kTmemBig : kTmemO) + c0;
-                    uint32_t v[16];
-                    tc::tmem_ld16(at, v);
-                    tc::tmem_wait_ld();
+                for (int k = 0; k < (D == 256 ? 2 : 1) * sets; ++k) {
+                    const uint32_t at = lanes + (D == 256 ? kTmemO + 32 * (k & 1) + (kTmemBig - kTmemO) * (k >> 1)
+                                                          : kTmemO + (kTmemBig - kTmemO) * k) + c0;
+#pragma unroll 1
+                    for (int h = 0; h < C; h += CW) {
+                        uint32_t v[CW];
+                        tmem_ld(at + h, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * m.factor[c0 + c]);
-                    tmem_st16(at, v);
+                        for (int c = 0; c < CW; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * m.factor[c0 + h + c]);
+                        tmem_st(at + h, v);
+                    }
                 }
                 tmem_wait_st();
             }
         }
-        if (tile >= 2) wait_warp(&m.pv_done[b], ((tile >> 1) - 1) & 1, a, abort);   // the P buffer is free
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.s_empty[b]);   // S^T has been read
+        if (tile >= 2) wait_warp(&m.pv_done[b], ((tile >> 1) - 1) & 1, a.status, abort);   // the P buffer is free
         uint8_t* row = sp + b * G::PB + tid * 128;
-        // Probabilities of columns c .. c + 7 into the position's row.
-        auto eight = [&](int c, auto masked) {
+#pragma unroll
+        for (int c = 0; c < C; c += 8) {
             uint32_t o[4];
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                float x[4];
-                logs(c + i, x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[k] = ex2(x[k]);
-                    if constexpr (decltype(masked)::value) x[k] = vis(c + i + k) ? x[k] : 0.0f;
-                }
-                l2[(c + i) / 2] = add2(l2[(c + i) / 2], pair(x[0], x[1]));
-                l2[(c + i) / 2 + 1] = add2(l2[(c + i) / 2 + 1], pair(x[2], x[3]));
-                o[i / 2] = pack_f16(x[0], x[1]);
-                o[i / 2 + 1] = pack_f16(x[2], x[3]);
+            for (int i = 0; i < 4; ++i) {
+                l2[c / 2 + i] = add2(l2[c / 2 + i], pair(s[c + 2 * i], s[c + 2 * i + 1]));
+                o[i] = pack_f16(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
             }
             if (G::BN == 128 || tid < G::BN)
-                *reinterpret_cast<uint4*>(row + (((c / 8) ^ (tid & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        };
-        if (all) {
-#pragma unroll
-            for (int c = 0; c < C; c += 8) eight(c, std::false_type{});
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; c += 8) eight(c, std::true_type{});
+                *reinterpret_cast<uint4*>(row + ((((c0 + c) / 8) ^ (tid & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.p_full[b]);
     }
+    // Epilogue: the rows' sums over the threads, then O^T.
     float l[C];
 #pragma unroll
     for (int c = 0; c < C; c += 2) {
         const float2 u = unpair(l2[c / 2]);
-        l[c] = u.x;
-        l[c + 1] = u.y;
+        l[c] = G::BN == 64 && tid >= 64 ? 0.0f : u.x;   // threads past BN held no position
+        l[c + 1] = G::BN == 64 && tid >= 64 ? 0.0f : u.y;
     }
-    // Epilogue: the rows' sums over the threads, then O^T.
-    if (G::BN == 64 && tid >= 64)
-#pragma unroll
-        for (int c = 0; c < C; ++c) l[c] = 0.0f;   // threads past BN held no position
-    warp_sums<NC>(l, lane);
-    if (lane < C) m.wsum[wq][lane] = l[0];
-    if constexpr (C == 64) m.wsum[wq][32 + lane] = l[1];
-    const uint32_t last = tile - 1;
-    wait_warp(&m.pv_done[last & 1], (last >> 1) & 1, a, abort);
-    tc::fence_after_sync();
-    sync_softmax();
+    warp_sums<C>(l, lane);
+    if (lane < C) m.wsum[wq][c0 + lane] = l[0];
+    sync_group(wg);
     const bool whole = p.t0 == 0 && p.t1 == p.nt;
-    const unsigned used = *(volatile unsigned*)&m.used[unit & 3];
     float* po = reinterpret_cast<float*>(part);
-    float* pm = po + kRows * D;
-    if (!whole && tid < p.rows) {
-        pm[2 * tid] = -m.cref[tid];
-        pm[2 * tid + 1] = m.wsum[0][tid] + m.wsum[1][tid] + m.wsum[2][tid] + m.wsum[3][tid];
+    if (tid < C) {
+        const int c = c0 + tid;
+        const float sum = m.wsum[0][c] + m.wsum[1][c] + m.wsum[2][c] + m.wsum[3][c];
+        if (whole) m.factor[c] = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw nothing: zeros
+        else *reinterpret_cast<float2*>(po + kRows * D + 2 * c) = make_float2(-m.cref[c], sum);
     }
+    const uint32_t last = tile - 1;
+    wait_warp(&m.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
+    tc::fence_after_sync();
+    sync_group(wg);
+    const unsigned used = *(volatile unsigned*)&m.used[unit & 7];
+    const int64_t* rowoff = m.rowoff[unit & 3] + c0;
 #pragma unroll 1
     for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
         const int blk = 4 * half + wq;
         if (blk >= G::NB) break;   // lanes past d (warp-uniform)
         const int e = 32 * blk + element_of<T>(lane);
-        const uint64_t bad = m.bad_draft[unit & 3][blk];
-        const bool badc = m.bad_ctx[unit & 3][blk] != 0;
+        const uint64_t bad = m.bad_ctx[unit & 7][blk] ? ~uint64_t(0) : m.bad_draft[unit & 7][blk];
+        const bool bad_all = m.bad_ctx[unit & 7][blk] != 0;
 #pragma unroll 1
-        for (int h = 0; h < C; h += 16) {
-            uint32_t v[16];
-            tc::tmem_ld16(lanes + kTmemO + 64 * half + h, v);
+        for (int h = 0; h < C; h += CW) {
+            uint32_t v[CW];
+            tmem_ld(lanes + kTmemO + 32 * half + c0 + h, v);
             tc::tmem_wait_ld();
             if (used != 1) {
-                uint32_t u[16];
-                tc::tmem_ld16(lanes + kTmemBig + 64 * half + h, u);
+                uint32_t u[CW];
+                tmem_ld(lanes + kTmemBig + 32 * half + c0 + h, u);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
+                for (int c = 0; c < CW; ++c)
                     v[c] = __float_as_uint((used & 1 ? __uint_as_float(v[c]) : 0.0f) + (used & 2 ? kBig * __uint_as_float(u[c]) : 0.0f));
             }
+            if (bad) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const int col = h + c;
-                if (col >= p.rows) continue;
-                float o = __uint_as_float(v[c]);
-                if (badc || (bad & seen[col])) o = __int_as_float(0x7fffffff);
-                if (whole) {
-                    const float sum = m.wsum[0][col] + m.wsum[1][col] + m.wsum[2][col] + m.wsum[3][col];
-                    const int row = p.row0 + col, tok = row / a.G;
-                    a.out[(p.q.tok0 + tok) * a.out_stride + (p.g * a.G + row - tok * a.G) * D + e] =
-                        __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(o, sum));
-                } else {
-                    po[col * D + e] = o;
+                for (int c = 0; c < CW; ++c)
+                    if (bad_all || (bad & seen[h + c])) v[c] = 0x7fffffffu;
+            }
+#pragma unroll
+            for (int c = 0; c < CW; ++c) {
+                if (c0 + h + c < p.rows) {
+                    const float o = __uint_as_float(v[c]);
+                    if (whole) a.out[rowoff[h + c] + e] = __float2bfloat16_rn(o * m.factor[c0 + h + c]);
+                    else po[(c0 + h + c) * D + e] = o;
                 }
             }
-        }
-        __syncwarp();
-        if (lane == 0) {
-            m.bad_draft[unit & 3][blk] = 0;
-            m.bad_ctx[unit & 3][blk] = 0;
         }
     }
     tc::fence_before_sync();
@@ -641,16 +642,16 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
 template <int T, int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     using G = Geo<T, D>;
+    using W = Walk<G::BN, G::NR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sh = smem;                 // fp16 tiles
-    uint8_t* sq = sh + kH * G::HB;      // queries
+    uint8_t* sv = smem;                 // V tiles
+    uint8_t* sq = sv + kV * G::VB;      // queries
     uint8_t* sp = sq + G::QB;           // P
     uint8_t* raw = sp + 2 * G::PB;      // packed tiles
     Misc& m = *reinterpret_cast<Misc*>(raw + G::NS * G::RAW);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    Cut* cuts = reinterpret_cast<Cut*>(a.ws);
-    uint8_t* parts = a.ws + (int64_t)a.ctas * sizeof(Cut);
+    volatile int* abort = &m.abort;
 
     pdl_launch_dependents();
     if (warp == 1) {
@@ -660,212 +661,304 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     if (tid == 0) {
         for (int i = 0; i < G::NS; ++i) {
             mbar_init(&m.raw_full[i], 1);
-            mbar_init(&m.raw_empty[i], kDq);
-        }
-        for (int i = 0; i < kH; ++i) {
-            mbar_init(&m.h_full[i], kDq);
-            mbar_init(&m.h_empty[i], 1);
+            mbar_init(&m.raw_empty[i], kDw);
+            mbar_init(&m.v_ok[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&m.k_full[i], kDw);
+            mbar_init(&m.k_empty[i], 1);
+            mbar_init(&m.v_full[i], kDw);
+            mbar_init(&m.v_empty[i], 1);
             mbar_init(&m.s_full[i], 1);
-            mbar_init(&m.s_empty[i], 4);
-            mbar_init(&m.p_full[i], 4);
+            mbar_init(&m.s_empty[i], 8);
+            mbar_init(&m.p_full[i], 8);
             mbar_init(&m.pv_done[i], 1);
+            mbar_init(&m.drain[i], 1);
         }
-        mbar_init(&m.q_full, 2);
+        mbar_init(&m.q_full, kDw);
         mbar_init(&m.q_empty, 1);
-        mbar_init(&m.o_empty, 4);
-        mbar_init(&m.drain, 1);
+        mbar_init(&m.o_empty, 8);
         m.abort = 0;
-        m.start_r = -1;
         fence_barrier_init();
     }
-    if (tid < 32) {
-        m.bad_draft[tid >> 3][tid & 7] = 0;
-        m.bad_ctx[tid >> 3][tid & 7] = 0;
+    if (tid >= 64 && tid < 128) {
+        m.bad_draft[(tid >> 3) & 7][tid & 7] = 0;
+        m.bad_ctx[(tid >> 3) & 7][tid & 7] = 0;
     }
-    // The list's length, then the request that holds this CTA's first tile.
-    int64_t total = 0, per = 0, x0 = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t carry = 0;
-#pragma unroll 1
-        for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
+    // The list's length, then the request that holds this CTA's first tile:
+    // running sums over the requests, kThreads of them at a time.
+    int total = 0, per = 0, x0 = 0;
+    {
+        Req q{0, 0, 0, 0};
+        int w = 0, upto = 0;   // this thread's request: its tiles, their end in the list
+        auto sums = [&](int r0, int carry) {
             const int r = r0 + tid;
-            const int64_t w = r < a.n_req ? work_of(a, req_of(a, r), G::BN) : 0;
-            int64_t v = w;
+            q = r < a.n_req ? req_of(a, r) : Req{0, 0, 0, 0};
+            w = work_of<G::BN, G::NR>(a, q);
+            int v = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += u;
             }
             __syncthreads();
             if (lane == 31) m.scan[warp] = v;
             __syncthreads();
-            int64_t before = carry, sum = carry;
+            int s = lane < kThreads / 32 ? m.scan[lane] : 0;
 #pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) {
-                if (i < warp) before += m.scan[i];
-                sum += m.scan[i];
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += u;
             }
-            if (pass == 1 && before + v - w <= x0 && x0 < before + v) {
-                m.start_r = r;
-                m.start_base = before + v - w;
+            upto = carry + v + (warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0);
+            return carry + __shfl_sync(0xffffffffu, s, 31);
+        };
+        auto found = [&](int r0) {
+            if (upto - w <= x0 && x0 < upto) {
+                m.start_r = r0 + tid;
+                m.start_base = upto - w;
+                m.start_q = q;
             }
-            carry = sum;
-        }
-        total = carry;
+        };
+#pragma unroll 1
+        for (int r0 = 0; r0 < a.n_req; r0 += kThreads) total = sums(r0, total);
         per = (total + a.ctas - 1) / a.ctas;
-        x0 = (int64_t)blockIdx.x * per;
+        x0 = (int)blockIdx.x * per;
+        if (a.n_req <= kThreads) {
+            found(0);
+        } else {
+            int carry = 0;
+#pragma unroll 1
+            for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
+                carry = sums(r0, carry);
+                found(r0);
+            }
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = m.tmem;
-    const int64_t x1 = min(x0 + per, total);
-    const bool works = x0 < x1;
-    const Walk begin{x0, works ? x1 : x0, works ? m.start_base : 0, works ? m.start_r : 0};
-    volatile int* abort = &m.abort;
-
-    if (tid == 0) {   // the cut at this CTA's start
-        Cut c{};
-        Walk w = begin;
-        Piece p;
-        if (w.next(a, G::BN, p) && p.t0 > 0) {
-            const int first = (int)(p.u0 / per);
-            if (first == (int)blockIdx.x - 1) {
-                c.rows = p.rows;
-                c.first = first;
-                c.last = (int)((p.u0 + p.nt - 1) / per);
-                c.first_slot = 2 * first + (p.u0 % per != 0);
-                c.tok0 = p.q.tok0;
-                c.row0 = p.row0;
-                c.g = p.g;
-            }
-        }
-        cuts[blockIdx.x] = c;
+    const int x1 = min(x0 + per, total);
+    W w{x0, x1, 0, 0, Req{0, 0, 0, 0}};
+    if (x0 < x1) {
+        w.base = m.start_base;
+        w.r = m.start_r;
+        w.q = m.start_q;
     }
-    __syncwarp();
+    Piece p;
 
-    // Registers: 80 + 176 + 2 x 128 per thread of the four warpgroups, the launch's 4 x 128.
-    if (warp >= 4 && warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        Walk w = begin;
-        Piece p;
+    // Registers per thread of the seven warpgroups: 56, 2 x 104, 2 x 56, 2 x 64 (the launch's 7 x 72).
+    if (warp >= kSm && warp < kKd) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int wg = (warp - kSm) >> 2;
+        uint8_t* parts = a.ws + (int64_t)a.ctas * sizeof(Cut) + 2 * (int64_t)blockIdx.x * part_bytes<D>();
         uint32_t tile = 0, unit = 0;
 #pragma unroll 1
-        for (; w.next(a, G::BN, p); ++unit) {
-            uint8_t* part = parts + (2 * (int64_t)blockIdx.x + (p.t0 == 0 && p.u0 != x0)) * G::PART;
-            if (p.rows <= 16) softmax_piece<T, D, 1>(a, m, sp, tmem, p, tile, unit, part);
-            else if (p.rows <= 32) softmax_piece<T, D, 2>(a, m, sp, tmem, p, tile, unit, part);
-            else softmax_piece<T, D, 4>(a, m, sp, tmem, p, tile, unit, part);
+        for (; w.next(a, p); ++unit) {
+            uint8_t* part = parts + (p.t0 == 0 && p.u0 != x0 ? part_bytes<D>() : 0);
+            if (p.rows <= 16) softmax_piece<T, D, 8>(a, m, sp, tmem, p, w.q.ctx, tile, unit, part, wg);
+            else if (p.rows <= 32) softmax_piece<T, D, 16>(a, m, sp, tmem, p, w.q.ctx, tile, unit, part, wg);
+            else if constexpr (G::NR == 64) softmax_piece<T, D, 32>(a, m, sp, tmem, p, w.q.ctx, tile, unit, part, wg);
         }
-    } else if (warp >= 8) {
-        // Decode: a thread takes one segment.  A warp's lanes are SPW
-        // positions by 32 / SPW segments of the row, so that its word loads
-        // fall into 32 different banks (a row's segments are 17, 9 or 11 words
-        // apart, odd; positions 1, 2 or 4 times that) and eight neighbouring
-        // lanes' 16-byte stores into the eight bank groups of swizzled rows.
-        Walk w = begin;
-        Piece p;
-        uint32_t n = 0, tile = 0, unit = 0;
-        const int dt = tid - 256;
-        static_assert(G::SEGS <= kDq * 32, "a segment per decoding thread");
-        const bool mine = dt < G::SEGS;
-        const int pos0 = mine ? ((dt / 32) * G::SPW + lane % G::SPW) * G::PPS : 0, seg0 = mine ? lane / G::SPW : 0;
+    } else if (warp >= kKd && warp < kVd) {
+        // K: a lane is a position; two warps per 32 positions share its items.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        uint32_t tile = 0;
+        const int wq = warp & 3, pos = 32 * wq + lane, h = (warp - kKd) >> 2;
 #pragma unroll 1
-        for (; w.next(a, G::BN, p); ++unit) {
+        while (w.next(a, p)) {
 #pragma unroll 1
             for (int t = p.t0; t < p.t1; ++t, ++tile) {
+                const uint32_t n = 2 * tile, st = n % G::NS, b = tile & 1;
+                wait_warp(&m.raw_full[st], (n / G::NS) & 1, a.status, abort);
+                if (tile >= 2) wait_warp(&m.k_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
+                tc::fence_after_sync();
+                if (32 * wq < G::BN) {
+                    const uint8_t* row = raw + st * G::RAW + pos * G::RB;
+                    const uint32_t to = tmem + ((uint32_t)(32 * wq) << 16) + kTmemK + b * G::KC;
 #pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int st = n % G::NS, hs = n % kH;
-                    wait_warp(&m.raw_full[st], (n / G::NS) & 1, a, abort);
-                    if (n >= kH) wait_warp(&m.h_empty[hs], (n / kH - 1) & 1, a, abort);
-                    const uint32_t* valid = reinterpret_cast<const uint32_t*>(&m.valid[tile & 15]);
-                    const Seg<T> seg(raw + st * G::RAW + pos0 * G::RB + seg0 * Seg<T>::BYTES);
-                    uint32_t db[2];
-                    bool good[2];
+                    for (int i = h; i < G::IPR; i += 2) {
+                        const Item<T, D> item(row + i * Item<T, D>::BYTES);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int pos = pos0 + (D == 32 ? i : 0);
-                        db[i] = seg.scale(i);
-                        good[i] = mine && ((valid[pos >> 5] >> (pos & 31)) & 1);
+                        for (int k = 0; k < Item<T, D>::NBLK; ++k) {
+                            const uint32_t d2 = hm::dup16(item.scale(k));
+                            uint32_t v[16];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint4 u = item.template chunk<false>(k, c, d2);
+                                v[4 * c] = u.x, v[4 * c + 1] = u.y, v[4 * c + 2] = u.z, v[4 * c + 3] = u.w;
+                            }
+                            tmem_st(to + i * (G::ITEM / 2) + 16 * k, v);
+                        }
                     }
-                    bool big = false;
-                    if (kv) {   // V: scales that are not finite, or too large for fp16 times a code
+                    tmem_wait_st();
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&m.k_full[b]);
+                    mbar_arrive(&m.raw_empty[st]);
+                }
+            }
+        }
+    } else if (warp >= kVd) {
+        // V: a warp's lanes are SPW positions by 32 / SPW items of the row, so
+        // that its word loads fall into 32 different banks (a row's items are
+        // 17, 9 or 11 words apart, odd; positions 1, 2 or 4 times that) and
+        // eight neighbouring lanes' 16-byte stores into the eight bank groups
+        // of swizzled rows.  Before a unit's first tile, its queries.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        constexpr int SPW = D <= 64 ? 32 : 2048 / D;
+        static_assert(G::ITEMS <= kDw * 32, "an item per decoding thread");
+        uint32_t tile = 0, unit = 0;
+        const int dt = tid - 32 * kVd;
+        const bool mine = dt < G::ITEMS;
+        const int pos = mine ? (dt / 32) * SPW + lane % SPW : 0, seg = mine ? lane / SPW : 0;
+#pragma unroll 1
+        for (; w.next(a, p); ++unit) {
+            {
+                // Row by row to fp16 times a power of two that brings the row's
+                // largest magnitude to 2^14 .. 2^15 (bf16's 8 bits are exact).
+                constexpr int LPR = D / 8, ROUNDS = G::NR * LPR / 256 > 0 ? G::NR * LPR / 256 : 1;   // threads per row
+                const int N = cols_of(p.rows), sub = dt % LPR, blk = sub >> 2, k = sub & 3;         // 32-block, chunk
+                uint4 u[ROUNDS];
+                int tok[ROUNDS], hd[ROUNDS];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float d = fabsf(h2f(db[i]));
-                            if (good[i] && !(d * code_max<T>() <= 65504.0f)) {
-                                big = big || d <= 65504.0f;
-                                if (!(d <= 65504.0f)) {
-                                    const int64_t j = (int64_t)t * G::BN + pos0 + (D == 32 ? i : 0) - p.q.ctx;
-                                    const int blk = D == 32 ? 0 : 2 * seg0 + i;
-                                    if (j < 0) atomicOr(&m.bad_ctx[unit & 3][blk], 1u);
-                                    else atomicOr(&m.bad_draft[unit & 3][blk], 1ull << (j & 63));
-                                    good[i] = false;
-                                }
+                for (int i = 0; i < ROUNDS; ++i) {
+                    const int row = p.row0 + i * (256 / LPR) + dt / LPR;
+                    tok[i] = row / a.G;
+                    hd[i] = p.g * a.G + row - tok[i] * a.G;
+                    u[i] = make_uint4(0, 0, 0, 0);
+                    if (row < p.row0 + p.rows) {
+                        const __nv_bfloat16* q = a.q + (w.q.tok0 + tok[i]) * a.q_stride + hd[i] * D + 32 * blk;
+                        if constexpr (T == T_Q8_0) {
+                            u[i] = *reinterpret_cast<const uint4*>(q + 8 * k);
+                        } else {
+                            const uint2 lo = *reinterpret_cast<const uint2*>(q + 4 * k), hi = *reinterpret_cast<const uint2*>(q + 16 + 4 * k);
+                            u[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                        }
+                    }
+                }
+                if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a.status, abort);
+#pragma unroll
+                for (int i = 0; i < ROUNDS; ++i) {
+                    const int row = i * (256 / LPR) + dt / LPR;
+                    if (i * 256 + (dt & ~31) >= N * LPR) continue;   // whole warps
+                    const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    float f[8], mx = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        f[2 * c] = __uint_as_float(x[c] << 16);
+                        f[2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u);
+                        mx = fmaxf(mx, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
+                    }
+#pragma unroll
+                    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 14;   // mx < 2^(ex + 15)
+                    if (mx == 0.0f || ex > 113) ex = 0;                       // nothing, or not finite
+                    ex = max(ex, -126);                                       // the factors stay normal
+                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+                    // slots 0, 2, 1, 3, ... of the loaded order
+                    *reinterpret_cast<uint4*>(sq + (sub >> 3) * (G::NR * 128) + row * 128 + (((sub & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(pack_f16(f[0] * down, f[2] * down), pack_f16(f[1] * down, f[3] * down),
+                                   pack_f16(f[4] * down, f[6] * down), pack_f16(f[5] * down, f[7] * down));
+                    if (sub == 0) {
+                        const bool live = row < p.rows;
+                        m.colc[unit & 3][row] = live ? a.scale * 1.44269504088896341f * up : 0.0f;
+                        m.seen[unit & 3][row] = live ? seen_of(a, w.q, tok[i]) : 0;
+                        m.rowoff[unit & 3][row] = (w.q.tok0 + tok[i]) * a.out_stride + hd[i] * D;
+                    }
+                }
+                // The flags of unit + 1 (last of unit - 7, long done) start clear;
+                // no warp reaches that unit's V before q_full.
+                if (dt < 8) {
+                    m.bad_draft[(unit + 1) & 7][dt] = 0;
+                    m.bad_ctx[(unit + 1) & 7][dt] = 0;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.q_full);
+            }
+#pragma unroll 1
+            for (int t = p.t0; t < p.t1; ++t, ++tile) {
+                const uint32_t n = 2 * tile + 1, st = n % G::NS, b = tile & 1;
+                if (lane == 0) {
+                    wait_lane(&m.v_ok[st], (n / G::NS) & 1, a.status, abort);   // big_tile is set
+                    wait_lane(&m.raw_full[st], (n / G::NS) & 1, a.status, abort);
+                    if (tile >= 2) wait_lane(&m.v_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
+                }
+                __syncwarp();
+                if (mine) {
+                    const uint32_t valid = reinterpret_cast<const uint32_t*>(&m.valid[tile & 15])[pos >> 5] >> (pos & 31);
+                    const bool big = *(volatile unsigned*)&m.big_tile[tile & 15] != 0;
+                    const Item<T, D> item(raw + st * G::RAW + pos * G::RB + seg * Item<T, D>::BYTES);
+                    uint8_t* line = sv + b * G::VB + seg * G::CHB + pos * 128;
+                    auto blocks = [&](auto is_big) {
+#pragma unroll
+                        for (int i = 0; i < Item<T, D>::NBLK; ++i) {
+                            const uint32_t db = item.scale(i), d2 = hm::dup16(db);
+                            bool good = valid & 1;
+                            if (good && (db & 0x7C00u) == 0x7C00u) {   // not finite
+                                const int j = t * G::BN + pos - w.q.ctx, blk = 2 * seg + i;
+                                if (j < 0) atomicOr(&m.bad_ctx[unit & 7][blk], 1u);
+                                else atomicOr(&m.bad_draft[unit & 7][blk], 1ull << (j & 63));
+                                good = false;
+                            }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                uint4 o = item.template chunk<decltype(is_big)::value>(i, c, d2);
+                                if (!good) o = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(line + (((4 * i + c) ^ (pos & 7)) << 4)) = o;
                             }
                         }
-                        big = vote_decode(big);
-                        if (dt == 0) m.big_tile[tile & 15] = big;
-                    }
-                    if (mine) {
-                        auto blocks = [&](auto is_big) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int pos = pos0 + (D == 32 ? i : 0);
-                                uint8_t* line = sh + hs * G::HB + seg0 * G::CHB + pos * 128;
-                                const uint32_t d2 = hm::dup16(db[i]);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    uint4 o = seg.template chunk<decltype(is_big)::value>(i, k, d2);
-                                    if (!good[i]) o = make_uint4(0, 0, 0, 0);
-                                    *reinterpret_cast<uint4*>(line + ((((D == 32 ? 0 : 4 * i) + k) ^ (pos & 7)) << 4)) = o;
-                                }
-                            }
-                        };
-                        if (big) blocks(std::true_type{});
-                        else blocks(std::false_type{});
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&m.raw_empty[st]);
-                        mbar_arrive(&m.h_full[hs]);
-                    }
+                    };
+                    if (big) blocks(std::true_type{});
+                    else blocks(std::false_type{});
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&m.v_full[b]);
+                    mbar_arrive(&m.raw_empty[st]);
                 }
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             // Copies: the tile's rows of every page it touches, K then V.
-            Walk w = begin;
-            Piece p;
             uint32_t n = 0, tile = 0;   // stages requested, tiles
             const uint64_t pol = policy_evict_first();
             bool ok = true;
-            const int page = 1 << a.pool.page_log2, span = min(page, G::BN), slabs = G::BN / span;
-            while (ok && w.next(a, G::BN, p)) {
-                const int64_t len = p.q.ctx + p.q.n;
-                const bool shared = groups_of(p.q, a.G) > 1;   // other row groups read these bytes too
+            const int pl = a.pool.page_log2, page = 1 << pl, span = min(page, G::BN), slabs = G::BN / span;
+            while (ok && w.next(a, p)) {
+                const int len = w.q.len;
+                const bool shared = groups_of(w.q, a.G, G::NR) > 1;   // other row groups read these bytes too
                 const int32_t* tab = a.table + (int64_t)p.r * a.table_stride;
+                // Page id of this lane's slab of tile t, -1 if it has none.
+                auto page_id = [&](int t) {
+                    const int pos = t * G::BN + lane * span;
+                    return t < p.t1 && lane < slabs && pos < len ? tab[pos >> pl] : -1;
+                };
+                int ahead = page_id(p.t0);
 #pragma unroll 1
                 for (int t = p.t0; ok && t < p.t1; ++t, ++tile) {
-                    const int64_t pos0 = (int64_t)t * G::BN, pos = pos0 + (int64_t)lane * span;
-                    const bool live = lane < slabs && pos < len;
-                    int id = -1;
-                    if (live) id = page_of(a.pool, tab, a.table_stride, pos, a.status);
+                    const int pos0 = t * G::BN, pos = pos0 + lane * span;
+                    int id = ahead;
+                    ahead = page_id(t + 1);
+                    if (lane < slabs && pos < len && (id < 0 || id >= a.pool.n_pages)) {
+                        atomicOr(a.status, STATUS_BAD_PAGE);
+                        id = -1;
+                    }
                     const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-                    const int rows = live && id >= 0 ? (int)min((int64_t)span, len - pos) : 0;
+                    const int rows = id >= 0 ? min(span, len - pos) : 0;
                     const uint32_t bytes = (uint32_t)(rows * G::RB + 15) & ~15u;   // whole slabs are multiples of 16
                     const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
                     // Lane L reports positions 4 L .. 4 L + 3, which lie in one page.
                     uint32_t bits = 0;
                     if (4 * lane < G::BN && ((have >> (4 * lane / span)) & 1)) {
-                        const int64_t left = len - (pos0 + 4 * lane);
+                        const int left = len - (pos0 + 4 * lane);
                         bits = left >= 4 ? 15u : left > 0 ? (1u << left) - 1 : 0u;
                     }
                     bits <<= 4 * (lane & 7);
@@ -873,11 +966,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     for (int o = 1; o < 8; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
                     if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(&m.valid[tile & 15])[lane >> 3] = bits;
                     __syncwarp();   // the valid words, before the arrival that publishes them
-                    const int64_t off = id >= 0 ? pool_row(a.pool, id, p.g, (int)(pos & (page - 1))) : 0;
+                    const int64_t off = id >= 0 ? pool_row(a.pool, id, p.g, pos & (page - 1)) : 0;
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv, ++n) {
                         const int st = n % G::NS;
-                        if (n >= G::NS && !wait_warp(&m.raw_empty[st], (n / G::NS - 1) & 1, a, abort)) {
+                        if (n >= G::NS && !wait_warp(&m.raw_empty[st], (n / G::NS - 1) & 1, a.status, abort)) {
                             ok = false;
                             break;
                         }
@@ -897,147 +990,120 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 for (uint32_t i = n > G::NS ? n - G::NS : 0; i < n; ++i)
                     mbar_wait_bounded(&m.raw_full[i % G::NS], (i / G::NS) & 1, a.status);
         } else if (warp == 1) {
-            // MMAs: the warp walks together, one lane issues.
-            Walk w = begin;
-            Piece p;
+            // Q K: the warp walks together, one lane issues.
             uint32_t tile = 0, unit = 0;
             bool ok = true;
             const bool leader = tc::elect_one();
-            int n_prev = 0;          // N of the pending P V product; 0: none
-            bool first_prev = false; // it is its unit's first
-            uint32_t unit_prev = 0;
-            unsigned used = 0;       // Misc::used of the pending product's unit
-            const uint64_t dk = tc::sdesc_k128(smem_u32(sh)), dq = tc::sdesc_k128(smem_u32(sq));
-            // d <= 64: one chunk only, read twice (rows 64 .. 127 of O^T are not used)
-            const uint64_t dv = sdesc_mn128(smem_u32(sh), D <= 64 ? 0 : G::CHB), dp = sdesc_mn128(smem_u32(sp), 0);
-            uint32_t hs = 0, hph = 0;    // buffer and phase of the next K or V tile
-            auto next_h = [&] {
-                if (++hs == kH) hs = 0, hph ^= 1;
-            };
-            uint32_t vs = 0, vph = 0;    // of the pending product's V tile
-            auto pv = [&](uint32_t i) {
-                const uint32_t b = i & 1;
-                ok = ok && wait_warp(&m.h_full[vs], vph, a, abort) && wait_warp(&m.p_full[b], (i >> 1) & 1, a, abort);
-                if (first_prev && unit_prev > 0) ok = ok && wait_warp(&m.o_empty, (unit_prev - 1) & 1, a, abort);
-                if (!ok) return;
-                tc::fence_after_sync();
-                const bool big = *(volatile unsigned*)&m.big_tile[i & 15] != 0;
-                const unsigned bit = big ? 2u : 1u;
-                if (first_prev) used = 0;
-                const bool fresh = !(used & bit);
-                used |= bit;
-                const uint32_t o = big ? kTmemBig : kTmemO, id = idesc_f16(n_prev, true);
-                const uint64_t da = dv + (uint64_t)(vs * (G::HB >> 4)), db = dp + (uint64_t)(b * (G::PB >> 4));
-                if (leader) {
-                    *(volatile unsigned*)&m.used[unit_prev & 3] = used;
-#pragma unroll
-                    for (int half = 0; half < (D == 256 ? 2 : 1); ++half)
-#pragma unroll
-                        for (int k = 0; k < G::BN / 16; ++k)
-                            tc::mma_bf16(tmem + o + 64 * half, da + (half * (G::CHB >> 3) + 128 * k), db + 128 * k, id,
-                                         !fresh || k > 0);
-                    tc::commit(&m.h_empty[vs]);
-                    tc::commit(&m.pv_done[b]);
-                }
-                __syncwarp();
-            };
-            while (ok && w.next(a, G::BN, p)) {
-                const int N = cols_of(p.rows);
-                const uint32_t id = idesc_f16(N, false);
+            const uint64_t dq = tc::sdesc_k128(smem_u32(sq));
+            for (; ok && w.next(a, p); ++unit) {
+                const uint32_t id = idesc_f16(cols_of(p.rows), false);
 #pragma unroll 1
-                for (int t = p.t0; ok && t < p.t1; ++t, ++tile) {
+                for (int t = p.t0; t < p.t1; ++t, ++tile) {
                     const uint32_t b = tile & 1;
-                    ok = ok && wait_warp(&m.h_full[hs], hph, a, abort);
-                    if (t == p.t0) ok = ok && wait_warp(&m.q_full, unit & 1, a, abort);
-                    if (tile >= 2) ok = ok && wait_warp(&m.s_empty[b], ((tile >> 1) - 1) & 1, a, abort);
+                    if (t == p.t0) ok = ok && wait_warp(&m.q_full, unit & 1, a.status, abort);
+                    ok = ok && wait_warp(&m.k_full[b], (tile >> 1) & 1, a.status, abort);
+                    if (tile >= 2) ok = ok && wait_warp(&m.s_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint64_t da = dk + (uint64_t)(hs * (G::HB >> 4));
                     if (leader) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            tc::mma_bf16(tmem + 64 * b, da + ((k >> 2) * (G::CHB >> 4) + 2 * (k & 3)),
-                                         dq + ((k >> 2) * (kRows * 8) + 2 * (k & 3)), id, k > 0);
-                        tc::commit(&m.h_empty[hs]);
+                            mma_ta(tmem + 64 * b, tmem + kTmemK + b * G::KC + 8 * k, dq + ((k >> 2) * (G::NR * 8) + 2 * (k & 3)), id, k > 0);
                         tc::commit(&m.s_full[b]);
+                        tc::commit(&m.k_empty[b]);
                         if (t == p.t1 - 1) tc::commit(&m.q_empty);
                     }
                     __syncwarp();
-                    next_h();
-                    if (n_prev) pv(tile - 1);
-                    vs = hs;
-                    vph = hph;
-                    next_h();
-                    n_prev = N;
-                    first_prev = t == p.t0;
-                    unit_prev = unit;
                 }
-                ++unit;
             }
-            if (ok && n_prev) pv(tile - 1);
             if (!ok) {   // let the products in flight end
-                if (leader) tc::commit(&m.drain);
+                if (leader) tc::commit(&m.drain[0]);
                 __syncwarp();
-                if (lane == 0) mbar_wait_bounded(&m.drain, 0, a.status);
+                if (lane == 0) mbar_wait_bounded(&m.drain[0], 0, a.status);
+                __syncwarp();
+            }
+        } else if (warp == 2) {
+            // P V.
+            uint32_t tile = 0, unit = 0;
+            bool ok = true;
+            const bool leader = tc::elect_one();
+            // d <= 64: one chunk only, read twice (rows 64 .. 127 of O^T are not used)
+            const uint64_t dv = sdesc_mn128(smem_u32(sv), D <= 64 ? 0 : G::CHB), dp = sdesc_mn128(smem_u32(sp), 0);
+            for (; ok && w.next(a, p); ++unit) {
+                const uint32_t id = idesc_f16(cols_of(p.rows), true);
+                unsigned used = 0;
+#pragma unroll 1
+                for (int t = p.t0; t < p.t1; ++t, ++tile) {
+                    const uint32_t b = tile & 1;
+                    ok = ok && wait_warp(&m.v_full[b], (tile >> 1) & 1, a.status, abort);
+                    if (t == p.t0 && unit > 0) ok = ok && wait_warp(&m.o_empty, (unit - 1) & 1, a.status, abort);
+                    ok = ok && wait_warp(&m.p_full[b], (tile >> 1) & 1, a.status, abort);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const bool big = *(volatile unsigned*)&m.big_tile[tile & 15] != 0;
+                    const unsigned bit = big ? 2u : 1u;
+                    const bool fresh = !(used & bit);
+                    used |= bit;
+                    const uint32_t o = tmem + (big ? kTmemBig : kTmemO);
+                    const uint64_t da = dv + (uint64_t)(b * (G::VB >> 4)), db = dp + (uint64_t)(b * (G::PB >> 4));
+                    if (leader) {
+                        *(volatile unsigned*)&m.used[unit & 7] = used;
+#pragma unroll
+                        for (int half = 0; half < (D == 256 ? 2 : 1); ++half)
+#pragma unroll
+                            for (int k = 0; k < G::BN / 16; ++k)
+                                tc::mma_bf16(o + 32 * half, da + (half * (G::CHB >> 3) + 128 * k), db + 128 * k, id, !fresh || k > 0);
+                        tc::commit(&m.pv_done[b]);
+                        tc::commit(&m.v_empty[b]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {
+                if (leader) tc::commit(&m.drain[1]);
+                __syncwarp();
+                if (lane == 0) mbar_wait_bounded(&m.drain[1], 0, a.status);
                 __syncwarp();
             }
         } else {
-            // Queries: row by row to fp16 times a power of two that brings the
-            // row's largest magnitude to 2^14 .. 2^15 (bf16's 8 bits are exact).
-            Walk w = begin;
-            Piece p;
-            uint32_t unit = 0;
-            constexpr int LPR = D / 8, RPW = 32 / LPR;   // lanes per row, rows per pass
-            const int sub = lane % LPR;
+            // The unit cut at this CTA's start, for join_kernel.
+            W first = w;
+            Cut c{};
+            if (first.next(a, p) && p.t0 > 0) {
+                const int from = p.u0 / per;
+                if (from == (int)blockIdx.x - 1) {
+                    c.rows = p.rows;
+                    c.first = from;
+                    c.last = (p.u0 + p.nt - 1) / per;
+                    c.first_slot = 2 * from + (p.u0 % per != 0);
+                    c.tok0 = first.q.tok0;
+                    c.row0 = p.row0;
+                    c.g = p.g;
+                }
+            }
+            if (lane == 0) reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = c;
+            // V scales: a finite one whose largest code leaves fp16's range makes its tile a large one.
+            uint32_t tile = 0;
 #pragma unroll 1
-            for (; w.next(a, G::BN, p); ++unit) {
-                if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a, abort);
-                const int N = cols_of(p.rows);
+            while (w.next(a, p)) {
+#pragma unroll 1
+                for (int t = p.t0; t < p.t1; ++t, ++tile) {
+                    const uint32_t n = 2 * tile + 1, st = n % G::NS;
+                    wait_warp(&m.raw_full[st], (n / G::NS) & 1, a.status, abort);
+                    const uint32_t* valid = reinterpret_cast<const uint32_t*>(&m.valid[tile & 15]);
+                    bool big = false;
 #pragma unroll 4
-                for (int i = (warp - 2) * RPW + lane / LPR; i < N; i += 2 * RPW) {   // N and the stride are multiples of RPW
-                    const bool live = i < p.rows;
-                    const int row = p.row0 + i, tok = live ? row / a.G : 0, h = live ? row - tok * a.G : 0;
-                    const __nv_bfloat16* q = a.q + (p.q.tok0 + tok) * a.q_stride + (int64_t)(p.g * a.G + h) * D;
-                    uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);   // four bf16 each
-                    const int b = sub >> 2, k = sub & 3;                  // 32-block, chunk
-                    if (live) {
-                        if constexpr (T == T_Q8_0) {
-                            const uint4 u = *reinterpret_cast<const uint4*>(q + 32 * b + 8 * k);
-                            lo = make_uint2(u.x, u.y);
-                            hi = make_uint2(u.z, u.w);
-                        } else {
-                            lo = *reinterpret_cast<const uint2*>(q + 32 * b + 4 * k);
-                            hi = *reinterpret_cast<const uint2*>(q + 32 * b + 16 + 4 * k);
-                        }
+                    for (int i = lane; i < G::BN * G::NB; i += 32) {
+                        const int pos = i / G::NB;
+                        const float d = fabsf(h2f(ld_u16(raw + st * G::RAW + i * Fmt<T>::BB)));
+                        big = big || (d <= 65504.0f && d * code_max<T>() > 65504.0f && ((valid[pos >> 5] >> (pos & 31)) & 1));
                     }
-                    const uint32_t u[4] = {lo.x, lo.y, hi.x, hi.y};
-                    float f[8], mx = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        f[2 * c] = __uint_as_float(u[c] << 16);
-                        f[2 * c + 1] = __uint_as_float(u[c] & 0xffff0000u);
-                        mx = fmaxf(mx, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
-                    }
-#pragma unroll
-                    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 14;   // mx < 2^(ex + 15)
-                    if (mx == 0.0f || ex > 113) ex = 0;                       // nothing, or not finite
-                    ex = max(ex, -126);                                       // the factors stay normal
-                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-                    uint4 o;   // slots 0, 2, 1, 3, ... of the loaded order
-                    o.x = pack_f16(f[0] * down, f[2] * down);
-                    o.y = pack_f16(f[1] * down, f[3] * down);
-                    o.z = pack_f16(f[4] * down, f[6] * down);
-                    o.w = pack_f16(f[5] * down, f[7] * down);
-                    *reinterpret_cast<uint4*>(sq + (sub >> 3) * (kRows * 128) + i * 128 + (((sub & 7) ^ (i & 7)) << 4)) = o;
-                    if (sub == 0) {
-                        m.colc[unit & 3][i] = live ? a.scale * 1.44269504088896341f * up : 0.0f;
-                        m.seen[unit & 3][i] = live ? seen_of(a, p.q, tok) : 0;
+                    big = __any_sync(0xffffffffu, big);
+                    if (lane == 0) {
+                        *(volatile unsigned*)&m.big_tile[tile & 15] = big;
+                        mbar_arrive(&m.v_ok[st]);
                     }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&m.q_full);
             }
         }
     }
@@ -1058,7 +1124,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a) {
     pdl_wait_prior();
     const Cut c = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x];
     const uint8_t* parts = a.ws + (int64_t)a.ctas * sizeof(Cut);
-    constexpr int64_t PART = (int64_t)kRows * (D + 2) * 4;
+    constexpr int64_t PART = part_bytes<D>();
     const int lane = threadIdx.x & 31;
     for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < c.rows; row += gridDim.y * kJoinWarps) {
         auto part = [&](int i) {   // piece i, 0 .. last - first
@@ -1126,11 +1192,15 @@ static cudaError_t launch_d(const Args& a, int d, cudaStream_t s) {
 
 }  // namespace tree
 
+// Tiles of the largest call of this shape.
+double attn_tree_max_tiles(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d) {
+    const int bn = d == 256 ? 64 : 128, nr = d == 256 ? 32 : 64;
+    return (double)n_req * n_kv * (((int64_t)max_q * (n_heads / n_kv) + nr - 1) / nr) * std::max<int64_t>(1, (max_pos + bn - 1) / bn);
+}
+
 // The grid: one CTA per SM, fewer when the call cannot have that many tiles.
 static int tree_ctas(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d, int sms) {
-    const int bn = d == 256 ? 64 : 128;
-    const double tiles = (double)n_req * n_kv * (((int64_t)max_q * (n_heads / n_kv) + tree::kRows - 1) / tree::kRows) *
-                         ((max_pos + bn - 1) / bn);
+    const double tiles = attn_tree_max_tiles(n_req, max_q, max_pos, n_heads, n_kv, d);
     return tiles < sms ? std::max(1, (int)tiles) : sms;
 }
 
@@ -1145,7 +1215,7 @@ cudaError_t launch_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_s
                              int n_heads, int n_kv, int d, float scale, void* out, int64_t out_stride, void* ws,
                              unsigned* status, int sms, cudaStream_t s) {
     const tree::Args a{static_cast<const __nv_bfloat16*>(q), n_tok, q_stride, K, V, Pool{n_pages, page_log2, n_kv, row_bytes},
-                       table, table_stride, ctx, cu, mask, (int)n_req, max_q, n_heads / n_kv, n_heads, scale,
+                       table, table_stride, ctx, cu, mask, (int)n_req, max_q, n_heads / n_kv, scale,
                        static_cast<__nv_bfloat16*>(out), out_stride, static_cast<uint8_t*>(ws),
                        tree_ctas(n_req, max_q, table_stride << page_log2, n_heads, n_kv, d, sms), status};
     switch (type) {

@@ -27,7 +27,7 @@
 // end.
 //
 // Warps: 0 copies (cp.async.bulk of the pages' contiguous head slabs into a
-// ring), 1 issues Q K, 2 issues P V, 3 looks at the V scales; 4-11 softmax and
+// ring), 1 issues Q K, 2 issues P V, 3 notes a cut unit; 4-11 softmax and
 // epilogue (two warpgroups, half of the rows each); 12-19 decode K; 20-27
 // decode V and load the unit's queries.  A tile is a chain of short steps, so
 // it is the number of warps on it that sets the rate: with one warpgroup each
@@ -148,7 +148,7 @@ struct __align__(16) Misc {
     unsigned bad_ctx[8][8];
     unsigned big_tile[16];       // by tile mod 16: the V tile is decoded times 2^-7
     unsigned used[8];            // by unit mod 8: bit 0 the plain sums, bit 1 the large tiles' sums hold something
-    uint64_t raw_full[8], raw_empty[8], v_ok[8], k_full[2], k_empty[2], v_full[kV], v_empty[kV], s_full[2], s_empty[2],
+    uint64_t raw_full[8], raw_empty[8], k_full[2], k_empty[2], v_full[kV], v_empty[kV], s_full[2], s_empty[2],
         p_full[2], pv_done[2];
     uint64_t q_full, q_empty, o_empty, drain[2];
     int scan[32];
@@ -226,12 +226,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// The warp's largest (NaN aside).
-__device__ __forceinline__ float warp_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Packed fp32 pairs (each half rounded as by itself).
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
     uint64_t d;
@@ -269,6 +263,19 @@ __device__ __forceinline__ bool vote_group(int wg, bool any) {   // true where a
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
         : "r"((uint32_t)any), "r"(1 + wg)
+        : "memory");
+    return r != 0;
+}
+// Barrier 3: the decoding warps of V.
+__device__ __forceinline__ bool vote_v(bool any) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 3, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)any)
         : "memory");
     return r != 0;
 }
@@ -419,21 +426,21 @@ template <int T, int D> struct Item {
 
 // -------------------------------------------------------------- softmax ----
 
-// Sums over the warp of v[0 .. C): lane l gets column l mod C in v[0], by
+// op over the warp of v[0 .. C): lane l gets column l mod C in v[0], by
 // exchanging halves.
-template <int C>
-__device__ __forceinline__ void warp_sums(float (&v)[C], int lane) {
+template <int C, class Op>
+__device__ __forceinline__ void warp_columns(float (&v)[C], int lane, Op op) {
 #pragma unroll
     for (int o = 16; o >= C; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int i = 0; i < C; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
 #pragma unroll
     for (int o = C / 2; o >= 1; o >>= 1)
 #pragma unroll
         for (int i = 0; i < o; ++i) {
             const bool up = lane & o;
             const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
         }
 }
 
@@ -502,16 +509,18 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                 tc::tmem_wait_ld();
             }
             const float* mul = m.colc[unit & 3] + c0;
-            float keep = 0.0f;
+            {
+                float y[C];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float y = __uint_as_float(s[c]) * mul[c];
-                if (!all) y = vis(c) ? y : -INFINITY;
-                else if (G::BN == 64) y = here ? y : -INFINITY;
-                y = warp_max(y);
-                if (lane == c) keep = y;
+                for (int c = 0; c < C; ++c) y[c] = __uint_as_float(s[c]) * mul[c];
+                if (!all || G::BN == 64) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) y[c] = vis(c) ? y[c] : -INFINITY;
+                }
+                warp_columns<C>(y, lane, [](float x, float z) { return fmaxf(x, z); });   // NaN aside
+                if (lane < C) m.wmax[wq][c0 + lane] = y[0];
+                load();   // the scores again: their registers held the maxima's exchange
             }
-            if (lane < C) m.wmax[wq][c0 + lane] = keep;
             sync_group(wg);
             if (tid < C) {
                 const int c = c0 + tid;
@@ -528,6 +537,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                 for (int c = 0; c < C; c += 2)
                     l2[c / 2] = mul2(l2[c / 2], *reinterpret_cast<const uint64_t*>(&m.factor[c0 + c]));
             }
+            tc::tmem_wait_ld();
             if (all) probabilities(std::false_type{});
             else probabilities(std::true_type{});
             if (!first) {
@@ -580,7 +590,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         l[c] = G::BN == 64 && tid >= 64 ? 0.0f : u.x;   // threads past BN held no position
         l[c + 1] = G::BN == 64 && tid >= 64 ? 0.0f : u.y;
     }
-    warp_sums<C>(l, lane);
+    warp_columns<C>(l, lane, [](float x, float y) { return x + y; });
     if (lane < C) m.wsum[wq][c0 + lane] = l[0];
     sync_group(wg);
     const bool whole = p.t0 == 0 && p.t1 == p.nt;
@@ -644,7 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     using G = Geo<T, D>;
     using W = Walk<G::BN, G::NR>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // Aligned by pointer arithmetic: through an integer the compiler would lose
+    // the address space, and every shared access would be a generic one.
+    uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
     uint8_t* sv = smem;                 // V tiles
     uint8_t* sq = sv + kV * G::VB;      // queries
     uint8_t* sp = sq + G::QB;           // P
@@ -662,7 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         for (int i = 0; i < G::NS; ++i) {
             mbar_init(&m.raw_full[i], 1);
             mbar_init(&m.raw_empty[i], kDw);
-            mbar_init(&m.v_ok[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m.k_full[i], kDw);
@@ -884,31 +895,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             for (int t = p.t0; t < p.t1; ++t, ++tile) {
                 const uint32_t n = 2 * tile + 1, st = n % G::NS, b = tile & 1;
                 if (lane == 0) {
-                    wait_lane(&m.v_ok[st], (n / G::NS) & 1, a.status, abort);   // big_tile is set
                     wait_lane(&m.raw_full[st], (n / G::NS) & 1, a.status, abort);
                     if (tile >= 2) wait_lane(&m.v_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
                 }
                 __syncwarp();
+                const bool valid = mine && ((reinterpret_cast<const uint32_t*>(&m.valid[tile & 15])[pos >> 5] >> (pos & 31)) & 1);
+                const Item<T, D> item(raw + st * G::RAW + pos * G::RB + seg * Item<T, D>::BYTES);
+                // Scales that are finite but too large for fp16 times a code make the tile a large one, those that are
+                // not finite are recorded.
+                bool big = false;
+                uint32_t good = 0;   // bit per block
+#pragma unroll
+                for (int i = 0; i < Item<T, D>::NBLK; ++i) {
+                    const float d = fabsf(h2f(item.scale(i)));
+                    if (valid) {
+                        good |= 1u << i;
+                        if (!(d * code_max<T>() <= 65504.0f)) {
+                            big = big || d <= 65504.0f;
+                            if (!(d <= 65504.0f)) {
+                                good ^= 1u << i;
+                                const int j = t * G::BN + pos - w.q.ctx, blk = 2 * seg + i;
+                                if (j < 0) atomicOr(&m.bad_ctx[unit & 7][blk], 1u);
+                                else atomicOr(&m.bad_draft[unit & 7][blk], 1ull << (j & 63));
+                            }
+                        }
+                    }
+                }
+                big = vote_v(big);
+                if (dt == 0) m.big_tile[tile & 15] = big;
                 if (mine) {
-                    const uint32_t valid = reinterpret_cast<const uint32_t*>(&m.valid[tile & 15])[pos >> 5] >> (pos & 31);
-                    const bool big = *(volatile unsigned*)&m.big_tile[tile & 15] != 0;
-                    const Item<T, D> item(raw + st * G::RAW + pos * G::RB + seg * Item<T, D>::BYTES);
                     uint8_t* line = sv + b * G::VB + seg * G::CHB + pos * 128;
                     auto blocks = [&](auto is_big) {
 #pragma unroll
                         for (int i = 0; i < Item<T, D>::NBLK; ++i) {
-                            const uint32_t db = item.scale(i), d2 = hm::dup16(db);
-                            bool good = valid & 1;
-                            if (good && (db & 0x7C00u) == 0x7C00u) {   // not finite
-                                const int j = t * G::BN + pos - w.q.ctx, blk = 2 * seg + i;
-                                if (j < 0) atomicOr(&m.bad_ctx[unit & 7][blk], 1u);
-                                else atomicOr(&m.bad_draft[unit & 7][blk], 1ull << (j & 63));
-                                good = false;
-                            }
+                            const uint32_t d2 = hm::dup16(item.scale(i));
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 uint4 o = item.template chunk<decltype(is_big)::value>(i, c, d2);
-                                if (!good) o = make_uint4(0, 0, 0, 0);
+                                if (!((good >> i) & 1)) o = make_uint4(0, 0, 0, 0);
                                 *reinterpret_cast<uint4*>(line + (((4 * i + c) ^ (pos & 7)) << 4)) = o;
                             }
                         }
@@ -1082,29 +1106,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 }
             }
             if (lane == 0) reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = c;
-            // V scales: a finite one whose largest code leaves fp16's range makes its tile a large one.
-            uint32_t tile = 0;
-#pragma unroll 1
-            while (w.next(a, p)) {
-#pragma unroll 1
-                for (int t = p.t0; t < p.t1; ++t, ++tile) {
-                    const uint32_t n = 2 * tile + 1, st = n % G::NS;
-                    wait_warp(&m.raw_full[st], (n / G::NS) & 1, a.status, abort);
-                    const uint32_t* valid = reinterpret_cast<const uint32_t*>(&m.valid[tile & 15]);
-                    bool big = false;
-#pragma unroll 4
-                    for (int i = lane; i < G::BN * G::NB; i += 32) {
-                        const int pos = i / G::NB;
-                        const float d = fabsf(h2f(ld_u16(raw + st * G::RAW + i * Fmt<T>::BB)));
-                        big = big || (d <= 65504.0f && d * code_max<T>() > 65504.0f && ((valid[pos >> 5] >> (pos & 31)) & 1));
-                    }
-                    big = __any_sync(0xffffffffu, big);
-                    if (lane == 0) {
-                        *(volatile unsigned*)&m.big_tile[tile & 15] = big;
-                        mbar_arrive(&m.v_ok[st]);
-                    }
-                }
-            }
         }
     }
     tc::fence_before_sync();

@@ -125,7 +125,7 @@ template <int T, int D> struct Geo {
     static constexpr int IPR = D / ITEM;                   // in a row
     static constexpr int KC = D / 2;                       // tensor-memory columns of a K tile
     static constexpr int FIXED = kV * VB + QB + 2 * PB;
-    static constexpr int MISC = 10240;
+    static constexpr int MISC = 10752;
     static constexpr int NS0 = (227 * 1024 - 1024 - MISC - FIXED) / RAW;
     static constexpr int NS = (NS0 > 8 ? 8 : NS0) & ~1;    // ring stages; even: V tiles always take the odd ones
     static constexpr int SMEM = 1024 + FIXED + NS * RAW + MISC;
@@ -133,6 +133,15 @@ template <int T, int D> struct Geo {
 };
 // A partial result: O [rows][D], reference and sum per row.
 template <int D> __host__ __device__ constexpr int64_t part_bytes() { return (int64_t)kRows * (D + 2) * 4; }
+
+// A piece of a unit: request, kv head, rows (0: no more pieces), tiles [t0,
+// t1) of nt.  One warp walks the list and hands the pieces to the others
+// through shared memory, so that their divisions are done once and take no
+// registers elsewhere.
+struct __align__(16) Piece {
+    Req q;
+    int r, g, row0, rows, t0, t1, nt, u0;   // u0: place of its tile 0 in the work list
+};
 
 struct __align__(16) Misc {
     float cmul[kRows];           // scale * log2 e * 2^e of the row's query
@@ -148,15 +157,16 @@ struct __align__(16) Misc {
     unsigned bad_ctx[8][8];
     unsigned big_tile[16];       // by tile mod 16: the V tile is decoded times 2^-7
     unsigned used[8];            // by unit mod 8: bit 0 the plain sums, bit 1 the large tiles' sums hold something
-    uint64_t raw_full[8], raw_empty[8], k_full[2], k_empty[2], v_full[kV], v_empty[kV], s_full[2], s_empty[2],
+    uint64_t raw_full[8], raw_empty[8], k_full[2], k_empty[2], v_full[kV], v_empty[kV], s_full[2],
         p_full[2], pv_done[2];
-    uint64_t q_full, q_empty, o_empty, drain[2];
+    uint64_t q_full, q_empty, o_empty, drain[2], piece_full[8], piece_free[8];
+    Piece piece[8];              // by unit mod 8
     int scan[32];
     Req start_q;
     int start_base, start_r, abort;
     uint32_t tmem;
 };
-static_assert(sizeof(Misc) <= 10240, "Misc");
+static_assert(sizeof(Misc) <= 10752, "Misc");
 
 // ------------------------------------------------------- the work list ----
 // Counts of tiles stay inside 31 bits (the host refuses more).
@@ -169,10 +179,6 @@ template <int BN, int NR> __device__ __forceinline__ int work_of(const Args& a, 
 // Columns (N of the MMAs) a unit of that many rows takes.
 __device__ __forceinline__ int cols_of(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// A piece of a unit: request, kv head, rows, tiles [t0, t1) of nt.
-struct Piece {
-    int r, g, row0, rows, t0, t1, nt, u0;   // u0: place of its tile 0 in the work list
-};
 // The pieces of the run [x, end) of the list; the present request r's tiles
 // start at base.
 template <int BN, int NR> struct Walk {
@@ -196,6 +202,7 @@ template <int BN, int NR> struct Walk {
         p.t0 = rel - unit * nt;
         p.t1 = min(nt, p.t0 + (end - x));
         p.u0 = x - p.t0;
+        p.q = q;
         x += p.t1 - p.t0;
         return true;
     }
@@ -354,6 +361,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsign
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// Whether the unit's piece (m.piece[unit mod 8]) is there; false after a failure.
+__device__ __forceinline__ bool piece_ready(Misc& m, uint32_t unit, unsigned* status) {
+    return wait_warp(&m.piece_full[unit & 7], (unit >> 3) & 1, status, &m.abort);
+}
+
 // --------------------------------------------------------------- decode ----
 // fp16 code * d (one rounding), in 16-byte chunks of eight.  The codes are
 // taken two at a time out of each word by a mask, which puts a 32-block's
@@ -448,21 +460,26 @@ __device__ __forceinline__ void warp_columns(float (&v)[C], int lane, Op op) {
 // (rows): C wg .. C wg + C - 1.  tile: running count of the CTA's tiles; unit:
 // of its pieces.
 template <int T, int D, int C>
-__device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* sp, uint32_t tmem, const Piece& p, int ctx,
-                                              uint32_t& tile, uint32_t unit, uint8_t* part, int wg) {
+__device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* sp, uint32_t tmem, const Piece& p, uint32_t& tile,
+                                              uint32_t unit, uint8_t* part, int wg) {
     using G = Geo<T, D>;
     constexpr int CW = C < 16 ? C : 16;   // columns of a tensor-memory access
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, tid = 32 * wq + lane, c0 = C * wg;
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
     const uint64_t* seen = m.seen[unit & 3] + c0;
     volatile int* abort = &m.abort;
+    const int t0 = p.t0, t1 = p.t1, ctx = p.q.ctx;
     uint64_t l2[C / 2];   // this thread's sums of probabilities, columns in pairs
 #pragma unroll
     for (int c = 0; c < C / 2; ++c) l2[c] = 0;
 #pragma unroll 1
-    for (int t = p.t0; t < p.t1; ++t, ++tile) {
+    for (int t = t0; t < t1; ++t, ++tile) {
         const uint32_t b = tile & 1;
-        wait_warp(&m.s_full[b], (tile >> 1) & 1, a.status, abort);
+        if (lane == 0) {
+            wait_lane(&m.s_full[b], (tile >> 1) & 1, a.status, abort);
+            if (tile >= 2) wait_lane(&m.pv_done[b], ((tile >> 1) - 1) & 1, a.status, abort);   // the P buffer is free
+        }
+        __syncwarp();
         tc::fence_after_sync();
         uint32_t s[C];   // scores, then probabilities
         auto load = [&] {
@@ -478,7 +495,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         const int j = pos0 + tid - ctx;         // drafted token at this position, if >= 0
         // Visibility of this position to column c.
         auto vis = [&](int c) { return here && (j < 0 || ((seen[c] >> (j & 63)) & 1)); };
-        const bool first = t == p.t0;
+        const bool first = t == t0;
         // Scores to probabilities (lifted) on the present references; the
         // largest of their logarithms.
         auto probabilities = [&](auto masked) {
@@ -561,10 +578,6 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                 tmem_wait_st();
             }
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m.s_empty[b]);   // S^T has been read
-        if (tile >= 2) wait_warp(&m.pv_done[b], ((tile >> 1) - 1) & 1, a.status, abort);   // the P buffer is free
         uint8_t* row = sp + b * G::PB + tid * 128;
 #pragma unroll
         for (int c = 0; c < C; c += 8) {
@@ -580,7 +593,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.p_full[b]);
+        if (lane == 0) mbar_arrive(&m.p_full[b]);   // and S^T has been read
     }
     // Epilogue: the rows' sums over the threads, then O^T.
     float l[C];
@@ -593,7 +606,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
     warp_columns<C>(l, lane, [](float x, float y) { return x + y; });
     if (lane < C) m.wsum[wq][c0 + lane] = l[0];
     sync_group(wg);
-    const bool whole = p.t0 == 0 && p.t1 == p.nt;
+    const bool whole = t0 == 0 && t1 == p.nt;
     float* po = reinterpret_cast<float*>(part);
     if (tid < C) {
         const int c = c0 + tid;
@@ -607,6 +620,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
     sync_group(wg);
     const unsigned used = *(volatile unsigned*)&m.used[unit & 7];
     const int64_t* rowoff = m.rowoff[unit & 3] + c0;
+    const int rows = p.rows;
 #pragma unroll 1
     for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
         const int blk = 4 * half + wq;
@@ -634,7 +648,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
             }
 #pragma unroll
             for (int c = 0; c < CW; ++c) {
-                if (c0 + h + c < p.rows) {
+                if (c0 + h + c < rows) {
                     const float o = __uint_as_float(v[c]);
                     if (whole) a.out[rowoff[h + c] + e] = __float2bfloat16_rn(o * m.factor[c0 + h + c]);
                     else po[(c0 + h + c) * D + e] = o;
@@ -644,7 +658,10 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
     }
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&m.o_empty);
+    if (lane == 0) {
+        mbar_arrive(&m.o_empty);
+        mbar_arrive(&m.piece_free[unit & 7]);
+    }
 }
 
 // --------------------------------------------------------------- kernel ----
@@ -652,7 +669,6 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
 template <int T, int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     using G = Geo<T, D>;
-    using W = Walk<G::BN, G::NR>;
     extern __shared__ uint8_t smem_raw[];
     // Aligned by pointer arithmetic: through an integer the compiler would lose
     // the address space, and every shared access would be a generic one.
@@ -681,7 +697,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             mbar_init(&m.v_full[i], kDw);
             mbar_init(&m.v_empty[i], 1);
             mbar_init(&m.s_full[i], 1);
-            mbar_init(&m.s_empty[i], 8);
             mbar_init(&m.p_full[i], 8);
             mbar_init(&m.pv_done[i], 1);
             mbar_init(&m.drain[i], 1);
@@ -689,6 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         mbar_init(&m.q_full, kDw);
         mbar_init(&m.q_empty, 1);
         mbar_init(&m.o_empty, 8);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&m.piece_full[i], 1);
+            mbar_init(&m.piece_free[i], 8);
+        }
         m.abort = 0;
         fence_barrier_init();
     }
@@ -751,43 +770,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     tc::fence_after_sync();
     const uint32_t tmem = m.tmem;
     const int x1 = min(x0 + per, total);
-    W w{x0, x1, 0, 0, Req{0, 0, 0, 0}};
-    if (x0 < x1) {
-        w.base = m.start_base;
-        w.r = m.start_r;
-        w.q = m.start_q;
-    }
-    Piece p;
-
-    // Registers per thread of the seven warpgroups: 56, 2 x 104, 2 x 56, 2 x 64 (the launch's 7 x 72).
+    // Registers per thread of the seven warpgroups: 48, 2 x 120, 2 x 48, 2 x 56, within the launch's 7 x 72.
     if (warp >= kSm && warp < kKd) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int wg = (warp - kSm) >> 2;
         uint8_t* parts = a.ws + (int64_t)a.ctas * sizeof(Cut) + 2 * (int64_t)blockIdx.x * part_bytes<D>();
         uint32_t tile = 0, unit = 0;
 #pragma unroll 1
-        for (; w.next(a, p); ++unit) {
+        for (;; ++unit) {
+            if (vote_group(wg, !piece_ready(m, unit, a.status))) break;
+            const Piece& p = m.piece[unit & 7];
+            const int rows = p.rows;
+            if (rows == 0) break;
             uint8_t* part = parts + (p.t0 == 0 && p.u0 != x0 ? part_bytes<D>() : 0);
-            if (p.rows <= 16) softmax_piece<T, D, 8>(a, m, sp, tmem, p, w.q.ctx, tile, unit, part, wg);
-            else if (p.rows <= 32) softmax_piece<T, D, 16>(a, m, sp, tmem, p, w.q.ctx, tile, unit, part, wg);
-            else if constexpr (G::NR == 64) softmax_piece<T, D, 32>(a, m, sp, tmem, p, w.q.ctx, tile, unit, part, wg);
+            if (rows <= 16) softmax_piece<T, D, 8>(a, m, sp, tmem, p, tile, unit, part, wg);
+            else if (rows <= 32) softmax_piece<T, D, 16>(a, m, sp, tmem, p, tile, unit, part, wg);
+            else if constexpr (G::NR == 64) softmax_piece<T, D, 32>(a, m, sp, tmem, p, tile, unit, part, wg);
         }
     } else if (warp >= kKd && warp < kVd) {
         // K: a lane is a position; two warps per 32 positions share its items.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         uint32_t tile = 0;
         const int wq = warp & 3, pos = 32 * wq + lane, h = (warp - kKd) >> 2;
+        const uint8_t* row0 = raw + pos * G::RB;
+        const uint32_t to0 = tmem + ((uint32_t)(32 * wq) << 16) + kTmemK;
+        uint32_t st = 0, rph = 0;   // the K tile's ring stage and its phase
 #pragma unroll 1
-        while (w.next(a, p)) {
+        for (uint32_t unit = 0; piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
+            const uint32_t end = tile + (m.piece[unit & 7].t1 - m.piece[unit & 7].t0);
 #pragma unroll 1
-            for (int t = p.t0; t < p.t1; ++t, ++tile) {
-                const uint32_t n = 2 * tile, st = n % G::NS, b = tile & 1;
-                wait_warp(&m.raw_full[st], (n / G::NS) & 1, a.status, abort);
-                if (tile >= 2) wait_warp(&m.k_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
+            for (; tile < end; ++tile) {
+                const uint32_t b = tile & 1;
+                if (lane == 0) {
+                    if (tile >= 2) wait_lane(&m.k_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
+                    wait_lane(&m.raw_full[st], rph, a.status, abort);
+                }
+                __syncwarp();
                 tc::fence_after_sync();
                 if (32 * wq < G::BN) {
-                    const uint8_t* row = raw + st * G::RAW + pos * G::RB;
-                    const uint32_t to = tmem + ((uint32_t)(32 * wq) << 16) + kTmemK + b * G::KC;
+                    const uint8_t* row = row0 + st * G::RAW;
+                    const uint32_t to = to0 + b * G::KC;
 #pragma unroll 1
                     for (int i = h; i < G::IPR; i += 2) {
                         const Item<T, D> item(row + i * Item<T, D>::BYTES);
@@ -811,6 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     mbar_arrive(&m.k_full[b]);
                     mbar_arrive(&m.raw_empty[st]);
                 }
+                if ((st += 2) == G::NS) st = 0, rph ^= 1;
             }
         }
     } else if (warp >= kVd) {
@@ -819,30 +842,34 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         // 17, 9 or 11 words apart, odd; positions 1, 2 or 4 times that) and
         // eight neighbouring lanes' 16-byte stores into the eight bank groups
         // of swizzled rows.  Before a unit's first tile, its queries.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         constexpr int SPW = D <= 64 ? 32 : 2048 / D;
         static_assert(G::ITEMS <= kDw * 32, "an item per decoding thread");
         uint32_t tile = 0, unit = 0;
         const int dt = tid - 32 * kVd;
         const bool mine = dt < G::ITEMS;
         const int pos = mine ? (dt / 32) * SPW + lane % SPW : 0, seg = mine ? lane / SPW : 0;
+        const uint8_t* src0 = raw + pos * G::RB + seg * Item<T, D>::BYTES;
+        uint8_t* line0 = sv + seg * G::CHB + pos * 128;
+        uint32_t st = 1, rph = 0;   // the V tile's ring stage and its phase
 #pragma unroll 1
-        for (; w.next(a, p); ++unit) {
+        for (;; ++unit) {
+            if (vote_v(!piece_ready(m, unit, a.status))) break;
+            const Piece& p = m.piece[unit & 7];
+            if (p.rows == 0) break;
             {
                 // Row by row to fp16 times a power of two that brings the row's
                 // largest magnitude to 2^14 .. 2^15 (bf16's 8 bits are exact).
                 constexpr int LPR = D / 8, ROUNDS = G::NR * LPR / 256 > 0 ? G::NR * LPR / 256 : 1;   // threads per row
-                const int N = cols_of(p.rows), sub = dt % LPR, blk = sub >> 2, k = sub & 3;         // 32-block, chunk
+                const int rows = p.rows, row0 = p.row0, tok0 = p.q.tok0, h0 = p.g * a.G;
+                const int N = cols_of(rows), sub = dt % LPR, blk = sub >> 2, k = sub & 3;           // 32-block, chunk
                 uint4 u[ROUNDS];
-                int tok[ROUNDS], hd[ROUNDS];
 #pragma unroll
                 for (int i = 0; i < ROUNDS; ++i) {
-                    const int row = p.row0 + i * (256 / LPR) + dt / LPR;
-                    tok[i] = row / a.G;
-                    hd[i] = p.g * a.G + row - tok[i] * a.G;
+                    const int row = i * (256 / LPR) + dt / LPR, tok = (row0 + row) / a.G;
                     u[i] = make_uint4(0, 0, 0, 0);
-                    if (row < p.row0 + p.rows) {
-                        const __nv_bfloat16* q = a.q + (w.q.tok0 + tok[i]) * a.q_stride + hd[i] * D + 32 * blk;
+                    if (row < rows) {
+                        const __nv_bfloat16* q = a.q + (tok0 + tok) * a.q_stride + (h0 + row0 + row - tok * a.G) * D + 32 * blk;
                         if constexpr (T == T_Q8_0) {
                             u[i] = *reinterpret_cast<const uint4*>(q + 8 * k);
                         } else {
@@ -851,7 +878,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                         }
                     }
                 }
+                uint64_t seen = 0;
+                int64_t rowoff = 0;
+                if (dt < rows) {
+                    const int tok = (row0 + dt) / a.G;
+                    seen = seen_of(a, p.q, tok);
+                    rowoff = (tok0 + tok) * a.out_stride + (h0 + row0 + dt - tok * a.G) * D;
+                }
                 if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a.status, abort);
+                if (dt < N) {
+                    m.seen[unit & 3][dt] = seen;
+                    m.rowoff[unit & 3][dt] = rowoff;
+                }
 #pragma unroll
                 for (int i = 0; i < ROUNDS; ++i) {
                     const int row = i * (256 / LPR) + dt / LPR;
@@ -874,12 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     *reinterpret_cast<uint4*>(sq + (sub >> 3) * (G::NR * 128) + row * 128 + (((sub & 7) ^ (row & 7)) << 4)) =
                         make_uint4(pack_f16(f[0] * down, f[2] * down), pack_f16(f[1] * down, f[3] * down),
                                    pack_f16(f[4] * down, f[6] * down), pack_f16(f[5] * down, f[7] * down));
-                    if (sub == 0) {
-                        const bool live = row < p.rows;
-                        m.colc[unit & 3][row] = live ? a.scale * 1.44269504088896341f * up : 0.0f;
-                        m.seen[unit & 3][row] = live ? seen_of(a, w.q, tok[i]) : 0;
-                        m.rowoff[unit & 3][row] = (w.q.tok0 + tok[i]) * a.out_stride + hd[i] * D;
-                    }
+                    if (sub == 0) m.colc[unit & 3][row] = row < rows ? a.scale * 1.44269504088896341f * up : 0.0f;
                 }
                 // The flags of unit + 1 (last of unit - 7, long done) start clear;
                 // no warp reaches that unit's V before q_full.
@@ -891,16 +924,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.q_full);
             }
+            int j = p.t0 * G::BN + pos - p.q.ctx;   // drafted token at the thread's position, if >= 0
+            const uint32_t end = tile + (p.t1 - p.t0);
 #pragma unroll 1
-            for (int t = p.t0; t < p.t1; ++t, ++tile) {
-                const uint32_t n = 2 * tile + 1, st = n % G::NS, b = tile & 1;
+            for (; tile < end; ++tile, j += G::BN) {
+                const uint32_t b = tile & 1;
                 if (lane == 0) {
-                    wait_lane(&m.raw_full[st], (n / G::NS) & 1, a.status, abort);
                     if (tile >= 2) wait_lane(&m.v_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
+                    wait_lane(&m.raw_full[st], rph, a.status, abort);
                 }
                 __syncwarp();
                 const bool valid = mine && ((reinterpret_cast<const uint32_t*>(&m.valid[tile & 15])[pos >> 5] >> (pos & 31)) & 1);
-                const Item<T, D> item(raw + st * G::RAW + pos * G::RB + seg * Item<T, D>::BYTES);
+                const Item<T, D> item(src0 + st * G::RAW);
                 // Scales that are finite but too large for fp16 times a code make the tile a large one, those that are
                 // not finite are recorded.
                 bool big = false;
@@ -914,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                             big = big || d <= 65504.0f;
                             if (!(d <= 65504.0f)) {
                                 good ^= 1u << i;
-                                const int j = t * G::BN + pos - w.q.ctx, blk = 2 * seg + i;
+                                const int blk = 2 * seg + i;
                                 if (j < 0) atomicOr(&m.bad_ctx[unit & 7][blk], 1u);
                                 else atomicOr(&m.bad_draft[unit & 7][blk], 1ull << (j & 63));
                             }
@@ -924,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 big = vote_v(big);
                 if (dt == 0) m.big_tile[tile & 15] = big;
                 if (mine) {
-                    uint8_t* line = sv + b * G::VB + seg * G::CHB + pos * 128;
+                    uint8_t* line = line0 + b * G::VB;
                     auto blocks = [&](auto is_big) {
 #pragma unroll
                         for (int i = 0; i < Item<T, D>::NBLK; ++i) {
@@ -946,60 +981,66 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     mbar_arrive(&m.v_full[b]);
                     mbar_arrive(&m.raw_empty[st]);
                 }
+                if ((st += 2) == G::NS + 1) st = 1, rph ^= 1;
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 0) {
             // Copies: the tile's rows of every page it touches, K then V.
             uint32_t n = 0, tile = 0;   // stages requested, tiles
             const uint64_t pol = policy_evict_first();
             bool ok = true;
-            const int pl = a.pool.page_log2, page = 1 << pl, span = min(page, G::BN), slabs = G::BN / span;
-            while (ok && w.next(a, p)) {
-                const int len = w.q.len;
-                const bool shared = groups_of(w.q, a.G, G::NR) > 1;   // other row groups read these bytes too
-                const int32_t* tab = a.table + (int64_t)p.r * a.table_stride;
-                // Page id of this lane's slab of tile t, -1 if it has none.
-                auto page_id = [&](int t) {
-                    const int pos = t * G::BN + lane * span;
-                    return t < p.t1 && lane < slabs && pos < len ? tab[pos >> pl] : -1;
-                };
-                int ahead = page_id(p.t0);
+            const int pl = a.pool.page_log2, sl = min(pl, G::BN == 64 ? 6 : 7);   // log2 of a slab's positions
+            const int span = 1 << sl, slabs = G::BN >> sl;
+            const int64_t page_bytes = ((int64_t)a.pool.n_kv << pl) * G::RB;
 #pragma unroll 1
-                for (int t = p.t0; ok && t < p.t1; ++t, ++tile) {
-                    const int pos0 = t * G::BN, pos = pos0 + lane * span;
+            for (uint32_t unit = 0; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
+                const Piece& p = m.piece[unit & 7];
+                const int len = p.q.len, t1 = p.t1;
+                const bool shared = groups_of(p.q, a.G, G::NR) > 1;   // other row groups read these bytes too
+                const int32_t* tab = a.table + (int64_t)p.r * a.table_stride;
+                const int64_t head = ((int64_t)p.g << pl) * G::RB;
+                int pos = p.t0 * G::BN + lane * span;   // this lane's slab
+                // Its page id, one tile ahead of the use.
+                auto page_id = [&](int at) { return lane < slabs && at < len ? tab[at >> pl] : -1; };
+                int ahead = page_id(pos);
+#pragma unroll 1
+                for (int t = p.t0; t < t1; ++t, ++tile, pos += G::BN) {
                     int id = ahead;
-                    ahead = page_id(t + 1);
-                    if (lane < slabs && pos < len && (id < 0 || id >= a.pool.n_pages)) {
+                    ahead = t + 1 < t1 ? page_id(pos + G::BN) : -1;
+                    const bool live = lane < slabs && pos < len;
+                    if (live && (id < 0 || id >= a.pool.n_pages)) {
                         atomicOr(a.status, STATUS_BAD_PAGE);
                         id = -1;
                     }
-                    const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-                    const int rows = id >= 0 ? min(span, len - pos) : 0;
+                    const int rows = id >= 0 && live ? min(span, len - pos) : 0;
                     const uint32_t bytes = (uint32_t)(rows * G::RB + 15) & ~15u;   // whole slabs are multiples of 16
-                    const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
-                    // Lane L reports positions 4 L .. 4 L + 3, which lie in one page.
-                    uint32_t bits = 0;
-                    if (4 * lane < G::BN && ((have >> (4 * lane / span)) & 1)) {
-                        const int left = len - (pos0 + 4 * lane);
-                        bits = left >= 4 ? 15u : left > 0 ? (1u << left) - 1 : 0u;
-                    }
-                    bits <<= 4 * (lane & 7);
+                    uint32_t sum = G::BN * G::RB;
+                    uint4 valid = make_uint4(~0u, ~0u, G::BN == 64 ? 0 : ~0u, G::BN == 64 ? 0 : ~0u);
+                    if (__any_sync(0xffffffffu, lane < slabs && rows < span)) {   // not whole
+                        sum = __reduce_add_sync(0xffffffffu, bytes);
+                        // Lane L reports positions 4 L .. 4 L + 3, which lie in one slab.
+                        const int left = __shfl_sync(0xffffffffu, rows, (4 * lane) >> sl) - ((4 * lane) & (span - 1));
+                        uint32_t bits = 4 * lane < G::BN ? (left >= 4 ? 15u : left > 0 ? (1u << left) - 1 : 0u) : 0u;
+                        bits <<= 4 * (lane & 7);
 #pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
-                    if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(&m.valid[tile & 15])[lane >> 3] = bits;
-                    __syncwarp();   // the valid words, before the arrival that publishes them
-                    const int64_t off = id >= 0 ? pool_row(a.pool, id, p.g, pos & (page - 1)) : 0;
-#pragma unroll 1
+                        for (int o = 1; o < 8; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+                        valid = make_uint4(__shfl_sync(0xffffffffu, bits, 0), __shfl_sync(0xffffffffu, bits, 8),
+                                           __shfl_sync(0xffffffffu, bits, 16), __shfl_sync(0xffffffffu, bits, 24));
+                    }
+                    if (lane == 0) m.valid[tile & 15] = valid;   // published by lane 0's arrival below
+                    const int64_t off = id >= 0 ? id * page_bytes + head + (pos & ((1 << pl) - 1)) * G::RB : 0;
+#pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++n) {
                         const int st = n % G::NS;
-                        if (n >= G::NS && !wait_warp(&m.raw_empty[st], (n / G::NS - 1) & 1, a.status, abort)) {
-                            ok = false;
-                            break;
+                        int good = 1;
+                        if (lane == 0) {
+                            if (n >= G::NS) good = wait_lane(&m.raw_empty[st], (n / G::NS - 1) & 1, a.status, abort);
+                            if (good) mbar_arrive_expect_tx(&m.raw_full[st], sum);
                         }
-                        if (lane == 0) mbar_arrive_expect_tx(&m.raw_full[st], sum);
-                        __syncwarp();
+                        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+                        if (!ok) break;
                         uint8_t* dst = raw + st * G::RAW + lane * span * G::RB;
                         const uint8_t* src = (kv ? a.V : a.K) + off;
                         if (bytes) {
@@ -1007,6 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                             else bulk_g2s(dst, src, bytes, &m.raw_full[st], pol);
                         }
                     }
+                    if (!ok) break;
                 }
             }
             // Copies in flight land before the CTA may leave.
@@ -1019,14 +1061,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             bool ok = true;
             const bool leader = tc::elect_one();
             const uint64_t dq = tc::sdesc_k128(smem_u32(sq));
-            for (; ok && w.next(a, p); ++unit) {
-                const uint32_t id = idesc_f16(cols_of(p.rows), false);
+            for (; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
+                const Piece& p = m.piece[unit & 7];
+                const uint32_t id = idesc_f16(cols_of(p.rows), false), begin = tile, end = tile + (p.t1 - p.t0);
 #pragma unroll 1
-                for (int t = p.t0; t < p.t1; ++t, ++tile) {
+                for (; tile < end; ++tile) {
                     const uint32_t b = tile & 1;
-                    if (t == p.t0) ok = ok && wait_warp(&m.q_full, unit & 1, a.status, abort);
-                    ok = ok && wait_warp(&m.k_full[b], (tile >> 1) & 1, a.status, abort);
-                    if (tile >= 2) ok = ok && wait_warp(&m.s_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
+                    int good = 1;
+                    if (lane == 0) {
+                        if (tile == begin) good = wait_lane(&m.q_full, unit & 1, a.status, abort);
+                        good = good && (tile < 2 || wait_lane(&m.p_full[b], ((tile >> 1) - 1) & 1, a.status, abort));   // S^T has been read
+                        good = good && wait_lane(&m.k_full[b], (tile >> 1) & 1, a.status, abort);
+                    }
+                    ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (leader) {
@@ -1035,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                             mma_ta(tmem + 64 * b, tmem + kTmemK + b * G::KC + 8 * k, dq + ((k >> 2) * (G::NR * 8) + 2 * (k & 3)), id, k > 0);
                         tc::commit(&m.s_full[b]);
                         tc::commit(&m.k_empty[b]);
-                        if (t == p.t1 - 1) tc::commit(&m.q_empty);
+                        if (tile == end - 1) tc::commit(&m.q_empty);
                     }
                     __syncwarp();
                 }
@@ -1053,15 +1100,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             const bool leader = tc::elect_one();
             // d <= 64: one chunk only, read twice (rows 64 .. 127 of O^T are not used)
             const uint64_t dv = sdesc_mn128(smem_u32(sv), D <= 64 ? 0 : G::CHB), dp = sdesc_mn128(smem_u32(sp), 0);
-            for (; ok && w.next(a, p); ++unit) {
-                const uint32_t id = idesc_f16(cols_of(p.rows), true);
+            for (; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
+                const Piece& p = m.piece[unit & 7];
+                const uint32_t id = idesc_f16(cols_of(p.rows), true), begin = tile, end = tile + (p.t1 - p.t0);
                 unsigned used = 0;
 #pragma unroll 1
-                for (int t = p.t0; t < p.t1; ++t, ++tile) {
+                for (; tile < end; ++tile) {
                     const uint32_t b = tile & 1;
-                    ok = ok && wait_warp(&m.v_full[b], (tile >> 1) & 1, a.status, abort);
-                    if (t == p.t0 && unit > 0) ok = ok && wait_warp(&m.o_empty, (unit - 1) & 1, a.status, abort);
-                    ok = ok && wait_warp(&m.p_full[b], (tile >> 1) & 1, a.status, abort);
+                    int good = 1;
+                    if (lane == 0) {
+                        if (tile == begin && unit > 0) good = wait_lane(&m.o_empty, (unit - 1) & 1, a.status, abort);
+                        good = good && wait_lane(&m.v_full[b], (tile >> 1) & 1, a.status, abort) &&
+                               wait_lane(&m.p_full[b], (tile >> 1) & 1, a.status, abort);
+                    }
+                    ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                     if (!ok) break;
                     tc::fence_after_sync();
                     const bool big = *(volatile unsigned*)&m.big_tile[tile & 15] != 0;
@@ -1090,22 +1142,40 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 __syncwarp();
             }
         } else {
-            // The unit cut at this CTA's start, for join_kernel.
-            W first = w;
+            // The pieces, and the unit cut at this CTA's start for join_kernel.
             Cut c{};
-            if (first.next(a, p) && p.t0 > 0) {
-                const int from = p.u0 / per;
-                if (from == (int)blockIdx.x - 1) {
-                    c.rows = p.rows;
-                    c.first = from;
-                    c.last = (p.u0 + p.nt - 1) / per;
-                    c.first_slot = 2 * from + (p.u0 % per != 0);
-                    c.tok0 = first.q.tok0;
-                    c.row0 = p.row0;
-                    c.g = p.g;
+            if (lane == 0) {
+                Walk<G::BN, G::NR> w{x0, x1, 0, 0, Req{0, 0, 0, 0}};
+                if (x0 < x1) {
+                    w.base = m.start_base;
+                    w.r = m.start_r;
+                    w.q = m.start_q;
+                }
+                for (uint32_t unit = 0;; ++unit) {
+                    Piece p;
+                    const bool more = w.next(a, p);
+                    if (!more) p.rows = 0;
+                    if (unit == 0 && more && p.t0 > 0) {
+                        const int from = p.u0 / per;
+                        if (from == (int)blockIdx.x - 1) {
+                            c.rows = p.rows;
+                            c.first = from;
+                            c.last = (p.u0 + p.nt - 1) / per;
+                            c.first_slot = 2 * from + (p.u0 % per != 0);
+                            c.tok0 = p.q.tok0;
+                            c.row0 = p.row0;
+                            c.g = p.g;
+                        }
+                    }
+                    if (unit >= 8 && !wait_lane(&m.piece_free[unit & 7], ((unit >> 3) - 1) & 1, a.status, abort)) break;
+                    if (more) m.piece[unit & 7] = p;
+                    else m.piece[unit & 7].rows = 0;
+                    mbar_arrive(&m.piece_full[unit & 7]);
+                    if (unit == 0) reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = c;
+                    if (!more) break;
                 }
             }
-            if (lane == 0) reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = c;
+            __syncwarp();
         }
     }
     tc::fence_before_sync();

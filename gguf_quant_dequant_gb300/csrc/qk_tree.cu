@@ -26,12 +26,12 @@
 // threads; the rows' sums of probabilities stay per thread until the unit's
 // end.
 //
-// Warps: 0 copies (cp.async.bulk of the pages' contiguous head slabs into a
-// ring), 1 issues Q K, 2 issues P V, 3 notes a cut unit; 4-11 softmax and
-// epilogue (two warpgroups, half of the rows each); 12-19 decode K; 20-27
-// decode V and load the unit's queries.  A tile is a chain of short steps, so
-// it is the number of warps on it that sets the rate: with one warpgroup each
-// for softmax and (K and V) decoding a tile took 5,000 clocks.  Every hand-over
+// Warps: 0 and 3 copy K and V (cp.async.bulk of the pages' contiguous head
+// slabs into a ring), 1 issues Q K, 2 issues P V; 4-11 softmax and epilogue
+// (two warpgroups, half of the rows each); 12-19 decode K; 20-27 decode V and
+// load the unit's queries.  A tile is a chain of short steps, so it is the
+// number of warps on it that sets the rate: with one warpgroup each for
+// softmax and (K and V) decoding a tile took 5,000 clocks.  Every hand-over
 // is an mbarrier with a bounded wait; after a wait has run out (status word)
 // the copies and MMAs stop, the other roles run through without waiting, and
 // the CTA leaves in order.
@@ -77,6 +77,7 @@ struct Args {
     const int32_t *ctx, *cu;
     const uint64_t* mask;
     int n_req, max_q, G;
+    uint32_t g_magic;   // ceil(2^19 / G): row / G = row * g_magic >> 19 for row < 4160, G <= 64
     float scale;
     __nv_bfloat16* out;
     int64_t out_stride;
@@ -107,6 +108,9 @@ __device__ __forceinline__ uint64_t seen_of(const Args& a, const Req& q, int i) 
     const uint64_t in = q.n >= 64 ? ~uint64_t(0) : (uint64_t(1) << q.n) - 1;
     return (a.mask ? a.mask[q.tok0 + i] : (i >= 63 ? ~uint64_t(0) : (uint64_t(2) << i) - 1)) & in;
 }
+
+// Token of a row: row / G.
+__device__ __forceinline__ int token_of(const Args& a, int row) { return (int)((uint32_t)row * a.g_magic >> 19); }
 
 // Geometry of one instantiation.
 template <int T, int D> struct Geo {
@@ -149,7 +153,7 @@ struct __align__(16) Misc {
     uint64_t seen[4][kRows];     // by unit mod 4, as the next two
     float colc[4][kRows];
     int64_t rowoff[4][kRows];    // the row's place in out
-    uint4 valid[16];             // by tile mod 16: bit per position that exists
+    uint4 valid[2][16];          // K's, V's copier: by tile mod 16, a bit per position that exists
     float ref[kRows], factor[kRows];
     float wsum[4][kRows];
     float wmax[4][kRows];
@@ -163,7 +167,7 @@ struct __align__(16) Misc {
     Piece piece[8];              // by unit mod 8
     int scan[32];
     Req start_q;
-    int start_base, start_r, abort;
+    int start_base, start_w, start_r, abort;
     uint32_t tmem;
 };
 static_assert(sizeof(Misc) <= 10752, "Misc");
@@ -182,11 +186,10 @@ __device__ __forceinline__ int cols_of(int rows) { return rows <= 16 ? 16 : rows
 // The pieces of the run [x, end) of the list; the present request r's tiles
 // start at base.
 template <int BN, int NR> struct Walk {
-    int x, end, base, r;
+    int x, end, base, w, r;   // w: the present request's tiles
     Req q;
     __device__ __forceinline__ bool next(const Args& a, Piece& p) {
         if (x >= end) return false;
-        int w = work_of<BN, NR>(a, q);
         while (x >= base + w) {
             base += w;
             q = req_of(a, ++r);
@@ -342,14 +345,16 @@ __device__ __forceinline__ void bulk_g2s_keep(void* dst, const void* src, uint32
 }
 
 // A wait of the roles that run on after a failure: no waiting once *abort is
-// set.  One lane polls, the warp waits for it.
+// set.  One lane polls, the warp waits for it.  Between looks the hardware
+// suspends the lane until the phase completes or 4 us have passed (warps that
+// spin take a third of the issue slots from the working ones); 2^19 looks are
+// 2 s.  Kept short: it stands in 20 places, and the roles' code has to stay in
+// the instruction cache together.
 __device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 1; i < kWaitSpins; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (uint32_t i = 0; i < (1u << 19); ++i) {
+        if (mbar_try_wait_sleep(bar, parity, 4000u)) return true;
         if (*abort) return false;
-        if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitNs) break;
     }
     *abort = 1;
     atomicOr(status, STATUS_TIMEOUT);
@@ -481,102 +486,88 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         }
         __syncwarp();
         tc::fence_after_sync();
-        uint32_t s[C];   // scores, then probabilities
-        auto load = [&] {
-#pragma unroll
-            for (int h = 0; h < C; h += CW) tmem_ld(lanes + 64 * b + c0 + h, *reinterpret_cast<uint32_t(*)[CW]>(&s[h]));
-        };
-        load();
         const int pos0 = t * G::BN;
-        const uint4 vw = m.valid[tile & 15];
+        const uint4 vw = m.valid[0][tile & 15];
         const bool all = pos0 + G::BN <= ctx && (vw.x & vw.y) == 0xffffffffu && (G::BN == 64 || (vw.z & vw.w) == 0xffffffffu);
         const uint32_t mine = wq == 0 ? vw.x : wq == 1 ? vw.y : wq == 2 ? vw.z : vw.w;
         const bool here = (mine >> lane) & 1;   // the position exists (false past BN)
         const int j = pos0 + tid - ctx;         // drafted token at this position, if >= 0
-        // Visibility of this position to column c.
-        auto vis = [&](int c) { return here && (j < 0 || ((seen[c] >> (j & 63)) & 1)); };
-        const bool first = t == t0;
-        // Scores to probabilities (lifted) on the present references; the
-        // largest of their logarithms.
-        auto probabilities = [&](auto masked) {
+        const float* mul = m.colc[unit & 3] + c0;
+        bool renew = t == t0;   // the references are to be found
+        uint32_t s[C];          // scores, then probabilities
+        // Once round for an ordinary tile; a first tile finds its references
+        // and comes round again, one whose scores outgrow them (x > kOver)
+        // goes through that after its first round.
+#pragma unroll 1
+        for (int round = 0;; ++round) {
+#pragma unroll
+            for (int h = 0; h < C; h += CW) tmem_ld(lanes + 64 * b + c0 + h, *reinterpret_cast<uint32_t(*)[CW]>(&s[h]));
+            tc::tmem_wait_ld();
+            if (!all || (G::BN == 64 && wq >= 2)) {
+                // A hidden score becomes the infinity that the column's
+                // multiplier turns into -inf.
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (!(here && (j < 0 || ((seen[c] >> (j & 63)) & 1)))) s[c] = mul[c] < 0.0f ? 0x7f800000u : 0xff800000u;
+            }
+            if (renew) {
+                renew = false;
+                float y[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) y[c] = __uint_as_float(s[c]) * mul[c];
+                warp_columns<C>(y, lane, [](float x, float z) { return fmaxf(x, z); });   // NaN aside
+                if (lane < C) m.wmax[wq][c0 + lane] = y[0];
+                sync_group(wg);
+                if (tid < C) {
+                    const int c = c0 + tid;
+                    const float top = fmaxf(fmaxf(m.wmax[0][c], m.wmax[1][c]), fmaxf(m.wmax[2][c], m.wmax[3][c]));
+                    const float old = t == t0 ? -INFINITY : m.ref[c], now = fmaxf(fmaxf(old, top), -INFINITY);   // never NaN
+                    m.factor[c] = old == -INFINITY ? 0.0f : ex2(old - now);
+                    m.ref[c] = now;
+                    m.cmul[c] = mul[tid];
+                    m.cref[c] = now == -INFINITY ? 1e30f : kLift - now;   // nothing visible yet: whatever comes outgrows it
+                }
+                sync_group(wg);
+                if (t != t0) {   // the sums on the new references
+#pragma unroll
+                    for (int c = 0; c < C; c += 2)
+                        l2[c / 2] = mul2(l2[c / 2], *reinterpret_cast<const uint64_t*>(&m.factor[c0 + c]));
+                    wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a.status, abort);   // O^T is at rest
+                    tc::fence_after_sync();
+                    const int sets = *(volatile unsigned*)&m.used[unit & 7] & 2 ? 2 : 1;   // the plain sums, the large tiles' too
+#pragma unroll 1
+                    for (int k = 0; k < (D == 256 ? 2 : 1) * sets; ++k) {
+                        const uint32_t at = lanes + (D == 256 ? kTmemO + 32 * (k & 1) + (kTmemBig - kTmemO) * (k >> 1)
+                                                              : kTmemO + (kTmemBig - kTmemO) * k) + c0;
+#pragma unroll 1
+                        for (int h = 0; h < C; h += 8) {
+                            uint32_t v[8];
+                            tmem_ld(at + h, v);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * m.factor[c0 + h + c]);
+                            tmem_st(at + h, v);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                continue;
+            }
+            // Scores to (lifted) probabilities on the present references.
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < C; c += 4) {
                 const float4 k = *reinterpret_cast<const float4*>(&m.cmul[c0 + c]), r = *reinterpret_cast<const float4*>(&m.cref[c0 + c]);
                 const float2 u = unpair(fma2(pair(s[c], s[c + 1]), pair(k.x, k.y), pair(r.x, r.y)));
                 const float2 v = unpair(fma2(pair(s[c + 2], s[c + 3]), pair(k.z, k.w), pair(r.z, r.w)));
-                float x[4] = {u.x, u.y, v.x, v.y};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // a hidden position: probability 0, whatever the score (and the reference: none yet is -inf)
-                    if constexpr (decltype(masked)::value) x[i] = vis(c + i) ? x[i] : -INFINITY;
-                    s[c + i] = __float_as_uint(ex2(x[i]));
-                }
-                mx = fmaxf(fmaxf(mx, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
+                mx = fmaxf(fmaxf(mx, fmaxf(u.x, u.y)), fmaxf(v.x, v.y));
+                s[c] = __float_as_uint(ex2(u.x));
+                s[c + 1] = __float_as_uint(ex2(u.y));
+                s[c + 2] = __float_as_uint(ex2(v.x));
+                s[c + 3] = __float_as_uint(ex2(v.y));
             }
-            return mx;
-        };
-        tc::tmem_wait_ld();
-        bool over = true;
-        if (!first) over = (all ? probabilities(std::false_type{}) : probabilities(std::true_type{})) > kOver;
-        if (vote_group(wg, over && (G::BN == 128 || tid < G::BN))) {
-            // New references: the rows' maxima over the tile.
-            if (!first) {
-                load();
-                tc::tmem_wait_ld();
-            }
-            const float* mul = m.colc[unit & 3] + c0;
-            {
-                float y[C];
-#pragma unroll
-                for (int c = 0; c < C; ++c) y[c] = __uint_as_float(s[c]) * mul[c];
-                if (!all || G::BN == 64) {
-#pragma unroll
-                    for (int c = 0; c < C; ++c) y[c] = vis(c) ? y[c] : -INFINITY;
-                }
-                warp_columns<C>(y, lane, [](float x, float z) { return fmaxf(x, z); });   // NaN aside
-                if (lane < C) m.wmax[wq][c0 + lane] = y[0];
-                load();   // the scores again: their registers held the maxima's exchange
-            }
-            sync_group(wg);
-            if (tid < C) {
-                const int c = c0 + tid;
-                const float top = fmaxf(fmaxf(m.wmax[0][c], m.wmax[1][c]), fmaxf(m.wmax[2][c], m.wmax[3][c]));
-                const float old = first ? -INFINITY : m.ref[c], now = fmaxf(fmaxf(old, top), -INFINITY);   // never NaN
-                m.factor[c] = old == -INFINITY ? 0.0f : ex2(old - now);
-                m.ref[c] = now;
-                m.cmul[c] = mul[tid];
-                m.cref[c] = kLift - now;
-            }
-            sync_group(wg);
-            if (!first) {
-#pragma unroll
-                for (int c = 0; c < C; c += 2)
-                    l2[c / 2] = mul2(l2[c / 2], *reinterpret_cast<const uint64_t*>(&m.factor[c0 + c]));
-            }
-            tc::tmem_wait_ld();
-            if (all) probabilities(std::false_type{});
-            else probabilities(std::true_type{});
-            if (!first) {
-                wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a.status, abort);   // O^T is at rest
-                tc::fence_after_sync();
-                const int sets = *(volatile unsigned*)&m.used[unit & 7] & 2 ? 2 : 1;   // the plain sums, the large tiles' too
-#pragma unroll 1
-                for (int k = 0; k < (D == 256 ? 2 : 1) * sets; ++k) {
-                    const uint32_t at = lanes + (D == 256 ? kTmemO + 32 * (k & 1) + (kTmemBig - kTmemO) * (k >> 1)
-                                                          : kTmemO + (kTmemBig - kTmemO) * k) + c0;
-#pragma unroll 1
-                    for (int h = 0; h < C; h += CW) {
-                        uint32_t v[CW];
-                        tmem_ld(at + h, v);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < CW; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * m.factor[c0 + h + c]);
-                        tmem_st(at + h, v);
-                    }
-                }
-                tmem_wait_st();
-            }
+            if (!vote_group(wg, mx > kOver) || round == 2) break;
+            renew = true;
         }
         uint8_t* row = sp + b * G::PB + tid * 128;
 #pragma unroll
@@ -612,7 +603,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         const int c = c0 + tid;
         const float sum = m.wsum[0][c] + m.wsum[1][c] + m.wsum[2][c] + m.wsum[3][c];
         if (whole) m.factor[c] = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw nothing: zeros
-        else *reinterpret_cast<float2*>(po + kRows * D + 2 * c) = make_float2(-m.cref[c], sum);
+        else *reinterpret_cast<float2*>(po + kRows * D + 2 * c) = make_float2(m.ref[c], sum);
     }
     const uint32_t last = tile - 1;
     wait_warp(&m.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
@@ -629,25 +620,25 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         const uint64_t bad = m.bad_ctx[unit & 7][blk] ? ~uint64_t(0) : m.bad_draft[unit & 7][blk];
         const bool bad_all = m.bad_ctx[unit & 7][blk] != 0;
 #pragma unroll 1
-        for (int h = 0; h < C; h += CW) {
-            uint32_t v[CW];
+        for (int h = 0; h < C; h += 8) {
+            uint32_t v[8];
             tmem_ld(lanes + kTmemO + 32 * half + c0 + h, v);
             tc::tmem_wait_ld();
             if (used != 1) {
-                uint32_t u[CW];
+                uint32_t u[8];
                 tmem_ld(lanes + kTmemBig + 32 * half + c0 + h, u);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < CW; ++c)
+                for (int c = 0; c < 8; ++c)
                     v[c] = __float_as_uint((used & 1 ? __uint_as_float(v[c]) : 0.0f) + (used & 2 ? kBig * __uint_as_float(u[c]) : 0.0f));
             }
             if (bad) {
 #pragma unroll
-                for (int c = 0; c < CW; ++c)
+                for (int c = 0; c < 8; ++c)
                     if (bad_all || (bad & seen[h + c])) v[c] = 0x7fffffffu;
             }
 #pragma unroll
-            for (int c = 0; c < CW; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 if (c0 + h + c < rows) {
                     const float o = __uint_as_float(v[c]);
                     if (whole) a.out[rowoff[h + c] + e] = __float2bfloat16_rn(o * m.factor[c0 + h + c]);
@@ -747,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             if (upto - w <= x0 && x0 < upto) {
                 m.start_r = r0 + tid;
                 m.start_base = upto - w;
+                m.start_w = w;
                 m.start_q = q;
             }
         };
@@ -770,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     tc::fence_after_sync();
     const uint32_t tmem = m.tmem;
     const int x1 = min(x0 + per, total);
-    // Registers per thread of the seven warpgroups: 48, 2 x 120, 2 x 48, 2 x 56, within the launch's 7 x 72.
+    // Registers per thread of the seven warpgroups: 56, 2 x 120, 2 x 48, 2 x 56, within the launch's 7 x 72.
     if (warp >= kSm && warp < kKd) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int wg = (warp - kSm) >> 2;
@@ -866,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 uint4 u[ROUNDS];
 #pragma unroll
                 for (int i = 0; i < ROUNDS; ++i) {
-                    const int row = i * (256 / LPR) + dt / LPR, tok = (row0 + row) / a.G;
+                    const int row = i * (256 / LPR) + dt / LPR, tok = token_of(a, row0 + row);
                     u[i] = make_uint4(0, 0, 0, 0);
                     if (row < rows) {
                         const __nv_bfloat16* q = a.q + (tok0 + tok) * a.q_stride + (h0 + row0 + row - tok * a.G) * D + 32 * blk;
@@ -881,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 uint64_t seen = 0;
                 int64_t rowoff = 0;
                 if (dt < rows) {
-                    const int tok = (row0 + dt) / a.G;
+                    const int tok = token_of(a, row0 + dt);
                     seen = seen_of(a, p.q, tok);
                     rowoff = (tok0 + tok) * a.out_stride + (h0 + row0 + dt - tok * a.G) * D;
                 }
@@ -934,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     wait_lane(&m.raw_full[st], rph, a.status, abort);
                 }
                 __syncwarp();
-                const bool valid = mine && ((reinterpret_cast<const uint32_t*>(&m.valid[tile & 15])[pos >> 5] >> (pos & 31)) & 1);
+                const bool valid = mine && ((reinterpret_cast<const uint32_t*>(&m.valid[1][tile & 15])[pos >> 5] >> (pos & 31)) & 1);
                 const Item<T, D> item(src0 + st * G::RAW);
                 // Scales that are finite but too large for fp16 times a code make the tile a large one, those that are
                 // not finite are recorded.
@@ -985,22 +977,53 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 0) {
-            // Copies: the tile's rows of every page it touches, K then V.
-            uint32_t n = 0, tile = 0;   // stages requested, tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 || warp == 3) {
+            // Copies: the tile's rows of every page it touches, K's by warp 0
+            // (which also walks the list and publishes the pieces), V's by warp 3.
+            const int kv = warp == 3;
+            const uint8_t* pool = kv ? a.V : a.K;
+            uint32_t tile = 0, st = kv, rph = 1;   // ring stage; phase of its release (the first round passes at once)
             const uint64_t pol = policy_evict_first();
             bool ok = true;
             const int pl = a.pool.page_log2, sl = min(pl, G::BN == 64 ? 6 : 7);   // log2 of a slab's positions
             const int span = 1 << sl, slabs = G::BN >> sl;
             const int64_t page_bytes = ((int64_t)a.pool.n_kv << pl) * G::RB;
+            const bool leader = tc::elect_one();
+            Walk<G::BN, G::NR> w{x0, x1, m.start_base, m.start_w, m.start_r, m.start_q};
 #pragma unroll 1
-            for (uint32_t unit = 0; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
-                const Piece& p = m.piece[unit & 7];
+            for (uint32_t unit = 0; ok; ++unit) {
+                Piece p;
+                if (kv) {
+                    if (!piece_ready(m, unit, a.status)) break;
+                    p = m.piece[unit & 7];
+                } else {
+                    const bool more = w.next(a, p);
+                    if (unit >= 8 && !wait_warp(&m.piece_free[unit & 7], ((unit >> 3) - 1) & 1, a.status, abort)) break;
+                    if (!more) p.rows = 0;
+                    if (lane == 0) {
+                        m.piece[unit & 7] = p;
+                        mbar_arrive(&m.piece_full[unit & 7]);
+                    }
+                    if (unit == 0) {   // a unit cut at this CTA's start, for join_kernel
+                        Cut c{};
+                        if (more && p.t0 > 0 && p.u0 / per == (int)blockIdx.x - 1) {
+                            c.rows = p.rows;
+                            c.first = (int)blockIdx.x - 1;
+                            c.last = (p.u0 + p.nt - 1) / per;
+                            c.first_slot = 2 * c.first + (p.u0 != c.first * per);
+                            c.tok0 = p.q.tok0;
+                            c.row0 = p.row0;
+                            c.g = p.g;
+                        }
+                        if (lane == 0) reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = c;
+                    }
+                }
+                if (p.rows == 0) break;
                 const int len = p.q.len, t1 = p.t1;
                 const bool shared = groups_of(p.q, a.G, G::NR) > 1;   // other row groups read these bytes too
                 const int32_t* tab = a.table + (int64_t)p.r * a.table_stride;
-                const int64_t head = ((int64_t)p.g << pl) * G::RB;
+                const uint8_t* head = pool + ((int64_t)p.g << pl) * G::RB;
                 int pos = p.t0 * G::BN + lane * span;   // this lane's slab
                 // Its page id, one tile ahead of the use.
                 auto page_id = [&](int at) { return lane < slabs && at < len ? tab[at >> pl] : -1; };
@@ -1029,32 +1052,38 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                         valid = make_uint4(__shfl_sync(0xffffffffu, bits, 0), __shfl_sync(0xffffffffu, bits, 8),
                                            __shfl_sync(0xffffffffu, bits, 16), __shfl_sync(0xffffffffu, bits, 24));
                     }
-                    if (lane == 0) m.valid[tile & 15] = valid;   // published by lane 0's arrival below
-                    const int64_t off = id >= 0 ? id * page_bytes + head + (pos & ((1 << pl) - 1)) * G::RB : 0;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++n) {
-                        const int st = n % G::NS;
-                        int good = 1;
-                        if (lane == 0) {
-                            if (n >= G::NS) good = wait_lane(&m.raw_empty[st], (n / G::NS - 1) & 1, a.status, abort);
-                            if (good) mbar_arrive_expect_tx(&m.raw_full[st], sum);
-                        }
-                        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
-                        if (!ok) break;
-                        uint8_t* dst = raw + st * G::RAW + lane * span * G::RB;
-                        const uint8_t* src = (kv ? a.V : a.K) + off;
-                        if (bytes) {
-                            if (shared) bulk_g2s_keep(dst, src, bytes, &m.raw_full[st]);
-                            else bulk_g2s(dst, src, bytes, &m.raw_full[st], pol);
+                    const uint32_t src_in = (pos & ((1 << pl) - 1)) * G::RB;   // inside the page's head
+                    int good = 1;
+                    if (lane == 0) {
+                        good = wait_lane(&m.raw_empty[st], rph, a.status, abort);
+                        m.valid[kv][tile & 15] = valid;   // published by the arrival
+                        if (good) mbar_arrive_expect_tx(&m.raw_full[st], sum);
+                    }
+                    ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+                    if (!ok) break;
+                    // One lane issues: with an issuing lane per slab the copies take several hundred clocks each.
+#pragma unroll 1
+                    for (int i = 0; i < slabs; ++i) {
+                        const uint32_t n = __shfl_sync(0xffffffffu, bytes, i);
+                        const int64_t off = __shfl_sync(0xffffffffu, id, i) * page_bytes + __shfl_sync(0xffffffffu, src_in, i);
+                        if (leader && n) {
+                            uint8_t* dst = raw + st * G::RAW + i * span * G::RB;
+                            if (shared) bulk_g2s_keep(dst, head + off, n, &m.raw_full[st]);
+                            else bulk_g2s(dst, head + off, n, &m.raw_full[st], pol);
                         }
                     }
-                    if (!ok) break;
+                    __syncwarp();
+                    if ((st += 2) >= G::NS) st = kv, rph ^= 1;
                 }
             }
             // Copies in flight land before the CTA may leave.
-            if (!ok)
-                for (uint32_t i = n > G::NS ? n - G::NS : 0; i < n; ++i)
-                    mbar_wait_bounded(&m.raw_full[i % G::NS], (i / G::NS) & 1, a.status);
+            if (!ok) {
+                const uint32_t last = tile < G::NS / 2 ? tile : G::NS / 2;   // requested and perhaps not yet seen
+                for (uint32_t i = 1; i <= last; ++i) {
+                    const uint32_t k = tile - i;
+                    mbar_wait_bounded(&m.raw_full[(2 * k + kv) % G::NS], (2 * k + kv) / G::NS & 1, a.status);
+                }
+            }
         } else if (warp == 1) {
             // Q K: the warp walks together, one lane issues.
             uint32_t tile = 0, unit = 0;
@@ -1093,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 if (lane == 0) mbar_wait_bounded(&m.drain[0], 0, a.status);
                 __syncwarp();
             }
-        } else if (warp == 2) {
+        } else {
             // P V.
             uint32_t tile = 0, unit = 0;
             bool ok = true;
@@ -1141,41 +1170,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 if (lane == 0) mbar_wait_bounded(&m.drain[1], 0, a.status);
                 __syncwarp();
             }
-        } else {
-            // The pieces, and the unit cut at this CTA's start for join_kernel.
-            Cut c{};
-            if (lane == 0) {
-                Walk<G::BN, G::NR> w{x0, x1, 0, 0, Req{0, 0, 0, 0}};
-                if (x0 < x1) {
-                    w.base = m.start_base;
-                    w.r = m.start_r;
-                    w.q = m.start_q;
-                }
-                for (uint32_t unit = 0;; ++unit) {
-                    Piece p;
-                    const bool more = w.next(a, p);
-                    if (!more) p.rows = 0;
-                    if (unit == 0 && more && p.t0 > 0) {
-                        const int from = p.u0 / per;
-                        if (from == (int)blockIdx.x - 1) {
-                            c.rows = p.rows;
-                            c.first = from;
-                            c.last = (p.u0 + p.nt - 1) / per;
-                            c.first_slot = 2 * from + (p.u0 % per != 0);
-                            c.tok0 = p.q.tok0;
-                            c.row0 = p.row0;
-                            c.g = p.g;
-                        }
-                    }
-                    if (unit >= 8 && !wait_lane(&m.piece_free[unit & 7], ((unit >> 3) - 1) & 1, a.status, abort)) break;
-                    if (more) m.piece[unit & 7] = p;
-                    else m.piece[unit & 7].rows = 0;
-                    mbar_arrive(&m.piece_full[unit & 7]);
-                    if (unit == 0) reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = c;
-                    if (!more) break;
-                }
-            }
-            __syncwarp();
         }
     }
     tc::fence_before_sync();
@@ -1286,7 +1280,8 @@ cudaError_t launch_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_s
                              int n_heads, int n_kv, int d, float scale, void* out, int64_t out_stride, void* ws,
                              unsigned* status, int sms, cudaStream_t s) {
     const tree::Args a{static_cast<const __nv_bfloat16*>(q), n_tok, q_stride, K, V, Pool{n_pages, page_log2, n_kv, row_bytes},
-                       table, table_stride, ctx, cu, mask, (int)n_req, max_q, n_heads / n_kv, scale,
+                       table, table_stride, ctx, cu, mask, (int)n_req, max_q, n_heads / n_kv,
+                       (uint32_t)(((1 << 19) + n_heads / n_kv - 1) / (n_heads / n_kv)), scale,
                        static_cast<__nv_bfloat16*>(out), out_stride, static_cast<uint8_t*>(ws),
                        tree_ctas(n_req, max_q, table_stride << page_log2, n_heads, n_kv, d, sms), status};
     switch (type) {

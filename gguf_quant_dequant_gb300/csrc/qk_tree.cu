@@ -23,8 +23,8 @@
 // only as a reference: a tile keeps the present reference unless some score
 // exceeds it by 2^8 (one vote), and only then the new maxima are found and O
 // and the sums are rescaled, so the ordinary tile has no reduction across
-// threads; the rows' sums of probabilities stay per thread until the unit's
-// end.
+// threads; the rows' sums of probabilities are one more product, with ones in
+// V's place, which leaves them in every lane.
 //
 // Warps: 0 and 3 copy K and V (cp.async.bulk of the pages' contiguous head
 // slabs into a ring), 1 issues Q K, 2 issues P V; 4-11 softmax and epilogue
@@ -128,7 +128,8 @@ template <int T, int D> struct Geo {
     static constexpr int ITEMS = BN * D / ITEM;            // of them in a tile
     static constexpr int IPR = D / ITEM;                   // in a row
     static constexpr int KC = D / 2;                       // tensor-memory columns of a K tile
-    static constexpr int FIXED = kV * VB + QB + 2 * PB;
+    static constexpr int TL = D == 256 ? 32 : 384;         // tensor-memory column of the rows' sums (S^T has 32 columns of 64 at d = 256)
+    static constexpr int FIXED = kV * VB + QB + 2 * PB + 1024;   // and the tile of ones
     static constexpr int MISC = 10752;
     static constexpr int NS0 = (227 * 1024 - 1024 - MISC - FIXED) / RAW;
     static constexpr int NS = (NS0 > 8 ? 8 : NS0) & ~1;    // ring stages; even: V tiles always take the odd ones
@@ -155,7 +156,6 @@ struct __align__(16) Misc {
     int64_t rowoff[4][kRows];    // the row's place in out
     uint4 valid[2][16];          // K's, V's copier: by tile mod 16, a bit per position that exists
     float ref[kRows], factor[kRows];
-    float wsum[4][kRows];
     float wmax[4][kRows];
     unsigned long long bad_draft[8][8];   // by unit mod 8, 32-block: drafted V rows that are not finite
     unsigned bad_ctx[8][8];
@@ -443,21 +443,21 @@ template <int T, int D> struct Item {
 
 // -------------------------------------------------------------- softmax ----
 
-// op over the warp of v[0 .. C): lane l gets column l mod C in v[0], by
-// exchanging halves.
-template <int C, class Op>
-__device__ __forceinline__ void warp_columns(float (&v)[C], int lane, Op op) {
+// The warp's maxima of v[0 .. C) (NaN aside): lane l gets column l mod C in
+// v[0], by exchanging halves.
+template <int C>
+__device__ __forceinline__ void warp_max_columns(float (&v)[C], int lane) {
 #pragma unroll
     for (int o = 16; o >= C; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+        for (int i = 0; i < C; ++i) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
 #pragma unroll
     for (int o = C / 2; o >= 1; o >>= 1)
 #pragma unroll
         for (int i = 0; i < o; ++i) {
             const bool up = lane & o;
             const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+            v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
         }
 }
 
@@ -474,9 +474,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
     const uint64_t* seen = m.seen[unit & 3] + c0;
     volatile int* abort = &m.abort;
     const int t0 = p.t0, t1 = p.t1, ctx = p.q.ctx;
-    uint64_t l2[C / 2];   // this thread's sums of probabilities, columns in pairs
-#pragma unroll
-    for (int c = 0; c < C / 2; ++c) l2[c] = 0;
+    const float* mul = m.colc[unit & 3] + c0;
 #pragma unroll 1
     for (int t = t0; t < t1; ++t, ++tile) {
         const uint32_t b = tile & 1;
@@ -492,35 +490,40 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         const uint32_t mine = wq == 0 ? vw.x : wq == 1 ? vw.y : wq == 2 ? vw.z : vw.w;
         const bool here = (mine >> lane) & 1;   // the position exists (false past BN)
         const int j = pos0 + tid - ctx;         // drafted token at this position, if >= 0
-        const float* mul = m.colc[unit & 3] + c0;
-        bool renew = t == t0;   // the references are to be found
-        uint32_t s[C];          // scores, then probabilities
-        // Once round for an ordinary tile; a first tile finds its references
-        // and comes round again, one whose scores outgrow them (x > kOver)
-        // goes through that after its first round.
+        uint8_t* row = sp + b * G::PB + tid * 128;
+        // CW scores from column h on.  A hidden score becomes the infinity
+        // that the column's multiplier turns into -inf.
+        auto load = [&](int h, uint32_t (&s)[CW]) {
+            tmem_ld(lanes + 64 * b + c0 + h, s);
+            tc::tmem_wait_ld();
+            if (!all) {
+#pragma unroll
+                for (int c = 0; c < CW; ++c)
+                    if (!(here && (j < 0 || ((seen[h + c] >> (j & 63)) & 1)))) s[c] = mul[h + c] < 0.0f ? 0x7f800000u : 0xff800000u;
+            }
+        };
+        // Once round for an ordinary tile; one whose scores outgrow the
+        // references (x > kOver) gets new ones and comes round again, and so
+        // does a unit's first tile.
+        bool renew = t == t0;
 #pragma unroll 1
         for (int round = 0;; ++round) {
-#pragma unroll
-            for (int h = 0; h < C; h += CW) tmem_ld(lanes + 64 * b + c0 + h, *reinterpret_cast<uint32_t(*)[CW]>(&s[h]));
-            tc::tmem_wait_ld();
-            if (!all || (G::BN == 64 && wq >= 2)) {
-                // A hidden score becomes the infinity that the column's
-                // multiplier turns into -inf.
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (!(here && (j < 0 || ((seen[c] >> (j & 63)) & 1)))) s[c] = mul[c] < 0.0f ? 0x7f800000u : 0xff800000u;
-            }
             if (renew) {
-                renew = false;
-                float y[C];
+#pragma unroll 1
+                for (int h = 0; h < (G::BN == 128 || wq < 2 ? C : 0); h += CW) {
+                    uint32_t s[CW];
+                    float y[CW];
+                    load(h, s);
 #pragma unroll
-                for (int c = 0; c < C; ++c) y[c] = __uint_as_float(s[c]) * mul[c];
-                warp_columns<C>(y, lane, [](float x, float z) { return fmaxf(x, z); });   // NaN aside
-                if (lane < C) m.wmax[wq][c0 + lane] = y[0];
+                    for (int c = 0; c < CW; ++c) y[c] = __uint_as_float(s[c]) * mul[h + c];
+                    warp_max_columns<CW>(y, lane);
+                    if (lane < CW) m.wmax[wq][c0 + h + lane] = y[0];
+                }
                 sync_group(wg);
                 if (tid < C) {
                     const int c = c0 + tid;
-                    const float top = fmaxf(fmaxf(m.wmax[0][c], m.wmax[1][c]), fmaxf(m.wmax[2][c], m.wmax[3][c]));
+                    float top = fmaxf(m.wmax[0][c], m.wmax[1][c]);
+                    if (G::BN == 128) top = fmaxf(top, fmaxf(m.wmax[2][c], m.wmax[3][c]));
                     const float old = t == t0 ? -INFINITY : m.ref[c], now = fmaxf(fmaxf(old, top), -INFINITY);   // never NaN
                     m.factor[c] = old == -INFINITY ? 0.0f : ex2(old - now);
                     m.ref[c] = now;
@@ -528,17 +531,14 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                     m.cref[c] = now == -INFINITY ? 1e30f : kLift - now;   // nothing visible yet: whatever comes outgrows it
                 }
                 sync_group(wg);
-                if (t != t0) {   // the sums on the new references
-#pragma unroll
-                    for (int c = 0; c < C; c += 2)
-                        l2[c / 2] = mul2(l2[c / 2], *reinterpret_cast<const uint64_t*>(&m.factor[c0 + c]));
-                    wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a.status, abort);   // O^T is at rest
+                if (t != t0) {   // the sums so far on the new references
+                    wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a.status, abort);
                     tc::fence_after_sync();
-                    const int sets = *(volatile unsigned*)&m.used[unit & 7] & 2 ? 2 : 1;   // the plain sums, the large tiles' too
+                    // the rows' sums, O^T, the large tiles' O^T
+                    const int sets = 1 + (*(volatile unsigned*)&m.used[unit & 7] & 2 ? 2 : 1) * (D == 256 ? 2 : 1);
 #pragma unroll 1
-                    for (int k = 0; k < (D == 256 ? 2 : 1) * sets; ++k) {
-                        const uint32_t at = lanes + (D == 256 ? kTmemO + 32 * (k & 1) + (kTmemBig - kTmemO) * (k >> 1)
-                                                              : kTmemO + (kTmemBig - kTmemO) * k) + c0;
+                    for (int k = 0; k < sets; ++k) {
+                        const uint32_t at = lanes + c0 + (k == 0 ? G::TL : D == 256 ? kTmemO + 32 * (k - 1) : kTmemO + 64 * (k - 1));
 #pragma unroll 1
                         for (int h = 0; h < C; h += 8) {
                             uint32_t v[8];
@@ -551,64 +551,44 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                     }
                     tmem_wait_st();
                 }
-                continue;
             }
-            // Scores to (lifted) probabilities on the present references.
+            // Scores to (lifted) probabilities, fp16, the position's row of P.
             float mx = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < (G::BN == 128 || wq < 2 ? C : 0); h += CW) {   // at d = 256 only 64 lanes are positions
+                uint32_t s[CW];
+                load(h, s);
+                const float4* k4 = reinterpret_cast<const float4*>(&m.cmul[c0 + h]);
+                const float4* r4 = reinterpret_cast<const float4*>(&m.cref[c0 + h]);
 #pragma unroll
-            for (int c = 0; c < C; c += 4) {
-                const float4 k = *reinterpret_cast<const float4*>(&m.cmul[c0 + c]), r = *reinterpret_cast<const float4*>(&m.cref[c0 + c]);
-                const float2 u = unpair(fma2(pair(s[c], s[c + 1]), pair(k.x, k.y), pair(r.x, r.y)));
-                const float2 v = unpair(fma2(pair(s[c + 2], s[c + 3]), pair(k.z, k.w), pair(r.z, r.w)));
-                mx = fmaxf(fmaxf(mx, fmaxf(u.x, u.y)), fmaxf(v.x, v.y));
-                s[c] = __float_as_uint(ex2(u.x));
-                s[c + 1] = __float_as_uint(ex2(u.y));
-                s[c + 2] = __float_as_uint(ex2(v.x));
-                s[c + 3] = __float_as_uint(ex2(v.y));
+                for (int c = 0; c < CW; c += 8) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 k = k4[(c + i) / 4], r = r4[(c + i) / 4];
+                        const float2 u = unpair(fma2(pair(s[c + i], s[c + i + 1]), pair(k.x, k.y), pair(r.x, r.y)));
+                        const float2 v = unpair(fma2(pair(s[c + i + 2], s[c + i + 3]), pair(k.z, k.w), pair(r.z, r.w)));
+                        mx = fmaxf(fmaxf(mx, fmaxf(u.x, u.y)), fmaxf(v.x, v.y));
+                        o[i / 2] = pack_f16(ex2(u.x), ex2(u.y));
+                        o[i / 2 + 1] = pack_f16(ex2(v.x), ex2(v.y));
+                    }
+                    *reinterpret_cast<uint4*>(row + ((((c0 + h + c) / 8) ^ (tid & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
             if (!vote_group(wg, mx > kOver) || round == 2) break;
             renew = true;
-        }
-        uint8_t* row = sp + b * G::PB + tid * 128;
-#pragma unroll
-        for (int c = 0; c < C; c += 8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                l2[c / 2 + i] = add2(l2[c / 2 + i], pair(s[c + 2 * i], s[c + 2 * i + 1]));
-                o[i] = pack_f16(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
-            }
-            if (G::BN == 128 || tid < G::BN)
-                *reinterpret_cast<uint4*>(row + ((((c0 + c) / 8) ^ (tid & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.p_full[b]);   // and S^T has been read
     }
-    // Epilogue: the rows' sums over the threads, then O^T.
-    float l[C];
-#pragma unroll
-    for (int c = 0; c < C; c += 2) {
-        const float2 u = unpair(l2[c / 2]);
-        l[c] = G::BN == 64 && tid >= 64 ? 0.0f : u.x;   // threads past BN held no position
-        l[c + 1] = G::BN == 64 && tid >= 64 ? 0.0f : u.y;
-    }
-    warp_columns<C>(l, lane, [](float x, float y) { return x + y; });
-    if (lane < C) m.wsum[wq][c0 + lane] = l[0];
-    sync_group(wg);
+    // Epilogue.
     const bool whole = t0 == 0 && t1 == p.nt;
     float* po = reinterpret_cast<float*>(part);
-    if (tid < C) {
-        const int c = c0 + tid;
-        const float sum = m.wsum[0][c] + m.wsum[1][c] + m.wsum[2][c] + m.wsum[3][c];
-        if (whole) m.factor[c] = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw nothing: zeros
-        else *reinterpret_cast<float2*>(po + kRows * D + 2 * c) = make_float2(m.ref[c], sum);
-    }
     const uint32_t last = tile - 1;
     wait_warp(&m.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
     tc::fence_after_sync();
-    sync_group(wg);
     const unsigned used = *(volatile unsigned*)&m.used[unit & 7];
     const int64_t* rowoff = m.rowoff[unit & 3] + c0;
     const int rows = p.rows;
@@ -621,8 +601,9 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         const bool bad_all = m.bad_ctx[unit & 7][blk] != 0;
 #pragma unroll 1
         for (int h = 0; h < C; h += 8) {
-            uint32_t v[8];
+            uint32_t v[8], l[8];
             tmem_ld(lanes + kTmemO + 32 * half + c0 + h, v);
+            tmem_ld(lanes + G::TL + c0 + h, l);   // every lane has the rows' sums
             tc::tmem_wait_ld();
             if (used != 1) {
                 uint32_t u[8];
@@ -639,10 +620,15 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
             }
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                if (c0 + h + c < rows) {
-                    const float o = __uint_as_float(v[c]);
-                    if (whole) a.out[rowoff[h + c] + e] = __float2bfloat16_rn(o * m.factor[c0 + h + c]);
-                    else po[(c0 + h + c) * D + e] = o;
+                const int col = c0 + h + c;
+                if (col < rows) {
+                    const float o = __uint_as_float(v[c]), sum = __uint_as_float(l[c]);
+                    if (whole) {   // a row that saw nothing: zeros
+                        a.out[rowoff[h + c] + e] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(o, sum));
+                    } else {
+                        po[col * D + e] = o;
+                        if (blk == 0 && lane == 0) *reinterpret_cast<float2*>(po + kRows * D + 2 * col) = make_float2(m.ref[col], sum);
+                    }
                 }
             }
         }
@@ -667,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     uint8_t* sv = smem;                 // V tiles
     uint8_t* sq = sv + kV * G::VB;      // queries
     uint8_t* sp = sq + G::QB;           // P
-    uint8_t* raw = sp + 2 * G::PB;      // packed tiles
+    uint8_t* raw = sp + 2 * G::PB + 1024;   // packed tiles; before them eight rows of ones
     Misc& m = *reinterpret_cast<Misc*>(raw + G::NS * G::RAW);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &m.abort;
@@ -702,6 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         m.abort = 0;
         fence_barrier_init();
     }
+    if (tid >= 128 && tid < 192) *reinterpret_cast<uint4*>(raw - 1024 + 16 * (tid - 128)) = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);
+    fence_proxy_async_smem();
     if (tid >= 64 && tid < 128) {
         m.bad_draft[(tid >> 3) & 7][tid & 7] = 0;
         m.bad_ctx[(tid >> 3) & 7][tid & 7] = 0;
@@ -1129,9 +1117,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             const bool leader = tc::elect_one();
             // d <= 64: one chunk only, read twice (rows 64 .. 127 of O^T are not used)
             const uint64_t dv = sdesc_mn128(smem_u32(sv), D <= 64 ? 0 : G::CHB), dp = sdesc_mn128(smem_u32(sp), 0);
+            // the rows' sums: a tile of ones in V's place (one 8-row atom, its row stride 0)
+            const uint64_t ones = tc::sdesc_k128(smem_u32(sp + 2 * G::PB)) & ~(uint64_t(0x3FFF) << 32);
             for (; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
                 const Piece& p = m.piece[unit & 7];
-                const uint32_t id = idesc_f16(cols_of(p.rows), true), begin = tile, end = tile + (p.t1 - p.t0);
+                const uint32_t id = idesc_f16(cols_of(p.rows), true), id1 = id & ~(1u << 15), begin = tile, end = tile + (p.t1 - p.t0);
                 unsigned used = 0;
 #pragma unroll 1
                 for (; tile < end; ++tile) {
@@ -1158,8 +1148,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
 #pragma unroll
                             for (int k = 0; k < G::BN / 16; ++k)
                                 tc::mma_bf16(o + 32 * half, da + (half * (G::CHB >> 3) + 128 * k), db + 128 * k, id, !fresh || k > 0);
-                        tc::commit(&m.pv_done[b]);
                         tc::commit(&m.v_empty[b]);
+#pragma unroll
+                        for (int k = 0; k < G::BN / 16; ++k)
+                            tc::mma_bf16(tmem + G::TL, ones, db + 128 * k, id1, tile > begin || k > 0);
+                        tc::commit(&m.pv_done[b]);
                     }
                     __syncwarp();
                 }

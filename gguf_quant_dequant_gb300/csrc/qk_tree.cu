@@ -123,7 +123,7 @@ template <int T, int D> struct Geo {
     static constexpr int VB = CH * CHB;                    // a V tile
     static constexpr int QB = CH * NR * 128;               // the unit's queries
     static constexpr int PB = BN * 128;                    // one P tile
-    static constexpr int RAW = BN * RB + 16;               // a packed tile (word loads may read 2 bytes past it)
+    static constexpr int RAW = BN * RB + (D == 32 ? 16 : 0);   // a packed tile (at d = 32 word loads read 2 bytes past it)
     static constexpr int ITEM = D == 32 ? 32 : 64;         // elements a decoding thread takes at once
     static constexpr int ITEMS = BN * D / ITEM;            // of them in a tile
     static constexpr int IPR = D / ITEM;                   // in a row
@@ -345,15 +345,13 @@ __device__ __forceinline__ void bulk_g2s_keep(void* dst, const void* src, uint32
 }
 
 // A wait of the roles that run on after a failure: no waiting once *abort is
-// set.  One lane polls, the warp waits for it.  Between looks the hardware
-// suspends the lane until the phase completes or 4 us have passed (warps that
-// spin take a third of the issue slots from the working ones); 2^19 looks are
-// 2 s.  Kept short: it stands in 20 places, and the roles' code has to stay in
-// the instruction cache together.
+// set.  One lane polls (the hardware suspends it for a while at each look), the
+// warp waits for it.  Kept short: it stands in 20 places, and the roles' code
+// has to stay in the instruction cache together.
 __device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < (1u << 19); ++i) {
-        if (mbar_try_wait_sleep(bar, parity, 4000u)) return true;
+    for (uint32_t i = 0; i < (1u << 24); ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
     }
     *abort = 1;
@@ -492,14 +490,19 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
         const int j = pos0 + tid - ctx;         // drafted token at this position, if >= 0
         uint8_t* row = sp + b * G::PB + tid * 128;
         // CW scores from column h on.  A hidden score becomes the infinity
-        // that the column's multiplier turns into -inf.
+        // that the column's multiplier turns into -inf.  (No branch per
+        // column: with them a tile with drafted positions took 10,000 clocks.)
+        const uint32_t* seen_j = reinterpret_cast<const uint32_t*>(seen) + (j >= 32 ? 1 : 0);   // the half with bit j
+        const uint32_t shift = j & 31, committed = j < 0, exists = here;
         auto load = [&](int h, uint32_t (&s)[CW]) {
             tmem_ld(lanes + 64 * b + c0 + h, s);
             tc::tmem_wait_ld();
             if (!all) {
 #pragma unroll
-                for (int c = 0; c < CW; ++c)
-                    if (!(here && (j < 0 || ((seen[h + c] >> (j & 63)) & 1)))) s[c] = mul[h + c] < 0.0f ? 0x7f800000u : 0xff800000u;
+                for (int c = 0; c < CW; ++c) {
+                    const uint32_t vis = ((seen_j[2 * (h + c)] >> shift) | committed) & exists;
+                    s[c] = vis ? s[c] : 0xff800000u ^ (__float_as_uint(mul[h + c]) & 0x80000000u);
+                }
             }
         };
         // Once round for an ordinary tile; one whose scores outgrow the
@@ -621,14 +624,13 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const int col = c0 + h + c;
-                if (col < rows) {
-                    const float o = __uint_as_float(v[c]), sum = __uint_as_float(l[c]);
-                    if (whole) {   // a row that saw nothing: zeros
-                        a.out[rowoff[h + c] + e] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(o, sum));
-                    } else {
-                        po[col * D + e] = o;
-                        if (blk == 0 && lane == 0) *reinterpret_cast<float2*>(po + kRows * D + 2 * col) = make_float2(m.ref[col], sum);
-                    }
+                const float o = __uint_as_float(v[c]), sum = __uint_as_float(l[c]);
+                if (whole) {   // a row that saw nothing: zeros
+                    const __nv_bfloat16 r = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(o, sum));
+                    if (col < rows) a.out[rowoff[h + c] + e] = r;
+                } else {
+                    if (col < rows) po[col * D + e] = o;
+                    if (blk == 0 && lane == c) *reinterpret_cast<float2*>(po + kRows * D + 2 * col) = make_float2(m.ref[col], sum);
                 }
             }
         }

@@ -123,10 +123,9 @@ template <int T, int D> struct Geo {
     static constexpr int VB = CH * CHB;                    // a V tile
     static constexpr int QB = CH * NR * 128;               // the unit's queries
     static constexpr int PB = BN * 128;                    // one P tile
-    static constexpr int RAW = BN * RB + (D == 32 ? 16 : 0);   // a packed tile (at d = 32 word loads read 2 bytes past it)
+    static constexpr int RAW = BN * RB;                    // a packed tile
     static constexpr int ITEM = D == 32 ? 32 : 64;         // elements a decoding thread takes at once
     static constexpr int ITEMS = BN * D / ITEM;            // of them in a tile
-    static constexpr int IPR = D / ITEM;                   // in a row
     static constexpr int KC = D / 2;                       // tensor-memory columns of a K tile
     static constexpr int TL = D == 256 ? 32 : 384;         // tensor-memory column of the rows' sums (S^T has 32 columns of 64 at d = 256)
     static constexpr int FIXED = kV * VB + QB + 2 * PB + 1024;   // and the tile of ones
@@ -385,50 +384,44 @@ __device__ __forceinline__ int element_of(int slot) {
 // Largest code magnitude.
 template <int T> __host__ __device__ constexpr float code_max() { return T == T_Q8_0 ? 128.0f : (T == T_Q5_0 ? 16.0f : 8.0f); }
 
-// What a decoding thread takes at once: 64 elements, two blocks (17, 9 or 11
-// words from a 4-byte aligned shared address), or at d = 32 one block, which
-// starts on a word or 2 bytes into one.
-template <int T, int D> struct Item {
-    static constexpr int BB = Fmt<T>::BB, NBLK = D == 32 ? 1 : 2, BYTES = NBLK * BB, W = D == 32 ? (BB + 2) / 4 : BYTES / 4;
-    uint32_t w[W];
-    bool odd;   // d = 32: the block starts 2 bytes into w[0]
-    __device__ __forceinline__ explicit Item(const uint8_t* p) {
-        odd = D == 32 && (reinterpret_cast<uintptr_t>(p) & 2);
-        if (odd) p -= 2;
+// One 32-block, read as words from a 2-byte aligned shared address.
+template <int T> struct Block {
+    static constexpr int W = Fmt<T>::BB / 4;   // words past the scale: 8, 4 or 5
+    uint32_t w[W], d;                          // d: the scale's bits
+    __device__ __forceinline__ explicit Block(const uint8_t* p) {
+        const uint32_t at = smem_u32(p), odd = at & 2;   // the block starts 2 bytes into a word
+        const uint8_t* q = p + 2 - (odd ^ 2);            // the word that holds the first byte past the scale
+        uint32_t prev = hm::lds32(q);
+        d = ld_u16(p);
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = hm::lds32(p + 4 * i);
+        for (int i = 0; i < W; ++i) {
+            const uint32_t next = hm::lds32(q + 4 * i + 4);
+            w[i] = __funnelshift_r(prev, next, 8 * (odd ^ 2));
+            prev = next;
+        }
     }
-    // Scale bits of block b; word i past block b's scale.
-    __device__ __forceinline__ uint32_t scale(int b) const {
-        return b ? w[BB / 4] >> 16 : (odd ? w[0] >> 16 : w[0] & 0xffffu);
-    }
-    __device__ __forceinline__ uint32_t word(int b, int i) const {
-        if (b) return w[(BB + 2) / 4 + i];
-        const uint32_t x = __funnelshift_r(w[i], w[i + 1], 16);
-        return D == 32 && odd ? w[i + 1] : x;
-    }
-    // Chunk k (0..3) of block b: code (exact) * d; a large tile takes the
+    // Chunk k (0..3): code (exact) * d; a large tile takes the
     // code times 2^-7, still exact.
     template <bool BIG>
-    __device__ __forceinline__ uint4 chunk(int b, int k, uint32_t d2) const {
+    __device__ __forceinline__ uint4 chunk(int k, uint32_t d2) const {
         using hm::and_or;
         using hm::and_xor;
         using hm::hadd2;
         const auto value = [d2](uint32_t code) { return hmul2(BIG ? hmul2(code, 0x20002000u) : code, d2); };
         if constexpr (T == T_Q8_0) {   // 0x6480 ^ byte = 1152 + (signed byte)
-            const uint32_t x = word(b, 2 * k), y = word(b, 2 * k + 1);
+            const uint32_t x = w[2 * k], y = w[2 * k + 1];
             return make_uint4(value(hadd2(and_xor(x, 0x00FF00FFu, 0x64806480u), 0xE480E480u)),
                               value(hadd2(and_xor(x >> 8, 0x00FF00FFu, 0x64806480u), 0xE480E480u)),
                               value(hadd2(and_xor(y, 0x00FF00FFu, 0x64806480u), 0xE480E480u)),
                               value(hadd2(and_xor(y >> 8, 0x00FF00FFu, 0x64806480u), 0xE480E480u)));
         } else if constexpr (T == T_Q4_0) {   // low nibbles 1024 + q - 1032, high ones 64 + q - 72
-            const uint32_t x = word(b, k), y = x >> 8;
+            const uint32_t x = w[k], y = x >> 8;
             return make_uint4(value(hadd2(and_or(x, 0x000F000Fu, 0x64006400u), 0xE408E408u)),
                               value(hadd2(and_or(y, 0x000F000Fu, 0x64006400u), 0xE408E408u)),
                               value(hadd2(and_or(x, 0x00F000F0u, 0x54005400u), 0xD480D480u)),
                               value(hadd2(and_or(y, 0x00F000F0u, 0x54005400u), 0xD480D480u)));
         } else {   // the fifth bits of 4 elements spread to bit 4 of their bytes; 1024 + q - 1040
-            const uint32_t qh = word(b, 0), x = word(b, 1 + k);
+            const uint32_t qh = w[0], x = w[1 + k];
             const uint32_t lo = (x & 0x0F0F0F0Fu) | ((((qh >> (4 * k)) & 15u) * 0x02040810u) & 0x10101010u);
             const uint32_t hi = ((x >> 4) & 0x0F0F0F0Fu) | ((((qh >> (16 + 4 * k)) & 15u) * 0x02040810u) & 0x10101010u);
             return make_uint4(value(hadd2(and_or(lo, 0x00FF00FFu, 0x64006400u), 0xE410E410u)),
@@ -460,13 +453,15 @@ __device__ __forceinline__ void warp_max_columns(float (&v)[C], int lane) {
 }
 
 // One piece of a unit by a softmax warpgroup (wg 0, 1), which has C columns
-// (rows): C wg .. C wg + C - 1.  tile: running count of the CTA's tiles; unit:
-// of its pieces.
-template <int T, int D, int C>
+// (rows; 8, 16 or 32): C wg .. C wg + C - 1.  tile: running count of the CTA's
+// tiles; unit: of its pieces.  The columns are walked eight at a time in rolled
+// loops: the roles share an instruction cache, and copies of this code for
+// each C, unrolled, made every role's tile a third slower.
+template <int T, int D>
 __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* sp, uint32_t tmem, const Piece& p, uint32_t& tile,
-                                              uint32_t unit, uint8_t* part, int wg) {
+                                              uint32_t unit, uint8_t* part, int wg, int C) {
     using G = Geo<T, D>;
-    constexpr int CW = C < 16 ? C : 16;   // columns of a tensor-memory access
+    constexpr int CW = 8;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, tid = 32 * wq + lane, c0 = C * wg;
     const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
     const uint64_t* seen = m.seen[unit & 3] + c0;
@@ -559,24 +554,20 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
             float mx = -INFINITY;
 #pragma unroll 1
             for (int h = 0; h < (G::BN == 128 || wq < 2 ? C : 0); h += CW) {   // at d = 256 only 64 lanes are positions
-                uint32_t s[CW];
+                uint32_t s[CW], o[4];
                 load(h, s);
                 const float4* k4 = reinterpret_cast<const float4*>(&m.cmul[c0 + h]);
                 const float4* r4 = reinterpret_cast<const float4*>(&m.cref[c0 + h]);
 #pragma unroll
-                for (int c = 0; c < CW; c += 8) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 k = k4[(c + i) / 4], r = r4[(c + i) / 4];
-                        const float2 u = unpair(fma2(pair(s[c + i], s[c + i + 1]), pair(k.x, k.y), pair(r.x, r.y)));
-                        const float2 v = unpair(fma2(pair(s[c + i + 2], s[c + i + 3]), pair(k.z, k.w), pair(r.z, r.w)));
-                        mx = fmaxf(fmaxf(mx, fmaxf(u.x, u.y)), fmaxf(v.x, v.y));
-                        o[i / 2] = pack_f16(ex2(u.x), ex2(u.y));
-                        o[i / 2 + 1] = pack_f16(ex2(v.x), ex2(v.y));
-                    }
-                    *reinterpret_cast<uint4*>(row + ((((c0 + h + c) / 8) ^ (tid & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 k = k4[i / 4], r = r4[i / 4];
+                    const float2 u = unpair(fma2(pair(s[i], s[i + 1]), pair(k.x, k.y), pair(r.x, r.y)));
+                    const float2 v = unpair(fma2(pair(s[i + 2], s[i + 3]), pair(k.z, k.w), pair(r.z, r.w)));
+                    mx = fmaxf(fmaxf(mx, fmaxf(u.x, u.y)), fmaxf(v.x, v.y));
+                    o[i / 2] = pack_f16(ex2(u.x), ex2(u.y));
+                    o[i / 2 + 1] = pack_f16(ex2(v.x), ex2(v.y));
                 }
+                *reinterpret_cast<uint4*>(row + ((((c0 + h) / 8) ^ (tid & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
             if (!vote_group(wg, mx > kOver) || round == 2) break;
             renew = true;
@@ -765,9 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             const int rows = p.rows;
             if (rows == 0) break;
             uint8_t* part = parts + (p.t0 == 0 && p.u0 != x0 ? part_bytes<D>() : 0);
-            if (rows <= 16) softmax_piece<T, D, 8>(a, m, sp, tmem, p, tile, unit, part, wg);
-            else if (rows <= 32) softmax_piece<T, D, 16>(a, m, sp, tmem, p, tile, unit, part, wg);
-            else if constexpr (G::NR == 64) softmax_piece<T, D, 32>(a, m, sp, tmem, p, tile, unit, part, wg);
+            softmax_piece<T, D>(a, m, sp, tmem, p, tile, unit, part, wg, cols_of(rows) / 2);
         }
     } else if (warp >= kKd && warp < kVd) {
         // K: a lane is a position; two warps per 32 positions share its items.
@@ -793,19 +782,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     const uint8_t* row = row0 + st * G::RAW;
                     const uint32_t to = to0 + b * G::KC;
 #pragma unroll 1
-                    for (int i = h; i < G::IPR; i += 2) {
-                        const Item<T, D> item(row + i * Item<T, D>::BYTES);
+                    for (int i = h; i < G::NB; i += 2) {
+                        const Block<T> blk(row + i * Fmt<T>::BB);
+                        const uint32_t d2 = hm::dup16(blk.d);
+                        uint32_t v[16];
 #pragma unroll
-                        for (int k = 0; k < Item<T, D>::NBLK; ++k) {
-                            const uint32_t d2 = hm::dup16(item.scale(k));
-                            uint32_t v[16];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint4 u = item.template chunk<false>(k, c, d2);
-                                v[4 * c] = u.x, v[4 * c + 1] = u.y, v[4 * c + 2] = u.z, v[4 * c + 3] = u.w;
-                            }
-                            tmem_st(to + i * (G::ITEM / 2) + 16 * k, v);
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 u = blk.template chunk<false>(c, d2);
+                            v[4 * c] = u.x, v[4 * c + 1] = u.y, v[4 * c + 2] = u.z, v[4 * c + 3] = u.w;
                         }
+                        tmem_st(to + 16 * i, v);
                     }
                     tmem_wait_st();
                 }
@@ -831,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         const int dt = tid - 32 * kVd;
         const bool mine = dt < G::ITEMS;
         const int pos = mine ? (dt / 32) * SPW + lane % SPW : 0, seg = mine ? lane / SPW : 0;
-        const uint8_t* src0 = raw + pos * G::RB + seg * Item<T, D>::BYTES;
+        const uint8_t* src0 = raw + pos * G::RB + seg * 2 * Fmt<T>::BB;
         uint8_t* line0 = sv + seg * G::CHB + pos * 128;
         uint32_t st = 1, rph = 0;   // the V tile's ring stage and its phase
 #pragma unroll 1
@@ -840,61 +826,58 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             const Piece& p = m.piece[unit & 7];
             if (p.rows == 0) break;
             {
-                // Row by row to fp16 times a power of two that brings the row's
-                // largest magnitude to 2^14 .. 2^15 (bf16's 8 bits are exact).
-                constexpr int LPR = D / 8, ROUNDS = G::NR * LPR / 256 > 0 ? G::NR * LPR / 256 : 1;   // threads per row
-                const int rows = p.rows, row0 = p.row0, tok0 = p.q.tok0, h0 = p.g * a.G;
-                const int N = cols_of(rows), sub = dt % LPR, blk = sub >> 2, k = sub & 3;           // 32-block, chunk
-                uint4 u[ROUNDS];
-#pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) {
-                    const int row = i * (256 / LPR) + dt / LPR, tok = token_of(a, row0 + row);
-                    u[i] = make_uint4(0, 0, 0, 0);
-                    if (row < rows) {
-                        const __nv_bfloat16* q = a.q + (tok0 + tok) * a.q_stride + (h0 + row0 + row - tok * a.G) * D + 32 * blk;
-                        if constexpr (T == T_Q8_0) {
-                            u[i] = *reinterpret_cast<const uint4*>(q + 8 * k);
-                        } else {
-                            const uint2 lo = *reinterpret_cast<const uint2*>(q + 4 * k), hi = *reinterpret_cast<const uint2*>(q + 16 + 4 * k);
-                            u[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                        }
-                    }
-                }
+                // The queries, a thread per 32 elements, to fp16 times a power of
+                // two that brings the row's largest magnitude to 2^14 .. 2^15
+                // (bf16's 8 bits are exact).
+                constexpr int TPR = D / 32;   // threads per row
+                static_assert(G::NR * TPR <= kDw * 32, "a thread per query block");
+                const int rows = p.rows, row = dt / TPR, sub = dt % TPR, N = cols_of(rows), tok = token_of(a, p.row0 + row);
+                const int head = p.g * a.G + p.row0 + row - tok * a.G;
+                const bool live = row < rows;
+                uint32_t x[16];   // pairs of elements
                 uint64_t seen = 0;
-                int64_t rowoff = 0;
-                if (dt < rows) {
-                    const int tok = token_of(a, row0 + dt);
-                    seen = seen_of(a, p.q, tok);
-                    rowoff = (tok0 + tok) * a.out_stride + (h0 + row0 + dt - tok * a.G) * D;
-                }
-                if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a.status, abort);
-                if (dt < N) {
-                    m.seen[unit & 3][dt] = seen;
-                    m.rowoff[unit & 3][dt] = rowoff;
-                }
-#pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) {
-                    const int row = i * (256 / LPR) + dt / LPR;
-                    if (i * 256 + (dt & ~31) >= N * LPR) continue;   // whole warps
-                    const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                    float f[8], mx = 0.0f;
+                if (live) {
+                    const uint4* q = reinterpret_cast<const uint4*>(a.q + (p.q.tok0 + tok) * a.q_stride + head * D + 32 * sub);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        f[2 * c] = __uint_as_float(x[c] << 16);
-                        f[2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u);
-                        mx = fmaxf(mx, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
+                        const uint4 u = q[c];
+                        x[4 * c] = u.x, x[4 * c + 1] = u.y, x[4 * c + 2] = u.z, x[4 * c + 3] = u.w;
                     }
+                    if (sub == 0) seen = seen_of(a, p.q, tok);
+                } else {
 #pragma unroll
-                    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 14;   // mx < 2^(ex + 15)
-                    if (mx == 0.0f || ex > 113) ex = 0;                       // nothing, or not finite
-                    ex = max(ex, -126);                                       // the factors stay normal
-                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-                    // slots 0, 2, 1, 3, ... of the loaded order
-                    *reinterpret_cast<uint4*>(sq + (sub >> 3) * (G::NR * 128) + row * 128 + (((sub & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(pack_f16(f[0] * down, f[2] * down), pack_f16(f[1] * down, f[3] * down),
-                                   pack_f16(f[4] * down, f[6] * down), pack_f16(f[5] * down, f[7] * down));
-                    if (sub == 0) m.colc[unit & 3][row] = row < rows ? a.scale * 1.44269504088896341f * up : 0.0f;
+                    for (int c = 0; c < 16; ++c) x[c] = 0;
+                }
+                uint32_t top = 0;   // largest magnitude, as bf16 bits
+#pragma unroll
+                for (int c = 0; c < 16; ++c) top = __vmaxu2(top, x[c] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+                for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                int ex = (int)(top >> 7) - 127 - 14;   // the largest magnitude is below 2^(ex + 15)
+                if (top == 0 || ex > 113) ex = 0;      // nothing, or not finite
+                ex = max(ex, -126);                    // the factors stay normal
+                const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+                if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a.status, abort);
+                if (row < N) {
+                    uint8_t* to = sq + (sub >> 1) * (G::NR * 128) + row * 128;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {   // element_of's order: 0, 2, 1, 3 of each four
+                        const int i = T == T_Q8_0 ? 4 * k : 2 * k, j = T == T_Q8_0 ? 4 * k + 2 : 8 + 2 * k;
+                        uint32_t o[4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t u = x[h ? j : i], v = x[(h ? j : i) + 1];
+                            o[2 * h] = pack_f16(__uint_as_float(u << 16) * down, __uint_as_float(v << 16) * down);
+                            o[2 * h + 1] = pack_f16(__uint_as_float(u & 0xffff0000u) * down, __uint_as_float(v & 0xffff0000u) * down);
+                        }
+                        *reinterpret_cast<uint4*>(to + ((((sub & 1) * 4 + k) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    if (sub == 0) {
+                        m.colc[unit & 3][row] = live ? a.scale * 1.44269504088896341f * up : 0.0f;
+                        m.seen[unit & 3][row] = seen;
+                        m.rowoff[unit & 3][row] = (p.q.tok0 + tok) * a.out_stride + head * D;
+                    }
                 }
                 // The flags of unit + 1 (last of unit - 7, long done) start clear;
                 // no warp reaches that unit's V before q_full.
@@ -917,24 +900,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 }
                 __syncwarp();
                 const bool valid = mine && ((reinterpret_cast<const uint32_t*>(&m.valid[1][tile & 15])[pos >> 5] >> (pos & 31)) & 1);
-                const Item<T, D> item(src0 + st * G::RAW);
+                const uint8_t* src = src0 + st * G::RAW;
                 // Scales that are finite but too large for fp16 times a code make the tile a large one, those that are
                 // not finite are recorded.
                 bool big = false;
                 uint32_t good = 0;   // bit per block
 #pragma unroll
-                for (int i = 0; i < Item<T, D>::NBLK; ++i) {
-                    const float d = fabsf(h2f(item.scale(i)));
-                    if (valid) {
-                        good |= 1u << i;
-                        if (!(d * code_max<T>() <= 65504.0f)) {
-                            big = big || d <= 65504.0f;
-                            if (!(d <= 65504.0f)) {
-                                good ^= 1u << i;
-                                const int blk = 2 * seg + i;
-                                if (j < 0) atomicOr(&m.bad_ctx[unit & 7][blk], 1u);
-                                else atomicOr(&m.bad_draft[unit & 7][blk], 1ull << (j & 63));
-                            }
+                for (int i = 0; i < G::ITEM / 32; ++i) {
+                    const float d = fabsf(h2f(ld_u16(src + i * Fmt<T>::BB)));
+                    if (valid) good |= 1u << i;
+                    if (valid && !(d * code_max<T>() <= 65504.0f)) {
+                        big = big || d <= 65504.0f;
+                        if (!(d <= 65504.0f)) {
+                            good ^= 1u << i;
+                            const int blk = 2 * seg + i;
+                            if (j < 0) atomicOr(&m.bad_ctx[unit & 7][blk], 1u);
+                            else atomicOr(&m.bad_draft[unit & 7][blk], 1ull << (j & 63));
                         }
                     }
                 }
@@ -943,12 +924,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 if (mine) {
                     uint8_t* line = line0 + b * G::VB;
                     auto blocks = [&](auto is_big) {
-#pragma unroll
-                        for (int i = 0; i < Item<T, D>::NBLK; ++i) {
-                            const uint32_t d2 = hm::dup16(item.scale(i));
+#pragma unroll 1
+                        for (int i = 0; i < G::ITEM / 32; ++i) {
+                            const Block<T> blk(src + i * Fmt<T>::BB);
+                            const uint32_t d2 = hm::dup16(blk.d);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                uint4 o = item.template chunk<decltype(is_big)::value>(i, c, d2);
+                                uint4 o = blk.template chunk<decltype(is_big)::value>(c, d2);
                                 if (!((good >> i) & 1)) o = make_uint4(0, 0, 0, 0);
                                 *reinterpret_cast<uint4*>(line + (((4 * i + c) ^ (pos & 7)) << 4)) = o;
                             }
@@ -1204,8 +1186,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a) {
                 f = pm[1] == 0.0f ? 0.0f : ex2(pm[0] - top);
                 lf = pm[1] == 0.0f ? 0.0f : f * pm[1];
             }
-#pragma unroll 4
-            for (int i = 0; i < 32 && i0 + i < n; ++i) {
+#pragma unroll 8
+            for (int i = 0; i < min(32, n - i0); ++i) {
                 const float fi = __shfl_sync(0xffffffffu, f, i);
                 sum += __shfl_sync(0xffffffffu, lf, i);
                 const float* po = part(i0 + i) + row * D + lane;
@@ -1213,7 +1195,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a) {
                 for (int e = 0; e < E; ++e) acc[e] += fi * po[32 * e];
             }
         }
-        const int rr = c.row0 + row, tok = rr / a.G;
+        const int rr = c.row0 + row, tok = token_of(a, rr);
         __nv_bfloat16* o = a.out + (c.tok0 + tok) * a.out_stride + (int64_t)(c.g * a.G + rr - tok * a.G) * D + lane;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[32 * e] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[e] / sum);

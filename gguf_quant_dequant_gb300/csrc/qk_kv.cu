@@ -26,7 +26,7 @@ namespace kv {
 // P_old are read, stack entries from n_free up and table entries from P_old
 // up are written.
 constexpr int kPlanThreads = 1024;
-constexpr int kTokensPerCta = 4096;
+constexpr int kTokensPerCta = 1024;
 
 struct PlanArgs {
     const int32_t *have, *start, *want;
@@ -185,8 +185,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 // 8 e .. 8 e + 7 (one 16-byte load of bf16, two of fp32, so a warp's loads
 // are contiguous), the block's maximum is two shuffles, and each lane rounds
 // its own eight codes with the quantizer's arithmetic (group_codes: the
-// IEEE division's rounding).  Streaming work: bounded by the bytes of the
-// rows read and the blocks written.
+// IEEE division's rounding).  A thread does its block of K and of V: the slot
+// and the indexes serve both and both loads are in flight together.
+// Streaming work: bounded by the bytes of the rows read and the blocks
+// written.
 constexpr int kAppendThreads = 256;
 
 struct AppendArgs {
@@ -207,7 +209,7 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, bool vec, fl
         const uint16_t* p = static_cast<const uint16_t*>(base) + at;
         uint32_t w[4];
         if (vec) {
-            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
         } else {
 #pragma unroll
@@ -221,7 +223,7 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, bool vec, fl
     } else {
         const float* p = static_cast<const float*>(base) + at;
         if (vec) {
-            const float4 f = *reinterpret_cast<const float4*>(p), g = *reinterpret_cast<const float4*>(p + 4);
+            const float4 f = __ldcs(reinterpret_cast<const float4*>(p)), g = __ldcs(reinterpret_cast<const float4*>(p + 4));
             x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w, x[4] = g.x, x[5] = g.y, x[6] = g.z, x[7] = g.w;
         } else {
 #pragma unroll
@@ -230,30 +232,13 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, bool vec, fl
     }
 }
 
-template <int T, bool BF16>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
-    constexpr int BB = Fmt<T>::BB;
+// The lane's part of one block, e of four, at dst (nullptr: nothing is written).
+template <int T>
+__device__ __forceinline__ void append_block(const float (&x)[8], uint8_t* dst, int e) {
     constexpr int kOff = T == T_Q8_0 ? 0 : (T == T_Q5_0 ? 16 : 8);
     constexpr int kLo = T == T_Q8_0 ? -128 : -kOff;
     constexpr int kHi = T == T_Q8_0 ? 127 : kOff - 1;
     constexpr float kDiv = T == T_Q8_0 ? 127.0f : (T == T_Q5_0 ? 15.0f : 7.0f);
-    const int64_t g = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 2;   // block of K, then of V
-    const int e = threadIdx.x & 3;
-    const bool isv = g >= a.n_blocks, live = g < 2 * a.n_blocks;
-    const int64_t b = isv ? g - a.n_blocks : g;
-    const int per_tok = a.pool.n_kv * a.nb;
-    const int64_t tok = live ? b / per_tok : 0;
-    const int in_tok = (int)(b - tok * per_tok), head = in_tok / a.nb, blk = in_tok - head * a.nb;
-    int64_t slot = live ? a.slots[tok] : -1;
-    if (slot >= 0 && (slot >> a.pool.page_log2) >= a.pool.n_pages) {
-        atomicOr(a.status, STATUS_BAD_PAGE);
-        slot = -1;
-    } else if (slot < -1) {
-        atomicOr(a.status, STATUS_BAD_PAGE);
-    }
-    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (slot >= 0)
-        load8<BF16>(isv ? a.v : a.k, tok * (isv ? a.v_stride : a.k_stride) + in_tok * 32 + 8 * e, isv ? a.v_vec : a.k_vec, x);
     float m = 0.0f;   // NaN elements are skipped, as the quantizer's scan does
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
@@ -269,10 +254,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
         for (int i = 0; i < 8; ++i) q[i] = (uint32_t)kOff;
     }
     const uint32_t w0 = ql::bytes4(q), w1 = ql::bytes4(q + 4);
-    uint8_t* dst = nullptr;
-    if (slot >= 0)
-        dst = (isv ? a.V : a.K) + pool_row(a.pool, slot >> a.pool.page_log2, head,
-                                           (int)(slot & ((1 << a.pool.page_log2) - 1))) + blk * BB;
     if constexpr (T == T_Q8_0) {
         if (dst) {
             if (e == 0) ql::st_u16(dst, db);
@@ -308,9 +289,34 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     }
 }
 
+template <int T, bool BF16>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+    const int64_t b = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 2;   // block of K and of V
+    const int e = threadIdx.x & 3;
+    const bool live = b < a.n_blocks;
+    const int per_tok = a.pool.n_kv * a.nb;
+    // 32-bit divisions where the count allows it (a 64-bit one is a hundred instructions)
+    const int64_t tok = !live ? 0 : a.n_blocks <= 0xffffffffll ? (int64_t)((uint32_t)b / (uint32_t)per_tok) : b / per_tok;
+    const int in_tok = live ? (int)(b - tok * per_tok) : 0, head = (int)((unsigned)in_tok / (unsigned)a.nb), blk = in_tok - head * a.nb;
+    int64_t slot = live ? a.slots[tok] : -1;
+    if (slot < -1 || (slot >= 0 && (slot >> a.pool.page_log2) >= a.pool.n_pages)) {
+        atomicOr(a.status, STATUS_BAD_PAGE);
+        slot = -1;
+    }
+    float k[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    int64_t at = 0;
+    if (slot >= 0) {
+        load8<BF16>(a.k, tok * a.k_stride + in_tok * 32 + 8 * e, a.k_vec, k);
+        load8<BF16>(a.v, tok * a.v_stride + in_tok * 32 + 8 * e, a.v_vec, v);
+        at = pool_row(a.pool, slot >> a.pool.page_log2, head, (int)(slot & ((1 << a.pool.page_log2) - 1))) + blk * Fmt<T>::BB;
+    }
+    append_block<T>(k, slot >= 0 ? a.K + at : nullptr, e);
+    append_block<T>(v, slot >= 0 ? a.V + at : nullptr, e);
+}
+
 template <int T>
 static cudaError_t append_t(const AppendArgs& a, bool bf16, cudaStream_t s) {
-    const int64_t grid = (2 * a.n_blocks * 4 + kAppendThreads - 1) / kAppendThreads;
+    const int64_t grid = (a.n_blocks * 4 + kAppendThreads - 1) / kAppendThreads;
     if (bf16) append_kernel<T, true><<<(unsigned)grid, kAppendThreads, 0, s>>>(a);
     else append_kernel<T, false><<<(unsigned)grid, kAppendThreads, 0, s>>>(a);
     return cudaGetLastError();

@@ -7,7 +7,7 @@
 //
 // The bound is the bytes: each logit read once and written once.  What may
 // change a logit is sparse in the vocabulary, so a CTA takes one slice of
-// SLICE tokens and a group of consecutive rows and keeps one 32-bit word
+// some tokens and a group of consecutive rows and keeps one 32-bit word
 // per token of the slice in shared memory: the count in the low 20 bits, 1 +
 // the index of the token's (last) bias entry in the high 12.  The words are
 // filled from the request's lists once and reused by its rows; a row's
@@ -21,7 +21,8 @@
 namespace qk {
 namespace lg {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kPerSm = 8;   // CTAs on an SM
+constexpr int kSliceMin = 512, kSliceMax = 6144;   // 8 x 24 KB of words fit an SM
 constexpr int kCountBits = 20;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
 
@@ -44,7 +45,7 @@ struct Args {
     int64_t grammar_stride;
     void* out;
     int64_t out_stride;
-    int rows_per_cta;
+    int rows_per_cta, slice;
 };
 
 // First row of request r, inside [0, n_rows].
@@ -65,18 +66,28 @@ template <> struct Elem<true> {
     static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
 };
 
-template <bool BF16, int SLICE, bool VEC>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const Args a) {
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kThreads, kPerSm) logits_kernel(const Args a) {
     using E = Elem<BF16>;
     using T = typename E::type;
-    __shared__ __align__(16) uint32_t word[SLICE];
+    extern __shared__ __align__(16) uint32_t word[];
     const int tid = threadIdx.x;
-    const int64_t v0 = (int64_t)blockIdx.x * SLICE;
-    const int nv = (int)min((int64_t)SLICE, a.vocab - v0);
+    const int64_t v0 = (int64_t)blockIdx.x * a.slice;
+    const int nv = (int)min((int64_t)a.slice, a.vocab - v0);
     const int64_t row_a = (int64_t)blockIdx.y * a.rows_per_cta, row_b = min(row_a + a.rows_per_cta, a.n_rows);
     int r = -1;
     int64_t r_lo = 0, r_hi = 0;   // rows the words stand for; none yet
-    bool listed = false;          // a request's rows (else: rows of no request)
+    bool listed = false, drafted = false;   // a request's rows (else: rows of no request); with drafted tokens
+    // A row's drafted ancestors that fall into the slice.
+    auto ancestors = [&](int64_t row, uint32_t by) {
+        const int64_t n = a.mask ? min((int64_t)64, r_hi - r_lo) : row - r_lo + 1;
+        const uint64_t bits = a.mask ? a.mask[row] : 0;
+        for (int64_t j = tid; j < n; j += kThreads)
+            if (!a.mask || ((bits >> j) & 1)) {
+                const int64_t t = a.draft[r_lo + j] - v0;
+                if (t >= 0 && t < nv) atomicAdd(&word[t], by);
+            }
+    };
     float rep = 1.0f, pres = 0.0f, freq = 0.0f;
     for (int64_t row = row_a; row < row_b; ++row) {
         if (row >= r_hi) {   // another request: its lists
@@ -91,8 +102,9 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const Args a) {
             listed = r >= 0 && row < row0_of(a, r + 1);
             r_lo = listed ? row0_of(a, r) : row;
             r_hi = listed ? row0_of(a, r + 1) : row + 1;
+            drafted = listed && a.draft != nullptr;
             __syncthreads();
-            for (int i = tid; i < SLICE; i += kThreads) word[i] = 0;
+            for (int i = tid; i < a.slice; i += kThreads) word[i] = 0;
             __syncthreads();
             if (listed) {
                 rep = a.rep[r];
@@ -113,22 +125,8 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const Args a) {
                     const int64_t t = ht[i] - v0;
                     if (t >= 0 && t < nv) atomicAdd(&word[t], 1u);
                 }
+                if (drafted) ancestors(row, 1u);
             }
-            __syncthreads();
-        }
-        const bool drafted = listed && a.draft != nullptr;
-        // The row's drafted ancestors that fall into the slice.
-        auto ancestors = [&](uint32_t by) {
-            const int64_t n = a.mask ? min((int64_t)64, r_hi - r_lo) : row - r_lo + 1;
-            const uint64_t bits = a.mask ? a.mask[row] : 0;
-            for (int64_t j = tid; j < n; j += kThreads)
-                if (!a.mask || ((bits >> j) & 1)) {
-                    const int64_t t = a.draft[r_lo + j] - v0;
-                    if (t >= 0 && t < nv) atomicAdd(&word[t], by);
-                }
-        };
-        if (drafted) {
-            ancestors(1u);
             __syncthreads();
         }
         const T* x = static_cast<const T*>(a.logits) + row * a.row_stride + v0;
@@ -149,42 +147,53 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const Args a) {
         if constexpr (VEC) {
             constexpr int N = E::N;
             const int nvec = nv / N;
-            for (int i = tid; i < nvec; i += kThreads) {
-                const uint4 u = reinterpret_cast<const uint4*>(x)[i];
-                const T* xe = reinterpret_cast<const T*>(&u);
-                const uint32_t ok = gr ? gr[(i * N) >> 5] >> ((i * N) & 31) : ~0u;
-                uint4 o;
-                T* oe = reinterpret_cast<T*>(&o);
+            // Two vectors at a time: with eight CTAs on an SM 64 KB of loads are in flight.
+            for (int i0 = tid; i0 < nvec; i0 += 2 * kThreads) {
+                uint4 u[2];
+                const bool two = i0 + kThreads < nvec;
+                u[0] = __ldcs(reinterpret_cast<const uint4*>(x) + i0);
+                if (two) u[1] = __ldcs(reinterpret_cast<const uint4*>(x) + i0 + kThreads);
 #pragma unroll
-                for (int j = 0; j < N; j += 4) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(&word[i * N + j]);
-                    oe[j] = E::put(one(E::get(xe[j]), w.x, (ok >> j) & 1));
-                    oe[j + 1] = E::put(one(E::get(xe[j + 1]), w.y, (ok >> (j + 1)) & 1));
-                    oe[j + 2] = E::put(one(E::get(xe[j + 2]), w.z, (ok >> (j + 2)) & 1));
-                    oe[j + 3] = E::put(one(E::get(xe[j + 3]), w.w, (ok >> (j + 3)) & 1));
+                for (int k = 0; k < 2; ++k) {
+                    if (k && !two) break;
+                    const int i = i0 + k * kThreads;
+                    const T* xe = reinterpret_cast<const T*>(&u[k]);
+                    const uint32_t ok = gr ? gr[(i * N) >> 5] >> ((i * N) & 31) : ~0u;
+                    uint4 o;
+                    T* oe = reinterpret_cast<T*>(&o);
+#pragma unroll
+                    for (int j = 0; j < N; j += 4) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(&word[i * N + j]);
+                        oe[j] = E::put(one(E::get(xe[j]), w.x, (ok >> j) & 1));
+                        oe[j + 1] = E::put(one(E::get(xe[j + 1]), w.y, (ok >> (j + 1)) & 1));
+                        oe[j + 2] = E::put(one(E::get(xe[j + 2]), w.z, (ok >> (j + 2)) & 1));
+                        oe[j + 3] = E::put(one(E::get(xe[j + 3]), w.w, (ok >> (j + 3)) & 1));
+                    }
+                    __stcs(&reinterpret_cast<uint4*>(y)[i], o);
                 }
-                reinterpret_cast<uint4*>(y)[i] = o;
             }
             for (int i = nvec * N + tid; i < nv; i += kThreads)
                 y[i] = E::put(one(E::get(x[i]), word[i], gr ? (gr[i >> 5] >> (i & 31)) & 1 : 1u));
         } else {
-#pragma unroll 4
+#pragma unroll 2
             for (int i = tid; i < nv; i += kThreads)
                 y[i] = E::put(one(E::get(x[i]), word[i], gr ? (gr[i >> 5] >> (i & 31)) & 1 : 1u));
         }
-        if (drafted && row + 1 < min(row_b, r_hi)) {   // the words serve another row
+        if (drafted && row + 1 < min(row_b, r_hi)) {   // the words serve the next row
             __syncthreads();
-            ancestors(0u - 1u);
+            ancestors(row, 0u - 1u);
+            ancestors(row + 1, 1u);
             __syncthreads();
         }
     }
 }
 
-template <bool BF16, int SLICE>
+template <bool BF16>
 static cudaError_t launch_s(const Args& a, bool vec, cudaStream_t s) {
-    const dim3 grid((unsigned)((a.vocab + SLICE - 1) / SLICE), (unsigned)((a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta));
-    if (vec) logits_kernel<BF16, SLICE, true><<<grid, kThreads, 0, s>>>(a);
-    else logits_kernel<BF16, SLICE, false><<<grid, kThreads, 0, s>>>(a);
+    const dim3 grid((unsigned)((a.vocab + a.slice - 1) / a.slice), (unsigned)((a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta));
+    const size_t smem = (size_t)a.slice * sizeof(uint32_t);
+    if (vec) logits_kernel<BF16, true><<<grid, kThreads, smem, s>>>(a);
+    else logits_kernel<BF16, false><<<grid, kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -199,11 +208,21 @@ cudaError_t launch_logits_process(const LogitsArgs& p, int sms, cudaStream_t s) 
     // row groups ask for.
     a.rows_per_cta = (int)std::max<int64_t>(std::min<int64_t>(8, std::max<int64_t>(1, p.n_rows / std::max<int64_t>(p.n_req, 1))),
                                             (p.n_rows + 65534) / 65535);
+    // The slice: as long as one round of the GPU's CTAs allows (a CTA reads its
+    // request's whole history), at most kSliceMax, then two rounds, three ...
+    // 384 x 128,256 logits took 103 us in 1.26 rounds of 4,096-token slices.
+    const int64_t groups = (p.n_rows + a.rows_per_cta - 1) / a.rows_per_cta, round = (int64_t)sms * lg::kPerSm;
+    int64_t slice = lg::kSliceMax;
+    for (int64_t w = 1; w <= 64; ++w) {
+        const int64_t n = std::max<int64_t>(1, w * round / groups);
+        slice = ((p.vocab + n - 1) / n + 31) / 32 * 32;   // whole words of the grammar mask
+        if (slice <= lg::kSliceMax) break;
+    }
+    a.slice = (int)std::min<int64_t>(std::max<int64_t>(slice, lg::kSliceMin), lg::kSliceMax);
     const int es = p.bf16 ? 2 : 4;
     const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
                      p.row_stride * es % 16 == 0 && p.out_stride * es % 16 == 0;
-    (void)sms;
-    return p.bf16 ? lg::launch_s<true, 4096>(a, vec, s) : lg::launch_s<false, 4096>(a, vec, s);
+    return p.bf16 ? lg::launch_s<true>(a, vec, s) : lg::launch_s<false>(a, vec, s);
 }
 
 }  // namespace qk

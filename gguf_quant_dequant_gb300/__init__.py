@@ -10,6 +10,7 @@ Type ids: Q4_K = 1, Q6_K = 2, Q8_0 = 3, Q5_0 = 4, Q4_0 = 5, Q5_K = 6, Q2_K = 7, 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -108,6 +109,8 @@ class QKError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load libqk.so (built in-tree by build.build()); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -132,6 +135,14 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_on(x, stream) -> int:
+    """The current stream of x's device, or the given one."""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(x.device.index)
 
 
 def _ptr(t) -> int | None:
@@ -279,51 +290,60 @@ def gemm(t: int, W, rows: int, cols: int, X, Y=None, ws=None, stream=None):
 
 
 # ------------------------------------- paged KV cache, tree attention, logits --
+# These calls are a few microseconds on the GPU, so their checks are kept to
+# what the C side cannot see: types, contiguity and element counts.
 
 TREE_MAX = 64
 
 
 def _dtype(x, what: str) -> int:
-    import torch
-    if x.dtype is torch.float32:
+    name = x.dtype.__str__()
+    if name == "torch.float32":
         return OUT_F32
-    if x.dtype is torch.bfloat16:
+    if name == "torch.bfloat16":
         return OUT_BF16
-    raise QKError(8, what, f"dtype {x.dtype}: float32 or bfloat16 expected")
+    raise QKError(8, what, f"dtype {name}: float32 or bfloat16 expected")
 
 
 def _rows(x, what: str) -> int:
     """Elements from row to row of a tensor whose rows are contiguous."""
+    shape, strides = x.shape, x.stride()
     want = 1
-    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        if size != 1 and stride != want:
-            raise QKError(8, what, f"strides {x.stride()} of shape {tuple(x.shape)}: contiguous rows expected")
-        want *= size
-    return x.stride(0) if x.shape[0] > 1 else want
+    for i in range(len(shape) - 1, 0, -1):
+        if strides[i] != want and shape[i] != 1:
+            raise QKError(8, what, f"strides {strides} of shape {tuple(shape)}: contiguous rows expected")
+        want *= shape[i]
+    return strides[0] if shape[0] > 1 else want
 
 
-def _of(x, dtype, what: str, shape=None):
-    """A contiguous array of the type (and shape) the C call reads, or None."""
-    if x is not None:
-        if x.dtype is not dtype or not x.is_contiguous():
-            raise QKError(8, what, f"contiguous {dtype} expected, got {x.dtype} with strides {x.stride()}")
-        if shape is not None and tuple(x.shape) != shape:
-            raise QKError(2, what, f"shape {tuple(x.shape)}, expected {shape}")
-    return _ptr(x)
+def _of(x, dtype, what: str, n: int):
+    """Pointer of a contiguous array of n elements of the type the C call
+    reads; None for None."""
+    if x is None:
+        return None
+    if x.dtype is not dtype or not x.is_contiguous():
+        raise QKError(8, what, f"contiguous {dtype} expected, got {x.dtype} with strides {x.stride()}")
+    if x.numel() != n:
+        raise QKError(2, what, f"{n} elements expected, got shape {tuple(x.shape)}")
+    return x.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def kv_page_bytes(t: int, n_kv: int, d: int, page: int) -> int:
+    return load().qk_kv_page_bytes(t, n_kv, d, page)
 
 
 def _pool_pages(t: int, K, V, n_kv: int, d: int, page: int, what: str) -> int:
     import torch
-    pb = load().qk_kv_page_bytes(t, n_kv, d, page)
+    pb = kv_page_bytes(t, n_kv, d, page)
     if pb == 0:
         raise QKError(2, what, f"no paged cache of type {t} with n_kv={n_kv}, d={d}, page={page}")
-    if _of(K, torch.uint8, what) is None or _of(V, torch.uint8, what) is None or K.numel() != V.numel() or K.numel() % pb:
+    n = K.numel()
+    if n % pb:
         raise QKError(2, what, f"K and V must be uint8 pools of the same whole number of {pb}-byte pages")
-    return K.numel() // pb
-
-
-def kv_page_bytes(t: int, n_kv: int, d: int, page: int) -> int:
-    return load().qk_kv_page_bytes(t, n_kv, d, page)
+    _of(K, torch.uint8, what, n)
+    _of(V, torch.uint8, what, n)
+    return n // pb
 
 
 def kv_plan(have, start, want, table, free_pages, n_free, page: int, cap: int, out=None, stream=None) -> dict:
@@ -333,18 +353,22 @@ def kv_plan(have, start, want, table, free_pages, n_free, page: int, cap: int, o
     "pos", "req" [cap]}.  out: a dict of such tensors to be written instead of
     new ones."""
     import torch
-    n, dev = have.shape[0], have.device
-    if out is None:
-        e = torch.empty(2 + 2 * n + 2 * cap, dtype=torch.int32, device=dev)
-        out = {"n_free": e[:1], "granted": e[1:1 + n], "cu": e[1 + n:2 + 2 * n], "pos": e[2 + 2 * n:2 + 2 * n + cap],
-               "req": e[2 + 2 * n + cap:], "slots": torch.empty(cap, dtype=torch.int64, device=dev)}
+    n, P, F = have.shape[0], table.shape[1], free_pages.shape[0]
     i32, w = torch.int32, "kv_plan"
-    _check(load().qk_kv_plan(
-        _of(have, i32, w), _of(start, i32, w, (n,)), _of(want, i32, w, (n,)), n, page,
-        _of(table, i32, w, (n, table.shape[1])), table.shape[1], _of(free_pages, i32, w), free_pages.numel(),
-        _of(n_free, i32, w), _of(out["n_free"], i32, w, (1,)), _of(out["granted"], i32, w, (n,)),
-        _of(out["cu"], i32, w, (n + 1,)), _of(out["slots"], torch.int64, w, (cap,)), _of(out["pos"], i32, w, (cap,)),
-        _of(out["req"], i32, w, (cap,)), cap, _stream(stream)), "qk_kv_plan")
+    ptrs = [_of(have, i32, w, n), _of(start, i32, w, n), _of(want, i32, w, n), _of(table, i32, w, n * P),
+            _of(free_pages, i32, w, F), _of(n_free, i32, w, 1)]
+    if out is None:
+        e = torch.empty(2 + 2 * n + 2 * cap, dtype=i32, device=have.device)
+        slots = torch.empty(cap, dtype=torch.int64, device=have.device)
+        at, q = e.data_ptr(), slots.data_ptr()
+        outs = (at, at + 4, at + 4 + 4 * n, q, at + 8 + 8 * n, at + 8 + 8 * n + 4 * cap)
+        a, b, c, d, f = e.split((1, n, n + 1, cap, cap))
+        out = {"n_free": a, "granted": b, "cu": c, "slots": slots, "pos": d, "req": f}
+    else:
+        outs = (_of(out["n_free"], i32, w, 1), _of(out["granted"], i32, w, n), _of(out["cu"], i32, w, n + 1),
+                _of(out["slots"], torch.int64, w, cap), _of(out["pos"], i32, w, cap), _of(out["req"], i32, w, cap))
+    _check(load().qk_kv_plan(ptrs[0], ptrs[1], ptrs[2], n, page, ptrs[3], P, ptrs[4], F, ptrs[5], outs[0], outs[1],
+                             outs[2], outs[3], outs[4], outs[5], cap, _stream_on(have, stream)), "qk_kv_plan")
     return out
 
 
@@ -357,20 +381,20 @@ def kv_append(t: int, k, v, slots, K, V, page: int, stream=None) -> None:
     if v.shape != k.shape or v.dtype is not k.dtype:
         raise QKError(2, w, "k and v differ in shape or type")
     pages = _pool_pages(t, K, V, n_kv, d, page, w)
-    _check(load().qk_kv_append(t, _ptr(k), _ptr(v), _dtype(k, w), n, _rows(k, w), _rows(v, w), n_kv, d,
-                               _of(slots, torch.int64, w, (n,)), _ptr(K), _ptr(V), pages, page, _stream(stream)),
-           "qk_kv_append")
+    _check(load().qk_kv_append(t, k.data_ptr(), v.data_ptr(), _dtype(k, w), n, _rows(k, w), _rows(v, w), n_kv, d,
+                               _of(slots, torch.int64, w, n), K.data_ptr(), V.data_ptr(), pages, page,
+                               _stream_on(k, stream)), "qk_kv_append")
 
 
 def kv_compact(t: int, K, V, page: int, n_kv: int, d: int, table, base, path, n_path, stream=None) -> None:
     """Move the accepted rows base + path[:, j] to base + j (qk_kv_compact):
     int32 CUDA table [n_req, P], base, n_path [n_req], path [n_req, m]."""
     import torch
-    w, i32, n = "kv_compact", torch.int32, base.shape[0]
+    w, i32, n, P, m = "kv_compact", torch.int32, base.shape[0], table.shape[1], path.shape[1]
     pages = _pool_pages(t, K, V, n_kv, d, page, w)
-    _check(load().qk_kv_compact(t, _ptr(K), _ptr(V), pages, page, n_kv, d, _of(table, i32, w, (n, table.shape[1])),
-                                table.shape[1], _of(base, i32, w), _of(path, i32, w, (n, path.shape[1])), path.shape[1],
-                                _of(n_path, i32, w, (n,)), n, _stream(stream)), "qk_kv_compact")
+    _check(load().qk_kv_compact(t, K.data_ptr(), V.data_ptr(), pages, page, n_kv, d, _of(table, i32, w, n * P), P,
+                                _of(base, i32, w, n), _of(path, i32, w, n * m), m, _of(n_path, i32, w, n), n,
+                                _stream_on(K, stream)), "qk_kv_compact")
 
 
 def attn_tree_workspace(t: int, n_req: int, max_q: int, max_pos: int, n_heads: int, n_kv: int, d: int) -> int:
@@ -386,22 +410,22 @@ def attn_tree(t: int, q, K, V, page: int, n_kv: int, table, ctx, cu, mask, max_q
     import torch
     w, i32 = "attn_tree", torch.int32
     n, n_heads, d = q.shape
-    r = ctx.shape[0]
-    if _dtype(q, w) != OUT_BF16:
+    r, P = ctx.shape[0], table.shape[1]
+    if q.dtype is not torch.bfloat16:
         raise QKError(8, w, "q must be bfloat16")
     if out is None:
         out = torch.empty((n, n_heads, d), dtype=torch.bfloat16, device=q.device)
     elif out.dtype is not torch.bfloat16 or out.shape != q.shape:
         raise QKError(2, w, "out must be bfloat16 of q's shape")
     pages = _pool_pages(t, K, V, n_kv, d, page, w)
-    P = table.shape[1]
+    L = load()
     if ws is None:
-        ws = torch.empty(max(load().qk_attn_tree_workspace(t, r, max_q, P * page, n_heads, n_kv, d), 16),
-                         dtype=torch.uint8, device=q.device)
-    _check(load().qk_attn_tree(t, _ptr(q), n, _rows(q, w), _ptr(K), _ptr(V), pages, page, _of(table, i32, w, (r, P)), P,
-                               _of(ctx, i32, w), _of(cu, i32, w, (r + 1,)), _of(mask, torch.int64, w, (n,)), r, max_q,
-                               n_heads, n_kv, d, scale, _ptr(out), _rows(out, w), _ptr(ws),
-                               ws.numel() * ws.element_size(), _stream(stream)), "qk_attn_tree")
+        ws = torch.empty(max(L.qk_attn_tree_workspace(t, r, max_q, P * page, n_heads, n_kv, d), 16), dtype=torch.uint8,
+                         device=q.device)
+    _check(L.qk_attn_tree(t, q.data_ptr(), n, _rows(q, w), K.data_ptr(), V.data_ptr(), pages, page,
+                          _of(table, i32, w, r * P), P, _of(ctx, i32, w, r), _of(cu, i32, w, r + 1),
+                          _of(mask, torch.int64, w, n), r, max_q, n_heads, n_kv, d, scale, out.data_ptr(), _rows(out, w),
+                          ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(q, stream)), "qk_attn_tree")
     return out
 
 
@@ -415,18 +439,19 @@ def logits_process(logits, cu, hist, hist_len, rep, pres, freq, draft=None, mask
     import torch
     w, i32, f32 = "logits_process", torch.int32, torch.float32
     n, V = logits.shape
-    r = cu.shape[0] - 1
+    r, H = cu.shape[0] - 1, hist.shape[1]
+    B = 0 if bias_tok is None else bias_tok.shape[1]
+    words = 0 if grammar is None else grammar.shape[1]
     if out is None:
         out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
     elif out.dtype is not logits.dtype or out.shape != logits.shape:
         raise QKError(2, w, "out must have the logits' type and shape")
-    B = 0 if bias_tok is None else bias_tok.shape[1]
     _check(load().qk_logits_process(
-        _ptr(logits), _dtype(logits, w), n, V, _rows(logits, w), _of(cu, i32, w), r, _of(hist, i32, w, (r, hist.shape[1])),
-        hist.shape[1], _of(hist_len, i32, w, (r,)), _of(rep, f32, w, (r,)), _of(pres, f32, w, (r,)), _of(freq, f32, w, (r,)),
-        _of(draft, i32, w, (n,)), _of(mask, torch.int64, w, (n,)), _of(bias_tok, i32, w, (r, B)),
-        _of(bias_val, f32, w, (r, B)) if B else None, B, _of(bias_len, i32, w, (r,)) if B else None,
-        _of(grammar, i32, w, None if grammar is None else (n, grammar.shape[1])), 0 if grammar is None else grammar.shape[1], _ptr(out), _rows(out, w), _stream(stream)),
+        logits.data_ptr(), _dtype(logits, w), n, V, _rows(logits, w), _of(cu, i32, w, r + 1), r, _of(hist, i32, w, r * H),
+        H, _of(hist_len, i32, w, r), _of(rep, f32, w, r), _of(pres, f32, w, r), _of(freq, f32, w, r),
+        _of(draft, i32, w, n), _of(mask, torch.int64, w, n), _of(bias_tok, i32, w, r * B),
+        _of(bias_val, f32, w, r * B) if B else None, B, _of(bias_len, i32, w, r) if B else None,
+        _of(grammar, i32, w, n * words), words, out.data_ptr(), _rows(out, w), _stream_on(logits, stream)),
         "qk_logits_process")
     return out
 

@@ -15,6 +15,7 @@ import pytest
 import torch
 
 import gguf_quant_dequant_gb300 as qk
+import oracle
 import paged_ref
 import synth
 from gpu_helpers import gpu, type_id  # noqa: F401
@@ -314,7 +315,6 @@ def test_a_step_in_a_graph(gpu):
     with torch.cuda.graph(graph):
         p, out = step()
     Kr, Vr = np.zeros((R, P * page, n_kv, qk.row_bytes(t, d)), np.uint8), np.zeros((R, P * page, n_kv, qk.row_bytes(t, d)), np.uint8)
-    import oracle
     for it in range(6):
         kv.normal_(generator=g)
         q.normal_(generator=g)
@@ -338,3 +338,78 @@ def test_a_step_in_a_graph(gpu):
         start.add_(3)
         want.copy_(start + n)
     qk.device_status()
+
+
+def test_references_that_grow_along_the_positions(gpu):
+    # Keys that point more and more along the query: every tile outgrows the
+    # references of the one before, in one CTA and across several.
+    for ctx, n_req in ((1500, 1), (700, 40)):
+        c = make("Q8_0", [ctx] * n_req, [3] * n_req, 4, 1, 64, 64, 620)
+        u = np.random.default_rng(1).standard_normal(64).astype(np.float32)
+        c["q"] = torch.from_numpy(np.broadcast_to(u, c["q"].shape).copy()).to(torch.bfloat16)
+        for r in range(n_req):
+            for p in range(ctx + 3):
+                k = (u * (p / 40.0) / 8.0).astype(np.float32)
+                c["K"][c["table"][r, p // 64], 0, p % 64] = oracle.quantize(qk.Q8_0, k[None])
+        run(c, gpu)
+
+
+def test_large_v_tiles_among_ordinary_ones(gpu):
+    # V past fp16's range in the first tile, in a middle one and in the last,
+    # with references that are renewed in between.
+    c = make("Q8_0", [600], [4], 4, 1, 128, 32, 630, q_scale=3.0)
+    for p in (5, 300, 601):
+        row = c["V"][c["table"][0, p // 32], 0, p % 32].reshape(4, 34)
+        row[:, :2] = np.array([3000.0], np.float16).view(np.uint8)
+        c["V"][c["table"][0, p // 32], 0, p % 32] = row.reshape(-1)
+    run(c, gpu)
+    c = make("Q4_0", [20, 300], [4, 4], 4, 2, 256, 32, 631, q_scale=3.0)
+    c["V"] = paged_ref.pool("Q4_0", len(c["V"]), 2, 32, 256, 632, d_scale=9000.0)     # every tile
+    run(c, gpu)
+
+
+def test_non_finite_v_in_the_context(gpu):
+    # A committed row with a NaN scale in one 32-block: that block of every token of its request and kv head, nothing else.
+    c = make("Q8_0", [150, 40], [3, 2], 4, 2, 128, 16, 640)
+    clean = c["V"].copy()
+    at = 70
+    c["V"][c["table"][0, at // 16], 1, at % 16, 34:36] = 0xFF
+    out = qk.attn_tree(qk.Q8_0, *to_dev(c, gpu))
+    qk.device_status()
+    ref = paged_ref.attn_tree("Q8_0", c["q"].double().numpy(), c["K"], clean, 16, 2, c["table"], c["ctx"], c["cu"], c["mask"], 3,
+                              c["scale"])
+    got = out.float().cpu()
+    assert torch.isnan(got[:3, 2:, 32:64]).all()
+    got[:3, 2:, 32:64] = torch.from_numpy(ref[0][:3, 2:, 32:64]).float()
+    check(c, got, ref)
+
+
+@pytest.mark.parametrize("n_req,n_kv", [(897, 1), (2000, 4)])
+def test_many_short_units(gpu, n_req, n_kv):
+    # More requests than the scan takes at once, and dozens of one-tile units
+    # per CTA.
+    rng = np.random.default_rng(n_req)
+    ctx, n = rng.integers(0, 40, n_req), rng.integers(0, 3, n_req)
+    ctx[rng.integers(0, n_req, 20)] = 300
+    run(make("Q4_0", ctx.tolist(), n.tolist(), 2 * n_kv, n_kv, 32, 16, 650), gpu)
+
+
+def test_negative_scale_and_zero_queries(gpu):
+    c = make("Q5_0", [130, 7], [5, 2], 8, 2, 64, 16, 660)
+    c["scale"] = -0.2
+    c["q"][1] = 0
+    run(c, gpu)
+
+
+def test_nan_query_stays_in_its_row(gpu):
+    c = make("Q8_0", [100], [3], 8, 2, 64, 16, 670)
+    dev = list(to_dev(c, gpu))
+    dev[0] = dev[0].clone()
+    dev[0][1, 5, 3] = float("nan")
+    out = qk.attn_tree(qk.Q8_0, *dev)
+    ref = paged_ref.attn_tree("Q8_0", c["q"].double().numpy(), c["K"], c["V"], 16, 2, c["table"], c["ctx"], c["cu"], c["mask"], 3,
+                              c["scale"])
+    assert torch.isnan(out[1, 5].float()).all()
+    got = out.float().cpu()
+    got[1, 5] = torch.from_numpy(ref[0][1, 5]).float()
+    check(c, got, ref)

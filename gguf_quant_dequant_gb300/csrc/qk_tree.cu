@@ -743,9 +743,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
     tc::fence_after_sync();
     const uint32_t tmem = m.tmem;
     const int x1 = min(x0 + per, total);
-    // Registers per thread of the seven warpgroups: 56, 2 x 120, 2 x 48, 2 x 56, within the launch's 7 x 72.
+    // Registers per thread of the seven warpgroups: 104, 2 x 88, 2 x 48, 2 x 64, within the launch's 7 x 72.
+    // (With fewer the copiers' loop spills, and a spill is a trip to L2: shared memory leaves no L1.)
     if (warp >= kSm && warp < kKd) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
         const int wg = (warp - kSm) >> 2;
         uint8_t* parts = a.ws + (int64_t)a.ctas * sizeof(Cut) + 2 * (int64_t)blockIdx.x * part_bytes<D>();
         uint32_t tile = 0, unit = 0;
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         // 17, 9 or 11 words apart, odd; positions 1, 2 or 4 times that) and
         // eight neighbouring lanes' 16-byte stores into the eight bank groups
         // of swizzled rows.  Before a unit's first tile, its queries.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         constexpr int SPW = D <= 64 ? 32 : 2048 / D;
         static_assert(G::ITEMS <= kDw * 32, "an item per decoding thread");
         uint32_t tile = 0, unit = 0;
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         if (warp == 0 || warp == 3) {
             // Copies: the tile's rows of every page it touches, K's by warp 0
             // (which also walks the list and publishes the pieces), V's by warp 3.

@@ -13,6 +13,10 @@
 // filled from the request's lists once and reused by its rows; a row's
 // ancestors are added before its pass and taken out after it.  Integer
 // atomics only, so the result does not depend on their order.
+// 384 rows of 128,256 fp32 logits with grammar masks (401 MB): 89 us, 4.5 TB/s,
+// 66 % of the measured copy rate; one row of 32,000: 5.0 us.  On
+// top of the bytes a CTA reads its request's history before its first row and
+// meets two barriers between rows; their shares were not taken apart.
 #include <algorithm>
 #include <cuda_bf16.h>
 

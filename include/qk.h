@@ -448,8 +448,10 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
  * (2^-10 (1 + A) + 2^-13) sum_t p_t |V[t]| + 2^-32 sum_t |V[t]|, and near
  * the rounding of the output in practice.  Cached K values beyond fp16's
  * range (|w| > 65504) may give NaN for the tokens that see them.
- * n_tok == 0 or n_req == 0 queues nothing.  Errors: QK_ERR_TYPE,
- * QK_ERR_SHAPE, QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_WORKSPACE. */
+ * At most 64 query heads to a kv head, n_req up to 65,535.  n_tok == 0 or
+ * n_req == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also when the
+ * tables could hold about 2^31 tiles or more), QK_ERR_NULL, QK_ERR_ALIGN,
+ * QK_ERR_WORKSPACE. */
 size_t qk_attn_tree_workspace(int type, int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d);
 qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const void* K, const void* V,
                        int64_t n_pages, int page, const int32_t* table, int64_t table_stride, const int32_t* ctx,

@@ -873,6 +873,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 if (top == 0 || ex > 113) ex = 0;      // nothing, or not finite
                 ex = max(ex, -126);                    // the factors stay normal
                 const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+                // The scores' multiplier.  Where it is 0 (the scale is, or the product underflows) every finite score is 0:
+                // no queries, and a multiplier that still turns a hidden score's infinity into -inf.
+                float mul = a.scale * 1.44269504088896341f * up;
+                if (mul == 0.0f) {
+                    mul = 1.0f;
+                    if (top < 0x7f80u)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) x[c] = 0;
+                }
                 if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a.status, abort);
                 if (row < N) {
                     uint8_t* to = sq + (sub >> 1) * (G::NR * 128) + row * 128;
@@ -889,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                         *reinterpret_cast<uint4*>(to + ((((sub & 1) * 4 + k) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                     if (sub == 0) {
-                        m.colc[unit & 3][row] = live ? a.scale * 1.44269504088896341f * up : 0.0f;
+                        m.colc[unit & 3][row] = mul;
                         m.seen[unit & 3][row] = seen;
                         m.rowoff[unit & 3][row] = (p.q.tok0 + tok) * a.out_stride + head * D;
                     }

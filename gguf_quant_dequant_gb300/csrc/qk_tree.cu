@@ -39,9 +39,12 @@
 // What is not visible never reaches a result: a masked score is replaced, not
 // added to; rows past the end are decoded as zeros; a V block whose scale is
 // not finite is decoded as zero and recorded, and the epilogue sets NaN for the
-// rows that do see it.  A V tile with values past fp16's range (scales up to
-// 65504 times a code of 128 are legal) is decoded times 2^-7 and summed apart
-// (O^T's second set of columns), which the epilogue adds times 2^7.
+// rows that do see it.  V blocks with values past fp16's range (scales up to
+// 65504 times a code of 128 are legal) are decoded times 2^-7, as a V tile of
+// their own with zeros in the other blocks' place, and summed apart (O^T's
+// second set of columns), which the epilogue adds times 2^7; the tile of the
+// other blocks has zeros in theirs.  So a large block, hidden or not, leaves
+// the others' bits alone, and a tile without one costs nothing more.
 //
 // Bounds and measurements (GB300, GPU time of a call in a replayed graph).  The
 // floor is the cache's bytes up to 80 (Q4_0) to 150 (Q8_0) rows a kv head, the
@@ -74,9 +77,9 @@ constexpr int kThreads = 28 * 32;
 constexpr int kSm = 4, kKd = 12, kVd = 20;   // first warps of softmax, K and V decoding
 constexpr int kDw = 8;                       // warps of each of these
 constexpr int kV = 2;                        // V tile buffers
-// Tensor memory: S^T twice 64 columns, O^T 64 (or two halves of 32 at d = 256), the large V tiles' O^T, K twice d / 2.
+// Tensor memory: S^T twice 64 columns, O^T 64 (or two halves of 32 at d = 256), the large V blocks' O^T, K twice d / 2.
 constexpr int kTmem = 512, kTmemO = 128, kTmemBig = 192, kTmemK = 256;
-constexpr float kBig = 128.0f;   // scale of the large V tiles
+constexpr float kBig = 128.0f;   // scale of the large V blocks
 constexpr float kLift = 7.0f;    // probabilities are held times 2^7 (fp16 keeps 2^-21 of the maximum at full precision)
 constexpr float kOver = 15.0f;   // and stay below 2^15
 constexpr int kRows = 64;        // most rows of a unit
@@ -172,11 +175,11 @@ struct __align__(16) Misc {
     float wmax[4][kRows];
     unsigned long long bad_draft[8][8];   // by unit mod 8, 32-block: drafted V rows that are not finite
     unsigned bad_ctx[8][8];
-    unsigned big_tile[16];       // by tile mod 16: the V tile is decoded times 2^-7
-    unsigned used[8];            // by unit mod 8: bit 0 the plain sums, bit 1 the large tiles' sums hold something
+    unsigned big_tile[16];       // by tile mod 16: the V tile is followed by one of its large blocks
+    unsigned used[8];            // by unit mod 8: whether the large blocks' sums hold something
     uint64_t raw_full[8], raw_empty[8], k_full[2], k_empty[2], v_full[kV], v_empty[kV], s_full[2],
         p_full[2], pv_done[2];
-    uint64_t q_full, q_empty, o_empty, drain[2], piece_full[8], piece_free[8];
+    uint64_t q_full, q_empty, o_empty, big_full, big_empty, drain[2], piece_full[8], piece_free[8];
     Piece piece[8];              // by unit mod 8
     int scan[32];
     Req start_q;
@@ -414,7 +417,7 @@ template <int T> struct Block {
             prev = next;
         }
     }
-    // Chunk k (0..3): code (exact) * d; a large tile takes the
+    // Chunk k (0..3): code (exact) * d; a large block takes the
     // code times 2^-7, still exact.
     template <bool BIG>
     __device__ __forceinline__ uint4 chunk(int k, uint32_t d2) const {
@@ -546,8 +549,8 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                 if (t != t0) {   // the sums so far on the new references
                     wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a.status, abort);
                     tc::fence_after_sync();
-                    // the rows' sums, O^T, the large tiles' O^T
-                    const int sets = 1 + (*(volatile unsigned*)&m.used[unit & 7] & 2 ? 2 : 1) * (D == 256 ? 2 : 1);
+                    // the rows' sums, O^T, the large blocks' O^T
+                    const int sets = 1 + (*(volatile unsigned*)&m.used[unit & 7] ? 2 : 1) * (D == 256 ? 2 : 1);
 #pragma unroll 1
                     for (int k = 0; k < sets; ++k) {
                         const uint32_t at = lanes + c0 + (k == 0 ? G::TL : D == 256 ? kTmemO + 32 * (k - 1) : kTmemO + 64 * (k - 1));
@@ -613,13 +616,12 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
             tmem_ld(lanes + kTmemO + 32 * half + c0 + h, v);
             tmem_ld(lanes + G::TL + c0 + h, l);   // every lane has the rows' sums
             tc::tmem_wait_ld();
-            if (used != 1) {
+            if (used) {
                 uint32_t u[8];
                 tmem_ld(lanes + kTmemBig + 32 * half + c0 + h, u);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    v[c] = __float_as_uint((used & 1 ? __uint_as_float(v[c]) : 0.0f) + (used & 2 ? kBig * __uint_as_float(u[c]) : 0.0f));
+                for (int c = 0; c < 8; ++c) v[c] = __float_as_uint(fmaf(kBig, __uint_as_float(u[c]), __uint_as_float(v[c])));
             }
             if (bad) {
 #pragma unroll
@@ -688,6 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         mbar_init(&m.q_full, kDw);
         mbar_init(&m.q_empty, 1);
         mbar_init(&m.o_empty, 8);
+        mbar_init(&m.big_full, kDw);
+        mbar_init(&m.big_empty, 1);
         for (int i = 0; i < 8; ++i) {
             mbar_init(&m.piece_full[i], 1);
             mbar_init(&m.piece_free[i], 8);
@@ -835,6 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         const uint8_t* src0 = raw + pos * G::RB + seg * 2 * Fmt<T>::BB;
         uint8_t* line0 = sv + seg * G::CHB + pos * 128;
         uint32_t st = 1, rph = 0;   // the V tile's ring stage and its phase
+        uint32_t bigs = 0;          // tiles with large blocks so far
 #pragma unroll 1
         for (;; ++unit) {
             if (vote_v(!piece_ready(m, unit, a.status))) break;
@@ -925,8 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 __syncwarp();
                 const bool valid = mine && ((reinterpret_cast<const uint32_t*>(&m.valid[1][tile & 15])[pos >> 5] >> (pos & 31)) & 1);
                 const uint8_t* src = src0 + st * G::RAW;
-                // Scales that are finite but too large for fp16 times a code make the tile a large one, those that are
-                // not finite are recorded.
+                // Blocks whose scale is finite but too large for fp16 times a code are large ones, those whose scale is
+                // not finite are recorded; both are zeros in the tile.
                 bool big = false;
                 uint32_t good = 0;   // bit per block
 #pragma unroll
@@ -934,9 +939,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     const float d = fabsf(h2f(ld_u16(src + i * Fmt<T>::BB)));
                     if (valid) good |= 1u << i;
                     if (valid && !(d * code_max<T>() <= 65504.0f)) {
+                        good ^= 1u << i;
                         big = big || d <= 65504.0f;
                         if (!(d <= 65504.0f)) {
-                            good ^= 1u << i;
                             const int blk = 2 * seg + i;
                             if (j < 0) atomicOr(&m.bad_ctx[unit & 7][blk], 1u);
                             else atomicOr(&m.bad_draft[unit & 7][blk], 1ull << (j & 63));
@@ -945,30 +950,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 }
                 big = vote_v(big);
                 if (dt == 0) m.big_tile[tile & 15] = big;
-                if (mine) {
-                    uint8_t* line = line0 + b * G::VB;
-                    auto blocks = [&](auto is_big) {
+                uint8_t* line = line0 + b * G::VB;
+                auto blocks = [&](auto is_big, uint32_t which) {
 #pragma unroll 1
-                        for (int i = 0; i < G::ITEM / 32; ++i) {
-                            const Block<T> blk(src + i * Fmt<T>::BB);
-                            const uint32_t d2 = hm::dup16(blk.d);
+                    for (int i = 0; i < G::ITEM / 32; ++i) {
+                        const Block<T> blk(src + i * Fmt<T>::BB);
+                        const uint32_t d2 = hm::dup16(blk.d);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint4 o = blk.template chunk<decltype(is_big)::value>(c, d2);
-                                if (!((good >> i) & 1)) o = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4*>(line + (((4 * i + c) ^ (pos & 7)) << 4)) = o;
-                            }
+                        for (int c = 0; c < 4; ++c) {
+                            uint4 o = blk.template chunk<decltype(is_big)::value>(c, d2);
+                            if (!((which >> i) & 1)) o = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(line + (((4 * i + c) ^ (pos & 7)) << 4)) = o;
                         }
-                    };
-                    if (big) blocks(std::true_type{});
-                    else blocks(std::false_type{});
-                }
+                    }
+                };
+                if (mine) blocks(std::false_type{}, good);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&m.v_full[b]);
-                    mbar_arrive(&m.raw_empty[st]);
+                if (lane == 0) mbar_arrive(&m.v_full[b]);
+                if (big) {   // then the large blocks, in the same buffer once its product is done
+                    if (lane == 0) wait_lane(&m.v_empty[b], (tile >> 1) & 1, a.status, abort);
+                    __syncwarp();
+                    uint32_t large = 0;
+#pragma unroll
+                    for (int i = 0; i < G::ITEM / 32; ++i) {
+                        const float d = fabsf(h2f(ld_u16(src + i * Fmt<T>::BB)));
+                        if (valid && d * code_max<T>() > 65504.0f && d <= 65504.0f) large |= 1u << i;
+                    }
+                    if (mine) blocks(std::true_type{}, large);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&m.big_full);
+                        wait_lane(&m.big_empty, bigs & 1, a.status, abort);
+                    }
+                    __syncwarp();
+                    ++bigs;
                 }
+                if (lane == 0) mbar_arrive(&m.raw_empty[st]);
                 if ((st += 2) == G::NS + 1) st = 1, rph ^= 1;
             }
         }
@@ -1120,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             }
         } else {
             // P V.
-            uint32_t tile = 0, unit = 0;
+            uint32_t tile = 0, unit = 0, bigs = 0;   // bigs: tiles with large blocks so far
             bool ok = true;
             const bool leader = tc::elect_one();
             // d <= 64: one chunk only, read twice (rows 64 .. 127 of O^T are not used)
@@ -1130,7 +1149,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             for (; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
                 const Piece& p = m.piece[unit & 7];
                 const uint32_t id = idesc_f16(cols_of(p.rows), true), id1 = id & ~(1u << 15), begin = tile, end = tile + (p.t1 - p.t0);
-                unsigned used = 0;
+                bool used = false;   // large blocks
 #pragma unroll 1
                 for (; tile < end; ++tile) {
                     const uint32_t b = tile & 1;
@@ -1144,24 +1163,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     if (!ok) break;
                     tc::fence_after_sync();
                     const bool big = *(volatile unsigned*)&m.big_tile[tile & 15] != 0;
-                    const unsigned bit = big ? 2u : 1u;
-                    const bool fresh = !(used & bit);
-                    used |= bit;
-                    const uint32_t o = tmem + (big ? kTmemBig : kTmemO);
                     const uint64_t da = dv + (uint64_t)(b * (G::VB >> 4)), db = dp + (uint64_t)(b * (G::PB >> 4));
                     if (leader) {
-                        *(volatile unsigned*)&m.used[unit & 7] = used;
+                        *(volatile unsigned*)&m.used[unit & 7] = used || big;
 #pragma unroll
                         for (int half = 0; half < (D == 256 ? 2 : 1); ++half)
 #pragma unroll
                             for (int k = 0; k < G::BN / 16; ++k)
-                                tc::mma_bf16(o + 32 * half, da + (half * (G::CHB >> 3) + 128 * k), db + 128 * k, id, !fresh || k > 0);
+                                tc::mma_bf16(tmem + kTmemO + 32 * half, da + (half * (G::CHB >> 3) + 128 * k), db + 128 * k, id, tile > begin || k > 0);
                         tc::commit(&m.v_empty[b]);
 #pragma unroll
                         for (int k = 0; k < G::BN / 16; ++k)
                             tc::mma_bf16(tmem + G::TL, ones, db + 128 * k, id1, tile > begin || k > 0);
-                        tc::commit(&m.pv_done[b]);
                     }
+                    if (big) {   // the same in the whole warp
+                        if (lane == 0) good = wait_lane(&m.big_full, bigs & 1, a.status, abort);
+                        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        if (leader) {
+#pragma unroll 1
+                            for (int i = 0; i < (D == 256 ? 2 : 1) * (G::BN / 16); ++i) {
+                                const int half = i / (G::BN / 16), k = i % (G::BN / 16);
+                                tc::mma_bf16(tmem + kTmemBig + 32 * half, da + (half * (G::CHB >> 3) + 128 * k), db + 128 * k, id, used || k > 0);
+                            }
+                            tc::commit(&m.big_empty);
+                        }
+                        used = true;
+                        ++bigs;
+                    }
+                    if (leader) tc::commit(&m.pv_done[b]);
                     __syncwarp();
                 }
             }

@@ -242,6 +242,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -400,6 +405,10 @@ __device__ __forceinline__ int element_of(int slot) {
 
 // Largest code magnitude.
 template <int T> __host__ __device__ constexpr float code_max() { return T == T_Q8_0 ? 128.0f : (T == T_Q5_0 ? 16.0f : 8.0f); }
+
+// Bits of the largest fp16 scale with which no code leaves fp16's range (65504
+// over a power of two).
+template <int T> __host__ __device__ constexpr uint32_t half_max_scale() { return 0x7BFFu - ((T == T_Q8_0 ? 7u : (T == T_Q5_0 ? 4u : 3u)) << 10); }
 
 // One 32-block, read as words from a 2-byte aligned shared address.
 template <int T> struct Block {
@@ -800,6 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 if (32 * wq < G::BN) {
                     const uint8_t* row = row0 + st * G::RAW;
                     const uint32_t to = to0 + b * G::KC;
+                    uint32_t top = 0;   // largest scale
 #pragma unroll 1
                     for (int i = h; i < G::NB; i += 2) {
                         const Block<T> blk(row + i * Fmt<T>::BB);
@@ -810,9 +820,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                             const uint4 u = blk.template chunk<false>(c, d2);
                             v[4 * c] = u.x, v[4 * c + 1] = u.y, v[4 * c + 2] = u.z, v[4 * c + 3] = u.w;
                         }
+                        top = max(top, blk.d & 0x7fffu);
                         tmem_st(to + 16 * i, v);
                     }
                     tmem_wait_st();
+                    // A value past fp16's range becomes NaN, and so does every score it enters: as an infinity it
+                    // could make the score -inf, and the position would be left out in silence.
+                    if (__any_sync(0xffffffffu, top > half_max_scale<T>())) {
+#pragma unroll 1
+                        for (int i = h; i < G::NB; i += 2) {
+                            uint32_t v[16];
+                            tmem_ld(to + 16 * i, v);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) v[c] = hfma2(v[c], 0u, v[c]);   // inf * 0 is NaN, x * 0 + x is x
+                            tmem_st(to + 16 * i, v);
+                        }
+                        tmem_wait_st();
+                    }
                 }
                 tc::fence_before_sync();
                 __syncwarp();

@@ -448,7 +448,7 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
  * |q_e K_te| of a visible position: |out - out_exact| <= 2^-8 |out_exact| +
  * (2^-10 (1 + A) + 2^-13) sum_t p_t |V[t]| + 2^-32 sum_t |V[t]|, and near
  * the rounding of the output in practice.  Cached K values beyond fp16's
- * range (|w| > 65504) may give NaN for the tokens that see them.
+ * range (|w| that rounds past 65504) give NaN for the tokens that see them.
  * At most 64 query heads to a kv head, n_req up to 65,535.  n_tok == 0 or
  * n_req == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also when the
  * tables could hold about 2^31 tiles or more), QK_ERR_NULL, QK_ERR_ALIGN,

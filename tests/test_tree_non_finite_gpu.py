@@ -1,0 +1,52 @@
+"""qk_attn_tree where a score has no finite value: cached K past fp16's range,
+non-finite queries and scales.  The tokens that see such a score give NaN,
+never a softmax without it; the others, and tokens that see nothing, are not
+touched.  Against paged_ref.py with the tolerance of test_tree_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+import gguf_quant_dequant_gb300 as qk
+import paged_ref
+from gpu_helpers import gpu, type_id  # noqa: F401
+from test_tree_gpu import check, make, run, to_dev
+
+pytestmark = pytest.mark.gpu
+
+BB = {"Q8_0": 34, "Q5_0": 22, "Q4_0": 18}
+
+
+def k_block(c, r, pos, g, blk):
+    row = c["K"][c["table"][r, pos // c["page"]], g, pos % c["page"]]
+    return row.reshape(-1, BB[c["name"]])[blk]
+
+
+@pytest.mark.parametrize("q_value", [1e-6, -1e-6])
+@pytest.mark.parametrize("name,scale,d", [("Q8_0", 1000.0, 64), ("Q8_0", 60000.0, 128), ("Q5_0", 6000.0, 64), ("Q4_0", 20000.0, 256)])
+def test_k_past_half_precision(gpu, name, scale, d, q_value):
+    # All codes of the block negative and the query of one sign, so that the overflowed score is one infinity.
+    c = make(name, [21, 40], [6, 2], 4, 2, d, 16, 900)
+    c["mask"][:6] = [1, 3, 7, 0b1001, 0b11001, 0b111111]
+    c["q"] = torch.full_like(c["q"], q_value)
+    ref = paged_ref.attn_tree(name, c["q"].double().numpy(), c["K"], c["V"], 16, 2, c["table"], c["ctx"], c["cu"], c["mask"], 6,
+                              c["scale"])
+    for g in range(2):
+        b = k_block(c, 0, 23, g, 1)                     # drafted token 2: tokens 2 and 5 see it
+        b[:] = 0x80 if name == "Q8_0" else 0            # the lowest code everywhere
+        b[:2] = np.array([scale], np.float16).view(np.uint8)
+    out = qk.attn_tree(type_id(name), *to_dev(c, gpu))
+    qk.device_status()
+    assert torch.isnan(out[[2, 5]].float()).all()
+    others = [0, 1, 3, 4, 6, 7]
+    check({**c, "q": c["q"][others]}, out[others], tuple(x[others] for x in ref))
+
+
+def test_k_within_half_precision_under_a_large_scale(gpu):
+    # Scales whose largest code would overflow, codes that do not: exact to the tolerance.
+    c = make("Q8_0", [150], [3], 4, 1, 64, 16, 910, q_scale=1e-5)
+    rng = np.random.default_rng(1)
+    for p in range(0, 153, 5):
+        b = k_block(c, 0, p, 0, p % 2)
+        b[:2] = np.array([600.0], np.float16).view(np.uint8)
+        b[2:] = rng.integers(-109, 110, 32).astype(np.int8).view(np.uint8)      # |w| <= 65400
+    run(c, gpu)

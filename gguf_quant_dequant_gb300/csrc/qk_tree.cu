@@ -903,14 +903,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 if (top == 0 || ex > 113) ex = 0;      // nothing, or not finite
                 ex = max(ex, -126);                    // the factors stay normal
                 const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-                // The scores' multiplier.  Where it is 0 (the scale is, or the product underflows) every finite score is 0:
-                // no queries, and a multiplier that still turns a hidden score's infinity into -inf.
+                // The scores' multiplier.  Two kinds of row get a multiplier of 1, which turns a hidden score's infinity
+                // into -inf, and queries that give the visible scores: NaN where the query or the multiplier is not finite
+                // (all of them infinite with one sign would be a softmax of nothing), 0 where the multiplier is 0 (the
+                // scale is, or the product underflows).
                 float mul = a.scale * 1.44269504088896341f * up;
-                if (mul == 0.0f) {
+                const bool no_score = top >= 0x7f80u || !(fabsf(mul) <= 3.402823466e38f);
+                if (no_score || mul == 0.0f) {
                     mul = 1.0f;
-                    if (top < 0x7f80u)
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) x[c] = 0;
+                    for (int c = 0; c < 16; ++c) x[c] = no_score ? 0x7fff7fffu : 0u;
                 }
                 if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a.status, abort);
                 if (row < N) {

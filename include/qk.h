@@ -426,8 +426,9 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
  *   s_t = scale * sum_e q[i, h, e] K[t, g, e],   t < ctx[r]: every one,
  *         t = ctx[r] + j: those with bit j of the token's mask set,
  *   out[i, h] = sum_t softmax(s)_t V[t, g].
- * With scale 0 that is the plain mean of the visible V.  A token that sees no
- * position gives zeros.  What a token does not see
+ * With scale 0 that is the plain mean of the visible V.  A query head with a
+ * NaN or an infinity, and a scale that is one, give NaN.  A token that sees no
+ * position gives zeros, whatever its query.  What a token does not see
  * never reaches its result, whatever it holds (NaN and infinities included);
  * stale bytes past a request's last position are not used.
  *   q      bf16 [n_tok, n_heads, d], q_stride elements from token to token (a

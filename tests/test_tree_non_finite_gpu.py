@@ -50,3 +50,42 @@ def test_k_within_half_precision_under_a_large_scale(gpu):
         b[:2] = np.array([600.0], np.float16).view(np.uint8)
         b[2:] = rng.integers(-109, 110, 32).astype(np.int8).view(np.uint8)      # |w| <= 65400
     run(c, gpu)
+
+
+@pytest.mark.parametrize("value", [np.inf, -np.inf])
+def test_infinite_query_against_codes_of_one_sign(gpu, value):
+    # Every score of the row is the same infinity: NaN, as for mixed ones.
+    c = make("Q8_0", [140], [3], 4, 2, 64, 16, 920)
+    codes = c["K"].reshape(-1, 34)[:, 2:].view(np.int8)
+    codes[:] = np.maximum(np.abs(codes.astype(np.int16)), 1).clip(1, 127).astype(np.int8)
+    d = c["K"].reshape(-1, 34)[:, :2].copy().view(np.float16)
+    c["K"].reshape(-1, 34)[:, :2] = np.maximum(d, np.float16(1e-3)).view(np.uint8)
+    c["mask"][:] = [1, 3, 0]
+    dev = list(to_dev(c, gpu))
+    ref = qk.attn_tree(qk.Q8_0, *dev)
+    check(c, ref)
+    dev[0] = dev[0].clone()
+    dev[0][1, 3, 9] = float(value)
+    out = qk.attn_tree(qk.Q8_0, *dev)
+    assert torch.isnan(out[1, 3].float()).all()
+    out[1, 3] = ref[1, 3]
+    assert torch.equal(out, ref)
+    # a row that sees nothing gives zeros, whatever its query holds
+    c = make("Q8_0", [0], [3], 4, 2, 64, 16, 921)
+    c["mask"][:] = [1, 0, 5]
+    dev = list(to_dev(c, gpu))
+    ref = qk.attn_tree(qk.Q8_0, *dev)
+    dev[0] = dev[0].clone()
+    dev[0][1, 3, 9] = float(value)
+    out = qk.attn_tree(qk.Q8_0, *dev)
+    assert torch.equal(out, ref) and not out[1].any()
+
+
+@pytest.mark.parametrize("scale", [np.inf, -np.inf, np.nan])
+def test_non_finite_scale(gpu, scale):
+    c = make("Q8_0", [0, 90], [3, 2], 4, 2, 64, 16, 930)
+    c["mask"][:3] = [1, 0, 7]
+    c["scale"] = scale
+    out = qk.attn_tree(qk.Q8_0, *to_dev(c, gpu)).float()
+    qk.device_status()
+    assert torch.isnan(out[[0, 2, 3, 4]]).all() and not out[1].any()

@@ -104,8 +104,8 @@ struct Args {
 };
 
 // A request: its first token's row, its tokens, its committed positions and
-// the positions walked (those past the table's end do not exist: they are
-// reported, and not walked).
+// the positions walked (those past the table's end, or past QK_TREE_MAX_POS, do not
+// exist: they are reported, and not walked).
 struct Req {
     int tok0, n, ctx, len;
 };
@@ -114,7 +114,7 @@ __device__ __forceinline__ Req req_of(const Args& a, int r) {
     const int n_tok = (int)a.n_tok;
     q.tok0 = min(max(a.cu[r], 0), n_tok);
     q.n = min(max(min(a.cu[r + 1], n_tok) - q.tok0, 0), a.max_q);
-    const int64_t ctx = max(a.ctx[r], 0), cap = a.table_stride << a.pool.page_log2;
+    const int64_t ctx = max(a.ctx[r], 0), cap = min(a.table_stride << a.pool.page_log2, (int64_t)QK_TREE_MAX_POS);
     q.ctx = (int)min(ctx, cap);
     q.len = (int)min(ctx + q.n, cap);
     if (q.n > 0 && ctx + q.n > cap) atomicOr(a.status, STATUS_BAD_PAGE);

@@ -346,6 +346,9 @@ qk_status qk_gemm(int type, const void* W, int64_t rows, int64_t cols,
 
 /* Most drafted tokens of one request (the width of a tree mask). */
 #define QK_TREE_MAX 64
+/* Most positions of one request that attention walks (indexes inside a tile
+ * past the last one still fit 32 bits). */
+#define QK_TREE_MAX_POS 2147483392
 /* Most requests one qk_kv_plan call takes. */
 #define QK_PLAN_MAX_REQ 8192
 
@@ -434,7 +437,9 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
  *   q      bf16 [n_tok, n_heads, d], q_stride elements from token to token (a
  *          multiple of 8), 16-byte aligned.
  *   ctx    int32 [n_req], cu int32 [n_req + 1] (non-decreasing, within 0 ..
- *          n_tok).  Requests may have no tokens.
+ *          n_tok).  Requests may have no tokens.  Positions past
+ *          QK_TREE_MAX_POS or past the table are not visible and reported as
+ *          a page outside the pool is.
  *   mask   uint64 [n_tok], bit j = the request's token j is visible (its own
  *          bit included where it sees itself); NULL = a plain chain: token i
  *          sees tokens 0 .. i.  n_req requests with one token each and mask

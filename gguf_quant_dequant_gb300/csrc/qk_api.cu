@@ -587,12 +587,13 @@ qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64
         if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "the lists must be 4-byte aligned");
     if (!aligned(mask, 8)) return fail(QK_ERR_ALIGN, "mask must be 8-byte aligned");
     if (out == logits && out_stride != row_stride) return fail(QK_ERR_ARG, "in place needs out_stride == row_stride");
+    unsigned* status = nullptr;
     int sms = 0;
-    const qk_status st = device_state(nullptr, &sms);
+    const qk_status st = device_state(&status, &sms);
     if (st != QK_OK) return st;
     const qk::LogitsArgs a{logits, dtype == QK_OUT_BF16, n_rows, vocab, row_stride, cu, n_req, hist, hist_stride, hist_len,
                            rep, pres, freq, draft, mask, bias_tok, bias_val, bias_stride, bias_len, grammar,
-                           grammar_stride, out, out_stride};
+                           grammar_stride, out, out_stride, status};
     cudaError_t e = qk::launch_logits_process(a, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "qk_logits_process launch");
     g_last_error.clear();
@@ -611,6 +612,7 @@ qk_status qk_device_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "qk_device_status");
     if (v & 1u) return fail(QK_ERR_TIMEOUT, "a bounded wait inside a kernel ran out (status 0x%x)", v);
     if (v & 2u) return fail(QK_ERR_ARG, "a page id or slot outside its KV pool (status 0x%x)", v);
+    if (v & 4u) return fail(QK_ERR_ARG, "a request's history and drafted tokens come to 2^20 or more (status 0x%x)", v);
     return QK_OK;
 }
 

@@ -101,6 +101,7 @@ struct LogitsArgs {
     int64_t grammar_stride;
     void* out;
     int64_t out_stride;
+    unsigned* status;
 };
 cudaError_t launch_logits_process(const LogitsArgs& a, int sms, cudaStream_t s);
 

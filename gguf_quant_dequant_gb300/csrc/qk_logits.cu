@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include "qk_internal.h"
+#include "qk_ptx.cuh"
 
 namespace qk {
 namespace lg {
@@ -49,6 +50,7 @@ struct Args {
     int64_t grammar_stride;
     void* out;
     int64_t out_stride;
+    unsigned* status;
     int rows_per_cta, slice;
 };
 
@@ -70,7 +72,11 @@ template <> struct Elem<true> {
     static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
 };
 
-template <bool BF16, bool VEC>
+// LONG: calls without masks whose chains could be longer than the words can
+// count (a carry would reach the bias index).  A request that is has its drafts
+// left out and is reported.  A variant of its own, because the look at it costs
+// registers: in the ordinary kernel it took 384 x 128,256 logits from 89 to 108 us.
+template <bool BF16, bool VEC, bool LONG>
 __global__ void __launch_bounds__(kThreads, kPerSm) logits_kernel(const Args a) {
     using E = Elem<BF16>;
     using T = typename E::type;
@@ -124,6 +130,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) logits_kernel(const Args a) 
                     __syncthreads();
                 }
                 const int nh = (int)min((int64_t)a.hist_len[r], a.hist_stride);
+                if constexpr (LONG) {
+                    if (max(nh, 0) + (r_hi - r_lo) > (int64_t)kCountMask) {
+                        drafted = false;
+                        if (tid == 0) atomicOr(a.status, STATUS_BAD_COUNT);
+                    }
+                }
                 const int32_t* ht = a.hist + r * a.hist_stride;
                 for (int i = tid; i < nh; i += kThreads) {
                     const int64_t t = ht[i] - v0;
@@ -196,8 +208,10 @@ template <bool BF16>
 static cudaError_t launch_s(const Args& a, bool vec, cudaStream_t s) {
     const dim3 grid((unsigned)((a.vocab + a.slice - 1) / a.slice), (unsigned)((a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta));
     const size_t smem = (size_t)a.slice * sizeof(uint32_t);
-    if (vec) logits_kernel<BF16, true><<<grid, kThreads, smem, s>>>(a);
-    else logits_kernel<BF16, false><<<grid, kThreads, smem, s>>>(a);
+    if (a.draft && !a.mask && a.hist_stride + a.n_rows > (int64_t)kCountMask)
+        logits_kernel<BF16, false, true><<<grid, kThreads, smem, s>>>(a);
+    else if (vec) logits_kernel<BF16, true, false><<<grid, kThreads, smem, s>>>(a);
+    else logits_kernel<BF16, false, false><<<grid, kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -206,7 +220,7 @@ static cudaError_t launch_s(const Args& a, bool vec, cudaStream_t s) {
 cudaError_t launch_logits_process(const LogitsArgs& p, int sms, cudaStream_t s) {
     lg::Args a{p.logits, p.n_rows, p.vocab, p.row_stride, p.cu, (int)p.n_req, p.hist, p.hist_stride, p.hist_len, p.rep,
                p.pres, p.freq, p.draft, p.mask, p.bias_tok, p.bias_val, p.bias_stride, p.bias_len, p.grammar,
-               p.grammar_stride, p.out, p.out_stride, 1};
+               p.grammar_stride, p.out, p.out_stride, p.status, 1};
     // Rows of one request share the slice's words: as many rows per CTA as a
     // request has on average, at most 8, and at least what the grid's 65,535
     // row groups ask for.

@@ -7,7 +7,7 @@
 namespace qk {
 
 // Device status bits (the word lives in qk_api.cu; kernels get its address).
-enum : unsigned { STATUS_TIMEOUT = 1u, STATUS_BAD_PAGE = 2u };
+enum : unsigned { STATUS_TIMEOUT = 1u, STATUS_BAD_PAGE = 2u, STATUS_BAD_COUNT = 4u };
 
 // Spin budget of one bounded mbarrier wait.  try_wait already suspends the
 // thread for a hardware-chosen interval per attempt, so this bound is far

@@ -481,7 +481,10 @@ qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride,
  *   draft  int32 [n_rows], the drafted token of each row, and mask uint64
  *          [n_rows] as in qk_attn_tree: bit j = the request's row j is an
  *          ancestor (the row itself too, when its own bit is set).  mask NULL:
- *          rows cu[r] .. the row itself.  draft NULL: no drafted tokens.
+ *          rows cu[r] .. the row itself; a request whose history and rows come
+ *          to 2^20 or more then has its drafted tokens left out, which
+ *          qk_device_status() reports as QK_ERR_ARG.  draft NULL: no drafted
+ *          tokens.
  *   bias_tok int32, bias_val fp32 [n_req, bias_stride], the first
  *          bias_len[r]; of entries with the same token the last counts;
  *          bias_stride at most 4095; bias_tok NULL: no biases.
@@ -524,7 +527,8 @@ qk_status qk_test_stalled_wait(uint32_t limit_us, void* stream);
 /* Synchronize `stream`, then read and clear this device's kernel status
  * word: QK_OK, QK_ERR_TIMEOUT when a bounded wait ran out since the last
  * call (the affected outputs are then invalid), or QK_ERR_ARG when a paged
- * call met a page id or slot outside its pool. */
+ * call met a page id or slot outside its pool or qk_logits_process a request
+ * with more tokens than it counts. */
 qk_status qk_device_status(void* stream);
 
 /* ------------------------------------------------------------------------

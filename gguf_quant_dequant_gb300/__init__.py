@@ -70,6 +70,8 @@ SIGNATURES = {
     "qk_attn_tree_workspace": (_sz, [_int, _i64, _int, _i64, _int, _int, _int]),
     "qk_attn_tree": (_int, [_int, _p, _i64, _i64, _p, _p, _i64, _int, _p, _i64, _p, _p, _p, _i64, _int, _int, _int, _int,
                             ctypes.c_float, _p, _i64, _p, _sz, _p]),
+    "qk_test_attn_tree_stalled": (_int, [_u32, _u32, _int, _p, _i64, _i64, _p, _p, _i64, _int, _p, _i64, _p, _p, _p, _i64,
+                                         _int, _int, _int, _int, ctypes.c_float, _p, _i64, _p, _sz, _p]),
     "qk_logits_process": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _i64,
                                  _p, _p, _i64, _p, _i64, _p]),
     "qk_unpack": (_int, [_int, _p, _i64, _p, _p, _p, _p, _p, _p]),
@@ -407,6 +409,18 @@ def attn_tree(t: int, q, K, V, page: int, n_kv: int, table, ctx, cu, mask, max_q
     q bf16 CUDA [n_tok, n_heads, d] (rows contiguous); table int32 [n_req, P],
     ctx int32 [n_req], cu int32 [n_req + 1], mask int64 [n_tok] (64 bits) or
     None -> out bf16 [n_tok, n_heads, d]."""
+    return _attn_tree("qk_attn_tree", (), t, q, K, V, page, n_kv, table, ctx, cu, mask, max_q, scale, out, ws, stream)
+
+
+def test_attn_tree_stalled(limit_us: int, tile: int, t: int, q, K, V, page: int, n_kv: int, table, ctx, cu, mask, max_q: int,
+                           scale: float, out=None, ws=None, stream=None):
+    """qk_test_attn_tree_stalled: attn_tree whose copies of V stop before each
+    CTA's tile number `tile`, the wait for them limited to limit_us."""
+    return _attn_tree("qk_test_attn_tree_stalled", (limit_us, tile), t, q, K, V, page, n_kv, table, ctx, cu, mask, max_q,
+                      scale, out, ws, stream)
+
+
+def _attn_tree(name: str, first: tuple, t, q, K, V, page, n_kv, table, ctx, cu, mask, max_q, scale, out, ws, stream):
     import torch
     w, i32 = "attn_tree", torch.int32
     n, n_heads, d = q.shape
@@ -422,10 +436,10 @@ def attn_tree(t: int, q, K, V, page: int, n_kv: int, table, ctx, cu, mask, max_q
     if ws is None:
         ws = torch.empty(max(L.qk_attn_tree_workspace(t, r, max_q, P * page, n_heads, n_kv, d), 16), dtype=torch.uint8,
                          device=q.device)
-    _check(L.qk_attn_tree(t, q.data_ptr(), n, _rows(q, w), K.data_ptr(), V.data_ptr(), pages, page,
-                          _of(table, i32, w, r * P), P, _of(ctx, i32, w, r), _of(cu, i32, w, r + 1),
-                          _of(mask, torch.int64, w, n), r, max_q, n_heads, n_kv, d, scale, out.data_ptr(), _rows(out, w),
-                          ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(q, stream)), "qk_attn_tree")
+    _check(getattr(L, name)(*first, t, q.data_ptr(), n, _rows(q, w), K.data_ptr(), V.data_ptr(), pages, page,
+                            _of(table, i32, w, r * P), P, _of(ctx, i32, w, r), _of(cu, i32, w, r + 1),
+                            _of(mask, torch.int64, w, n), r, max_q, n_heads, n_kv, d, scale, out.data_ptr(), _rows(out, w),
+                            ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(q, stream)), name)
     return out
 
 

@@ -522,10 +522,11 @@ size_t qk_attn_tree_workspace(int type, int64_t n_req, int max_q, int64_t max_po
     return (size_t)qk::attn_tree_ws_bytes(n_req, max_q, max_pos, n_heads, n_kv, d, sm_count_or_default());
 }
 
-qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const void* K, const void* V,
-                       int64_t n_pages, int page, const int32_t* table, int64_t table_stride, const int32_t* ctx,
-                       const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q, int n_heads, int n_kv, int d,
-                       float scale, void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream) {
+static qk_status attn_tree(uint32_t looks, uint32_t hold, int type, const void* q, int64_t n_tok, int64_t q_stride,
+                           const void* K, const void* V, int64_t n_pages, int page, const int32_t* table,
+                           int64_t table_stride, const int32_t* ctx, const int32_t* cu, const uint64_t* mask, int64_t n_req,
+                           int max_q, int n_heads, int n_kv, int d, float scale, void* out, int64_t out_stride, void* ws,
+                           size_t ws_bytes, void* stream) {
     qk_status st = check_pool(type, n_kv, d, page, n_pages, K, V);
     if (st != QK_OK) return st;
     if (!count_ok(table_stride) || !count_ok(n_tok) ||
@@ -550,11 +551,29 @@ qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride,
     cudaError_t e = qk::launch_attn_tree(type, q, n_tok, q_stride, static_cast<const uint8_t*>(K),
                                          static_cast<const uint8_t*>(V), n_pages, page_log2(page),
                                          (int)qk_row_bytes(type, d), table, table_stride, ctx, cu, mask, n_req, max_q,
-                                         n_heads, n_kv, d, scale, out, out_stride, ws, status, sms,
+                                         n_heads, n_kv, d, scale, out, out_stride, ws, status, looks, hold, sms,
                                          static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "qk_attn_tree launch");
     g_last_error.clear();
     return QK_OK;
+}
+
+qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const void* K, const void* V,
+                       int64_t n_pages, int page, const int32_t* table, int64_t table_stride, const int32_t* ctx,
+                       const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q, int n_heads, int n_kv, int d,
+                       float scale, void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream) {
+    return attn_tree(qk::kTreeLooks, ~0u, type, q, n_tok, q_stride, K, V, n_pages, page, table, table_stride, ctx, cu,
+                     mask, n_req, max_q, n_heads, n_kv, d, scale, out, out_stride, ws, ws_bytes, stream);
+}
+
+qk_status qk_test_attn_tree_stalled(uint32_t limit_us, uint32_t tile, int type, const void* q, int64_t n_tok,
+                                    int64_t q_stride, const void* K, const void* V, int64_t n_pages, int page,
+                                    const int32_t* table, int64_t table_stride, const int32_t* ctx, const int32_t* cu,
+                                    const uint64_t* mask, int64_t n_req, int max_q, int n_heads, int n_kv, int d, float scale,
+                                    void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream) {
+    if (limit_us < 1 || limit_us > 2000000) return fail(QK_ERR_ARG, "limit_us=%u outside 1..2000000", limit_us);
+    return attn_tree((limit_us * 1000u + qk::kTreeLookNs - 1) / qk::kTreeLookNs, tile, type, q, n_tok, q_stride, K, V, n_pages, page, table, table_stride, ctx, cu, mask,
+                     n_req, max_q, n_heads, n_kv, d, scale, out, out_stride, ws, ws_bytes, stream);
 }
 
 qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,

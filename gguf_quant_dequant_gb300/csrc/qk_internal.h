@@ -73,11 +73,13 @@ cudaError_t launch_kv_compact(uint8_t* K, uint8_t* V, int64_t n_pages, int page_
                               cudaStream_t s);
 int64_t attn_tree_ws_bytes(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d, int sms);
 double attn_tree_max_tiles(int64_t n_req, int max_q, int64_t max_pos, int n_heads, int n_kv, int d);
+// A wait's limit is kTreeLooks looks of kTreeLookNs (2 s).
+constexpr uint32_t kTreeLookNs = 4000, kTreeLooks = 2000000000u / kTreeLookNs;
 cudaError_t launch_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride, const uint8_t* K, const uint8_t* V,
                              int64_t n_pages, int page_log2, int row_bytes, const int32_t* table, int64_t table_stride,
                              const int32_t* ctx, const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q,
                              int n_heads, int n_kv, int d, float scale, void* out, int64_t out_stride, void* ws,
-                             unsigned* status, int sms, cudaStream_t s);
+                             unsigned* status, uint32_t looks, uint32_t hold, int sms, cudaStream_t s);
 
 // Penalties, biases and grammar masks on logits (qk_logits.cu); the members
 // are qk_logits_process's arguments.

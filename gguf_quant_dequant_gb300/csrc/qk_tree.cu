@@ -32,9 +32,10 @@
 // load the unit's queries.  A tile is a chain of short steps, so it is the
 // number of warps on it that sets the rate: with one warpgroup each for
 // softmax and (K and V) decoding a tile took 5,000 clocks.  Every hand-over
-// is an mbarrier with a bounded wait; after a wait has run out (status word)
-// the copies and MMAs stop, the other roles run through without waiting, and
-// the CTA leaves in order.
+// is an mbarrier with a bounded wait (2 s); after a wait has run out (status
+// word) the copies and MMAs stop, the other roles run through without waiting
+// and without storing results, what is in flight ends, and the CTA leaves in
+// order.
 //
 // What is not visible never reaches a result: a masked score is replaced, not
 // added to; rows past the end are decoded as zeros; a V block whose scale is
@@ -62,7 +63,6 @@
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <type_traits>
 
 #include "qk_formats.cuh"
 #include "qk_hunits.cuh"
@@ -101,6 +101,8 @@ struct Args {
     uint8_t* ws;
     int ctas;
     unsigned* status;
+    uint32_t looks;     // limit of a wait for V's copies, in looks of kTreeLookNs (kTreeLooks but in a test)
+    uint32_t hold;      // tile at which a CTA's V copies stop (a test's; ordinarily none)
 };
 
 // A request: its first token's row, its tokens, its committed positions and
@@ -169,7 +171,7 @@ struct __align__(16) Misc {
     float cref[kRows];           // kLift less the row's reference
     uint64_t seen[4][kRows];     // by unit mod 4, as the next two
     float colc[4][kRows];
-    int64_t rowoff[4][kRows];    // the row's place in out
+    int64_t rowoff[4][kRows];    // the row's place in out, -1 for columns that are no row
     uint4 valid[2][16];          // K's, V's copier: by tile mod 16, a bit per position that exists
     float ref[kRows], factor[kRows];
     float wmax[4][kRows];
@@ -366,28 +368,44 @@ __device__ __forceinline__ void bulk_g2s_keep(void* dst, const void* src, uint32
 }
 
 // A wait of the roles that run on after a failure: no waiting once *abort is
-// set.  One lane polls (the hardware suspends it for a while at each look), the
-// warp waits for it.  Kept short: it stands in 20 places, and the roles' code
-// has to stay in the instruction cache together.
-__device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
+// set (they then arrive for work that was not done, but never on raw_empty, so
+// that no copy is requested into a stage that another is still on its way to).
+// One lane looks; a look at a phase that does not complete lasts kTreeLookNs
+// (the hardware's suspension: 4.01 us measured), so the limit of the looks is one
+// of time.  The warp waits for that lane.  Kept short: it stands in 20 places, and
+// the roles' code has to stay in the instruction cache together (with the timer
+// read in this loop the measured calls took 2 to 16 % longer, with a suspension of
+// its own up to 10 %).
+__device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, const Args& a, volatile int* abort,
+                                          uint32_t looks = kTreeLooks) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < (1u << 24); ++i) {
+    for (uint32_t i = 0; i < looks; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
     }
     *abort = 1;
-    atomicOr(status, STATUS_TIMEOUT);
+    atomicOr(a.status, STATUS_TIMEOUT);
     return false;
 }
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
+// Copies or products in flight, after a failure.
+__device__ __forceinline__ void wait_drained(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kTreeLooks && !mbar_try_wait(bar, parity); ++i) {}
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Args& a, volatile int* abort) {
     int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = wait_lane(bar, parity, status, abort);
+    if ((threadIdx.x & 31) == 0) ok = wait_lane(bar, parity, a, abort);
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
+// Whether a wait of the CTA has run out, the same in the whole warp.  A role
+// that runs on arrives on its barriers without having waited, but only after it
+// has seen *abort; so who finds it clear after a wait of its own was let
+// through by work that was done.
+__device__ __forceinline__ bool failed(volatile int* abort) { return __any_sync(0xffffffffu, *abort != 0); }
 
 // Whether the unit's piece (m.piece[unit mod 8]) is there; false after a failure.
-__device__ __forceinline__ bool piece_ready(Misc& m, uint32_t unit, unsigned* status) {
-    return wait_warp(&m.piece_full[unit & 7], (unit >> 3) & 1, status, &m.abort);
+__device__ __forceinline__ bool piece_ready(Misc& m, uint32_t unit, const Args& a) {
+    return wait_warp(&m.piece_full[unit & 7], (unit >> 3) & 1, a, &m.abort);
 }
 
 // --------------------------------------------------------------- decode ----
@@ -426,14 +444,12 @@ template <int T> struct Block {
             prev = next;
         }
     }
-    // Chunk k (0..3): code (exact) * d; a large block takes the
-    // code times 2^-7, still exact.
-    template <bool BIG>
+    // Chunk k (0..3): code (exact) * d.
     __device__ __forceinline__ uint4 chunk(int k, uint32_t d2) const {
         using hm::and_or;
         using hm::and_xor;
         using hm::hadd2;
-        const auto value = [d2](uint32_t code) { return hmul2(BIG ? hmul2(code, 0x20002000u) : code, d2); };
+        const auto value = [d2](uint32_t code) { return hmul2(code, d2); };
         if constexpr (T == T_Q8_0) {   // 0x6480 ^ byte = 1152 + (signed byte)
             const uint32_t x = w[2 * k], y = w[2 * k + 1];
             return make_uint4(value(hadd2(and_xor(x, 0x00FF00FFu, 0x64806480u), 0xE480E480u)),
@@ -498,8 +514,8 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
     for (int t = t0; t < t1; ++t, ++tile) {
         const uint32_t b = tile & 1;
         if (lane == 0) {
-            wait_lane(&m.s_full[b], (tile >> 1) & 1, a.status, abort);
-            if (tile >= 2) wait_lane(&m.pv_done[b], ((tile >> 1) - 1) & 1, a.status, abort);   // the P buffer is free
+            wait_lane(&m.s_full[b], (tile >> 1) & 1, a, abort);
+            if (tile >= 2) wait_lane(&m.pv_done[b], ((tile >> 1) - 1) & 1, a, abort);   // the P buffer is free
         }
         __syncwarp();
         tc::fence_after_sync();
@@ -556,7 +572,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                 }
                 sync_group(wg);
                 if (t != t0) {   // the sums so far on the new references
-                    wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a.status, abort);
+                    wait_warp(&m.pv_done[b ^ 1], ((tile - 1) >> 1) & 1, a, abort);
                     tc::fence_after_sync();
                     // the rows' sums, O^T, the large blocks' O^T
                     const int sets = 1 + (*(volatile unsigned*)&m.used[unit & 7] ? 2 : 1) * (D == 256 ? 2 : 1);
@@ -607,13 +623,15 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
     const bool whole = t0 == 0 && t1 == p.nt;
     float* po = reinterpret_cast<float*>(part);
     const uint32_t last = tile - 1;
-    wait_warp(&m.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
+    wait_warp(&m.pv_done[last & 1], (last >> 1) & 1, a, abort);
     tc::fence_after_sync();
     const unsigned used = *(volatile unsigned*)&m.used[unit & 7];
     const int64_t* rowoff = m.rowoff[unit & 3] + c0;
     const int rows = p.rows;
+    // After a failure rowoff may never have been written: nothing is stored.
+    const int halves = failed(abort) ? 0 : (D == 256 ? 2 : 1);
 #pragma unroll 1
-    for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
+    for (int half = 0; half < halves; ++half) {
         const int blk = 4 * half + wq;
         if (blk >= G::NB) break;   // lanes past d (warp-uniform)
         const int e = 32 * blk + element_of<T>(lane);
@@ -643,7 +661,7 @@ __device__ __forceinline__ void softmax_piece(const Args& a, Misc& m, uint8_t* s
                 const float o = __uint_as_float(v[c]), sum = __uint_as_float(l[c]);
                 if (whole) {   // a row that saw nothing: zeros
                     const __nv_bfloat16 r = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(o, sum));
-                    if (col < rows) a.out[rowoff[h + c] + e] = r;
+                    if (rowoff[h + c] >= 0) a.out[rowoff[h + c] + e] = r;
                 } else {
                     if (col < rows) po[col * D + e] = o;
                     if (blk == 0 && lane == c) *reinterpret_cast<float2*>(po + kRows * D + 2 * col) = make_float2(m.ref[col], sum);
@@ -779,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         uint32_t tile = 0, unit = 0;
 #pragma unroll 1
         for (;; ++unit) {
-            if (vote_group(wg, !piece_ready(m, unit, a.status))) break;
+            if (vote_group(wg, !piece_ready(m, unit, a))) break;
             const Piece& p = m.piece[unit & 7];
             const int rows = p.rows;
             if (rows == 0) break;
@@ -795,14 +813,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         const uint32_t to0 = tmem + ((uint32_t)(32 * wq) << 16) + kTmemK;
         uint32_t st = 0, rph = 0;   // the K tile's ring stage and its phase
 #pragma unroll 1
-        for (uint32_t unit = 0; piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
+        for (uint32_t unit = 0; piece_ready(m, unit, a) && m.piece[unit & 7].rows; ++unit) {
             const uint32_t end = tile + (m.piece[unit & 7].t1 - m.piece[unit & 7].t0);
 #pragma unroll 1
             for (; tile < end; ++tile) {
                 const uint32_t b = tile & 1;
                 if (lane == 0) {
-                    if (tile >= 2) wait_lane(&m.k_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
-                    wait_lane(&m.raw_full[st], rph, a.status, abort);
+                    if (tile >= 2) wait_lane(&m.k_empty[b], ((tile >> 1) - 1) & 1, a, abort);
+                    wait_lane(&m.raw_full[st], rph, a, abort);
                 }
                 __syncwarp();
                 tc::fence_after_sync();
@@ -817,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                         uint32_t v[16];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const uint4 u = blk.template chunk<false>(c, d2);
+                            const uint4 u = blk.chunk(c, d2);
                             v[4 * c] = u.x, v[4 * c + 1] = u.y, v[4 * c + 2] = u.z, v[4 * c + 3] = u.w;
                         }
                         top = max(top, blk.d & 0x7fffu);
@@ -843,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&m.k_full[b]);
-                    mbar_arrive(&m.raw_empty[st]);
+                    if (!*abort) mbar_arrive(&m.raw_empty[st]);   // after a failure the copy may still be under way
                 }
                 if ((st += 2) == G::NS) st = 0, rph ^= 1;
             }
@@ -867,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
         uint32_t bigs = 0;          // tiles with large blocks so far
 #pragma unroll 1
         for (;; ++unit) {
-            if (vote_v(!piece_ready(m, unit, a.status))) break;
+            if (vote_v(!piece_ready(m, unit, a))) break;
             const Piece& p = m.piece[unit & 7];
             if (p.rows == 0) break;
             {
@@ -914,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) x[c] = no_score ? 0x7fff7fffu : 0u;
                 }
-                if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a.status, abort);
+                if (unit > 0) wait_warp(&m.q_empty, (unit - 1) & 1, a, abort);
                 if (row < N) {
                     uint8_t* to = sq + (sub >> 1) * (G::NR * 128) + row * 128;
 #pragma unroll
@@ -932,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     if (sub == 0) {
                         m.colc[unit & 3][row] = mul;
                         m.seen[unit & 3][row] = seen;
-                        m.rowoff[unit & 3][row] = (p.q.tok0 + tok) * a.out_stride + head * D;
+                        m.rowoff[unit & 3][row] = live ? (p.q.tok0 + tok) * a.out_stride + head * D : -1;
                     }
                 }
                 // The flags of unit + 1 (last of unit - 7, long done) start clear;
@@ -951,8 +969,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             for (; tile < end; ++tile, j += G::BN) {
                 const uint32_t b = tile & 1;
                 if (lane == 0) {
-                    if (tile >= 2) wait_lane(&m.v_empty[b], ((tile >> 1) - 1) & 1, a.status, abort);
-                    wait_lane(&m.raw_full[st], rph, a.status, abort);
+                    if (tile >= 2) wait_lane(&m.v_empty[b], ((tile >> 1) - 1) & 1, a, abort);
+                    wait_lane(&m.raw_full[st], rph, a, abort, a.looks);
                 }
                 __syncwarp();
                 const bool valid = mine && ((reinterpret_cast<const uint32_t*>(&m.valid[1][tile & 15])[pos >> 5] >> (pos & 31)) & 1);
@@ -978,25 +996,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                 big = vote_v(big);
                 if (dt == 0) m.big_tile[tile & 15] = big;
                 uint8_t* line = line0 + b * G::VB;
-                auto blocks = [&](auto is_big, uint32_t which) {
+                auto blocks = [&](uint32_t which, uint32_t times) {   // the others are zeros; times: the scales' factor, two halves
 #pragma unroll 1
                     for (int i = 0; i < G::ITEM / 32; ++i) {
                         const Block<T> blk(src + i * Fmt<T>::BB);
-                        const uint32_t d2 = hm::dup16(blk.d);
+                        const uint32_t d2 = times == 0x3C003C00u ? hm::dup16(blk.d) : hmul2(hm::dup16(blk.d), times);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            uint4 o = blk.template chunk<decltype(is_big)::value>(c, d2);
+                            uint4 o = blk.chunk(c, d2);
                             if (!((which >> i) & 1)) o = make_uint4(0, 0, 0, 0);
                             *reinterpret_cast<uint4*>(line + (((4 * i + c) ^ (pos & 7)) << 4)) = o;
                         }
                     }
                 };
-                if (mine) blocks(std::false_type{}, good);
+                if (mine) blocks(good, 0x3C003C00u);   // 1
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.v_full[b]);
                 if (big) {   // then the large blocks, in the same buffer once its product is done
-                    if (lane == 0) wait_lane(&m.v_empty[b], (tile >> 1) & 1, a.status, abort);
+                    if (lane == 0) wait_lane(&m.v_empty[b], (tile >> 1) & 1, a, abort);
                     __syncwarp();
                     uint32_t large = 0;
 #pragma unroll
@@ -1004,17 +1022,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                         const float d = fabsf(h2f(ld_u16(src + i * Fmt<T>::BB)));
                         if (valid && d * code_max<T>() > 65504.0f && d <= 65504.0f) large |= 1u << i;
                     }
-                    if (mine) blocks(std::true_type{}, large);
+                    if (mine) blocks(large, 0x20002000u);   // 2^-7 (exact: a large scale is above 2^8)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&m.big_full);
-                        wait_lane(&m.big_empty, bigs & 1, a.status, abort);
+                        wait_lane(&m.big_empty, bigs & 1, a, abort);
                     }
                     __syncwarp();
                     ++bigs;
                 }
-                if (lane == 0) mbar_arrive(&m.raw_empty[st]);
+                if (lane == 0 && !*abort) mbar_arrive(&m.raw_empty[st]);
                 if ((st += 2) == G::NS + 1) st = 1, rph ^= 1;
             }
         }
@@ -1037,11 +1055,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             for (uint32_t unit = 0; ok; ++unit) {
                 Piece p;
                 if (kv) {
-                    if (!piece_ready(m, unit, a.status)) break;
+                    ok = piece_ready(m, unit, a);
+                    if (!ok) break;
                     p = m.piece[unit & 7];
                 } else {
                     const bool more = w.next(a, p);
-                    if (unit >= 8 && !wait_warp(&m.piece_free[unit & 7], ((unit >> 3) - 1) & 1, a.status, abort)) break;
+                    if (unit >= 8 && (!wait_warp(&m.piece_free[unit & 7], ((unit >> 3) - 1) & 1, a, abort) || failed(abort))) { ok = false; break; }
                     if (!more) p.rows = 0;
                     if (lane == 0) {
                         m.piece[unit & 7] = p;
@@ -1062,7 +1081,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     }
                 }
                 if (p.rows == 0) break;
-                const int len = p.q.len, t1 = p.t1;
+                const int len = p.q.len;
+                const bool held = kv && a.hold - tile < (uint32_t)(p.t1 - p.t0);   // the copies stop inside the unit
+                const int t1 = held ? p.t0 + (int)(a.hold - tile) : p.t1;
                 const bool shared = groups_of(p.q, a.G, G::NR) > 1;   // other row groups read these bytes too
                 const int32_t* tab = a.table + (int64_t)p.r * a.table_stride;
                 const uint8_t* head = pool + ((int64_t)p.g << pl) * G::RB;
@@ -1097,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     const uint32_t src_in = (pos & ((1 << pl) - 1)) * G::RB;   // inside the page's head
                     int good = 1;
                     if (lane == 0) {
-                        good = wait_lane(&m.raw_empty[st], rph, a.status, abort);
+                        good = wait_lane(&m.raw_empty[st], rph, a, abort);
                         m.valid[kv][tile & 15] = valid;   // published by the arrival
                         if (good) mbar_arrive_expect_tx(&m.raw_full[st], sum);
                     }
@@ -1117,22 +1138,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     __syncwarp();
                     if ((st += 2) >= G::NS) st = kv, rph ^= 1;
                 }
+                if (held) break;
             }
-            // Copies in flight land before the CTA may leave.
-            if (!ok) {
-                const uint32_t last = tile < G::NS / 2 ? tile : G::NS / 2;   // requested and perhaps not yet seen
-                for (uint32_t i = 1; i <= last; ++i) {
-                    const uint32_t k = tile - i;
-                    mbar_wait_bounded(&m.raw_full[(2 * k + kv) % G::NS], (2 * k + kv) / G::NS & 1, a.status);
-                }
-            }
+            // Copies in flight land before the CTA may leave: the last phase of each stage (of one that was never used, the
+            // phase before its first).
+            if (failed(abort))
+#pragma unroll 1
+                for (uint32_t s = kv; s < G::NS; s += 2) wait_drained(&m.raw_full[s], rph ^ (s < st));
         } else if (warp == 1) {
             // Q K: the warp walks together, one lane issues.
             uint32_t tile = 0, unit = 0;
             bool ok = true;
             const bool leader = tc::elect_one();
             const uint64_t dq = tc::sdesc_k128(smem_u32(sq));
-            for (; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
+            for (; ok && (ok = piece_ready(m, unit, a)) && m.piece[unit & 7].rows; ++unit) {
                 const Piece& p = m.piece[unit & 7];
                 const uint32_t id = idesc_f16(cols_of(p.rows), false), begin = tile, end = tile + (p.t1 - p.t0);
 #pragma unroll 1
@@ -1140,9 +1159,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     const uint32_t b = tile & 1;
                     int good = 1;
                     if (lane == 0) {
-                        if (tile == begin) good = wait_lane(&m.q_full, unit & 1, a.status, abort);
-                        good = good && (tile < 2 || wait_lane(&m.p_full[b], ((tile >> 1) - 1) & 1, a.status, abort));   // S^T has been read
-                        good = good && wait_lane(&m.k_full[b], (tile >> 1) & 1, a.status, abort);
+                        if (tile == begin) good = wait_lane(&m.q_full, unit & 1, a, abort);
+                        good = good && (tile < 2 || wait_lane(&m.p_full[b], ((tile >> 1) - 1) & 1, a, abort));   // S^T has been read
+                        good = good && wait_lane(&m.k_full[b], (tile >> 1) & 1, a, abort);
                     }
                     ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                     if (!ok) break;
@@ -1158,10 +1177,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     __syncwarp();
                 }
             }
-            if (!ok) {   // let the products in flight end
+            if (failed(abort)) {   // let the products in flight end
                 if (leader) tc::commit(&m.drain[0]);
                 __syncwarp();
-                if (lane == 0) mbar_wait_bounded(&m.drain[0], 0, a.status);
+                if (lane == 0) wait_drained(&m.drain[0], 0);
                 __syncwarp();
             }
         } else {
@@ -1173,7 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
             const uint64_t dv = sdesc_mn128(smem_u32(sv), D <= 64 ? 0 : G::CHB), dp = sdesc_mn128(smem_u32(sp), 0);
             // the rows' sums: a tile of ones in V's place (one 8-row atom, its row stride 0)
             const uint64_t ones = tc::sdesc_k128(smem_u32(sp + 2 * G::PB)) & ~(uint64_t(0x3FFF) << 32);
-            for (; ok && piece_ready(m, unit, a.status) && m.piece[unit & 7].rows; ++unit) {
+            for (; ok && (ok = piece_ready(m, unit, a)) && m.piece[unit & 7].rows; ++unit) {
                 const Piece& p = m.piece[unit & 7];
                 const uint32_t id = idesc_f16(cols_of(p.rows), true), id1 = id & ~(1u << 15), begin = tile, end = tile + (p.t1 - p.t0);
                 bool used = false;   // large blocks
@@ -1182,9 +1201,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     const uint32_t b = tile & 1;
                     int good = 1;
                     if (lane == 0) {
-                        if (tile == begin && unit > 0) good = wait_lane(&m.o_empty, (unit - 1) & 1, a.status, abort);
-                        good = good && wait_lane(&m.v_full[b], (tile >> 1) & 1, a.status, abort) &&
-                               wait_lane(&m.p_full[b], (tile >> 1) & 1, a.status, abort);
+                        if (tile == begin && unit > 0) good = wait_lane(&m.o_empty, (unit - 1) & 1, a, abort);
+                        good = good && wait_lane(&m.v_full[b], (tile >> 1) & 1, a, abort) &&
+                               wait_lane(&m.p_full[b], (tile >> 1) & 1, a, abort);
                     }
                     ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                     if (!ok) break;
@@ -1204,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                             tc::mma_bf16(tmem + G::TL, ones, db + 128 * k, id1, tile > begin || k > 0);
                     }
                     if (big) {   // the same in the whole warp
-                        if (lane == 0) good = wait_lane(&m.big_full, bigs & 1, a.status, abort);
+                        if (lane == 0) good = wait_lane(&m.big_full, bigs & 1, a, abort);
                         ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                         if (!ok) break;
                         tc::fence_after_sync();
@@ -1223,10 +1242,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Args a) {
                     __syncwarp();
                 }
             }
-            if (!ok) {
+            if (failed(abort)) {
                 if (leader) tc::commit(&m.drain[1]);
                 __syncwarp();
-                if (lane == 0) mbar_wait_bounded(&m.drain[1], 0, a.status);
+                if (lane == 0) wait_drained(&m.drain[1], 0);
                 __syncwarp();
             }
         }
@@ -1337,12 +1356,12 @@ cudaError_t launch_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_s
                              int64_t n_pages, int page_log2, int row_bytes, const int32_t* table, int64_t table_stride,
                              const int32_t* ctx, const int32_t* cu, const uint64_t* mask, int64_t n_req, int max_q,
                              int n_heads, int n_kv, int d, float scale, void* out, int64_t out_stride, void* ws,
-                             unsigned* status, int sms, cudaStream_t s) {
+                             unsigned* status, uint32_t looks, uint32_t hold, int sms, cudaStream_t s) {
     const tree::Args a{static_cast<const __nv_bfloat16*>(q), n_tok, q_stride, K, V, Pool{n_pages, page_log2, n_kv, row_bytes},
                        table, table_stride, ctx, cu, mask, (int)n_req, max_q, n_heads / n_kv,
                        (uint32_t)(((1 << 19) + n_heads / n_kv - 1) / (n_heads / n_kv)), scale,
                        static_cast<__nv_bfloat16*>(out), out_stride, static_cast<uint8_t*>(ws),
-                       tree_ctas(n_req, max_q, table_stride << page_log2, n_heads, n_kv, d, sms), status};
+                       tree_ctas(n_req, max_q, table_stride << page_log2, n_heads, n_kv, d, sms), status, looks, hold};
     switch (type) {
     case T_Q8_0: return tree::launch_d<T_Q8_0>(a, d, s);
     case T_Q5_0: return tree::launch_d<T_Q5_0>(a, d, s);

@@ -524,6 +524,17 @@ qk_status qk_unpack(int type, const void* W, int64_t nblocks, int16_t* codes,
  * Afterwards qk_device_status() reports QK_ERR_TIMEOUT (and clears it). */
 qk_status qk_test_stalled_wait(uint32_t limit_us, void* stream);
 
+/* The same inside attention: qk_attn_tree in which each CTA's copies of V stop
+ * before its tile number `tile` (from 0, counted over its units) and the wait
+ * for them is limited to limit_us (1 .. 2,000,000; else QK_ERR_ARG).  A CTA that
+ * comes so far gives up, and the call's results are then invalid; nothing
+ * outside out and ws is written. */
+qk_status qk_test_attn_tree_stalled(uint32_t limit_us, uint32_t tile, int type, const void* q, int64_t n_tok,
+                                    int64_t q_stride, const void* K, const void* V, int64_t n_pages, int page,
+                                    const int32_t* table, int64_t table_stride, const int32_t* ctx, const int32_t* cu,
+                                    const uint64_t* mask, int64_t n_req, int max_q, int n_heads, int n_kv, int d, float scale,
+                                    void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronize `stream`, then read and clear this device's kernel status
  * word: QK_OK, QK_ERR_TIMEOUT when a bounded wait ran out since the last
  * call (the affected outputs are then invalid), or QK_ERR_ARG when a paged

@@ -394,8 +394,11 @@ cudaError_t launch_kv_plan(const int32_t* have, const int32_t* start, const int3
                            int32_t* pos, int32_t* req, int64_t cap, int sms, cudaStream_t s) {
     const kv::PlanArgs a{have, start, want, n_req, page_log2, table, table_stride, free_pages, free_cap, n_free,
                          n_free_out, granted, cu, slots, pos, req, cap};
-    const int smem = 3 * (n_req + 1) * (int)sizeof(int);
-    const cudaError_t e = cudaFuncSetAttribute(kv::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // The limit is the kernel's, not the launch's: always the largest call's, so that another thread's smaller call
+    // cannot lower it between these two lines.
+    auto bytes = [](int n) { return 3 * (n + 1) * (int)sizeof(int); };
+    const int smem = bytes(n_req);
+    const cudaError_t e = cudaFuncSetAttribute(kv::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(QK_PLAN_MAX_REQ));
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>(std::max<int64_t>(1, (cap + kv::kTokensPerCta - 1) / kv::kTokensPerCta), sms);
     kv::plan_kernel<<<(unsigned)grid, kv::kPlanThreads, smem, s>>>(a);

@@ -3,7 +3,9 @@
 Every computation runs in the library's CUDA kernels; this module passes
 device pointers, sizes and the current CUDA stream of PyTorch tensors, and
 raises QKError on a non-zero status.  There is no CPU fallback: if libqk.so
-has not been built, load() raises.
+has not been built, load() raises.  stream= of a call is a torch stream or a
+raw handle; a result or a workspace that the call allocates for itself is then
+taken as under torch.cuda.stream(stream).
 
 Type ids: Q4_K = 1, Q6_K = 2, Q8_0 = 3, Q5_0 = 4, Q4_0 = 5, Q5_K = 6, Q2_K = 7, Q3_K = 8.
 """
@@ -147,6 +149,29 @@ def _stream_on(x, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(x.device.index)
 
 
+def _empty(size, dtype, like, stream, kept: bool = True):
+    """A new tensor beside `like` for a call on `stream`.  For another stream
+    than the current one it comes from that stream's memory, as inside
+    torch.cuda.stream(stream): the caching allocator could otherwise hand out
+    bytes that earlier work of the current stream still uses, or hand them on
+    while the call's kernels run.  kept: the caller gets the tensor and may use
+    it on the current stream too."""
+    import torch
+    dev = like.device
+    if stream is None or dev.type != "cuda":
+        return torch.empty(size, dtype=dtype, device=dev)
+    handle = _stream(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(dev.index):
+        return torch.empty(size, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        x = torch.empty(size, dtype=dtype, device=dev)
+    if kept:
+        x.record_stream(torch.cuda.current_stream(dev))
+    return x
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -167,7 +192,7 @@ def dequant(t: int, W, rows: int, cols: int, out=None, bf16: bool = False, strea
     """W: uint8 CUDA tensor of packed blocks -> out [rows, cols] fp32 / bf16."""
     import torch
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16 if bf16 else torch.float32, device=W.device)
+        out = _empty((rows, cols), torch.bfloat16 if bf16 else torch.float32, W, stream)
     _check(load().qk_dequant(t, _ptr(W), rows, cols, _ptr(out), OUT_BF16 if bf16 else OUT_F32,
                              _stream(stream)), "qk_dequant")
     return out
@@ -179,7 +204,7 @@ def quantize(t: int, w, out=None, stream=None):
     import torch
     rows, cols = w.shape
     if out is None:
-        out = torch.empty(rows * row_bytes(t, cols), dtype=torch.uint8, device=w.device)
+        out = _empty(rows * row_bytes(t, cols), torch.uint8, w, stream)
     _check(load().qk_quantize(t, _ptr(w), rows, cols, _ptr(out), _stream(stream)), "qk_quantize")
     return out
 
@@ -191,7 +216,7 @@ def quantize_imatrix(t: int, w, imp, out=None, stream=None):
     import torch
     rows, cols = w.shape
     if out is None:
-        out = torch.empty(rows * row_bytes(t, cols), dtype=torch.uint8, device=w.device)
+        out = _empty(rows * row_bytes(t, cols), torch.uint8, w, stream)
     _check(load().qk_quantize_imatrix(t, _ptr(w), rows, cols, _ptr(imp), _ptr(out), _stream(stream)),
            "qk_quantize_imatrix")
     return out
@@ -208,10 +233,10 @@ def attn_decode(t: int, q, K, V, T: int, n_heads: int, n_kv: int, d: int, scale:
     [n_heads, d]."""
     import torch
     if out is None:
-        out = torch.empty((n_heads, d), dtype=torch.float32, device=q.device)
+        out = _empty((n_heads, d), torch.float32, q, stream)
     need = attn_decode_workspace(t, T, n_heads, n_kv, d)
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        ws = _empty(max(need, 16), torch.uint8, q, stream, kept=False)
     _check(load().qk_attn_decode(t, _ptr(q), _ptr(K), _ptr(V), T, n_heads, n_kv, d, scale, _ptr(out), _ptr(ws),
                                  ws.numel() * ws.element_size(), _stream(stream)), "qk_attn_decode")
     return out
@@ -221,7 +246,7 @@ def gemv_swiglu(t: int, Wg, Wu, rows: int, cols: int, x, h=None, stream=None):
     """Decode SwiGLU: x fp32 CUDA [cols] -> h = SiLU(Wg x) * (Wu x), fp32 [rows]."""
     import torch
     if h is None:
-        h = torch.empty(rows, dtype=torch.float32, device=x.device)
+        h = _empty(rows, torch.float32, x, stream)
     _check(load().qk_gemv_swiglu(t, _ptr(Wg), _ptr(Wu), rows, cols, _ptr(x), _ptr(h), _stream(stream)),
            "qk_gemv_swiglu")
     return h
@@ -236,10 +261,10 @@ def gemv(t: int, W, rows: int, cols: int, x, y=None, ws=None, stream=None):
     import torch
     M = x.shape[0] if x.dim() == 2 else 1
     if y is None:
-        y = torch.empty((M, rows), dtype=torch.float32, device=x.device)
+        y = _empty((M, rows), torch.float32, x, stream)
     need = gemv_workspace(t, rows, cols, M)
     if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        ws = _empty(need, torch.uint8, x, stream, kept=False)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(load().qk_gemv(t, _ptr(W), rows, cols, _ptr(x), M, _ptr(y), _ptr(ws), nbytes, _stream(stream)),
            "qk_gemv")
@@ -252,7 +277,7 @@ def gemv_noalloc(t: int, W, rows: int, cols: int, x, y=None, stream=None):
     import torch
     M = x.shape[0] if x.dim() == 2 else 1
     if y is None:
-        y = torch.empty((M, rows), dtype=torch.float32, device=x.device)
+        y = _empty((M, rows), torch.float32, x, stream)
     _check(load().qk_gemv_noalloc(t, _ptr(W), rows, cols, _ptr(x), M, _ptr(y), _stream(stream)),
            "qk_gemv_noalloc")
     return y
@@ -264,7 +289,7 @@ def gemv_batch(t: int, Ws, rows, cols: int, x, ys=None, stream=None):
     import torch
     n = len(Ws)
     if ys is None:
-        ys = [torch.empty(r, dtype=torch.float32, device=x.device) for r in rows]
+        ys = [_empty(r, torch.float32, x, stream) for r in rows]
     Wp = (_p * n)(*[_ptr(w) for w in Ws])
     rp = (_i64 * n)(*rows)
     yp = (_p * n)(*[_ptr(y) for y in ys])
@@ -281,10 +306,10 @@ def gemm(t: int, W, rows: int, cols: int, X, Y=None, ws=None, stream=None):
     import torch
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, rows), dtype=torch.float32, device=X.device)
+        Y = _empty((M, rows), torch.float32, X, stream)
     need = gemm_workspace(t, rows, cols, M)
     if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+        ws = _empty(need, torch.uint8, X, stream, kept=False)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(load().qk_gemm(t, _ptr(W), rows, cols, _ptr(X), M, _ptr(Y), _ptr(ws), nbytes, _stream(stream)),
            "qk_gemm")
@@ -360,8 +385,8 @@ def kv_plan(have, start, want, table, free_pages, n_free, page: int, cap: int, o
     ptrs = [_of(have, i32, w, n), _of(start, i32, w, n), _of(want, i32, w, n), _of(table, i32, w, n * P),
             _of(free_pages, i32, w, F), _of(n_free, i32, w, 1)]
     if out is None:
-        e = torch.empty(2 + 2 * n + 2 * cap, dtype=i32, device=have.device)
-        slots = torch.empty(cap, dtype=torch.int64, device=have.device)
+        e = _empty(2 + 2 * n + 2 * cap, i32, have, stream)
+        slots = _empty(cap, torch.int64, have, stream)
         at, q = e.data_ptr(), slots.data_ptr()
         outs = (at, at + 4, at + 4 + 4 * n, q, at + 8 + 8 * n, at + 8 + 8 * n + 4 * cap)
         a, b, c, d, f = e.split((1, n, n + 1, cap, cap))
@@ -428,14 +453,14 @@ def _attn_tree(name: str, first: tuple, t, q, K, V, page, n_kv, table, ctx, cu, 
     if q.dtype is not torch.bfloat16:
         raise QKError(8, w, "q must be bfloat16")
     if out is None:
-        out = torch.empty((n, n_heads, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((n, n_heads, d), torch.bfloat16, q, stream)
     elif out.dtype is not torch.bfloat16 or out.shape != q.shape:
         raise QKError(2, w, "out must be bfloat16 of q's shape")
     pages = _pool_pages(t, K, V, n_kv, d, page, w)
     L = load()
     if ws is None:
-        ws = torch.empty(max(L.qk_attn_tree_workspace(t, r, max_q, P * page, n_heads, n_kv, d), 16), dtype=torch.uint8,
-                         device=q.device)
+        ws = _empty(max(L.qk_attn_tree_workspace(t, r, max_q, P * page, n_heads, n_kv, d), 16), torch.uint8, q, stream,
+                    kept=False)
     _check(getattr(L, name)(*first, t, q.data_ptr(), n, _rows(q, w), K.data_ptr(), V.data_ptr(), pages, page,
                             _of(table, i32, w, r * P), P, _of(ctx, i32, w, r), _of(cu, i32, w, r + 1),
                             _of(mask, torch.int64, w, n), r, max_q, n_heads, n_kv, d, scale, out.data_ptr(), _rows(out, w),
@@ -457,7 +482,7 @@ def logits_process(logits, cu, hist, hist_len, rep, pres, freq, draft=None, mask
     B = 0 if bias_tok is None else bias_tok.shape[1]
     words = 0 if grammar is None else grammar.shape[1]
     if out is None:
-        out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+        out = _empty((n, V), logits.dtype, logits, stream)
     elif out.dtype is not logits.dtype or out.shape != logits.shape:
         raise QKError(2, w, "out must have the logits' type and shape")
     _check(load().qk_logits_process(
@@ -474,12 +499,11 @@ def unpack(t: int, W, nblocks: int, stream=None):
     """-> (codes int16 [nblocks, elems], sc int16 [nblocks, 16], mins uint8
     [nblocks, 16], d f32 [nblocks], dmin f32 [nblocks]) as CUDA tensors."""
     import torch
-    dev = W.device
-    codes = torch.empty((nblocks, block_elems(t)), dtype=torch.int16, device=dev)
-    sc = torch.empty((nblocks, 16), dtype=torch.int16, device=dev)
-    mins = torch.empty((nblocks, 16), dtype=torch.uint8, device=dev)
-    d = torch.empty(nblocks, dtype=torch.float32, device=dev)
-    dmin = torch.empty(nblocks, dtype=torch.float32, device=dev)
+    codes = _empty((nblocks, block_elems(t)), torch.int16, W, stream)
+    sc = _empty((nblocks, 16), torch.int16, W, stream)
+    mins = _empty((nblocks, 16), torch.uint8, W, stream)
+    d = _empty(nblocks, torch.float32, W, stream)
+    dmin = _empty(nblocks, torch.float32, W, stream)
     _check(load().qk_unpack(t, _ptr(W), nblocks, _ptr(codes), _ptr(sc), _ptr(mins), _ptr(d), _ptr(dmin),
                             _stream(stream)), "qk_unpack")
     return codes, sc, mins, d, dmin

@@ -157,9 +157,9 @@ def _empty(size, dtype, like, stream, kept: bool = True):
     while the call's kernels run.  kept: the caller gets the tensor and may use
     it on the current stream too."""
     import torch
+    if stream is None or not like.is_cuda:
+        return torch.empty(size, dtype=dtype, device=like.device)
     dev = like.device
-    if stream is None or dev.type != "cuda":
-        return torch.empty(size, dtype=dtype, device=dev)
     handle = _stream(stream)
     if handle == torch._C._cuda_getCurrentRawStream(dev.index):
         return torch.empty(size, dtype=dtype, device=dev)
@@ -318,7 +318,8 @@ def gemm(t: int, W, rows: int, cols: int, X, Y=None, ws=None, stream=None):
 
 # ------------------------------------- paged KV cache, tree attention, logits --
 # These calls are a few microseconds on the GPU, so their checks are kept to
-# what the C side cannot see: types, contiguity and element counts.
+# what the C side cannot see: types, contiguity, element counts and that the
+# memory is the GPU's.
 
 TREE_MAX = 64
 
@@ -332,19 +333,26 @@ def _dtype(x, what: str) -> int:
     raise QKError(8, what, f"dtype {name}: float32 or bfloat16 expected")
 
 
+def _on_gpu(x, what: str) -> None:
+    if not x.is_cuda:
+        raise QKError(8, what, f"a CUDA tensor expected, got one on {x.device}")
+
+
 def _rows(x, what: str) -> int:
-    """Elements from row to row of a tensor whose rows are contiguous."""
+    """Elements from row to row of a CUDA tensor whose rows are contiguous."""
     shape, strides = x.shape, x.stride()
     want = 1
     for i in range(len(shape) - 1, 0, -1):
         if strides[i] != want and shape[i] != 1:
             raise QKError(8, what, f"strides {strides} of shape {tuple(shape)}: contiguous rows expected")
         want *= shape[i]
+    if not x.is_cuda:
+        _on_gpu(x, what)
     return strides[0] if shape[0] > 1 else want
 
 
 def _of(x, dtype, what: str, n: int):
-    """Pointer of a contiguous array of n elements of the type the C call
+    """Pointer of a contiguous CUDA array of n elements of the type the C call
     reads; None for None."""
     if x is None:
         return None
@@ -352,6 +360,8 @@ def _of(x, dtype, what: str, n: int):
         raise QKError(8, what, f"contiguous {dtype} expected, got {x.dtype} with strides {x.stride()}")
     if x.numel() != n:
         raise QKError(2, what, f"{n} elements expected, got shape {tuple(x.shape)}")
+    if not x.is_cuda:
+        _on_gpu(x, what)
     return x.data_ptr()
 
 
@@ -461,6 +471,9 @@ def _attn_tree(name: str, first: tuple, t, q, K, V, page, n_kv, table, ctx, cu, 
     if ws is None:
         ws = _empty(max(L.qk_attn_tree_workspace(t, r, max_q, P * page, n_heads, n_kv, d), 16), torch.uint8, q, stream,
                     kept=False)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        _on_gpu(ws, w)
+        raise QKError(8, w, f"contiguous ws expected, got strides {ws.stride()}")
     _check(getattr(L, name)(*first, t, q.data_ptr(), n, _rows(q, w), K.data_ptr(), V.data_ptr(), pages, page,
                             _of(table, i32, w, r * P), P, _of(ctx, i32, w, r), _of(cu, i32, w, r + 1),
                             _of(mask, torch.int64, w, n), r, max_q, n_heads, n_kv, d, scale, out.data_ptr(), _rows(out, w),

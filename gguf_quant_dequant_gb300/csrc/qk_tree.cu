@@ -47,19 +47,29 @@
 // other blocks has zeros in theirs.  So a large block, hidden or not, leaves
 // the others' bits alone, and a tile without one costs nothing more.
 //
+// Roundings to fewer than 32 bits, besides the bf16 output: a cached value
+// (code * d has up to 19 bits) and a probability are fp16, 11 bits, because they
+// are operands of the tensor cores, whose next wider type has half the rate and
+// takes twice the memory (shared memory is full); probabilities are lifted by
+// 2^7 so that those down to 2^-21 of the reference keep all 11 bits.
+// Scores, references, sums and O are fp32.  Relative to the 64-bit result the
+// error is 1.70e-3 to 1.72e-3 over the measured calls; rounding that result
+// to bf16 alone gives 1.66e-3 to 1.67e-3.
+//
 // Bounds and measurements (GB300, GPU time of a call in a replayed graph).  The
 // floor is the cache's bytes up to 80 (Q4_0) to 150 (Q8_0) rows a kv head, the
 // tensor rate above.  64 requests of 500 to 15,000 positions, Q8_0, 4 to 8
-// tokens, 32 / 8 heads of 128 (1.04 GB): 301 us, 3.47 TB/s, 51 % of the measured
-// copy rate; one request of 32,765 positions, 16 tokens (71 MB): 45 us, 23 %; 27
-// ragged Q4_0 requests in pages of 16 (121 MB): 113 us, 16 %; 64-token trees, 8
-// heads to a kv head, Q5_0, d = 64 (12.4 GFLOP): 108 us; one token over 212
-// positions: 11.6 us.  A copy of this kernel without decoding, softmax and
-// products (wrong results, only timed) took 192, 33, 92 and 60 us for the four
-// large ones, so copies and hand-overs are more than half of each.  A further
+// tokens, 32 / 8 heads of 128 (1.04 GB): 306 us, 3.41 TB/s, 50 % of the measured
+// copy rate; one request of 32,765 positions, 16 tokens (71 MB): 45 us, 24 %; 27
+// ragged Q4_0 requests in pages of 16 (121 MB): 111 us, 16 %; 64-token trees, 8
+// heads to a kv head, Q5_0, d = 64 (12.4 GFLOP): 104 us; one token over 212
+// positions: 11.7 us.  A copy of an earlier build (46, 114, 110 and 308 us) without
+// decoding, softmax and products, only timed, took 33, 92, 60 and 192 us for the
+// four large ones, so copies and hand-overs are more than half of each.  A further
 // tile of a long request costs its CTA 1.45 us; in a trace 15,000 clocks passed
-// from a unit's last tile to the next unit's first.  In the second case 62 % of
-// the issue slots were used while an SM was active, without local spills.
+// from a unit's last tile to the next unit's first.  Issue slots used while an SM
+// was active: 62 % (second case), 74 % (first: 1,935 instructions a scheduler and
+// tile, the ALU pipe 52 %), without local spills.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -447,14 +447,20 @@ qk_status qk_kv_compact(int type, void* K, void* V, int64_t n_pages, int page, i
  *   max_q  at least the most tokens of one request, at most QK_TREE_MAX;
  *          tokens past it are not computed.
  *   out    bf16 [n_tok, n_heads, d], out_stride elements from token to token,
- *          2-byte aligned; rows of no request are not written.
+ *          2-byte aligned, apart from the inputs; rows of no request are not
+ *          written.
  *   ws     at least qk_attn_tree_workspace(..) bytes, 16-byte aligned;
  *          max_pos = table_stride * page.
- * fp32 scores, softmax and sums.  Accuracy, with A the largest |scale| sum_e
- * |q_e K_te| of a visible position: |out - out_exact| <= 2^-8 |out_exact| +
- * (2^-10 (1 + A) + 2^-13) sum_t p_t |V[t]| + 2^-32 sum_t |V[t]|, and near
- * the rounding of the output in practice.  Cached K values beyond fp16's
- * range (|w| that rounds past 65504) give NaN for the tokens that see them.
+ * Cached values (code * d) and probabilities are rounded to fp16 as operands
+ * of the tensor cores; scores, softmax statistics and sums are fp32.
+ * Accuracy, with A the largest |scale| sum_e |q_e K_te| of a visible
+ * position: |out - out_exact| <= 2^-8 |out_exact| + (2^-10 (1 + A) + 2^-13)
+ * sum_t p_t |V[t]| + 2^-32 sum_t |V[t]|, and 2 to 4 % above the rounding of
+ * the output in practice.  qk_attn_decode, which keeps the codes exact and
+ * hands out fp32, has a bound that does not grow with A and takes less time
+ * for one token over one request's cache (32,000 positions, Q8_0, 32 / 8 heads
+ * of 128: 25 us against 36).  Cached K values beyond fp16's range (|w| that
+ * rounds past 65504) give NaN for the tokens that see them.
  * At most 64 query heads to a kv head, n_req up to 65,535.  n_tok == 0 or
  * n_req == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also when the
  * tables could hold about 2^31 tiles or more), QK_ERR_NULL, QK_ERR_ALIGN,
@@ -470,7 +476,9 @@ qk_status qk_attn_tree(int type, const void* q, int64_t n_tok, int64_t q_stride,
  * request r.  With c the number of times token v stands in the request's
  * history and among the row's drafted ancestors,
  *   y = x > 0 ? x / rep[r] : x * rep[r],  then  y - freq[r] * c - pres[r]   (c > 0; else y = x)
- *   y + bias of token v (if listed),
+ *   y + bias of token v (if listed; after the penalties, so that a bias shifts
+ *   the result by its own value whatever rep is: samplers that add biases to
+ *   the logits first differ for tokens that have both),
  *   -inf where the row's grammar bit of v is 0.
  *   logits [n_rows, vocab], dtype QK_OUT_F32 or QK_OUT_BF16, aligned to the
  *          element, row_stride elements from row to row; out likewise (its

@@ -76,6 +76,11 @@ SIGNATURES = {
                                          _int, _int, _int, _int, ctypes.c_float, _p, _i64, _p, _sz, _p]),
     "qk_logits_process": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _i64,
                                  _p, _p, _i64, _p, _i64, _p]),
+    "qk_norm_rope": (_int, [_p, _p, _int, _i64, _i64, _i64, _int, _int, _int, _p, _p, _p, ctypes.c_float, _p, _int, _int, _p, _p,
+                            _int, _i64, _i64, _p]),
+    "qk_kv_append_rope": (_int, [_int, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _int, _int, _int, _p, _p, _p, ctypes.c_float,
+                                 _p, _int, _int, _p, _p, _p, _i64, _int, _p, _i64, _p]),
+    "qk_verify_tree": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p]),
     "qk_unpack": (_int, [_int, _p, _i64, _p, _p, _p, _p, _p, _p]),
     "qk_device_status": (_int, [_p]),
     "qk_test_stalled_wait": (_int, [ctypes.c_uint32, _p]),
@@ -434,6 +439,71 @@ def kv_compact(t: int, K, V, page: int, n_kv: int, d: int, table, base, path, n_
                                 _stream_on(K, stream)), "qk_kv_compact")
 
 
+def _like_rows(out, n: int, h: int, d: int, dtype, like, stream, what: str):
+    if out is None:
+        return _empty((n, h, d), dtype, like, stream)
+    if out.dtype is not dtype or out.shape != (n, h, d):
+        raise QKError(2, what, f"{dtype} of shape {(n, h, d)} expected, got {out.dtype} of {tuple(out.shape)}")
+    return out
+
+
+def norm_rope(q, k, pos, freq, q_norm=None, k_norm=None, eps: float = 1e-6, pairs: bool = False, out_dtype=None, q_out=None,
+              k_out=None, stream=None):
+    """Norms of q and k heads and their rotation by position (qk_norm_rope): q
+    [n_tok, n_heads, d], k [n_tok, n_kv, d] fp32 or bf16 CUDA (rows
+    contiguous); pos int32 [n_tok], freq fp32 [rot / 2] (None: no rotation);
+    q_norm, k_norm fp32 [d] or None -> (q_out, k_out) of out_dtype (q's own by
+    default).  q or k may be None."""
+    import torch
+    w, f32 = "norm_rope", torch.float32
+    x = q if q is not None else k
+    if x is None:
+        raise QKError(4, w, "q or k expected")
+    n, _, d = x.shape
+    hq, hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    if q is not None and k is not None and (k.dtype is not q.dtype or k.shape[0] != n or k.shape[2] != d):
+        raise QKError(2, w, "q and k differ in type, tokens or width")
+    out_dtype = out_dtype or x.dtype
+    if q is not None:
+        q_out = _like_rows(q_out, n, hq, d, out_dtype, x, stream, w)
+    if k is not None:
+        k_out = _like_rows(k_out, n, hk, d, out_dtype, x, stream, w)
+    y = q_out if q is not None else k_out
+    rot = 0 if freq is None else 2 * freq.shape[0]
+    _check(load().qk_norm_rope(
+        _ptr(q), _ptr(k), _dtype(x, w), n, 0 if q is None else _rows(q, w), 0 if k is None else _rows(k, w), hq, hk, d,
+        _of(pos, torch.int32, w, n) if rot else None, _of(q_norm, f32, w, d), _of(k_norm, f32, w, d), eps, _of(freq, f32, w, rot // 2),
+        rot, pairs, None if q is None else q_out.data_ptr(), None if k is None else k_out.data_ptr(), _dtype(y, w),
+        0 if q is None else _rows(q_out, w), 0 if k is None else _rows(k_out, w), _stream_on(x, stream)), "qk_norm_rope")
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+def kv_append_rope(t: int, q, k, v, pos, freq, slots, K, V, page: int, q_norm=None, k_norm=None, eps: float = 1e-6,
+                   pairs: bool = False, q_out=None, stream=None):
+    """norm_rope on the way into the paged cache (qk_kv_append_rope): k, v
+    [n_tok, n_kv, d] quantized into the uint8 pools K, V at slots int64 [n_tok],
+    keys normed and rotated; q [n_tok, n_heads, d] (or None) -> q_out bf16."""
+    import torch
+    w, f32 = "kv_append_rope", torch.float32
+    n, n_kv, d = k.shape
+    if v.shape != k.shape or v.dtype is not k.dtype:
+        raise QKError(2, w, "k and v differ in shape or type")
+    h = 0
+    if q is not None:
+        h = q.shape[1]
+        if q.dtype is not k.dtype or q.shape[0] != n or q.shape[2] != d:
+            raise QKError(2, w, "q and k differ in type, tokens or width")
+        q_out = _like_rows(q_out, n, h, d, torch.bfloat16, k, stream, w)
+    pages = _pool_pages(t, K, V, n_kv, d, page, w)
+    rot = 0 if freq is None else 2 * freq.shape[0]
+    _check(load().qk_kv_append_rope(
+        t, _ptr(q), k.data_ptr(), v.data_ptr(), _dtype(k, w), n, _rows(q, w) if h else 0, _rows(k, w), _rows(v, w), h, n_kv, d,
+        _of(pos, torch.int32, w, n) if rot else None, _of(q_norm, f32, w, d), _of(k_norm, f32, w, d), eps, _of(freq, f32, w, rot // 2),
+        rot, pairs, _of(slots, torch.int64, w, n), K.data_ptr(), V.data_ptr(), pages, page, q_out.data_ptr() if h else None,
+        _rows(q_out, w) if h else 0, _stream_on(k, stream)), "qk_kv_append_rope")
+    return q_out if q is not None else None
+
+
 def attn_tree_workspace(t: int, n_req: int, max_q: int, max_pos: int, n_heads: int, n_kv: int, d: int) -> int:
     return load().qk_attn_tree_workspace(t, n_req, max_q, max_pos, n_heads, n_kv, d)
 
@@ -505,6 +575,35 @@ def logits_process(logits, cu, hist, hist_len, rep, pres, freq, draft=None, mask
         _of(bias_val, f32, w, r * B) if B else None, B, _of(bias_len, i32, w, r) if B else None,
         _of(grammar, i32, w, n * words), words, out.data_ptr(), _rows(out, w), _stream_on(logits, stream)),
         "qk_logits_process")
+    return out
+
+
+def verify_tree(logits, cu, draft, mask, temp, u_accept, u_sample, probs=None, max_path: int = TREE_MAX, out=None,
+                stream=None) -> dict:
+    """Drafted trees judged against the target's probabilities (qk_verify_tree):
+    logits fp32 or bf16 CUDA [n_rows, vocab]; cu int32 [n_req + 1]; draft
+    int32, mask int64 (or None: chains), u_accept fp32 [n_rows]; temp, u_sample
+    fp32 [n_req]; probs fp32 [n_rows, vocab] or None -> {"path", "tokens" int32
+    [n_req, max_path], "n_path" int32 [n_req]}.  out: such a dict to be written
+    instead of new tensors."""
+    import torch
+    w, i32, f32 = "verify_tree", torch.int32, torch.float32
+    n, V = logits.shape
+    r = cu.shape[0] - 1
+    if probs is not None and (probs.dtype is not f32 or probs.shape != logits.shape):
+        raise QKError(2, w, "probs must be float32 of the logits' shape")
+    if out is None:
+        e = _empty(r * (2 * max_path + 1), i32, logits, stream)
+        a, b, c = e.split((r * max_path, r * max_path, r))
+        out = {"path": a.view(r, max_path), "tokens": b.view(r, max_path), "n_path": c}
+    elif out["path"].dim() != 2:
+        raise QKError(2, w, f"path of two dimensions expected, got shape {tuple(out['path'].shape)}")
+    P = out["path"].shape[1]
+    _check(load().qk_verify_tree(
+        logits.data_ptr(), _dtype(logits, w), n, V, _rows(logits, w), _of(cu, i32, w, r + 1), r, _of(draft, i32, w, n),
+        _of(mask, torch.int64, w, n), _of(temp, f32, w, r), _of(u_accept, f32, w, n), _of(u_sample, f32, w, r), _ptr(probs),
+        0 if probs is None else _rows(probs, w), _of(out["path"], i32, w, r * P), P, _of(out["n_path"], i32, w, r),
+        _of(out["tokens"], i32, w, r * P), _stream_on(logits, stream)), "qk_verify_tree")
     return out
 
 

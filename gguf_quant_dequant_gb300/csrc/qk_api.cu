@@ -619,6 +619,121 @@ qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64
     return QK_OK;
 }
 
+// Shared checks of the calls that norm and rotate heads.
+static qk_status check_rope(const void* q, const void* k, int dtype, int64_t n_tok, int64_t q_stride, int64_t k_stride, int n_heads,
+                            int n_kv, int d, const int32_t* pos, const float* q_norm, const float* k_norm, float eps,
+                            const float* freq, int rot) {
+    if (dtype != QK_OUT_F32 && dtype != QK_OUT_BF16) return fail(QK_ERR_ARG, "bad dtype %d", dtype);
+    if (!(eps >= 0.0f && eps <= 3.4e38f)) return fail(QK_ERR_ARG, "eps=%g: finite and not negative expected", eps);
+    if (d != 32 && d != 64 && d != 128 && d != 256) return fail(QK_ERR_SHAPE, "d=%d: 32, 64, 128 or 256 expected", d);
+    if (rot < 0 || rot > d || rot % 16 != 0) return fail(QK_ERR_SHAPE, "rot=%d: a multiple of 16 up to d expected", rot);
+    if (n_heads < 0 || n_heads > 65536 || n_kv < 0 || n_kv > 65536 || !count_ok(n_tok))
+        return fail(QK_ERR_SHAPE, "bad n_tok=%lld, n_heads=%d or n_kv=%d", (long long)n_tok, n_heads, n_kv);
+    if (n_tok == 0) return QK_OK;
+    if ((n_heads > 0 && (q_stride < (int64_t)n_heads * d || !count_ok(q_stride))) ||
+        (n_kv > 0 && (k_stride < (int64_t)n_kv * d || !count_ok(k_stride))))
+        return fail(QK_ERR_SHAPE, "bad strides q_stride=%lld k_stride=%lld", (long long)q_stride, (long long)k_stride);
+    if ((n_heads > 0 && !q) || (n_kv > 0 && !k) || (rot > 0 && (!pos || !freq)))
+        return fail(QK_ERR_NULL, "q, k, pos or freq is NULL");
+    const size_t es = dtype == QK_OUT_BF16 ? 2 : 4;
+    if ((n_heads > 0 && !aligned(q, es)) || (n_kv > 0 && !aligned(k, es)))
+        return fail(QK_ERR_ALIGN, "q and k must be aligned to their element");
+    for (const void* p : {(const void*)pos, (const void*)freq, (const void*)q_norm, (const void*)k_norm})
+        if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "pos, freq and the norms must be 4-byte aligned");
+    return QK_OK;
+}
+
+qk_status qk_norm_rope(const void* q, const void* k, int dtype, int64_t n_tok, int64_t q_stride, int64_t k_stride, int n_heads,
+                       int n_kv, int d, const int32_t* pos, const float* q_norm, const float* k_norm, float eps,
+                       const float* freq, int rot, int pairs, void* q_out, void* k_out, int out_dtype, int64_t qo_stride,
+                       int64_t ko_stride, void* stream) {
+    qk_status st = check_rope(q, k, dtype, n_tok, q_stride, k_stride, n_heads, n_kv, d, pos, q_norm, k_norm, eps, freq, rot);
+    if (st != QK_OK) return st;
+    if (out_dtype != QK_OUT_F32 && out_dtype != QK_OUT_BF16) return fail(QK_ERR_ARG, "bad out_dtype %d", out_dtype);
+    if (n_tok == 0 || (n_heads == 0 && n_kv == 0)) return QK_OK;
+    if ((n_heads > 0 && (qo_stride < (int64_t)n_heads * d || !count_ok(qo_stride))) ||
+        (n_kv > 0 && (ko_stride < (int64_t)n_kv * d || !count_ok(ko_stride))))
+        return fail(QK_ERR_SHAPE, "bad strides qo_stride=%lld ko_stride=%lld", (long long)qo_stride, (long long)ko_stride);
+    if ((n_heads > 0 && !q_out) || (n_kv > 0 && !k_out)) return fail(QK_ERR_NULL, "q_out or k_out is NULL");
+    const size_t eo = out_dtype == QK_OUT_BF16 ? 2 : 4;
+    if ((n_heads > 0 && !aligned(q_out, eo)) || (n_kv > 0 && !aligned(k_out, eo)))
+        return fail(QK_ERR_ALIGN, "q_out and k_out must be aligned to their element");
+    if ((n_heads > 0 && q_out == q && (qo_stride != q_stride || out_dtype != dtype)) ||
+        (n_kv > 0 && k_out == k && (ko_stride != k_stride || out_dtype != dtype)))
+        return fail(QK_ERR_ARG, "in place needs equal strides and types");
+    int sms = 0;
+    st = device_state(nullptr, &sms);
+    if (st != QK_OK) return st;
+    const qk::RopeArgs a{q, k, dtype == QK_OUT_BF16, n_tok, q_stride, k_stride, n_heads, n_kv, d, pos, q_norm, k_norm, eps,
+                         freq, rot, pairs != 0, q_out, qo_stride};
+    cudaError_t e = qk::launch_norm_rope(a, k_out, out_dtype == QK_OUT_BF16, ko_stride, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
+qk_status qk_kv_append_rope(int type, const void* q, const void* k, const void* v, int dtype, int64_t n_tok, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, int n_heads, int n_kv, int d, const int32_t* pos,
+                            const float* q_norm, const float* k_norm, float eps, const float* freq, int rot, int pairs,
+                            const int64_t* slots, void* K, void* V, int64_t n_pages, int page, void* q_out,
+                            int64_t q_out_stride, void* stream) {
+    qk_status st = check_pool(type, n_kv, d, page, n_pages, K, V);
+    if (st != QK_OK) return st;
+    st = check_rope(q, k, dtype, n_tok, q_stride, k_stride, n_heads, n_kv, d, pos, q_norm, k_norm, eps, freq, rot);
+    if (st != QK_OK) return st;
+    if (n_tok == 0) return QK_OK;
+    if (v_stride < (int64_t)n_kv * d || !count_ok(v_stride) ||
+        (n_heads > 0 && (q_out_stride < (int64_t)n_heads * d || !count_ok(q_out_stride))))
+        return fail(QK_ERR_SHAPE, "bad strides v_stride=%lld q_out_stride=%lld", (long long)v_stride, (long long)q_out_stride);
+    if (!v || !slots || (n_heads > 0 && !q_out)) return fail(QK_ERR_NULL, "v, slots or q_out is NULL");
+    if (!aligned(v, dtype == QK_OUT_BF16 ? 2 : 4) || !aligned(slots, 8) || (n_heads > 0 && !aligned(q_out, 2)))
+        return fail(QK_ERR_ALIGN, "v must be aligned to its element, slots to 8 bytes, q_out to 2");
+    if (n_heads > 0 && q_out == q && (q_out_stride != q_stride || dtype != QK_OUT_BF16))
+        return fail(QK_ERR_ARG, "in place needs equal strides and types");
+    unsigned* status = nullptr;
+    int sms = 0;
+    st = device_state(&status, &sms);
+    if (st != QK_OK) return st;
+    const qk::RopeArgs a{q, k, dtype == QK_OUT_BF16, n_tok, q_stride, k_stride, n_heads, n_kv, d, pos, q_norm, k_norm, eps,
+                         freq, rot, pairs != 0, q_out, q_out_stride};
+    cudaError_t e = qk::launch_kv_append_rope(type, a, v, v_stride, slots, static_cast<uint8_t*>(K), static_cast<uint8_t*>(V),
+                                              n_pages, page_log2(page), (int)qk_row_bytes(type, d), status, sms,
+                                              static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_kv_append_rope launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
+qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride, const int32_t* cu,
+                         int64_t n_req, const int32_t* draft, const uint64_t* mask, const float* temp, const float* u_accept,
+                         const float* u_sample, const float* probs, int64_t probs_stride, int32_t* path, int64_t path_stride,
+                         int32_t* n_path, int32_t* tokens, void* stream) {
+    if (dtype != QK_OUT_F32 && dtype != QK_OUT_BF16) return fail(QK_ERR_ARG, "bad dtype %d", dtype);
+    if (!count_ok(n_rows) || !count_ok(vocab) || vocab < 1 || n_req < 0 || n_req > (1 << 27))
+        return fail(QK_ERR_SHAPE, "bad n_rows=%lld, vocab=%lld or n_req=%lld", (long long)n_rows, (long long)vocab,
+                    (long long)n_req);
+    if (path_stride < 1 || !count_ok(path_stride)) return fail(QK_ERR_SHAPE, "bad path_stride=%lld", (long long)path_stride);
+    if (n_req == 0) return QK_OK;
+    if (row_stride < vocab || !count_ok(row_stride) || (probs && (probs_stride < vocab || !count_ok(probs_stride))))
+        return fail(QK_ERR_SHAPE, "bad strides row_stride=%lld probs_stride=%lld", (long long)row_stride, (long long)probs_stride);
+    if (!cu || !temp || !u_sample || !path || !n_path || !tokens || (n_rows > 0 && (!logits || !draft || !u_accept)))
+        return fail(QK_ERR_NULL, "NULL pointer argument");
+    if (!aligned(logits, dtype == QK_OUT_BF16 ? 2 : 4)) return fail(QK_ERR_ALIGN, "logits must be aligned to their element");
+    for (const void* p : {(const void*)cu, (const void*)draft, (const void*)temp, (const void*)u_accept, (const void*)u_sample,
+                          (const void*)probs, (const void*)path, (const void*)n_path, (const void*)tokens})
+        if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "the lists and probs must be 4-byte aligned");
+    if (!aligned(mask, 8)) return fail(QK_ERR_ALIGN, "mask must be 8-byte aligned");
+    int sms = 0;
+    const qk_status st = device_state(nullptr, &sms);
+    if (st != QK_OK) return st;
+    const qk::VerifyArgs a{logits, dtype == QK_OUT_BF16, n_rows, vocab, row_stride, cu, n_req, draft, mask, temp, u_accept,
+                           u_sample, probs, probs_stride, path, path_stride, n_path, tokens};
+    cudaError_t e = qk::launch_verify_tree(a, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_verify_tree launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
 qk_status qk_device_status(void* stream) {
     unsigned* status = nullptr;
     qk_status st = device_state(&status, nullptr);

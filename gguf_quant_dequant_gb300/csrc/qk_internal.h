@@ -107,6 +107,45 @@ struct LogitsArgs {
 };
 cudaError_t launch_logits_process(const LogitsArgs& a, int sms, cudaStream_t s);
 
+// Norms and rotation of heads (qk_rope.cu); the members are the arguments of
+// qk_norm_rope that qk_kv_append_rope has too.
+struct RopeArgs {
+    const void *q, *k;
+    bool bf16;
+    int64_t n_tok, q_stride, k_stride;
+    int n_heads, n_kv, d;
+    const int32_t* pos;
+    const float *q_norm, *k_norm;
+    float eps;
+    const float* freq;
+    int rot;
+    bool pairs;
+    void* q_out;
+    int64_t qo_stride;
+};
+cudaError_t launch_norm_rope(const RopeArgs& a, void* k_out, bool out16, int64_t ko_stride, int sms, cudaStream_t s);
+cudaError_t launch_kv_append_rope(int type, const RopeArgs& a, const void* v, int64_t v_stride, const int64_t* slots, uint8_t* K,
+                                  uint8_t* V, int64_t n_pages, int page_log2, int row_bytes, unsigned* status, int sms,
+                                  cudaStream_t s);
+
+// Drafted trees against the target's probabilities (qk_verify.cu); the members
+// are qk_verify_tree's arguments.
+struct VerifyArgs {
+    const void* logits;
+    bool bf16;
+    int64_t n_rows, vocab, row_stride;
+    const int32_t* cu;
+    int64_t n_req;
+    const int32_t* draft;
+    const uint64_t* mask;
+    const float *temp, *u_accept, *u_sample, *probs;
+    int64_t probs_stride;
+    int32_t* path;
+    int64_t path_stride;
+    int32_t *n_path, *tokens;
+};
+cudaError_t launch_verify_tree(const VerifyArgs& a, int sms, cudaStream_t s);
+
 // One thread waiting on an mbarrier nothing arrives on (bounded by limit_ns).
 cudaError_t launch_stalled_wait(unsigned* status, uint64_t limit_ns, cudaStream_t s);
 

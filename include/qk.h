@@ -409,6 +409,56 @@ qk_status qk_kv_plan(const int32_t* have, const int32_t* start, const int32_t* w
 qk_status qk_kv_append(int type, const void* k, const void* v, int dtype, int64_t n_tok, int64_t k_stride, int64_t v_stride,
                        int n_kv, int d, const int64_t* slots, void* K, void* V, int64_t n_pages, int page, void* stream);
 
+/* Norms of query and key heads with the position rotation in the same pass:
+ * rows in, rows out.  For a head x [d] of token i,
+ *   y = (x * inv) * w,  inv = 1 / sqrt(sum_e x_e^2 / d + eps)   (w given; else y = x)
+ *   a = pos[i] * freq[j],  j < rot / 2:
+ *   (y_p, y_q) -> (y_p cos a - y_q sin a, y_q cos a + y_p sin a)
+ * with (p, q) = (j, j + rot / 2), or (2j, 2j + 1) when pairs is non-zero; the
+ * elements from rot on are not turned.
+ *   q [n_tok, n_heads, d], k [n_tok, n_kv, d], dtype QK_OUT_F32 or
+ *          QK_OUT_BF16, aligned to the element; q_stride and k_stride elements
+ *          from token to token, so that slices of a fused projection's output
+ *          serve as they are.  n_heads or n_kv may be 0 (that pointer is then
+ *          ignored).
+ *   d      32, 64, 128 or 256; rot a multiple of 16, 0 .. d (0: no rotation;
+ *          pos and freq are then ignored).
+ *   pos    int32 [n_tok], any value; freq fp32 [rot / 2], angle per position
+ *          (frequency scaling of any kind goes in here).  A frequency that is
+ *          not finite, or 2^64 and more, gives NaN.
+ *   q_norm, k_norm fp32 [d] or NULL (no norm); eps >= 0 and finite.
+ *   q_out, k_out like q and k with their own strides, of out_dtype, aligned to
+ *          the element.  In place (the same pointer, stride and type) is fine,
+ *          any other overlap is not.
+ * Rows on 16-byte boundaries are read and written faster.
+ * Every square, sum, quotient, root and product above is rounded to fp32 by
+ * itself, the squares are added by neighbours (x0^2 + x1^2, .., then those
+ * sums by neighbours), and cos and sin are the fp32 nearest to their exact
+ * values, up to one value in some ten thousand that is the next one: angles are
+ * kept to 2^-96 of a turn, so far positions lose nothing.  Results are then
+ * rounded once to out_dtype.
+ * n_tok == 0, or no heads, queues nothing.  Errors: QK_ERR_SHAPE, QK_ERR_NULL,
+ * QK_ERR_ALIGN, QK_ERR_ARG (dtype, eps). */
+qk_status qk_norm_rope(const void* q, const void* k, int dtype, int64_t n_tok, int64_t q_stride, int64_t k_stride, int n_heads,
+                       int n_kv, int d, const int32_t* pos, const float* q_norm, const float* k_norm, float eps,
+                       const float* freq, int rot, int pairs, void* q_out, void* k_out, int out_dtype, int64_t qo_stride,
+                       int64_t ko_stride, void* stream);
+
+/* qk_norm_rope on the way into the paged cache, and qk_kv_append, in one
+ * launch: keys normed, rotated and quantized into their slots, values
+ * quantized, queries normed, rotated and written as bf16 for qk_attn_tree.
+ * Arguments as those two calls'; the cached bytes are those that qk_kv_append
+ * writes for qk_norm_rope's fp32 keys.  pos is the position that a token is
+ * rotated by (in a drafted tree its depth after the text), apart from the
+ * place that slots gives its row.  n_heads == 0: no queries.
+ *   q_out  bf16 [n_tok, n_heads, d], q_out_stride elements from token to token.
+ * Errors: those of the two calls. */
+qk_status qk_kv_append_rope(int type, const void* q, const void* k, const void* v, int dtype, int64_t n_tok, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, int n_heads, int n_kv, int d, const int32_t* pos,
+                            const float* q_norm, const float* k_norm, float eps, const float* freq, int rot, int pairs,
+                            const int64_t* slots, void* K, void* V, int64_t n_pages, int page, void* q_out,
+                            int64_t q_out_stride, void* stream);
+
 /* Keep the accepted path of each request's drafted tree: the rows at
  * positions base[r] + path[r * path_stride + j] move to base[r] + j, for j <
  * n_path[r], in both pools, as if all were read before any is written.
@@ -507,6 +557,49 @@ qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64
                             const int32_t* draft, const uint64_t* mask, const int32_t* bias_tok, const float* bias_val,
                             int64_t bias_stride, const int32_t* bias_len, const uint32_t* grammar, int64_t grammar_stride,
                             void* out, int64_t out_stride, void* stream);
+
+/* Drafted trees judged against the target's probabilities, from given random
+ * numbers: the accepted path of every request (as qk_kv_compact wants it), its
+ * tokens, and one token more.  Rows cu[r] .. cu[r + 1] - 1 of the logits are
+ * the nodes of request r's tree, as in qk_attn_tree and qk_logits_process; row
+ * i of them predicts what follows node i.  Node 0 is the root (a token that
+ * stands already), the parent of another node is its nearest ancestor: the
+ * highest bit of its mask below its own (mask NULL: a chain).  Nodes without an
+ * ancestor, and nodes past QK_TREE_MAX of a request, are never reached.
+ * With e_v = exp((x_v - max x) / temp[r]) for the logits x of the node that the
+ * path has reached (fp32; sums and comparisons in 64 bits), its children are
+ * tried by rising index; child c with token y = draft[c] is taken when
+ *   u_accept[c] * q_y * sum_v W_v < W_y,
+ * probs NULL (drafts picked without probabilities): q = 1, and W = e without
+ *   the tokens of the children refused before;
+ * probs given: q = the node's row of probs, the probabilities that its
+ *   children were drawn from (each on its own), and W_v = max(e_v - tau q_v, 0)
+ *   with tau (as fp32) the sum of the sums of W at the refusals before.
+ * Where none is taken, the token after the path is the first v with
+ * sum_{v' <= v} W_v' > u_sample[r] * sum W (of e, where W has nothing left).  So
+ * with u uniform in [0, 1) the tokens are distributed as the target's, whatever
+ * was drafted.  A temperature below 2^-20 (or NaN) is greedy: the child that
+ * carries the largest logit's token (the lowest of equals), and that token at
+ * the end.
+ *   logits [n_rows, vocab], dtype QK_OUT_F32 or QK_OUT_BF16, aligned to the
+ *          element, row_stride elements from row to row.  NaN counts as -inf; a
+ *          row with +inf has its mass there; a row of -inf only gives the
+ *          token -1 and no child.
+ *   draft  int32 [n_rows]; tokens outside 0 .. vocab - 1 are refused.
+ *   probs  fp32 [n_rows, vocab], probs_stride elements from row to row, or NULL.
+ *   temp, u_sample fp32 [n_req]; u_accept fp32 [n_rows].
+ *   path   int32 [n_req, path_stride]: the path's nodes from the root on;
+ *          tokens int32, the same shape: the tokens of path[1], path[2], .. and
+ *          the token after the path; n_path int32 [n_req] of each (0 for a
+ *          request without rows); entries behind them are -1.  A path ends at
+ *          path_stride nodes (the last one's children are then not tried).
+ * Deterministic.  n_req == 0 queues nothing.  n_req is at most 2^27.
+ * Errors: QK_ERR_SHAPE (also vocab or path_stride below 1), QK_ERR_NULL,
+ * QK_ERR_ALIGN, QK_ERR_ARG. */
+qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride, const int32_t* cu,
+                         int64_t n_req, const int32_t* draft, const uint64_t* mask, const float* temp, const float* u_accept,
+                         const float* u_sample, const float* probs, int64_t probs_stride, int32_t* path, int64_t path_stride,
+                         int32_t* n_path, int32_t* tokens, void* stream);
 
 /* Test hook: unpack nblocks consecutive blocks into their integer fields.
  *   codes int16 [nblocks * block_elems]: Q4_K 0..15, Q5_K 0..31, Q6_K 0..63,

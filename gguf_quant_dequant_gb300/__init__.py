@@ -81,6 +81,9 @@ SIGNATURES = {
     "qk_kv_append_rope": (_int, [_int, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _int, _int, _int, _p, _p, _p, ctypes.c_float,
                                  _p, _int, _int, _p, _p, _p, _i64, _int, _p, _i64, _p]),
     "qk_verify_tree": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p]),
+    "qk_moe_workspace": (_sz, [_i64, _int, _int, _i64]),
+    "qk_moe_ffn": (_int, [_int, _p, _p, _int, _p, _int, _i64, _i64, _p, _int, _int, ctypes.c_float, _p, _i64, _p, _p, _p, _p,
+                          _sz, _p]),
     "qk_unpack": (_int, [_int, _p, _i64, _p, _p, _p, _p, _p, _p]),
     "qk_device_status": (_int, [_p]),
     "qk_test_stalled_wait": (_int, [ctypes.c_uint32, _p]),
@@ -576,6 +579,44 @@ def logits_process(logits, cu, hist, hist_len, rep, pres, freq, draft=None, mask
         _of(grammar, i32, w, n * words), words, out.data_ptr(), _rows(out, w), _stream_on(logits, stream)),
         "qk_logits_process")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def moe_workspace(n_tok: int, k: int, n_exp: int, rows: int) -> int:
+    return load().qk_moe_workspace(n_tok, k, n_exp, rows)
+
+
+def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x, k: int, router=None, norm: bool = True,
+            scale: float = 1.0, ids=None, gate=None, out=None, ws=None, stream=None):
+    """A mixture-of-experts layer (qk_moe_ffn): packed uint8 Wg, Wu [n_exp,
+    rows, cols] of type t, Wd [n_exp, cols, rows] of type t_down; x fp32 CUDA
+    [n_tok, cols]; router fp32 [n_exp, cols], or None with ids int32 and gate
+    fp32 [n_tok, k] given -> (out fp32 [n_tok, cols], ids, gate)."""
+    import torch
+    w, i32, f32 = "moe_ffn", torch.int32, torch.float32
+    n = x.shape[0]
+    up, down = n_exp * rows * row_bytes(t, cols), n_exp * cols * row_bytes(t_down, rows)
+    if not (up and down):
+        raise QKError(2, w, f"no packed experts of n_exp={n_exp}, rows={rows}, cols={cols} in types {t}, {t_down}")
+    if router is None and (ids is None or gate is None):
+        raise QKError(4, w, "a router, or ids and gate, expected")
+    if ids is None:
+        ids = _empty((n, k), i32, x, stream)
+    if gate is None:
+        gate = _empty((n, k), f32, x, stream)
+    if out is None:
+        out = _empty((n, cols), f32, x, stream)
+    if ws is None:
+        ws = _empty(max(moe_workspace(n, k, n_exp, rows), 16), torch.uint8, x, stream, kept=False)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        _on_gpu(ws, w)
+        raise QKError(8, w, f"contiguous ws expected, got strides {ws.stride()}")
+    u8 = torch.uint8
+    _check(load().qk_moe_ffn(t, _of(Wg, u8, w, up), _of(Wu, u8, w, up), t_down, _of(Wd, u8, w, down), n_exp, rows, cols,
+                             _of(router, f32, w, n_exp * cols), k, norm, scale, _of(x, f32, w, n * cols), n, _of(ids, i32, w, n * k),
+                             _of(gate, f32, w, n * k), _of(out, f32, w, n * cols), ws.data_ptr(), ws.numel() * ws.element_size(),
+                             _stream_on(x, stream)), "qk_moe_ffn")
+    return out, ids, gate
 
 
 def verify_tree(logits, cu, draft, mask, temp, u_accept, u_sample, probs=None, max_path: int = TREE_MAX, out=None,

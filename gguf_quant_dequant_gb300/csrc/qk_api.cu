@@ -734,6 +734,44 @@ qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t 
     return QK_OK;
 }
 
+static bool moe_shape_ok(int64_t n_tok, int k, int n_exp, int64_t rows) {
+    return n_tok >= 0 && n_tok <= QK_MOE_MAX_TOK && n_exp >= 1 && n_exp <= QK_MOE_MAX_EXP && k >= 1 && k <= QK_MOE_MAX_K &&
+           k <= n_exp && rows >= 1 && rows <= (1 << 18);
+}
+
+size_t qk_moe_workspace(int64_t n_tok, int k, int n_exp, int64_t rows) {
+    return moe_shape_ok(n_tok, k, n_exp, rows) ? (size_t)qk::moe_ws_bytes((int)n_tok, k, n_exp, rows) : 0;
+}
+
+qk_status qk_moe_ffn(int type, const void* Wg, const void* Wu, int type_down, const void* Wd, int n_exp, int64_t rows,
+                     int64_t cols, const float* router, int k, int norm, float scale, const float* x, int64_t n_tok,
+                     int32_t* ids, float* gate, float* out, void* ws, size_t ws_bytes, void* stream) {
+    if (!known_type(type) || !known_type(type_down)) return fail(QK_ERR_TYPE, "unknown quant type %d or %d", type, type_down);
+    if (!moe_shape_ok(n_tok, k, n_exp, rows) || cols < 1 || cols > (1 << 18) || cols % block_elems(type) != 0 ||
+        rows % block_elems(type_down) != 0)
+        return fail(QK_ERR_SHAPE, "bad expert layer n_tok=%lld k=%d n_exp=%d rows=%lld cols=%lld", (long long)n_tok, k, n_exp,
+                    (long long)rows, (long long)cols);
+    if (router && !(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(QK_ERR_ARG, "scale=%g: finite expected", scale);
+    if (n_tok == 0) return QK_OK;
+    if (!Wg || !Wu || !Wd || !x || !ids || !gate || !out || !ws) return fail(QK_ERR_NULL, "NULL pointer argument");
+    for (const void* p : {Wg, Wu, Wd, (const void*)router, (const void*)x, (const void*)ws})
+        if (!aligned(p, 16)) return fail(QK_ERR_ALIGN, "the weights, router, x and ws must be 16-byte aligned");
+    for (const void* p : {(const void*)ids, (const void*)gate, (const void*)out})
+        if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "ids, gate and out must be 4-byte aligned");
+    const size_t need = qk_moe_workspace(n_tok, k, n_exp, rows);
+    if (ws_bytes < need) return fail(QK_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    unsigned* status = nullptr;
+    int sms = 0;
+    const qk_status st = device_state(&status, &sms);
+    if (st != QK_OK) return st;
+    const qk::MoeArgs a{type, Wg, Wu, type_down, Wd, n_exp, rows, cols, router, k, norm != 0, scale, x, (int)n_tok, ids, gate,
+                        out, ws};
+    const cudaError_t e = qk::launch_moe_ffn(a, status, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_moe_ffn launch");
+    g_last_error.clear();
+    return QK_OK;
+}
+
 qk_status qk_device_status(void* stream) {
     unsigned* status = nullptr;
     qk_status st = device_state(&status, nullptr);

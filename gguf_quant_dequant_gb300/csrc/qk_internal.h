@@ -146,6 +146,28 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify_tree(const VerifyArgs& a, int sms, cudaStream_t s);
 
+// A mixture-of-experts layer (qk_moe.cu); the members are qk_moe_ffn's
+// arguments.
+struct MoeArgs {
+    int type;
+    const void *Wg, *Wu;
+    int type_down;
+    const void* Wd;
+    int n_exp;
+    int64_t rows, cols;
+    const float* router;
+    int k;
+    bool norm;
+    float scale;
+    const float* x;
+    int n_tok;
+    int32_t* ids;
+    float *gate, *out;
+    void* ws;
+};
+int64_t moe_ws_bytes(int n_tok, int k, int n_exp, int64_t rows);
+cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStream_t s);
+
 // One thread waiting on an mbarrier nothing arrives on (bounded by limit_ns).
 cudaError_t launch_stalled_wait(unsigned* status, uint64_t limit_ns, cudaStream_t s);
 

@@ -226,6 +226,42 @@ qk_status qk_quantize_imatrix(int type, const float* w, int64_t rows, int64_t co
 qk_status qk_gemv_swiglu(int type, const void* Wg, const void* Wu, int64_t rows, int64_t cols,
                          const float* x, float* h, void* stream);
 
+/* Most tokens, experts per token and experts of a qk_moe_ffn call. */
+#define QK_MOE_MAX_TOK 64
+#define QK_MOE_MAX_K 16
+#define QK_MOE_MAX_EXP 512
+
+/* A mixture-of-experts layer for a few tokens (a decode batch, a drafted
+ * tree), over packed expert weights:
+ *   l = R x [n_exp],  the k largest of l (of equals the lowest index),
+ *   gate_j = scale * exp(l_j) / sum exp(l)   over the k chosen (norm) or over
+ *            all experts (norm == 0),
+ *   out = sum_j gate_j * Wd_j (SiLU(Wg_j x) * (Wu_j x))   over the chosen.
+ *   type, Wg, Wu  packed blocks [n_exp, rows, cols], one type for both;
+ *   type_down, Wd packed blocks [n_exp, cols, rows] of any type; 16-byte
+ *          aligned (the layouts of a GGUF file's expert tensors).
+ *   router fp32 [n_exp, cols], 16-byte aligned; ids and gate are then written.
+ *          NULL: ids and gate are given (any other router); a pair whose id is
+ *          outside 0 .. n_exp - 1 adds nothing, an id that a token has twice
+ *          counts twice.  norm and scale are then ignored.
+ *   x      fp32 [n_tok, cols], 16-byte aligned; n_tok 0 .. QK_MOE_MAX_TOK.
+ *   ids    int32 [n_tok, k], gate fp32 [n_tok, k], by falling logit; k 1 ..
+ *          QK_MOE_MAX_K and at most n_exp.
+ *   out    fp32 [n_tok, cols], apart from x; fully overwritten.
+ *   ws     at least qk_moe_workspace(..) bytes, 16-byte aligned.
+ * Every expert that some token chose is read once (in groups of eight of its
+ * tokens).  Two launches, three with a router.  Accuracy: each product as
+ * qk_gemv's (1e-4 * sum |w x| + 1e-6 of its own inputs), the SiLU and the sum
+ * over experts in fp32; the router's logits are fp32 sums.  A logit that is
+ * NaN gives NaN gates for its token.  Deterministic.
+ * n_tok == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also rows or
+ * cols below 1 or above 2^18), QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG (scale
+ * not finite), QK_ERR_WORKSPACE. */
+size_t qk_moe_workspace(int64_t n_tok, int k, int n_exp, int64_t rows);
+qk_status qk_moe_ffn(int type, const void* Wg, const void* Wu, int type_down, const void* Wd, int n_exp, int64_t rows,
+                     int64_t cols, const float* router, int k, int norm, float scale, const float* x, int64_t n_tok,
+                     int32_t* ids, float* gate, float* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Workspace bytes qk_gemv needs for this problem: 0 for every shape (the
  * kernel prepares its activations in shared memory).  Kept so that callers
  * written against a workspace-taking GEMV need no change. */

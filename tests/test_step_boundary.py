@@ -114,3 +114,40 @@ def test_signatures_are_the_header_s(lib):
     assert ctypes.sizeof(ctypes.c_void_p) == 8
     for name, n in (("qk_norm_rope", len(ROPE)), ("qk_kv_append_rope", len(APPEND)), ("qk_verify_tree", len(VERIFY))):
         assert len(qk.SIGNATURES[name][1]) == n
+
+
+MOE = dict(type=qk.Q4_K, Wg=F, Wu=F, type_down=qk.Q6_K, Wd=F, n_exp=8, rows=512, cols=256, router=F, k=2, norm=1, scale=1.0, x=F,
+           n_tok=3, ids=F, gate=F, out=F, ws=F, ws_bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(type=0), TYPE), (dict(type_down=9), TYPE), (dict(n_exp=0), SHAPE), (dict(n_exp=513), SHAPE), (dict(k=0), SHAPE),
+    (dict(k=9), SHAPE), (dict(n_exp=64, k=17), SHAPE), (dict(rows=0), SHAPE), (dict(rows=500), SHAPE), (dict(cols=300), SHAPE),
+    (dict(cols=0), SHAPE), (dict(rows=(1 << 18) + 256), SHAPE), (dict(cols=(1 << 18) + 256), SHAPE), (dict(n_tok=65), SHAPE),
+    (dict(n_tok=-1), SHAPE), (dict(scale=float("nan")), ARG), (dict(Wg=None), NULL), (dict(Wu=None), NULL), (dict(Wd=None), NULL),
+    (dict(x=None), NULL), (dict(ids=None), NULL), (dict(gate=None), NULL), (dict(out=None), NULL), (dict(ws=None), NULL),
+    (dict(Wg=F + 8), ALIGN), (dict(router=F + 4), ALIGN), (dict(x=F + 8), ALIGN), (dict(ws=F + 8), ALIGN), (dict(ids=F + 2), ALIGN),
+    (dict(out=F + 1), ALIGN), (dict(ws_bytes=100), 5)])
+def test_moe_ffn_refusals(lib, kw, status):
+    assert call(lib.qk_moe_ffn, MOE, **kw) == status
+    assert lib.qk_last_error()
+
+
+def test_moe_sizes_and_binding_refusals(lib):
+    assert len(qk.SIGNATURES["qk_moe_ffn"][1]) == len(MOE)
+    assert qk.moe_workspace(3, 2, 8, 512) >= 3 * 2 * 512 * 4 + 3 * 8 * 4
+    assert qk.moe_workspace(65, 2, 8, 512) == 0 and qk.moe_workspace(3, 9, 8, 512) == 0
+    assert call(lib.qk_moe_ffn, MOE, n_tok=0, x=None, ws=None, ws_bytes=0) == 0
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    up, down, x = 2 * 512 * 144, 2 * 256 * 420, torch.zeros((3, 256))
+    args = (qk.Q4_K, u8(up), u8(up), qk.Q6_K, u8(down), 2, 512, 256)
+
+    def refused(status, *a, **kw):
+        with pytest.raises(qk.QKError) as e:
+            qk.moe_ffn(*a, **kw)
+        assert e.value.status == status, e.value
+
+    refused(4, *args, x, 2)
+    refused(2, *args[:6], 500, 256, x, 2, router=torch.zeros((2, 256)))
+    refused(2, qk.Q4_K, u8(up - 1), *args[2:], x, 2, router=torch.zeros((2, 256)))
+    refused(8, *args, x, 2, router=torch.zeros((2, 256)))          # host tensors

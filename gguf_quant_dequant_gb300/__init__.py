@@ -81,7 +81,7 @@ SIGNATURES = {
     "qk_kv_append_rope": (_int, [_int, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _int, _int, _int, _p, _p, _p, ctypes.c_float,
                                  _p, _int, _int, _p, _p, _p, _i64, _int, _p, _i64, _p]),
     "qk_verify_tree": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p]),
-    "qk_moe_workspace": (_sz, [_i64, _int, _int, _i64]),
+    "qk_moe_workspace": (_sz, [_int, _int, _int, _i64, _i64, _int, _i64]),
     "qk_moe_ffn": (_int, [_int, _p, _p, _int, _p, _int, _i64, _i64, _p, _int, _int, ctypes.c_float, _p, _i64, _p, _p, _p, _p,
                           _sz, _p]),
     "qk_unpack": (_int, [_int, _p, _i64, _p, _p, _p, _p, _p, _p]),
@@ -582,8 +582,8 @@ def logits_process(logits, cu, hist, hist_len, rep, pres, freq, draft=None, mask
 
 
 @functools.lru_cache(maxsize=256)
-def moe_workspace(n_tok: int, k: int, n_exp: int, rows: int) -> int:
-    return load().qk_moe_workspace(n_tok, k, n_exp, rows)
+def moe_workspace(t: int, t_down: int, n_exp: int, rows: int, cols: int, k: int, n_tok: int) -> int:
+    return load().qk_moe_workspace(t, t_down, n_exp, rows, cols, k, n_tok)
 
 
 def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x, k: int, router=None, norm: bool = True,
@@ -607,7 +607,7 @@ def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x
     if out is None:
         out = _empty((n, cols), f32, x, stream)
     if ws is None:
-        ws = _empty(max(moe_workspace(n, k, n_exp, rows), 16), torch.uint8, x, stream, kept=False)
+        ws = _empty(max(moe_workspace(t, t_down, n_exp, rows, cols, k, n), 16), torch.uint8, x, stream, kept=False)
     elif not (ws.is_cuda and ws.is_contiguous()):
         _on_gpu(ws, w)
         raise QKError(8, w, f"contiguous ws expected, got strides {ws.stride()}")

@@ -734,21 +734,35 @@ qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t 
     return QK_OK;
 }
 
-static bool moe_shape_ok(int64_t n_tok, int k, int n_exp, int64_t rows) {
+static bool moe_shape_ok(int type, int type_down, int64_t n_tok, int k, int n_exp, int64_t rows, int64_t cols) {
     return n_tok >= 0 && n_tok <= QK_MOE_MAX_TOK && n_exp >= 1 && n_exp <= QK_MOE_MAX_EXP && k >= 1 && k <= QK_MOE_MAX_K &&
-           k <= n_exp && rows >= 1 && rows <= (1 << 18);
+           k <= n_exp && rows >= 1 && rows <= (1 << 18) && rows % block_elems(type_down) == 0 && cols >= 1 && cols <= (1 << 18) &&
+           cols % block_elems(type) == 0;
 }
 
-size_t qk_moe_workspace(int64_t n_tok, int k, int n_exp, int64_t rows) {
-    return moe_shape_ok(n_tok, k, n_exp, rows) ? (size_t)qk::moe_ws_bytes((int)n_tok, k, n_exp, rows) : 0;
+static qk::MoeArgs moe_args(int type, int type_down, int n_exp, int64_t rows, int64_t cols, int k, int64_t n_tok) {
+    qk::MoeArgs a{};
+    a.type = type;
+    a.type_down = type_down;
+    a.n_exp = n_exp;
+    a.rows = rows;
+    a.cols = cols;
+    a.k = k;
+    a.n_tok = (int)n_tok;
+    return a;
+}
+
+size_t qk_moe_workspace(int type, int type_down, int n_exp, int64_t rows, int64_t cols, int k, int64_t n_tok) {
+    if (!known_type(type) || !known_type(type_down) || !moe_shape_ok(type, type_down, n_tok, k, n_exp, rows, cols) || n_tok == 0)
+        return 0;
+    return (size_t)qk::moe_ws_bytes(moe_args(type, type_down, n_exp, rows, cols, k, n_tok), sm_count_or_default());
 }
 
 qk_status qk_moe_ffn(int type, const void* Wg, const void* Wu, int type_down, const void* Wd, int n_exp, int64_t rows,
                      int64_t cols, const float* router, int k, int norm, float scale, const float* x, int64_t n_tok,
                      int32_t* ids, float* gate, float* out, void* ws, size_t ws_bytes, void* stream) {
     if (!known_type(type) || !known_type(type_down)) return fail(QK_ERR_TYPE, "unknown quant type %d or %d", type, type_down);
-    if (!moe_shape_ok(n_tok, k, n_exp, rows) || cols < 1 || cols > (1 << 18) || cols % block_elems(type) != 0 ||
-        rows % block_elems(type_down) != 0)
+    if (!moe_shape_ok(type, type_down, n_tok, k, n_exp, rows, cols))
         return fail(QK_ERR_SHAPE, "bad expert layer n_tok=%lld k=%d n_exp=%d rows=%lld cols=%lld", (long long)n_tok, k, n_exp,
                     (long long)rows, (long long)cols);
     if (router && !(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(QK_ERR_ARG, "scale=%g: finite expected", scale);
@@ -758,14 +772,24 @@ qk_status qk_moe_ffn(int type, const void* Wg, const void* Wu, int type_down, co
         if (!aligned(p, 16)) return fail(QK_ERR_ALIGN, "the weights, router, x and ws must be 16-byte aligned");
     for (const void* p : {(const void*)ids, (const void*)gate, (const void*)out})
         if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "ids, gate and out must be 4-byte aligned");
-    const size_t need = qk_moe_workspace(n_tok, k, n_exp, rows);
-    if (ws_bytes < need) return fail(QK_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     unsigned* status = nullptr;
     int sms = 0;
+    const size_t need = qk_moe_workspace(type, type_down, n_exp, rows, cols, k, n_tok);
+    if (ws_bytes < need) return fail(QK_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     const qk_status st = device_state(&status, &sms);
     if (st != QK_OK) return st;
-    const qk::MoeArgs a{type, Wg, Wu, type_down, Wd, n_exp, rows, cols, router, k, norm != 0, scale, x, (int)n_tok, ids, gate,
-                        out, ws};
+    qk::MoeArgs a = moe_args(type, type_down, n_exp, rows, cols, k, n_tok);
+    a.Wg = Wg;
+    a.Wu = Wu;
+    a.Wd = Wd;
+    a.router = router;
+    a.norm = norm != 0;
+    a.scale = scale;
+    a.x = x;
+    a.ids = ids;
+    a.gate = gate;
+    a.out = out;
+    a.ws = ws;
     const cudaError_t e = qk::launch_moe_ffn(a, status, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "qk_moe_ffn launch");
     g_last_error.clear();

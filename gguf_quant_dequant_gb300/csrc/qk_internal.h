@@ -165,7 +165,7 @@ struct MoeArgs {
     float *gate, *out;
     void* ws;
 };
-int64_t moe_ws_bytes(int n_tok, int k, int n_exp, int64_t rows);
+int64_t moe_ws_bytes(const MoeArgs& m, int sms);   // types, sizes and n_tok only
 cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStream_t s);
 
 // One thread waiting on an mbarrier nothing arrives on (bounded by limit_ns).

@@ -57,50 +57,110 @@ static cudaError_t route(const float* x, const float* router, int64_t cols, int 
     return cudaLaunchKernelEx(&cfg, route_kernel<TT>, x, router, cols, n_tok, n_exp, logits);
 }
 
+// out[tok] = sum over the token's experts of gate * y, y the slices' sums added
+// in order.  Everything comes from L2: 61 tokens of 8 experts of 2048 rows read
+// 4 MB.
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids,
+                                                          const float* __restrict__ gate, int n_exp, int n_tok, int k, int64_t cols,
+                                                          int slices, float* __restrict__ out) {
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int64_t c = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) * 4;
+    const int tok = blockIdx.y;
+    if (c >= cols) return;
+    const int64_t slice = (int64_t)n_tok * k * cols;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int j = 0; j < k; ++j) {
+        const int pair = tok * k + j, e = __ldcg(ids + pair);
+        if (e < 0 || e >= n_exp) continue;   // nothing was written for it
+        const float g = __ldcg(gate + pair);
+        const float* src = y + (int64_t)pair * cols + c;
+        float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+        for (int s = 1; s < slices; ++s) {
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(src + s * slice));
+            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        }
+        acc.x += g * v.x, acc.y += g * v.y, acc.z += g * v.z, acc.w += g * v.w;
+    }
+    float* o = out + (int64_t)tok * cols + c;   // 4-byte aligned
+    o[0] = acc.x, o[1] = acc.y, o[2] = acc.z, o[3] = acc.w;
+}
+
 static int64_t logits_bytes(int n_tok, int n_exp) { return ((int64_t)n_tok * n_exp * 4 + 15) & ~(int64_t)15; }
 
 }  // namespace moe
 
-int64_t moe_ws_bytes(int n_tok, int k, int n_exp, int64_t rows) {
-    return moe::logits_bytes(n_tok, n_exp) + (int64_t)n_tok * k * rows * 4;
+// The arguments of the two products and their workspace: the router's logits,
+// the sums of `up`, those of `down`.
+static cudaError_t set_up(const MoeArgs& m, int sms, moe::Args& up, moe::Args& down, int64_t* bytes) {
+    up = moe::Args{};
+    up.cols = m.cols;
+    up.rows = m.rows;
+    up.n_exp = m.n_exp;
+    up.n_tok = m.n_tok;
+    up.k = m.k;
+    up.pairs = m.n_tok * m.k;
+    down = up;
+    down.cols = m.rows;
+    down.rows = m.cols;
+    cudaError_t e = moe::launch_up(m.type, up, sms, nullptr, false);
+    if (e == cudaSuccess) e = moe::launch_down(m.type_down, down, sms, nullptr, false);
+    if (e != cudaSuccess) return e;
+    bytes[0] = moe::logits_bytes(m.n_tok, m.n_exp);
+    bytes[1] = (int64_t)2 * up.slices * up.pairs * m.rows * 4;
+    bytes[2] = (int64_t)down.slices * up.pairs * m.cols * 4;
+    return e;
+}
+
+int64_t moe_ws_bytes(const MoeArgs& m, int sms) {
+    moe::Args up, down;
+    int64_t bytes[3];
+    return set_up(m, sms, up, down, bytes) == cudaSuccess ? bytes[0] + bytes[1] + bytes[2] : 0;
 }
 
 cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStream_t s) {
+    moe::Args up, down;
+    int64_t bytes[3];
+    cudaError_t e = set_up(m, sms, up, down, bytes);
+    if (e != cudaSuccess) return e;
     float* logits = static_cast<float*>(m.ws);
-    float* h = logits + moe::logits_bytes(m.n_tok, m.n_exp) / 4;
+    float* sums = logits + bytes[0] / 4;
+    float* y = sums + bytes[1] / 4;
     if (m.router) {
-        const cudaError_t e = m.n_tok == 1 ? moe::route<1>(m.x, m.router, m.cols, m.n_tok, m.n_exp, logits, s)
-                                           : moe::route<8>(m.x, m.router, m.cols, m.n_tok, m.n_exp, logits, s);
+        e = m.n_tok == 1 ? moe::route<1>(m.x, m.router, m.cols, m.n_tok, m.n_exp, logits, s)
+                         : moe::route<8>(m.x, m.router, m.cols, m.n_tok, m.n_exp, logits, s);
         if (e != cudaSuccess) return e;
     }
-    moe::Args a{};
-    a.x = m.x;
-    a.cols = m.cols;
-    a.rows = m.rows;
-    a.W0 = static_cast<const uint8_t*>(m.Wg);
-    a.W1 = static_cast<const uint8_t*>(m.Wu);
-    a.n_exp = m.n_exp;
-    a.n_tok = m.n_tok;
-    a.k = m.k;
-    a.pairs = m.n_tok * m.k;
-    a.logits = m.router ? logits : nullptr;
-    a.norm = m.norm;
-    a.scale = m.scale;
-    a.ids = m.ids;
-    a.gate = m.gate;
-    a.out = h;
-    a.status = status;
-    moe::Args b = a;
-    const cudaError_t e = moe::launch_up(m.type, a, sms, s);
+    up.x = m.x;
+    up.W0 = static_cast<const uint8_t*>(m.Wg);
+    up.W1 = static_cast<const uint8_t*>(m.Wu);
+    up.logits = m.router ? logits : nullptr;
+    up.norm = m.norm;
+    up.scale = m.scale;
+    up.out = sums;
+    down.x = sums;
+    down.slices_in = up.slices;
+    down.W0 = down.W1 = static_cast<const uint8_t*>(m.Wd);
+    down.out = y;
+    up.ids = down.ids = m.ids;
+    up.gate = down.gate = m.gate;
+    up.status = down.status = status;
+    e = moe::launch_up(m.type, up, sms, s, true);
+    if (e == cudaSuccess) e = moe::launch_down(m.type_down, down, sms, s, true);
     if (e != cudaSuccess) return e;
-    b.x = h;
-    b.cols = m.rows;
-    b.rows = m.cols;
-    b.W0 = static_cast<const uint8_t*>(m.Wd);
-    b.W1 = nullptr;
-    b.logits = nullptr;
-    b.out = m.out;
-    return moe::launch_down(m.type_down, b, sms, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((m.cols / 4 + moe::kSumThreads - 1) / moe::kSumThreads), (unsigned)m.n_tok);
+    cfg.blockDim = dim3(moe::kSumThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe::sum_kernel, (const float*)y, (const int32_t*)m.ids, (const float*)m.gate, m.n_exp, m.n_tok,
+                              m.k, m.cols, down.slices, m.out);
 }
 
 }  // namespace qk

@@ -4,7 +4,9 @@
 namespace qk {
 namespace moe {
 
-cudaError_t launch_up(int type, Args& a, int sms, cudaStream_t s) { return launch_product<false>(type, a, sms, s); }
+cudaError_t launch_up(int type, Args& a, int sms, cudaStream_t s, bool launch) {
+    return launch_product<false>(type, a, sms, s, launch);
+}
 
 }  // namespace moe
 }  // namespace qk

@@ -249,15 +249,15 @@ qk_status qk_gemv_swiglu(int type, const void* Wg, const void* Wu, int64_t rows,
  *          QK_MOE_MAX_K and at most n_exp.
  *   out    fp32 [n_tok, cols], apart from x; fully overwritten.
  *   ws     at least qk_moe_workspace(..) bytes, 16-byte aligned.
- * Every expert that some token chose is read once (in groups of eight of its
- * tokens).  Two launches, three with a router.  Accuracy: each product as
+ * Every expert that some token chose is read once per four or eight of its
+ * tokens.  Three launches, four with a router.  Accuracy: each product as
  * qk_gemv's (1e-4 * sum |w x| + 1e-6 of its own inputs), the SiLU and the sum
  * over experts in fp32; the router's logits are fp32 sums.  A logit that is
  * NaN gives NaN gates for its token.  Deterministic.
  * n_tok == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also rows or
  * cols below 1 or above 2^18), QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG (scale
  * not finite), QK_ERR_WORKSPACE. */
-size_t qk_moe_workspace(int64_t n_tok, int k, int n_exp, int64_t rows);
+size_t qk_moe_workspace(int type, int type_down, int n_exp, int64_t rows, int64_t cols, int k, int64_t n_tok);
 qk_status qk_moe_ffn(int type, const void* Wg, const void* Wu, int type_down, const void* Wd, int n_exp, int64_t rows,
                      int64_t cols, const float* router, int k, int norm, float scale, const float* x, int64_t n_tok,
                      int32_t* ids, float* gate, float* out, void* ws, size_t ws_bytes, void* stream);

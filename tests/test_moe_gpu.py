@@ -221,7 +221,7 @@ def test_streams_and_graph(gpu):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(u, v) for u, v in zip(a, b))
-    ws = torch.empty(qk.moe_workspace(n, k, E, rows), dtype=torch.uint8, device=gpu)
+    ws = torch.empty(qk.moe_workspace(qk.Q4_K, qk.Q6_K, E, rows, cols, k, n), dtype=torch.uint8, device=gpu)
     outs = [[torch.zeros_like(v) for v in want[0]] for _ in range(2)]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):           # two calls that share a workspace

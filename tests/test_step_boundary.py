@@ -135,8 +135,10 @@ def test_moe_ffn_refusals(lib, kw, status):
 
 def test_moe_sizes_and_binding_refusals(lib):
     assert len(qk.SIGNATURES["qk_moe_ffn"][1]) == len(MOE)
-    assert qk.moe_workspace(3, 2, 8, 512) >= 3 * 2 * 512 * 4 + 3 * 8 * 4
-    assert qk.moe_workspace(65, 2, 8, 512) == 0 and qk.moe_workspace(3, 9, 8, 512) == 0
+    assert qk.moe_workspace(qk.Q4_K, qk.Q6_K, 8, 512, 256, 2, 3) >= 3 * 2 * (2 * 512 + 256) * 4 + 3 * 8 * 4
+    for bad in ((qk.Q4_K, qk.Q6_K, 8, 512, 256, 2, 65), (qk.Q4_K, qk.Q6_K, 8, 512, 256, 9, 3), (0, qk.Q6_K, 8, 512, 256, 2, 3),
+                (qk.Q4_K, qk.Q6_K, 8, 512, 300, 2, 3)):
+        assert qk.moe_workspace(*bad) == 0
     assert call(lib.qk_moe_ffn, MOE, n_tok=0, x=None, ws=None, ws_bytes=0) == 0
     u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
     up, down, x = 2 * 512 * 144, 2 * 256 * 420, torch.zeros((3, 256))

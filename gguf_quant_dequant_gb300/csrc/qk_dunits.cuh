@@ -2,13 +2,21 @@
 // weight rows x 256 weights against NT (4 or 8) rows of x, each weight
 // converted once.
 //
-// Arithmetic as qk_hunits.cuh: exact integer codes less an offset as fp16 A
-// fragments, x as hi + lo fp16 terms after a power of two per 32-block, fp32
-// sums scaled per block.  There a warp's four column groups hold four parts of
-// K for one row of x; here all sixteen k of an MMA come from one 32-block and
-// the eight columns are rows of x: four rows by (hi, lo), or eight rows with hi
-// and lo in two MMAs.  So one MMA serves four rows instead of one, and a
-// thread's sums are whole: row g and g + 8 against its own row(s) of x.
+// Arithmetic: integer codes as exact fp16 A fragments, x as hi + lo fp16 terms
+// after a power of two per 32-block, fp32 sums scaled per block.  The types
+// without a min hold the code less its offset (placed in the mantissa of a
+// magic value and brought down by one exact add, as in qk_hunits.cuh).  The
+// types with a min hold the code itself, as the fp16 subnormal whose bits it is
+// (q 2^-24, or 2^k that for a code k bits up): one mask and nothing else, the
+// power of two goes into the scale; w = ds q - dm is then summed as ds sum(q x)
+// - dm sum(x), so the error is a fraction of sum (|ds q| + |dm|) |x|.  (With the
+// nearest code to dm / ds taken off first, as the decode GEMV does, it would be
+// one of sum |w x|, for 45 % more instructions.)
+// In qk_hunits.cuh a warp's four column groups hold four parts of K for one row
+// of x; here all sixteen k of an MMA come from one 32-block and the eight
+// columns are rows of x: four rows by (hi, lo), or eight rows with hi and lo in
+// two MMAs.  So one MMA serves four rows instead of one, and a thread's sums are
+// whole: row g and g + 8 against its own row(s) of x.
 //
 // Thread (g, t) supplies rows g and g + 8; of a 32-block's eight code words
 // (four weights each) it takes words 2t and 2t + 1 in steps 0 and 1, or, where
@@ -28,14 +36,14 @@ using namespace hm;
 
 // Prepared x of one unit: NT = 4 [block][row][plane][64 bytes], NT = 8
 // [block][plane][row][64 bytes] (conflict-free for the B loads); the words of a
-// plane in their order, or 0, 4, 1, 5, .. (kW4).  xm [block][row]: sum, 2^e,
-// sums of the halves.
+// plane in their order, or 0, 4, 1, 5, .. (kW4).  xm [block][row]: the block's
+// sum twice (kHalves: its halves' sums), 2^e twice.
 template <int NT>
 __device__ __forceinline__ uint32_t x_off(int blk, int row, int plane) {
     return NT == 4 ? (uint32_t)(blk * 512 + row * 128 + plane * 64) : (uint32_t)(blk * 1024 + plane * 512 + row * 64);
 }
 constexpr int kXRow = 8 * 128;   // bytes of a row of x in a unit
-template <int NT, bool W4>
+template <int NT, bool W4, bool HALVES>
 __device__ __forceinline__ void put_x(float4 a, float4 b, uint8_t* xb, float4* xm, int row, int lane) {
     const int blk = lane >> 2, q = lane & 3;
     uint32_t hi[4], lo[4];
@@ -52,7 +60,7 @@ __device__ __forceinline__ void put_x(float4 a, float4 b, uint8_t* xb, float4* x
         *reinterpret_cast<uint4*>(h + 16 * q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(l + 16 * q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    if (q == 0) xm[blk * NT + row] = m;
+    if (q == 0) xm[blk * NT + row] = HALVES ? make_float4(m.z, m.w, m.y, m.y) : make_float4(m.x, m.x, m.y, m.y);
 }
 
 // Word at a 2-byte-aligned shared address.
@@ -79,47 +87,71 @@ __device__ __forceinline__ void frag(uint32_t (&A)[4], uint32_t w0, uint32_t w1,
     A[3] = hadd2(and_or(w1 >> 8, M, G), o1);
 }
 
-// Scales of a block for rows g and g + 8: per half where scaled by sixteens
-// (else [0] alone), and the negative residuals of the types with a min.
+// Scales of a block as (row g, row g + 8): per half where scaled by sixteens
+// (else [0] alone), and the negative mins of the types with a min.
 struct Scale {
-    float f[2][2], n[2][2];   // [row][half]
+    float2 f[2], n[2];
 };
 
 // A decoder: UB bytes per row and unit, kW4 (above), kG16 (scaled by
-// sixteens), kMin (has a residual), block(pair c, b), Ctx, load(ctx, r0, r1,
-// lane), pair(ctx, c, lane, A, s): fragments A[b][step] and scales s[b] of the
-// pair's two blocks.
+// sixteens), kMin (has a min), block(pair c, b), Ctx, load(ctx, r0, r1, lane),
+// pair(ctx, c, lane, A, s): fragments A[b][step] and scales s[b] of the pair's
+// two blocks; pairs are taken in their order.
 template <int T> struct DU;
+
+// Q4_K and Q5_K: d * sc and dmin * m of the thread's own pair of blocks, by 2^24
+// and 2^20 (the codes' places).
+struct RowMin {
+    float2 ds, ndm;
+};
+template <bool HIGH>   // the second block's codes are four bits up
+__device__ __forceinline__ RowMin row_min(const uint4& h, int t) {
+    const uint32_t f = HU<T_Q4_K>::fields(h, t);
+    const float d = h2f(h.x & 0xFFFFu), dmin = h2f(h.x >> 16);
+    constexpr float kM = 8388608.0f;   // 2^23
+    auto two = [&](uint32_t s0, uint32_t s1) {
+        return __fadd2_rn(make_float2(__uint_as_float(__byte_perm(f, 0x4B000000u, s0)), __uint_as_float(__byte_perm(f, 0x4B000000u, s1))),
+                          make_float2(-kM, -kM));
+    };
+    const float d24 = d * 0x1p24f;
+    return {__fmul2_rn(make_float2(d24, HIGH ? d * 0x1p20f : d24), two(0x7650, 0x7651)),
+            __fmul2_rn(make_float2(-dmin, -dmin), two(0x7652, 0x7653))};
+}
+__device__ __forceinline__ void scales_min(const RowMin& p0, const RowMin& p1, int src, Scale (&s)[2]) {
+    s[0].f[0] = make_float2(from(p0.ds.x, src), from(p1.ds.x, src));
+    s[1].f[0] = make_float2(from(p0.ds.y, src), from(p1.ds.y, src));
+    s[0].n[0] = make_float2(from(p0.ndm.x, src), from(p1.ndm.x, src));
+    s[1].n[0] = make_float2(from(p0.ndm.y, src), from(p1.ndm.y, src));
+}
+// Four A registers of raw codes under mask M of each half word.
+__device__ __forceinline__ void frag_raw(uint32_t (&A)[4], uint32_t w0, uint32_t w1, uint32_t M) {
+    A[0] = w0 & M;
+    A[1] = w1 & M;
+    A[2] = (w0 >> 8) & M;
+    A[3] = (w1 >> 8) & M;
+}
 
 template <> struct DU<T_Q4_K> {
     static constexpr int UB = 144;
     static constexpr bool kW4 = false, kG16 = false, kMin = true;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
-        HU<T_Q4_K>::Row p0, p1;
+        RowMin p0, p1;
         const uint8_t *r0, *r1;
     };
     __device__ static __forceinline__ void load(Ctx& x, const uint8_t* r0, const uint8_t* r1, int lane) {
-        x.p0 = HU<T_Q4_K>::row_params<true>(lds128(r0), lane & 3, 15.0f);
-        x.p1 = HU<T_Q4_K>::row_params<true>(lds128(r1), lane & 3, 15.0f);
+        x.p0 = row_min<true>(lds128(r0), lane & 3);
+        x.p1 = row_min<true>(lds128(r1), lane & 3);
         x.r0 = r0 + 16 + 8 * (lane & 3);
         x.r1 = r1 + 16 + 8 * (lane & 3);
     }
-    __device__ static __forceinline__ void scales(const HU<T_Q4_K>::Row& p0, const HU<T_Q4_K>::Row& p1, int src, Scale (&s)[2]) {
-        s[0].f[0][0] = from(p0.ds.x, src), s[1].f[0][0] = from(p0.ds.y, src);
-        s[0].f[1][0] = from(p1.ds.x, src), s[1].f[1][0] = from(p1.ds.y, src);
-        s[0].n[0][0] = from(p0.nr.x, src), s[1].n[0][0] = from(p0.nr.y, src);
-        s[0].n[1][0] = from(p1.nr.x, src), s[1].n[1][0] = from(p1.nr.y, src);
-    }
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
-        const int src = (lane & 28) | c;
         const uint2 w0 = lds64(x.r0 + 32 * c), w1 = lds64(x.r1 + 32 * c);
-        const uint32_t l0 = from(x.p0.clo, src), l1 = from(x.p1.clo, src), h0 = from(x.p0.chi, src), h1 = from(x.p1.chi, src);
-        frag(A[0][0], w0.x, w1.x, 0x000F000Fu, 0x64006400u, l0, l1);
-        frag(A[0][1], w0.y, w1.y, 0x000F000Fu, 0x64006400u, l0, l1);
-        frag(A[1][0], w0.x, w1.x, 0x00F000F0u, 0x54005400u, h0, h1);
-        frag(A[1][1], w0.y, w1.y, 0x00F000F0u, 0x54005400u, h0, h1);
-        scales(x.p0, x.p1, src, s);
+        frag_raw(A[0][0], w0.x, w1.x, 0x000F000Fu);
+        frag_raw(A[0][1], w0.y, w1.y, 0x000F000Fu);
+        frag_raw(A[1][0], w0.x, w1.x, 0x00F000F0u);
+        frag_raw(A[1][1], w0.y, w1.y, 0x00F000F0u);
+        scales_min(x.p0, x.p1, (lane & 28) | c, s);
     }
 };
 
@@ -128,32 +160,30 @@ template <> struct DU<T_Q5_K> {
     static constexpr bool kW4 = false, kG16 = false, kMin = true;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
-        HU<T_Q4_K>::Row p0, p1;
+        RowMin p0, p1;
         const uint8_t *r0, *r1;
-        uint2 v0, v1;   // the fifth bits of the thread's words, all blocks
+        uint2 v0, v1;   // the fifth bits of the thread's words, four bits up, moved down two bits a pair
     };
     __device__ static __forceinline__ void load(Ctx& x, const uint8_t* r0, const uint8_t* r1, int lane) {
-        x.p0 = HU<T_Q4_K>::row_params<false>(lds128(r0), lane & 3, 31.0f);
-        x.p1 = HU<T_Q4_K>::row_params<false>(lds128(r1), lane & 3, 31.0f);
+        x.p0 = row_min<false>(lds128(r0), lane & 3);
+        x.p1 = row_min<false>(lds128(r1), lane & 3);
         x.v0 = lds64(r0 + 16 + 8 * (lane & 3));
         x.v1 = lds64(r1 + 16 + 8 * (lane & 3));
         x.r0 = r0 + 48 + 8 * (lane & 3);
         x.r1 = r1 + 48 + 8 * (lane & 3);
     }
-    __device__ static __forceinline__ uint32_t low(uint32_t w, uint32_t v, int c) { return and_or(w, 0x0F0F0F0Fu, ((v >> (2 * c)) << 4) & 0x10101010u); }
-    __device__ static __forceinline__ uint32_t high(uint32_t w, uint32_t v, int c) {
-        return and_or(w >> 4, 0x0F0F0F0Fu, ((v >> (2 * c)) << 3) & 0x10101010u);
-    }
-    __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
-        const int src = (lane & 28) | c;
+    // Code bytes of the low and high nibbles with their fifth bits (bits 0 and 1 of v's bytes).
+    __device__ static __forceinline__ uint32_t low(uint32_t w, uint32_t v) { return and_or(w, 0x0F0F0F0Fu, (v << 4) & 0x10101010u); }
+    __device__ static __forceinline__ uint32_t high(uint32_t w, uint32_t v) { return and_or(w >> 4, 0x0F0F0F0Fu, (v << 3) & 0x10101010u); }
+    __device__ static __forceinline__ void pair(Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const uint2 w0 = lds64(x.r0 + 32 * c), w1 = lds64(x.r1 + 32 * c);
-        const uint32_t l0 = from(x.p0.clo, src), l1 = from(x.p1.clo, src), h0 = from(x.p0.chi, src), h1 = from(x.p1.chi, src);
-        constexpr uint32_t M = 0x001F001Fu, G = 0x64006400u;
-        frag(A[0][0], low(w0.x, x.v0.x, c), low(w1.x, x.v1.x, c), M, G, l0, l1);
-        frag(A[0][1], low(w0.y, x.v0.y, c), low(w1.y, x.v1.y, c), M, G, l0, l1);
-        frag(A[1][0], high(w0.x, x.v0.x, c), high(w1.x, x.v1.x, c), M, G, h0, h1);
-        frag(A[1][1], high(w0.y, x.v0.y, c), high(w1.y, x.v1.y, c), M, G, h0, h1);
-        DU<T_Q4_K>::scales(x.p0, x.p1, src, s);
+        constexpr uint32_t M = 0x001F001Fu;
+        frag_raw(A[0][0], low(w0.x, x.v0.x), low(w1.x, x.v1.x), M);
+        frag_raw(A[0][1], low(w0.y, x.v0.y), low(w1.y, x.v1.y), M);
+        frag_raw(A[1][0], high(w0.x, x.v0.x), high(w1.x, x.v1.x), M);
+        frag_raw(A[1][1], high(w0.y, x.v0.y), high(w1.y, x.v1.y), M);
+        x.v0.x >>= 2, x.v0.y >>= 2, x.v1.x >>= 2, x.v1.y >>= 2;
+        scales_min(x.p0, x.p1, (lane & 28) | c, s);
     }
 };
 
@@ -206,8 +236,7 @@ template <> struct DU<T_Q6_K> {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                s[b].f[0][h] = from(x.f0[2 * b + h], src);
-                s[b].f[1][h] = from(x.f1[2 * b + h], src);
+                s[b].f[h] = make_float2(from(x.f0[2 * b + h], src), from(x.f1[2 * b + h], src));
             }
     }
 };
@@ -233,8 +262,7 @@ struct Blocks32 {
     __device__ static __forceinline__ void scales(const Ctx& x, int src, Scale (&s)[2]) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            s[b].f[0][0] = from(x.d0[b], src);
-            s[b].f[1][0] = from(x.d1[b], src);
+            s[b].f[0] = make_float2(from(x.d0[b], src), from(x.d1[b], src));
         }
     }
 };
@@ -306,33 +334,38 @@ template <> struct DU<T_Q2_K> {
     static constexpr bool kW4 = true, kG16 = true, kMin = true;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
-        HU<T_Q2_K>::Row p0, p1;
+        float f0[4], f1[4], n0[4], n1[4];   // of the thread's own pair: block, half; scales by 2^24 less the codes' place
         const uint8_t *r0, *r1;
     };
+    __device__ static __forceinline__ void own(const uint8_t* r, int t, float (&f)[4], float (&n)[4]) {
+        const uint32_t sm = lds32(r + 4 * t), dd = lds32(r + 80);   // (scale, min) bytes; d, dmin
+        const uint32_t sc = sm & 0x0F0F0F0Fu, mn = (sm >> 4) & 0x0F0F0F0Fu;
+        const float d = h2f(dd & 0xFFFFu) * (t & 1 ? 0x1p20f : 0x1p24f), dmin = h2f(dd >> 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[k] = (k < 2 ? d : d * 0.25f) * ubyte_f(sc, k);
+            n[k] = -dmin * ubyte_f(mn, k);
+        }
+    }
     __device__ static __forceinline__ void load(Ctx& x, const uint8_t* r0, const uint8_t* r1, int lane) {
         const int t = lane & 3;
-        const float m0 = t & 1 ? 64.0f : 1024.0f, m1 = t & 1 ? 16.0f : 256.0f;
-        x.p0 = HU<T_Q2_K>::row_params(r0, t, m0, m1);
-        x.p1 = HU<T_Q2_K>::row_params(r1, t, m0, m1);
+        own(r0, t, x.f0, x.n0);
+        own(r1, t, x.f1, x.n1);
         x.r0 = r0 + 16 + 4 * t;
         x.r1 = r1 + 16 + 4 * t;
     }
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const int src = (lane & 28) | c;
-        const bool up = c & 1;
-        const uint32_t M[2] = {up ? 0x00300030u : 0x00030003u, up ? 0x00C000C0u : 0x000C000Cu};
-        const uint32_t G[2] = {up ? 0x54005400u : 0x64006400u, up ? 0x4C004C00u : 0x5C005C00u};
+        const uint32_t M0 = c & 1 ? 0x00300030u : 0x00030003u;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t w0 = lds32(x.r0 + 32 * (c >> 1) + 16 * j), w1 = lds32(x.r1 + 32 * (c >> 1) + 16 * j);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int k = 2 * b + j;
-                frag(A[b][j], w0, w1, M[b], G[b], from(x.p0.cst[k], src), from(x.p1.cst[k], src));
-                s[b].f[0][j] = from(x.p0.ds[k], src);
-                s[b].f[1][j] = from(x.p1.ds[k], src);
-                s[b].n[0][j] = -from(x.p0.r[k], src);
-                s[b].n[1][j] = -from(x.p1.r[k], src);
+                frag_raw(A[b][j], w0, w1, b ? M0 << 2 : M0);
+                s[b].f[j] = make_float2(from(x.f0[k], src), from(x.f1[k], src));
+                s[b].n[j] = make_float2(from(x.n0[k], src), from(x.n1[k], src));
             }
         }
     }
@@ -381,72 +414,87 @@ template <> struct DU<T_Q3_K> {
                 A[b][j][1] = cv(w1, x.m1[j]);
                 A[b][j][2] = cv(w0 >> 8, x.m0[j] >> 8);
                 A[b][j][3] = cv(w1 >> 8, x.m1[j] >> 8);
-                s[b].f[0][j] = from(x.f0[2 * b + j], src);
-                s[b].f[1][j] = from(x.f1[2 * b + j], src);
+                s[b].f[j] = make_float2(from(x.f0[2 * b + j], src), from(x.f1[2 * b + j], src));
             }
         }
     }
 };
 
 // One unit of two tiles of rows (a0, a1 and b0, b1: rows g and g + 8 of each)
-// against the same rows of x: y[0], y[1] += rows g, g + 8 against row t of x
-// (NT = 4); y[0], y[1] row 2t and y[2], y[3] row 2t + 1 (NT = 8).  nvb: 32-blocks
-// of the unit that exist.
+// against the same rows of x: y[0] += (row g, row g + 8) against row t of x (NT =
+// 4); y[0] against row 2t and y[1] against row 2t + 1 (NT = 8).  nvb: 32-blocks of
+// the unit that exist.
 template <int T, int NT>
 __device__ __forceinline__ void run_unit(const uint8_t* a0, const uint8_t* a1, const uint8_t* b0, const uint8_t* b1,
-                                         const uint8_t* xb, const float4* xm, int lane, int nvb, float (&ya)[NT / 2],
-                                         float (&yb)[NT / 2]) {
+                                         const uint8_t* xb, const float4* xm, int lane, int nvb, float2 (&ya)[NT / 4],
+                                         float2 (&yb)[NT / 4]) {
     using D = DU<T>;
     const int g = lane >> 2, t = lane & 3;
     typename D::Ctx cx[2];
     D::load(cx[0], a0, a1, lane);
     D::load(cx[1], b0, b1, lane);
     const uint8_t* bp = NT == 4 ? xb + x_off<4>(0, g >> 1, g & 1) + 16 * t : xb + x_off<8>(0, g, 0) + 16 * t;
+    // Half of the pairs unrolled: the code of all four is fetched longer than it runs where few units follow one another.
+#pragma unroll 1
+    for (int c2 = 0; c2 < 4; c2 += 2) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint4 B[2], L[2];
-        float4 m[2][NT / 4];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int blk = D::block(c, b);
-            B[b] = lds128(bp + blk * (NT == 4 ? 512 : 1024));
-            if (NT == 8) L[b] = lds128(bp + blk * 1024 + 512);
-#pragma unroll
-            for (int k = 0; k < NT / 4; ++k) m[b][k] = xm[blk * NT + (NT == 4 ? t : 2 * t + k)];
-        }
-#pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-            uint32_t A[2][2][4];
-            Scale s[2];
-            D::pair(cx[tile], c, lane, A, s);
-            float(&y)[NT / 2] = tile ? yb : ya;
+        for (int c1 = 0; c1 < 2; ++c1) {
+            const int c = c2 + c1;
+            uint4 B[2], L[2];
+            float4 m[2][NT / 4];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                // a short last unit holds stale bytes behind its blocks
-                if ((T == T_Q8_0 || T == T_Q5_0 || T == T_Q4_0) && D::block(c, b) >= nvb) continue;
-                float C[2][4];
-                mma16816_z(C[0], A[b][0][0], A[b][0][1], A[b][0][2], A[b][0][3], B[b].x, B[b].y);
-                if constexpr (D::kG16) mma16816_z(C[1], A[b][1][0], A[b][1][1], A[b][1][2], A[b][1][3], B[b].z, B[b].w);
-                else mma16816(C[0], A[b][1][0], A[b][1][1], A[b][1][2], A[b][1][3], B[b].z, B[b].w);
-                if constexpr (NT == 8) {
-                    mma16816(C[0], A[b][0][0], A[b][0][1], A[b][0][2], A[b][0][3], L[b].x, L[b].y);
-                    mma16816(C[D::kG16], A[b][1][0], A[b][1][1], A[b][1][2], A[b][1][3], L[b].z, L[b].w);
+                const int blk = D::block(c, b);
+                B[b] = lds128(bp + blk * (NT == 4 ? 512 : 1024));
+                if (NT == 8) L[b] = lds128(bp + blk * 1024 + 512);
+#pragma unroll
+                for (int k = 0; k < NT / 4; ++k) {
+                    const float4* p = xm + blk * NT + (NT == 4 ? t : 2 * t + k);
+                    if constexpr (D::kMin) {
+                        m[b][k] = *p;
+                    } else {
+                        const float2 up = reinterpret_cast<const float2*>(p)[1];
+                        m[b][k] = make_float4(0.0f, 0.0f, up.x, up.y);
+                    }
                 }
+            }
 #pragma unroll
-                for (int k = 0; k < NT / 4; ++k)
+            for (int tile = 0; tile < 2; ++tile) {
+                uint32_t A[2][2][4];
+                Scale s[2];
+                D::pair(cx[tile], c, lane, A, s);
+                float2(&y)[NT / 4] = tile ? yb : ya;
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float& v = y[2 * k + r];
-                        // this row of x: columns (hi, lo) of NT = 4, one column of NT = 8
-                        auto sum = [&](int h) { return NT == 4 ? C[h][2 * r] + C[h][2 * r + 1] : C[h][2 * r + k]; };
+                for (int b = 0; b < 2; ++b) {
+                    // a short last unit holds stale bytes behind its blocks
+                    if ((T == T_Q8_0 || T == T_Q5_0 || T == T_Q4_0) && D::block(c, b) >= nvb) continue;
+                    float C[2][4];
+                    mma16816_z(C[0], A[b][0][0], A[b][0][1], A[b][0][2], A[b][0][3], B[b].x, B[b].y);
+                    if constexpr (D::kG16) mma16816_z(C[1], A[b][1][0], A[b][1][1], A[b][1][2], A[b][1][3], B[b].z, B[b].w);
+                    else mma16816(C[0], A[b][1][0], A[b][1][1], A[b][1][2], A[b][1][3], B[b].z, B[b].w);
+                    if constexpr (NT == 8) {
+                        mma16816(C[0], A[b][0][0], A[b][0][1], A[b][0][2], A[b][0][3], L[b].x, L[b].y);
+                        mma16816(C[D::kG16], A[b][1][0], A[b][1][1], A[b][1][2], A[b][1][3], L[b].z, L[b].w);
+                    }
+#pragma unroll
+                    for (int k = 0; k < NT / 4; ++k) {
+                        // rows g, g + 8 against this row of x: columns (hi, lo) of NT = 4, one column of NT = 8
+                        auto sum = [&](int h) {
+                            return NT == 4 ? make_float2(C[h][0] + C[h][1], C[h][2] + C[h][3]) : make_float2(C[h][k], C[h][2 + k]);
+                        };
                         const float4 x = m[b][k];
-                        if constexpr (D::kG16) v = fmaf(x.y, fmaf(s[b].f[r][0], sum(0), s[b].f[r][1] * sum(1)), v);
-                        else v = fmaf(s[b].f[r][0] * x.y, sum(0), v);
+                        const float2 up = make_float2(x.z, x.w);
+                        if constexpr (D::kG16) y[k] = __ffma2_rn(up, __ffma2_rn(s[b].f[0], sum(0), __fmul2_rn(s[b].f[1], sum(1))), y[k]);
+                        else y[k] = __ffma2_rn(s[b].f[0], __fmul2_rn(sum(0), up), y[k]);
                         if constexpr (D::kMin) {
-                            if constexpr (D::kG16) v = fmaf(s[b].n[r][0], x.z, fmaf(s[b].n[r][1], x.w, v));
-                            else v = fmaf(s[b].n[r][0], x.x, v);
+                            if constexpr (D::kG16) {
+                                y[k] = __ffma2_rn(s[b].n[0], make_float2(x.x, x.x), __ffma2_rn(s[b].n[1], make_float2(x.y, x.y), y[k]));
+                            } else {
+                                y[k] = __ffma2_rn(s[b].n[0], make_float2(x.x, x.y), y[k]);
+                            }
                         }
                     }
+                }
             }
         }
     }

@@ -224,25 +224,34 @@ __device__ __forceinline__ void cp_async16_stream(uint32_t dst, const void* src,
         : "memory");
 }
 
-// 16 rows of one unit: `off` is the byte offset of row 0's unit, `bytes` what
-// each row has of it.  Eight lanes take 128 bytes of a row, four rows at a time.
+// A lane's chunks of a tile: numbers lane, lane + 32, .. of its 16 * kChunks,
+// row by row (neighbouring lanes read neighbouring chunks); the offsets of
+// their rows are kept.
 template <int T>
-__device__ __forceinline__ void fetch_tile(const uint8_t* W, int64_t off, uint32_t rb, int bytes, uint32_t dst, int lane, uint64_t pol) {
-    using S = Slot<T>;
-    const int c = lane & 7;
+struct Chunks {
+    static constexpr int kN = (kTileRows * Slot<T>::kChunks + 31) / 32;
+    uint32_t row[kN];   // row * row_bytes
+    __device__ __forceinline__ void set(uint32_t rb, int lane) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = 4 * j + (lane >> 3);
-        const int64_t at = off + (int64_t)row * rb;
-        const uint8_t* src = W + (at & ~(int64_t)15);
-        const int need = (int)(at & 15) + bytes;
+        for (int i = 0; i < kN; ++i) row[i] = (uint32_t)((lane + 32 * i) / Slot<T>::kChunks) * rb;
+    }
+    // 16 rows of one unit to dst: `src` is the first byte of row 0's part, `bytes` what each row has of the unit.
+    __device__ __forceinline__ void fetch(const uint8_t* src, int bytes, uint32_t dst, int lane, uint64_t pol) const {
+        using S = Slot<T>;
 #pragma unroll
-        for (int h = 0; h < (S::kChunks + 7) / 8; ++h) {
-            const int ch = c + 8 * h;
-            cp_async16_stream(dst + row * S::kRow + 16 * ch, src + 16 * ch, pol, ch < S::kChunks && 16 * ch < need);
+        for (int i = 0; i < kN; ++i) {
+            const int at = lane + 32 * i, r = at / S::kChunks, c16 = 16 * (at - r * S::kChunks);
+            const bool in = (kTileRows * S::kChunks) % 32 == 0 || i + 1 < kN || at < kTileRows * S::kChunks;
+            const uint8_t* p = src + row[i];
+            if (S::kSkew == 0) {
+                cp_async16_stream(dst + r * S::kRow + c16, p + c16, pol, in);
+            } else {
+                const uint32_t skew = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+                cp_async16_stream(dst + r * S::kRow + c16, p - skew + c16, pol, in && c16 < (int)skew + bytes);
+            }
         }
     }
-}
+};
 
 template <int T, int NT, bool DOWN>
 __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
 #pragma unroll
                 for (int m = 0; m < kAt; ++m)
                     if (i0 + m < nu * n)
-                        dm::put_x<NT, U::kW4>(a[m], b[m], xb + un[m] * (NT * dm::kXRow), xm + un[m] * 8 * NT, at[m], lane);
+                        dm::put_x<NT, U::kW4, U::kMin && U::kG16>(a[m], b[m], xb + un[m] * (NT * dm::kXRow), xm + un[m] * 8 * NT, at[m], lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&xfull[set]);
@@ -346,6 +355,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     const uint64_t pol = policy_evict_first();
     uint8_t* slots = smem + p.off_ring + warp * (4 * S::kTile);   // two steps of two tiles
     const uint32_t slots_u32 = smem_u32(slots);
+    Chunks<T> chunks;
+    chunks.set(rb, lane);
     // A step: one unit of a job.
     struct Step {
         int64_t job;
@@ -364,8 +375,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
         if (s.job < j1) {
             const int64_t at = (int64_t)s.u * S::kUB;
             const int bytes = (int)min((int64_t)S::kUB, (int64_t)rb - at);
-            fetch_tile<T>(p.W0, s.off0 + at, rb, bytes, slots_u32 + slot * (2 * S::kTile), lane, pol);
-            fetch_tile<T>(p.W1, s.off1 + at, rb, bytes, slots_u32 + slot * (2 * S::kTile) + S::kTile, lane, pol);
+            chunks.fetch(p.W0 + s.off0 + at, bytes, slots_u32 + slot * (2 * S::kTile), lane, pol);
+            chunks.fetch(p.W1 + s.off1 + at, bytes, slots_u32 + slot * (2 * S::kTile) + S::kTile, lane, pol);
         }
         cp_async_commit();
     };
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     };
     while (cur.job < j1 && !dead) {
         const int me = (int)(cur.job / p.jobs), j = (int)(cur.job - (int64_t)me * p.jobs), g = me / p.slices, u0 = cur.u;
-        float ya[NT / 2] = {}, yb[NT / 2] = {};
+        float2 ya[NT / 4] = {}, yb[NT / 4] = {};
         leave(me);
         if (dead) break;
         const uint8_t* xb = xbuf + ((me - e0) & 1) * x_set;
@@ -422,11 +433,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
             const int i = NT == 4 ? t : 2 * t + k;
             if (i < n) {
                 float* o = p.out + ((int64_t)sl * p.pairs + tb.pairs[beg + i]) * p.rows + (int64_t)j * (DOWN ? 2 * kTileRows : kTileRows) + g8;
-                o[0] = ya[2 * k];
-                o[8] = ya[2 * k + 1];
+                o[0] = ya[k].x;
+                o[8] = ya[k].y;
                 float* o2 = DOWN ? o + kTileRows : o + stack;
-                o2[0] = yb[2 * k];
-                o2[8] = yb[2 * k + 1];
+                o2[0] = yb[k].x;
+                o2[8] = yb[k].y;
             }
         }
         cur = ahead;

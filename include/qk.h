@@ -250,10 +250,12 @@ qk_status qk_gemv_swiglu(int type, const void* Wg, const void* Wu, int64_t rows,
  *   out    fp32 [n_tok, cols], apart from x; fully overwritten.
  *   ws     at least qk_moe_workspace(..) bytes, 16-byte aligned.
  * Every expert that some token chose is read once per four or eight of its
- * tokens.  Three launches, four with a router.  Accuracy: each product as
- * qk_gemv's (1e-4 * sum |w x| + 1e-6 of its own inputs), the SiLU and the sum
- * over experts in fp32; the router's logits are fp32 sums.  A logit that is
- * NaN gives NaN gates for its token.  Deterministic.
+ * tokens.  Three launches, four with a router.  Accuracy: each product is
+ * within 2^-17 * sum_k (|scale code| + |min|) |x_k| + 1e-6 of its exact value
+ * (for the types without a min that is sum |w x|; about 2^-22 in practice), the
+ * SiLU and the sum over experts are fp32; the router's logits are fp32 sums.
+ * A logit that is NaN ranks first and gives NaN gates for its token.
+ * Deterministic.
  * n_tok == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also rows or
  * cols below 1 or above 2^18), QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG (scale
  * not finite), QK_ERR_WORKSPACE. */

@@ -1,12 +1,13 @@
 """The expert layer against the oracle: the router's choice, and the products
-of the chosen experts within a bound that follows from the GEMV's.
+of the chosen experts within a bound that follows from each product's.
 
-With g, u the oracle's products and Sg, Su their sums |w x|, the kernel's are
-within eg = 1e-4 Sg + 1e-6 (and eu) of them; |SiLU'| <= 1.1, so h is within
-eh = 1.1 eg (|u| + eu) + |SiLU(g)| eu + 2^-20 |h|.  The down product of h' is
-within 1e-4 sum |w h'| + 1e-6 of its exact value, and sum |w| eh of the
-oracle's; the gates' own error and the fp32 sum over k experts add (k + 24)
-2^-24 of the terms' magnitude."""
+A product of a row w = ds q - dm with x is within e = 2^-17 sum (|ds q| + |dm|)
+|x| + 1e-6: x as two fp16 terms is 2^-22 off, the fp32 sums have one rounding
+(or, inside an MMA, truncation) per 16 weights, block and slice of at most 2^6
+blocks, up to 2^7 of 2^-24 together.  |SiLU'| <= 1.1, so h = SiLU(g) u is within
+eh = 1.1 eg (|u| + eu) + |SiLU(g)| eu + 2^-20 |h|, the down product of h within
+its own e and sum |w| eh; the gates' error and the fp32 sum over k experts add
+(k + 24) 2^-24 of the terms' magnitude."""
 import numpy as np
 import pytest
 import torch
@@ -29,16 +30,26 @@ def layer(seed, E, rows, cols, up, down):
 def reference(W, E, rows, cols, up, down, x, ids, gate):
     """fp64 output and its bound, by the oracle's dequantized weights."""
     n, k = ids.shape
-    tu, td = type_id(up), type_id(down)
     out, tol = np.zeros((n, cols)), np.zeros((n, cols))
     cache = {}
-    size = lambda w, r: len(w) // (E * r)  # noqa: E731
     silu = lambda z: z / (1 + np.exp(-np.clip(z, -700, 700)))  # noqa: E731
+
+    def mat(w, name, e, r, c):
+        """Expert e's weights, and |ds q| + |dm| of each."""
+        t, b = type_id(name), w.reshape(E, -1)[e]
+        v = np.asarray(oracle.dequant(t, b, r, c), np.float64)
+        if name not in ("Q4_K", "Q5_K", "Q2_K"):
+            return v, np.abs(v)
+        _, _, mins, _, dmin = oracle.unpack(t, b, r * c // 256)
+        each = 16 if name == "Q2_K" else 32
+        dm = np.abs((np.asarray(mins, np.float64).reshape(-1, 16)[:, :256 // each] * np.asarray(dmin, np.float64).reshape(-1, 1)))
+        dm = np.repeat(dm, each, 1).reshape(r, c)
+        sign = np.repeat(np.repeat(np.sign(np.asarray(dmin, np.float64)).reshape(-1, 1), 256, 1), 1, 1).reshape(r, c)
+        return v, np.abs(v + sign * dm) + dm
 
     def mats(e):
         if e not in cache:
-            cut = lambda w, t, r, c: np.asarray(oracle.dequant(t, w.reshape(E * r, -1)[e * r:(e + 1) * r].reshape(-1), r, c), np.float64)  # noqa: E731
-            cache[e] = cut(W[0], tu, rows, cols), cut(W[1], tu, rows, cols), cut(W[2], td, cols, rows)
+            cache[e] = mat(W[0], up, e, rows, cols), mat(W[1], up, e, rows, cols), mat(W[2], down, e, cols, rows)
         return cache[e]
 
     for i in range(n):
@@ -46,16 +57,16 @@ def reference(W, E, rows, cols, up, down, x, ids, gate):
             e = int(ids[i, j])
             if not 0 <= e < E:
                 continue
-            wg, wu, wd = mats(e)
+            (wg, mg), (wu, mu), (wd, md) = mats(e)
             xi = x[i].astype(np.float64)
             g, u = wg @ xi, wu @ xi
-            eg, eu = (1e-4 * (np.abs(w) @ np.abs(xi)) + 1e-6 for w in (wg, wu))
+            eg, eu = (2.0**-17 * (m @ np.abs(xi)) + 1e-6 for m in (mg, mu))
             h = silu(g) * u
             eh = 1.1 * eg * (np.abs(u) + eu) + np.abs(silu(g)) * eu + 2.0**-20 * np.abs(h)
             a = abs(float(gate[i, j]))
-            big = np.abs(wd) @ (np.abs(h) + eh)
+            big = md @ (np.abs(h) + eh)
             out[i] += float(gate[i, j]) * (wd @ h)
-            tol[i] += a * (np.abs(wd) @ eh + 1e-4 * big + 1e-6) + a * big * (k + 24) * 2.0**-24
+            tol[i] += a * (np.abs(wd) @ eh + 2.0**-17 * big + 1e-6) + a * big * (k + 24) * 2.0**-24
     return out, tol
 
 

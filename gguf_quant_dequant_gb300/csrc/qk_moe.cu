@@ -1,60 +1,137 @@
-// qk_moe.cu -- a mixture-of-experts layer (qk_moe_ffn): the router's logits,
-// and the launches of the layer.
+// qk_moe.cu -- a mixture-of-experts layer (qk_moe_ffn): the router, the last
+// sum, and the launches of the layer.
+#include <cooperative_groups.h>
+
 #include "qk_internal.h"
 #include "qk_moe.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace qk {
 namespace moe {
 
-// Router logits [n_tok, n_exp] = x R^T in fp32: a warp per expert and TT
-// tokens, a lane's products in four running sums.  The matrix is read once per
-// TT tokens (L2 serves the repeats); a megabyte of it, so latency bounds it.
-constexpr int kRouteWarps = 4;
+// Order-preserving image of a float: one for both zeros, NaN above all.
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t u = __float_as_uint(v), mag = u & 0x7fffffffu;
+    if (mag > 0x7f800000u) return 0xffffffffu;
+    return (u >> 31) && mag ? ~u : mag | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+
+// One warp, one token: the k largest of n logits (logit(e); the lowest index of
+// equals), their softmax over all n or over the k.
+template <int NE, class F>
+__device__ __forceinline__ void choose(F logit, int n, int k, bool norm, float scale, int lane, int32_t* ids, float* gate) {
+    uint32_t key[NE];
+    float l[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < n ? logit(e) : -INFINITY;
+        key[i] = e < n ? key_of(l[i]) : 0u;
+    }
+    float top = 0.0f, mine = 0.0f, sum = 0.0f;   // lane j holds the j-th chosen
+    uint32_t taken = 0;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = 0;
+        int at = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (!(taken >> i & 1) && lane + 32 * i < n && (at == 0x7fffffff || key[i] > best)) {
+                best = key[i];
+                at = lane + 32 * i;
+            }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, at == 0x7fffffff ? 0u : best);
+        at = __reduce_min_sync(0xffffffffu, at != 0x7fffffff && best == most ? at : 0x7fffffff);
+        if ((at & 31) == lane) taken |= 1u << (at >> 5);
+        const float v = value_of(most);
+        if (j == 0) top = v;
+        const float e = expf(v - top);
+        if (norm) sum += e;
+        if (lane == j) mine = e;
+        if (lane == 0) ids[j] = at;
+    }
+    if (!norm) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) sum += lane + 32 * i < n ? expf(l[i] - top) : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane < k) gate[lane] = mine / sum * scale;
+}
+
+// The router: logits x R^T in fp32 (a lane's products in four running sums),
+// then the choice.  A cluster of CTAs takes TT tokens and shares out the
+// experts, a warp per expert; its logits meet in shared memory and CTA t
+// chooses for token t.  One launch: a first version that left the choice to
+// every CTA of the next kernel added 5 us there for 61 tokens of 128 experts.
+constexpr int kRouteCluster = 8, kRouteWarps = 16;
 
 template <int TT>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const float* __restrict__ x, const float* __restrict__ router,
-                                                                 int64_t cols, int n_tok, int n_exp, float* __restrict__ logits) {
-    const int lane = threadIdx.x & 31, e = blockIdx.x * kRouteWarps + (threadIdx.x >> 5), t0 = blockIdx.y * TT;
+                                                                 int64_t cols, int n_tok, int n_exp, int k, bool norm, float scale,
+                                                                 int32_t* __restrict__ ids, float* __restrict__ gate) {
+    __shared__ float logits[TT][QK_MOE_MAX_EXP / kRouteCluster];
+    cg::cluster_group cl = cg::this_cluster();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cl.block_rank();
+    const int t0 = (int)(blockIdx.x / kRouteCluster) * TT;
+    const int per = (n_exp + kRouteCluster - 1) / kRouteCluster, e0 = rank * per, e1 = min(e0 + per, n_exp);
     pdl_launch_dependents();
     pdl_wait_prior();   // x
-    if (e >= n_exp) return;
-    float4 acc[TT];
+    for (int e = e0 + warp; e < e1; e += kRouteWarps) {
+        float4 acc[TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float* w = router + (int64_t)e * cols;
-#pragma unroll 4
-    for (int64_t c = lane * 4; c < cols; c += 128) {
-        const float4 r = *reinterpret_cast<const float4*>(w + c);
+        for (int t = 0; t < TT; ++t) acc[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float* w = router + (int64_t)e * cols;
+#pragma unroll(TT == 1 ? 8 : 2)
+        for (int64_t c = lane * 4; c < cols; c += 128) {
+            const float4 r = __ldcs(reinterpret_cast<const float4*>(w + c));
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float4 v = *reinterpret_cast<const float4*>(x + (int64_t)min(t0 + t, n_tok - 1) * cols + c);
+                acc[t].x = fmaf(r.x, v.x, acc[t].x);
+                acc[t].y = fmaf(r.y, v.y, acc[t].y);
+                acc[t].z = fmaf(r.z, v.z, acc[t].z);
+                acc[t].w = fmaf(r.w, v.w, acc[t].w);
+            }
+        }
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const float4 v = *reinterpret_cast<const float4*>(x + (int64_t)min(t0 + t, n_tok - 1) * cols + c);
-            acc[t].x = fmaf(r.x, v.x, acc[t].x);
-            acc[t].y = fmaf(r.y, v.y, acc[t].y);
-            acc[t].z = fmaf(r.z, v.z, acc[t].z);
-            acc[t].w = fmaf(r.w, v.w, acc[t].w);
+            float v = (acc[t].x + acc[t].y) + (acc[t].z + acc[t].w);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) logits[t][e - e0] = v;
         }
     }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        float v = (acc[t].x + acc[t].y) + (acc[t].z + acc[t].w);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0 && t0 + t < n_tok) logits[(int64_t)(t0 + t) * n_exp + e] = v;
+    cl.sync();
+    for (int t = rank; t < TT; t += kRouteCluster) {
+        const int tok = t0 + t;
+        if (warp != 0 || tok >= n_tok) continue;
+        auto logit = [&](int e) { return cl.map_shared_rank(&logits[t][0], e / per)[e % per]; };
+        int32_t* io = ids + (int64_t)tok * k;
+        float* go = gate + (int64_t)tok * k;
+        if (n_exp <= 128) choose<4>(logit, n_exp, k, norm, scale, lane, io, go);
+        else if (n_exp <= 256) choose<8>(logit, n_exp, k, norm, scale, lane, io, go);
+        else choose<16>(logit, n_exp, k, norm, scale, lane, io, go);
     }
+    cl.sync();   // nobody leaves while its logits are read
 }
 
 template <int TT>
-static cudaError_t route(const float* x, const float* router, int64_t cols, int n_tok, int n_exp, float* logits, cudaStream_t s) {
+static cudaError_t route(const MoeArgs& m, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((n_exp + kRouteWarps - 1) / kRouteWarps), (unsigned)((n_tok + TT - 1) / TT));
+    cfg.gridDim = dim3((unsigned)((m.n_tok + TT - 1) / TT * kRouteCluster));
     cfg.blockDim = dim3(kRouteWarps * 32);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kRouteCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, route_kernel<TT>, x, router, cols, n_tok, n_exp, logits);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, route_kernel<TT>, m.x, m.router, m.cols, m.n_tok, m.n_exp, m.k, m.norm, m.scale, m.ids, m.gate);
 }
 
 // out[tok] = sum over the token's experts of gate * y, y the slices' sums added
@@ -88,12 +165,10 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const float* __restric
     o[0] = acc.x, o[1] = acc.y, o[2] = acc.z, o[3] = acc.w;
 }
 
-static int64_t logits_bytes(int n_tok, int n_exp) { return ((int64_t)n_tok * n_exp * 4 + 15) & ~(int64_t)15; }
-
 }  // namespace moe
 
-// The arguments of the two products and their workspace: the router's logits,
-// the sums of `up`, those of `down`.
+// The arguments of the two products and their workspace: the sums of `up`, then
+// those of `down`.
 static cudaError_t set_up(const MoeArgs& m, int sms, moe::Args& up, moe::Args& down, int64_t* bytes) {
     up = moe::Args{};
     up.cols = m.cols;
@@ -108,44 +183,37 @@ static cudaError_t set_up(const MoeArgs& m, int sms, moe::Args& up, moe::Args& d
     cudaError_t e = moe::launch_up(m.type, up, sms, nullptr, false);
     if (e == cudaSuccess) e = moe::launch_down(m.type_down, down, sms, nullptr, false);
     if (e != cudaSuccess) return e;
-    bytes[0] = moe::logits_bytes(m.n_tok, m.n_exp);
-    bytes[1] = (int64_t)2 * up.slices * up.pairs * m.rows * 4;
-    bytes[2] = (int64_t)down.slices * up.pairs * m.cols * 4;
+    bytes[0] = (int64_t)2 * up.slices * up.pairs * m.rows * 4;
+    bytes[1] = (int64_t)down.slices * up.pairs * m.cols * 4;
     return e;
 }
 
 int64_t moe_ws_bytes(const MoeArgs& m, int sms) {
     moe::Args up, down;
-    int64_t bytes[3];
-    return set_up(m, sms, up, down, bytes) == cudaSuccess ? bytes[0] + bytes[1] + bytes[2] : 0;
+    int64_t bytes[2];
+    return set_up(m, sms, up, down, bytes) == cudaSuccess ? bytes[0] + bytes[1] : 0;
 }
 
 cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStream_t s) {
     moe::Args up, down;
-    int64_t bytes[3];
+    int64_t bytes[2];
     cudaError_t e = set_up(m, sms, up, down, bytes);
     if (e != cudaSuccess) return e;
-    float* logits = static_cast<float*>(m.ws);
-    float* sums = logits + bytes[0] / 4;
-    float* y = sums + bytes[1] / 4;
+    float* sums = static_cast<float*>(m.ws);
+    float* y = sums + bytes[0] / 4;
     if (m.router) {
-        e = m.n_tok == 1 ? moe::route<1>(m.x, m.router, m.cols, m.n_tok, m.n_exp, logits, s)
-                         : moe::route<8>(m.x, m.router, m.cols, m.n_tok, m.n_exp, logits, s);
+        e = m.n_tok == 1 ? moe::route<1>(m, s) : moe::route<8>(m, s);
         if (e != cudaSuccess) return e;
     }
     up.x = m.x;
     up.W0 = static_cast<const uint8_t*>(m.Wg);
     up.W1 = static_cast<const uint8_t*>(m.Wu);
-    up.logits = m.router ? logits : nullptr;
-    up.norm = m.norm;
-    up.scale = m.scale;
     up.out = sums;
     down.x = sums;
     down.slices_in = up.slices;
     down.W0 = down.W1 = static_cast<const uint8_t*>(m.Wd);
     down.out = y;
     up.ids = down.ids = m.ids;
-    up.gate = down.gate = m.gate;
     up.status = down.status = status;
     e = moe::launch_up(m.type, up, sms, s, true);
     if (e == cudaSuccess) e = moe::launch_down(m.type_down, down, sms, s, true);

@@ -18,7 +18,8 @@
 //     and the sums of the stage's warps took longer than the products: 61
 //     tokens, 8 of 128 experts of 2048 x 768: 374 us a layer.
 //   * Two more warps prepare the activations of the next (group, slice) while
-//     the others work on one: x in `up`, SiLU(g) * u in `down`.
+//     the others work on one: x in `up`, SiLU(g) * u in `down` (the first two are
+//     prepared by all).
 //   * Slices of K leave partial sums, added in order by whoever reads them: the
 //     preparation of `down`, and a last kernel that also weighs and adds the
 //     experts.  The result does not depend on timing.
@@ -47,11 +48,7 @@ struct Args {
     uint32_t row_bytes;
     const uint8_t *W0, *W1;     // up: gate and up matrices; down: its matrix, twice
     int n_exp, n_tok, k, pairs;
-    const float* logits;        // router's logits [n_tok, n_exp] (up only), or nullptr: ids are given
-    bool norm;
-    float scale;
-    int32_t* ids;               // [n_tok, k]
-    float* gate;
+    const int32_t* ids;         // [n_tok, k]
     float* out;                 // up: [2][slices][pairs][rows]; down: [slices][pairs][rows]
     int nxb, nunits;            // of a row: 32-blocks, units
     int ku, slices;             // units of a slice; slices of a row
@@ -61,82 +58,6 @@ struct Args {
     uint32_t off_pairs, off_gexp, off_gbeg, off_gcnt, off_bar, off_x, off_ring;
     unsigned* status;
 };
-
-// ------------------------------------------------------- choice of experts --
-// Order-preserving image of a float: one for both zeros, NaN above all.
-__device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v), mag = u & 0x7fffffffu;
-    if (mag > 0x7f800000u) return 0xffffffffu;
-    return (u >> 31) && mag ? ~u : mag | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
-
-// One warp, one token: the k largest of n logits (the lowest index of equals),
-// their softmax over all n or over the k.
-template <int NE>
-__device__ __forceinline__ void choose(const float* lg, int n, int k, bool norm, float scale, int lane, uint16_t* ids, int32_t* ids_out,
-                                       float* gate_out) {
-    uint32_t key[NE];
-    float l[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < n ? __ldcg(lg + e) : -INFINITY;
-        key[i] = e < n ? key_of(l[i]) : 0u;
-    }
-    float top = 0.0f, mine = 0.0f, sum = 0.0f;   // lane j holds the j-th chosen
-    uint32_t taken = 0;
-    for (int j = 0; j < k; ++j) {
-        uint32_t best = 0;
-        int at = 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (!(taken >> i & 1) && lane + 32 * i < n && (at == 0x7fffffff || key[i] > best)) {
-                best = key[i];
-                at = lane + 32 * i;
-            }
-        const uint32_t most = __reduce_max_sync(0xffffffffu, at == 0x7fffffff ? 0u : best);
-        at = __reduce_min_sync(0xffffffffu, at != 0x7fffffff && best == most ? at : 0x7fffffff);
-        if ((at & 31) == lane) taken |= 1u << (at >> 5);
-        const float v = value_of(most);
-        if (j == 0) top = v;
-        const float e = expf(v - top);
-        if (norm) sum += e;
-        if (lane == j) mine = e;
-        if (lane == 0) {
-            ids[j] = (uint16_t)at;
-            if (ids_out) ids_out[j] = at;
-        }
-    }
-    if (!norm) {
-#pragma unroll
-        for (int i = 0; i < NE; ++i) sum += lane + 32 * i < n ? expf(l[i] - top) : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    if (gate_out && lane < k) gate_out[lane] = mine / sum * scale;
-}
-
-// The ids of all pairs in shared memory (kNone: none), chosen from the router's
-// logits (the first CTA hands them out) or read.
-__device__ __forceinline__ void gather_ids(const Args& p, uint16_t* ids) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (p.logits) {
-        for (int tok = warp; tok < p.n_tok; tok += blockDim.x >> 5) {
-            const float* lg = p.logits + (int64_t)tok * p.n_exp;
-            int32_t* io = blockIdx.x == 0 ? p.ids + (int64_t)tok * p.k : nullptr;
-            float* go = blockIdx.x == 0 ? p.gate + (int64_t)tok * p.k : nullptr;
-            if (p.n_exp <= 128) choose<4>(lg, p.n_exp, p.k, p.norm, p.scale, lane, ids + tok * p.k, io, go);
-            else if (p.n_exp <= 256) choose<8>(lg, p.n_exp, p.k, p.norm, p.scale, lane, ids + tok * p.k, io, go);
-            else choose<16>(lg, p.n_exp, p.k, p.norm, p.scale, lane, ids + tok * p.k, io, go);
-        }
-    } else {
-        for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
-            const int e = __ldcg(p.ids + i);
-            ids[i] = e >= 0 && e < p.n_exp ? (uint16_t)e : kNone;
-        }
-    }
-}
 
 struct Tables {
     uint16_t *pairs, *gexp, *gbeg, *gcnt;   // pairs by expert; expert, first pair and pairs of a group
@@ -148,6 +69,21 @@ struct Tables {
 template <int CAP>
 __device__ __forceinline__ void make_groups(const Args& p, const Tables& t, const uint16_t* ids, int* scratch) {
     const int tid = threadIdx.x, lane = tid & 31;
+    if (p.n_tok == 1) {   // every pair is a group of its own
+        if (tid < 32) {
+            const bool ok = lane < p.pairs && ids[lane] != kNone;   // at most 16
+            const unsigned m = __ballot_sync(0xffffffffu, ok);
+            const int at = __popc(m & ((1u << lane) - 1));
+            if (ok) {
+                t.pairs[at] = (uint16_t)lane;
+                t.gexp[at] = ids[lane];
+                t.gbeg[at] = (uint16_t)at;
+                t.gcnt[at] = 1;
+            }
+            if (lane == 0) *t.n = __popc(m);
+        }
+        return;
+    }
     int* count = scratch;
     int* offs = scratch + p.n_exp;
     for (int e = tid; e < p.n_exp; e += blockDim.x) count[e] = 0;
@@ -282,11 +218,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
         fence_barrier_init();
     }
     pdl_launch_dependents();
-    pdl_wait_prior();   // the router's logits, or the sums of `up` and the ids
+    pdl_wait_prior();   // the ids; x or the sums of `up`
     {
         uint16_t* ids = reinterpret_cast<uint16_t*>(smem + p.off_ring);   // before the first fetch
         int* scratch = reinterpret_cast<int*>(smem + p.off_ring + 2 * ((p.pairs + 7) & ~7));
-        gather_ids(p, ids);
+        for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
+            const int e = __ldcg(p.ids + i);
+            ids[i] = e >= 0 && e < p.n_exp ? (uint16_t)e : kNone;
+        }
         __syncthreads();
         make_groups<NT>(p, tb, ids, scratch);
         __syncthreads();
@@ -297,58 +236,51 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     if (j0 >= j1) return;
     const int e0 = (int)(j0 / p.jobs), e1 = (int)((j1 - 1) / p.jobs);   // my (group, slice)s
 
-    if (warp >= p.nw) {
-        // ---------------- prepares activations ----------------
-        for (int e = e0; e <= e1; ++e) {
-            const int set = (e - e0) & 1, turn = (e - e0) >> 1;
-            if (turn > 0 && !mbar_wait_abortable(&xfree[set], (uint32_t)(turn - 1) & 1u, p.status, abort)) return;
-            const int g = e / p.slices, u0 = (e - g * p.slices) * p.ku, nu = min(p.ku, p.nunits - u0);
-            const int n = tb.gcnt[g], beg = tb.gbeg[g];
-            uint8_t* xb = xbuf + set * x_set;
-            float4* xm = reinterpret_cast<float4*>(xb + x_bytes);
-            constexpr int kAt = 2;   // in flight at a time
-            for (int i0 = (warp - p.nw) * kAt; i0 < nu * n; i0 += kPrepWarps * kAt) {
-                float4 a[kAt], b[kAt];
-                int at[kAt], un[kAt];
+    // The activations of (group, slice) e into its set: items (unit, pair) from `first` on, every `step`-th two.
+    auto prepare = [&](int e, int first, int step) {
+        const int set = (e - e0) & 1, g = e / p.slices, u0 = (e - g * p.slices) * p.ku, nu = min(p.ku, p.nunits - u0);
+        const int n = tb.gcnt[g], beg = tb.gbeg[g];
+        uint8_t* xb = xbuf + set * x_set;
+        float4* xm = reinterpret_cast<float4*>(xb + x_bytes);
+        for (int i0 = 2 * first; i0 < nu * n; i0 += 2 * step) {
+            float4 a[2], b[2];
+            int at[2], un[2];
 #pragma unroll
-                for (int m = 0; m < kAt; ++m) {
-                    const int i = min(i0 + m, nu * n - 1);
-                    un[m] = i / n;
-                    at[m] = i - un[m] * n;
-                    const int pair = tb.pairs[beg + at[m]], u = u0 + un[m];
-                    a[m] = b[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (8 * u + (lane >> 2) < p.nxb) {
-                        const float4* src = reinterpret_cast<const float4*>(
-                            p.x + (int64_t)(DOWN ? pair : pair / p.k) * p.cols + (int64_t)u * kUnitW + 8 * lane);
+            for (int m = 0; m < 2; ++m) {
+                const int i = min(i0 + m, nu * n - 1);
+                un[m] = i / n;
+                at[m] = i - un[m] * n;
+                const int pair = tb.pairs[beg + at[m]], u = u0 + un[m];
+                a[m] = b[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (8 * u + (lane >> 2) < p.nxb) {
+                    const float4* src = reinterpret_cast<const float4*>(
+                        p.x + (int64_t)(DOWN ? pair : pair / p.k) * p.cols + (int64_t)u * kUnitW + 8 * lane);
+                    if constexpr (!DOWN) {
                         a[m] = __ldcg(src);
                         b[m] = __ldcg(src + 1);
-                        if constexpr (DOWN) {
-                            const int64_t slice = (int64_t)p.pairs * p.cols / 4, up = slice * p.slices_in;
-                            float4 c = __ldcg(src + up), d = __ldcg(src + up + 1);
-                            for (int k = 1; k < p.slices_in; ++k) {
-                                const float4 a2 = __ldcg(src + k * slice), b2 = __ldcg(src + k * slice + 1);
-                                const float4 c2 = __ldcg(src + up + k * slice), d2 = __ldcg(src + up + k * slice + 1);
-                                a[m].x += a2.x, a[m].y += a2.y, a[m].z += a2.z, a[m].w += a2.w;
-                                b[m].x += b2.x, b[m].y += b2.y, b[m].z += b2.z, b[m].w += b2.w;
-                                c.x += c2.x, c.y += c2.y, c.z += c2.z, c.w += c2.w;
-                                d.x += d2.x, d.y += d2.y, d.z += d2.z, d.w += d2.w;
-                            }
-                            auto h = [](float g, float u) { return g / (1.0f + expf(-g)) * u; };   // SiLU(g) u
-                            a[m] = make_float4(h(a[m].x, c.x), h(a[m].y, c.y), h(a[m].z, c.z), h(a[m].w, c.w));
-                            b[m] = make_float4(h(b[m].x, d.x), h(b[m].y, d.y), h(b[m].z, d.z), h(b[m].w, d.w));
+                    } else {
+                        const int64_t slice = (int64_t)p.pairs * p.cols / 4, up = slice * p.slices_in;
+                        float4 c = a[m], d = a[m];
+                        auto add = [](float4& v, float4 w) { v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w; };
+#pragma unroll 4
+                        for (int k = 0; k < p.slices_in; ++k) {
+                            add(a[m], __ldcg(src + k * slice));
+                            add(b[m], __ldcg(src + k * slice + 1));
+                            add(c, __ldcg(src + up + k * slice));
+                            add(d, __ldcg(src + up + k * slice + 1));
                         }
+                        auto h = [](float g, float u) { return g / (1.0f + expf(-g)) * u; };   // SiLU(g) u
+                        a[m] = make_float4(h(a[m].x, c.x), h(a[m].y, c.y), h(a[m].z, c.z), h(a[m].w, c.w));
+                        b[m] = make_float4(h(b[m].x, d.x), h(b[m].y, d.y), h(b[m].z, d.z), h(b[m].w, d.w));
                     }
                 }
-#pragma unroll
-                for (int m = 0; m < kAt; ++m)
-                    if (i0 + m < nu * n)
-                        dm::put_x<NT, U::kW4, U::kMin && U::kG16>(a[m], b[m], xb + un[m] * (NT * dm::kXRow), xm + un[m] * 8 * NT, at[m], lane);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&xfull[set]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                if (i0 + m < nu * n)
+                    dm::put_x<NT, U::kW4, U::kMin && U::kG16>(a[m], b[m], xb + un[m] * (NT * dm::kXRow), xm + un[m] * 8 * NT, at[m], lane);
         }
-        return;
-    }
+    };
 
     // ---------------- multiplies ----------------
     const int g8 = lane >> 2, t = lane & 3;
@@ -386,10 +318,24 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
         if (s.job < j1) enter(s);
     };
     Step cur, ahead;
-    cur.job = j0 + warp;
+    cur.job = warp < p.nw ? j0 + warp : j1;
     if (cur.job < j1) enter(cur);
     ahead = cur;
     fetch(ahead, 0);
+    // All warps prepare the first two sets, then two of them the others while the rest multiplies.
+    prepare(e0, warp, p.nw + kPrepWarps);
+    if (e0 < e1) prepare(e0 + 1, warp, p.nw + kPrepWarps);
+    __syncthreads();
+    if (warp >= p.nw) {
+        for (int e = e0 + 2; e <= e1; ++e) {
+            const int set = (e - e0) & 1, turn = (e - e0) >> 1;
+            if (!mbar_wait_abortable(&xfree[set], (uint32_t)(turn - 1) & 1u, p.status, abort)) return;
+            prepare(e, warp - p.nw, kPrepWarps);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&xfull[set]);
+        }
+        return;
+    }
     int slot = 0, e = e0 - 1;   // e: the activations in use
     bool dead = false;
     // Leaves the activations up to those before `to` (in their order: a set is free when every warp has left it).
@@ -399,7 +345,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&xfree[(e - e0) & 1]);
             }
-            if (e + 1 <= e1 && !mbar_wait_abortable(&xfull[(e + 1 - e0) & 1], (uint32_t)((e + 1 - e0) >> 1) & 1u, p.status, abort)) dead = true;
+            const int turn = (e + 1 - e0) >> 1;
+            if (e + 1 <= e1 && turn > 0 && !mbar_wait_abortable(&xfull[(e + 1 - e0) & 1], (uint32_t)(turn - 1) & 1u, p.status, abort))
+                dead = true;
         }
     };
     while (cur.job < j1 && !dead) {

@@ -135,7 +135,7 @@ def test_moe_ffn_refusals(lib, kw, status):
 
 def test_moe_sizes_and_binding_refusals(lib):
     assert len(qk.SIGNATURES["qk_moe_ffn"][1]) == len(MOE)
-    assert qk.moe_workspace(qk.Q4_K, qk.Q6_K, 8, 512, 256, 2, 3) >= 3 * 2 * (2 * 512 + 256) * 4 + 3 * 8 * 4
+    assert qk.moe_workspace(qk.Q4_K, qk.Q6_K, 8, 512, 256, 2, 3) >= 3 * 2 * (2 * 512 + 256) * 4
     for bad in ((qk.Q4_K, qk.Q6_K, 8, 512, 256, 2, 65), (qk.Q4_K, qk.Q6_K, 8, 512, 256, 9, 3), (0, qk.Q6_K, 8, 512, 256, 2, 3),
                 (qk.Q4_K, qk.Q6_K, 8, 512, 300, 2, 3)):
         assert qk.moe_workspace(*bad) == 0

@@ -736,7 +736,7 @@ qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t 
 
 static bool moe_shape_ok(int type, int type_down, int64_t n_tok, int k, int n_exp, int64_t rows, int64_t cols) {
     return n_tok >= 0 && n_tok <= QK_MOE_MAX_TOK && n_exp >= 1 && n_exp <= QK_MOE_MAX_EXP && k >= 1 && k <= QK_MOE_MAX_K &&
-           k <= n_exp && rows >= 1 && rows <= (1 << 18) && rows % block_elems(type_down) == 0 && cols >= 1 && cols <= (1 << 18) &&
+           k <= n_exp && rows >= 1 && rows <= (1 << 16) && rows % block_elems(type_down) == 0 && cols >= 1 && cols <= (1 << 16) &&
            cols % block_elems(type) == 0;
 }
 

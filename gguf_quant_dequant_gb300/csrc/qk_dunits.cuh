@@ -63,18 +63,23 @@ __device__ __forceinline__ void put_x(float4 a, float4 b, uint8_t* xb, float4* x
     if (q == 0) xm[blk * NT + row] = HALVES ? make_float4(m.z, m.w, m.y, m.y) : make_float4(m.x, m.x, m.y, m.y);
 }
 
-// Word at a 2-byte-aligned shared address.
-__device__ __forceinline__ uint32_t word_a2(const uint8_t* p) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    const uint8_t* b = reinterpret_cast<const uint8_t*>(a & ~uintptr_t(3));
-    return __funnelshift_r(lds32(b), lds32(b + 4), (uint32_t)(a & 3) * 8);
-}
-__device__ __forceinline__ uint2 words2_a2(const uint8_t* p) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    const uint8_t* b = reinterpret_cast<const uint8_t*>(a & ~uintptr_t(3));
-    const uint32_t sh = (uint32_t)(a & 3) * 8, w0 = lds32(b), w1 = lds32(b + 4), w2 = lds32(b + 8);
-    return make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
-}
+// Words of a row that starts on an even shared address: aligned words joined
+// by a shift that is the row's own.
+struct Even {
+    const uint8_t* p;   // the word boundary at or before the row
+    uint32_t sh;
+    __device__ __forceinline__ void set(const uint8_t* r) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(r);
+        p = reinterpret_cast<const uint8_t*>(a & ~uintptr_t(3));
+        sh = (uint32_t)(a & 2) * 8;
+    }
+    // The word at byte o of the row (a multiple of 4), and the two from it on.
+    __device__ __forceinline__ uint32_t word(int o) const { return __funnelshift_r(lds32(p + o), lds32(p + o + 4), sh); }
+    __device__ __forceinline__ uint2 words(int o) const {
+        const uint32_t w0 = lds32(p + o), w1 = lds32(p + o + 4), w2 = lds32(p + o + 8);
+        return make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
+    }
+};
 template <class V>
 __device__ __forceinline__ V from(V v, int src) { return __shfl_sync(0xffffffffu, v, src); }
 
@@ -195,7 +200,7 @@ template <> struct DU<T_Q6_K> {
     __device__ static __forceinline__ int block(int c, int b) { return 4 * (c >> 1) + (c & 1) + 2 * b; }
     struct Ctx {
         float f0[4], f1[4];   // d * scale of the thread's own pair: block, half
-        const uint8_t *r0, *r1;
+        Even r0, r1;
         uint32_t h0[2], h1[2];   // high bits of the current half
     };
     __device__ static __forceinline__ void own(const uint8_t* r, int t, float (&f)[4]) {
@@ -208,20 +213,20 @@ template <> struct DU<T_Q6_K> {
     __device__ static __forceinline__ void load(Ctx& x, const uint8_t* r0, const uint8_t* r1, int lane) {
         own(r0, lane & 3, x.f0);
         own(r1, lane & 3, x.f1);
-        x.r0 = r0 + 4 * (lane & 3);
-        x.r1 = r1 + 4 * (lane & 3);
+        x.r0.set(r0 + 4 * (lane & 3));
+        x.r1.set(r1 + 4 * (lane & 3));
     }
     __device__ static __forceinline__ void pair(Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const int src = (lane & 28) | c, th = c >> 1, gl = c & 1, sh = 4 - 2 * gl;
         if (gl == 0) {
-            x.h0[0] = word_a2(x.r0 + 128 + 32 * th), x.h0[1] = word_a2(x.r0 + 144 + 32 * th);
-            x.h1[0] = word_a2(x.r1 + 128 + 32 * th), x.h1[1] = word_a2(x.r1 + 144 + 32 * th);
+            x.h0[0] = x.r0.word(128 + 32 * th), x.h0[1] = x.r0.word(144 + 32 * th);
+            x.h1[0] = x.r1.word(128 + 32 * th), x.h1[1] = x.r1.word(144 + 32 * th);
         }
         const uint32_t CLO = dup16(0xE420u), CHI = dup16(0xD600u);   // -(1024 + 32), -(64 + 32)
         auto cv = [](uint32_t lo, uint32_t m1, uint32_t hi, uint32_t m2, uint32_t mg) { return and_or(lo, m1, and_or(hi, m2, mg)); };
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t q0 = word_a2(x.r0 + 64 * th + 32 * gl + 16 * j), q1 = word_a2(x.r1 + 64 * th + 32 * gl + 16 * j);
+            const uint32_t q0 = x.r0.word(64 * th + 32 * gl + 16 * j), q1 = x.r1.word(64 * th + 32 * gl + 16 * j);
             const uint32_t v0 = x.h0[j] << sh, v1 = x.h1[j] << sh, e0 = x.h0[j] >> (8 - sh), e1 = x.h1[j] >> (8 - sh);
             A[0][j][0] = hadd2(cv(q0, 0x000F000Fu, v0, 0x00300030u, 0x64006400u), CLO);
             A[0][j][1] = hadd2(cv(q1, 0x000F000Fu, v1, 0x00300030u, 0x64006400u), CLO);
@@ -247,17 +252,18 @@ struct Blocks32 {
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
         float d0[2], d1[2];   // the thread's own pair
-        const uint8_t *r0, *r1;
+        Even q0[2], q1[2];    // behind the scales of the first pair's blocks; a pair is a multiple of 4 bytes
     };
     __device__ static __forceinline__ void load(Ctx& x, const uint8_t* r0, const uint8_t* r1, int lane) {
+        static_assert(2 * BB % 4 == 0, "pairs keep the alignment");
         const int t = lane & 3;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             x.d0[b] = h2f(ld_u16(r0 + BB * (2 * t + b)));
             x.d1[b] = h2f(ld_u16(r1 + BB * (2 * t + b)));
+            x.q0[b].set(r0 + BB * b + 2);
+            x.q1[b].set(r1 + BB * b + 2);
         }
-        x.r0 = r0;
-        x.r1 = r1;
     }
     __device__ static __forceinline__ void scales(const Ctx& x, int src, Scale (&s)[2]) {
 #pragma unroll
@@ -274,8 +280,8 @@ template <> struct DU<T_Q8_0> : Blocks32<34> {
         const uint32_t C = dup16(0xE480u);   // -(1024 + 128)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int at = 34 * (2 * c + b) + 2 + 8 * (lane & 3);
-            const uint2 w0 = words2_a2(x.r0 + at), w1 = words2_a2(x.r1 + at);
+            const int at = 68 * c + 8 * (lane & 3);
+            const uint2 w0 = x.q0[b].words(at), w1 = x.q1[b].words(at);
             const uint32_t u0[2] = {w0.x, w0.y}, u1[2] = {w1.x, w1.y};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -297,8 +303,8 @@ template <> struct DU<T_Q4_0> : Blocks32<18> {
         const uint32_t LO = dup16(0xE408u), HI = dup16(0xD480u);   // -(1024 + 8), -(64 + 8)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int at = 18 * (2 * c + b) + 2 + 4 * (lane & 3);
-            const uint32_t w0 = word_a2(x.r0 + at), w1 = word_a2(x.r1 + at);
+            const int at = 36 * c + 4 * (lane & 3);
+            const uint32_t w0 = x.q0[b].word(at), w1 = x.q1[b].word(at);
             frag(A[b][0], w0, w1, 0x000F000Fu, 0x64006400u, LO, LO);
             frag(A[b][1], w0, w1, 0x00F000F0u, 0x54005400u, HI, HI);
         }
@@ -317,9 +323,8 @@ template <> struct DU<T_Q5_0> : Blocks32<22> {
         auto hi = [&](uint32_t w, uint32_t q) { return and_or(w >> 4, 0x0F0F0F0Fu, HU<T_Q5_0>::spread(q >> (16 + 4 * t))); };
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int at = 22 * (2 * c + b) + 2;
-            const uint32_t w0 = word_a2(x.r0 + at + 4 + 4 * t), w1 = word_a2(x.r1 + at + 4 + 4 * t);
-            const uint32_t q0 = word_a2(x.r0 + at), q1 = word_a2(x.r1 + at);
+            const uint32_t w0 = x.q0[b].word(44 * c + 4 + 4 * t), w1 = x.q1[b].word(44 * c + 4 + 4 * t);
+            const uint32_t q0 = x.q0[b].word(44 * c), q1 = x.q1[b].word(44 * c);
             frag(A[b][0], lo(w0, q0), lo(w1, q1), 0x001F001Fu, 0x64006400u, C, C);
             frag(A[b][1], hi(w0, q0), hi(w1, q1), 0x001F001Fu, 0x64006400u, C, C);
         }
@@ -378,10 +383,12 @@ template <> struct DU<T_Q3_K> {
     struct Ctx {
         float f0[4], f1[4];
         uint32_t m0[2], m1[2];   // mask bits of the thread's words, all blocks
-        const uint8_t *r0, *r1;
+        Even r0, r1;             // from byte 4t on
     };
     __device__ static __forceinline__ void own(const uint8_t* r, int t, float (&f)[4]) {
-        const uint32_t l = word_a2(r + 96 + 4 * (t & 1)), u = word_a2(r + 104);
+        Even w;
+        w.set(r);
+        const uint32_t l = w.word(96 + 4 * (t & 1)), u = w.word(104);
         const uint32_t S = ((l >> (4 * (t >> 1))) & 0x0F0F0F0Fu) | (((u >> (2 * t)) & 0x03030303u) << 4);
         const float d = h2f(ld_u16(r + 108));
 #pragma unroll
@@ -391,16 +398,16 @@ template <> struct DU<T_Q3_K> {
         const int t = lane & 3;
         own(r0, t, x.f0);
         own(r1, t, x.f1);
-        x.m0[0] = word_a2(r0 + 4 * t), x.m0[1] = word_a2(r0 + 16 + 4 * t);
-        x.m1[0] = word_a2(r1 + 4 * t), x.m1[1] = word_a2(r1 + 16 + 4 * t);
-        x.r0 = r0 + 32 + 4 * t;
-        x.r1 = r1 + 32 + 4 * t;
+        x.r0.set(r0 + 4 * t);
+        x.r1.set(r1 + 4 * t);
+        x.m0[0] = x.r0.word(0), x.m0[1] = x.r0.word(16);
+        x.m1[0] = x.r1.word(0), x.m1[1] = x.r1.word(16);
     }
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const int src = (lane & 28) | c, tp = c >> 1, j0 = 2 * (c & 1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t w0 = word_a2(x.r0 + 32 * tp + 16 * j), w1 = word_a2(x.r1 + 32 * tp + 16 * j);
+            const uint32_t w0 = x.r0.word(32 + 32 * tp + 16 * j), w1 = x.r1.word(32 + 32 * tp + 16 * j);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 // the code's two bits 2 jb .. of a byte, its mask bit moved from 4 tp + jb to 2 jb + 2; magic 2^(10 - 2 jb)

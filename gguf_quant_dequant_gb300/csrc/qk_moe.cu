@@ -62,46 +62,75 @@ __device__ __forceinline__ void choose(F logit, int n, int k, bool norm, float s
 
 // The router: logits x R^T in fp32 (a lane's products in four running sums),
 // then the choice.  A cluster of CTAs takes TT tokens and shares out the
-// experts, a warp per expert; its logits meet in shared memory and CTA t
-// chooses for token t.  One launch: a first version that left the choice to
-// every CTA of the next kernel added 5 us there for 61 tokens of 128 experts.
-constexpr int kRouteCluster = 8, kRouteWarps = 16;
+// experts, a warp per expert (or several, by columns, where there are fewer
+// experts than warps); its logits meet in shared memory and CTA t chooses for
+// token t.  Latency bounds it: the tokens go through shared memory, so that a
+// lane's eight loads of the router are in flight at a time.  In one launch: a
+// first version that left the choice to every CTA of the next kernel added 5 us
+// there for 61 tokens of 128 experts.
+constexpr int kRouteCluster = 8, kRouteWarps = 16, kRouteCols = 2048;   // columns of the tokens in shared memory at a time
 
 template <int TT>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const float* __restrict__ x, const float* __restrict__ router,
                                                                  int64_t cols, int n_tok, int n_exp, int k, bool norm, float scale,
                                                                  int32_t* __restrict__ ids, float* __restrict__ gate) {
-    __shared__ float logits[TT][QK_MOE_MAX_EXP / kRouteCluster];
+    constexpr int kPer = QK_MOE_MAX_EXP / kRouteCluster;
+    __shared__ float logits[TT][kPer], parts[kPer][TT];   // [expert's part] where warps share a row
+    __shared__ __align__(16) float xs[TT * kRouteCols];
     cg::cluster_group cl = cg::this_cluster();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cl.block_rank();
-    const int t0 = (int)(blockIdx.x / kRouteCluster) * TT;
-    const int per = (n_exp + kRouteCluster - 1) / kRouteCluster, e0 = rank * per, e1 = min(e0 + per, n_exp);
+    const int t0 = (int)(blockIdx.x / kRouteCluster) * TT, width = (int)cols;
+    const int per = (n_exp + kRouteCluster - 1) / kRouteCluster, e0 = rank * per, mine = max(0, min(per, n_exp - e0));
+    // Fewer experts than warps: several warps to a row of the router.
+    const int share = per >= kRouteWarps ? 1 : kRouteWarps / per, part = warp % share;
+    const bool on = warp < kRouteWarps / share * share;
     pdl_launch_dependents();
     pdl_wait_prior();   // x
-    for (int e = e0 + warp; e < e1; e += kRouteWarps) {
-        float4 acc[TT];
+    for (int i = threadIdx.x; i < kPer * TT; i += kRouteWarps * 32) (&parts[0][0])[i] = 0.0f;
+    for (int base = 0; base < width; base += kRouteCols) {
+        const int n = min(kRouteCols, width - base);
+        __syncthreads();   // all are done with the columns before
+        for (int i = threadIdx.x; i < TT * (n / 4); i += kRouteWarps * 32) {
+            const int t = i / (n / 4), c = 4 * (i - t * (n / 4));
+            cp_async16(&xs[t * kRouteCols + c], x + (int64_t)min(t0 + t, n_tok - 1) * cols + base + c);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        for (int e = warp / share; e < mine && on; e += kRouteWarps / share) {
+            float4 acc[TT];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float* w = router + (int64_t)e * cols;
-#pragma unroll(TT == 1 ? 8 : 2)
-        for (int64_t c = lane * 4; c < cols; c += 128) {
-            const float4 r = __ldcs(reinterpret_cast<const float4*>(w + c));
+            for (int t = 0; t < TT; ++t) acc[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float* w = router + (int64_t)(e0 + e) * cols + base;
+            const int c0 = lane * 4 + part * 128, steps = c0 < n ? (n - 1 - c0) / (128 * share) + 1 : 0;
+#pragma unroll 8
+            for (int i = 0; i < steps; ++i) {
+                const int c = c0 + i * 128 * share;
+                const float4 r = __ldg(reinterpret_cast<const float4*>(w + c));
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const float4 v = *reinterpret_cast<const float4*>(&xs[t * kRouteCols + c]);
+                    acc[t].x = fmaf(r.x, v.x, acc[t].x);
+                    acc[t].y = fmaf(r.y, v.y, acc[t].y);
+                    acc[t].z = fmaf(r.z, v.z, acc[t].z);
+                    acc[t].w = fmaf(r.w, v.w, acc[t].w);
+                }
+            }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const float4 v = *reinterpret_cast<const float4*>(x + (int64_t)min(t0 + t, n_tok - 1) * cols + c);
-                acc[t].x = fmaf(r.x, v.x, acc[t].x);
-                acc[t].y = fmaf(r.y, v.y, acc[t].y);
-                acc[t].z = fmaf(r.z, v.z, acc[t].z);
-                acc[t].w = fmaf(r.w, v.w, acc[t].w);
+                float v = (acc[t].x + acc[t].y) + (acc[t].z + acc[t].w);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) parts[e * share + part][t] += v;
             }
         }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            float v = (acc[t].x + acc[t].y) + (acc[t].z + acc[t].w);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) logits[t][e - e0] = v;
-        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < mine * TT; i += kRouteWarps * 32) {
+        const int e = i / TT, t = i - e * TT;
+        float v = 0.0f;
+        for (int q = 0; q < share; ++q) v += parts[e * share + q][t];
+        logits[t][e] = v;
     }
     cl.sync();
     for (int t = rank; t < TT; t += kRouteCluster) {
@@ -135,34 +164,39 @@ static cudaError_t route(const MoeArgs& m, cudaStream_t s) {
 }
 
 // out[tok] = sum over the token's experts of gate * y, y the slices' sums added
-// in order.  Everything comes from L2: 61 tokens of 8 experts of 2048 rows read
-// 4 MB.
-constexpr int kSumThreads = 128;
-__global__ void __launch_bounds__(kSumThreads) sum_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids,
-                                                          const float* __restrict__ gate, int n_exp, int n_tok, int k, int64_t cols,
-                                                          int slices, float* __restrict__ out) {
+// in order.  A thread per expert and four columns, so that all loads are in
+// flight at once (they come from L2); the experts are then added in order.
+constexpr int kSumCols = 32;   // threads' columns of a CTA, four each
+__global__ void __launch_bounds__(kSumCols * QK_MOE_MAX_K) sum_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids,
+                                                                      const float* __restrict__ gate, int n_exp, int n_tok, int k,
+                                                                      int64_t cols, int slices, float* __restrict__ out) {
+    __shared__ float4 part[QK_MOE_MAX_K][kSumCols];
+    const int64_t c = ((int64_t)blockIdx.x * kSumCols + threadIdx.x) * 4;
+    const int tok = blockIdx.y, j = threadIdx.y, pair = tok * k + j;
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int64_t c = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) * 4;
-    const int tok = blockIdx.y;
-    if (c >= cols) return;
-    const int64_t slice = (int64_t)n_tok * k * cols;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-    for (int j = 0; j < k; ++j) {
-        const int pair = tok * k + j, e = __ldcg(ids + pair);
-        if (e < 0 || e >= n_exp) continue;   // nothing was written for it
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int e = __ldcg(ids + pair);
+    if (c < cols && e >= 0 && e < n_exp) {   // (nothing was written for a pair without an expert)
         const float g = __ldcg(gate + pair);
-        const float* src = y + (int64_t)pair * cols + c;
-        float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-        for (int s = 1; s < slices; ++s) {
-            const float4 w = __ldcg(reinterpret_cast<const float4*>(src + s * slice));
+        const float4* src = reinterpret_cast<const float4*>(y + (int64_t)pair * cols + c);
+        const int64_t slice = (int64_t)n_tok * k * cols / 4;
+#pragma unroll 4
+        for (int s = 0; s < slices; ++s) {
+            const float4 w = __ldcg(src + s * slice);
             v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
         }
-        acc.x += g * v.x, acc.y += g * v.y, acc.z += g * v.z, acc.w += g * v.w;
+        v.x *= g, v.y *= g, v.z *= g, v.w *= g;
+    }
+    part[j][threadIdx.x] = v;
+    __syncthreads();
+    if (j != 0 || c >= cols) return;
+    for (int q = 1; q < k; ++q) {
+        const float4 w = part[q][threadIdx.x];
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
     float* o = out + (int64_t)tok * cols + c;   // 4-byte aligned
-    o[0] = acc.x, o[1] = acc.y, o[2] = acc.z, o[3] = acc.w;
+    o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
 }
 
 }  // namespace moe
@@ -202,7 +236,7 @@ cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStre
     float* sums = static_cast<float*>(m.ws);
     float* y = sums + bytes[0] / 4;
     if (m.router) {
-        e = m.n_tok == 1 ? moe::route<1>(m, s) : moe::route<8>(m, s);
+        e = m.n_tok == 1 ? moe::route<1>(m, s) : moe::route<4>(m, s);
         if (e != cudaSuccess) return e;
     }
     up.x = m.x;
@@ -219,8 +253,8 @@ cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStre
     if (e == cudaSuccess) e = moe::launch_down(m.type_down, down, sms, s, true);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((m.cols / 4 + moe::kSumThreads - 1) / moe::kSumThreads), (unsigned)m.n_tok);
-    cfg.blockDim = dim3(moe::kSumThreads);
+    cfg.gridDim = dim3((unsigned)((m.cols / 4 + moe::kSumCols - 1) / moe::kSumCols), (unsigned)m.n_tok);
+    cfg.blockDim = dim3(moe::kSumCols, (unsigned)m.k);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

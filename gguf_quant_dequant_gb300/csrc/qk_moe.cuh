@@ -18,7 +18,7 @@
 //     and the sums of the stage's warps took longer than the products: 61
 //     tokens, 8 of 128 experts of 2048 x 768: 374 us a layer.
 //   * Two more warps prepare the activations of the next (group, slice) while
-//     the others work on one: x in `up`, SiLU(g) * u in `down` (the first two are
+//     the others work on one: x in `up`, SiLU(g) * u in `down` (the first is
 //     prepared by all).
 //   * Slices of K leave partial sums, added in order by whoever reads them: the
 //     preparation of `down`, and a last kernel that also weighs and adds the
@@ -65,76 +65,76 @@ struct Tables {
 };
 
 // ids (shared, one per pair, kNone = none) -> groups of at most CAP pairs, by
-// expert, an expert's pairs in order.  scratch: 2 * n_exp words.
+// expert, an expert's pairs in order.  scratch: 3 * n_exp + 1 words, zeroed.  A
+// pair's place among its expert's is the number of earlier tokens that chose
+// it, from a mask of tokens per expert; given ids may name an expert twice for
+// one token: then the pairs are counted one after another.
 template <int CAP>
-__device__ __forceinline__ void make_groups(const Args& p, const Tables& t, const uint16_t* ids, int* scratch) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (p.n_tok == 1) {   // every pair is a group of its own
-        if (tid < 32) {
-            const bool ok = lane < p.pairs && ids[lane] != kNone;   // at most 16
-            const unsigned m = __ballot_sync(0xffffffffu, ok);
-            const int at = __popc(m & ((1u << lane) - 1));
-            if (ok) {
-                t.pairs[at] = (uint16_t)lane;
-                t.gexp[at] = ids[lane];
-                t.gbeg[at] = (uint16_t)at;
-                t.gcnt[at] = 1;
+__device__ __forceinline__ void make_groups(const Args& p, const Tables& t, const uint16_t* ids, uint32_t* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, nt = (int)blockDim.x;
+    uint32_t* mask = scratch;                  // [n_exp][2]: tokens
+    uint32_t* offs = scratch + 2 * p.n_exp;    // [n_exp]: first place
+    uint32_t* twice = scratch + 3 * p.n_exp;
+    for (int i = tid; i < p.pairs; i += nt) {
+        const int e = ids[i], tok = i / p.k;
+        if (e != kNone && (atomicOr(&mask[2 * e + (tok >> 5)], 1u << (tok & 31)) >> (tok & 31) & 1)) *twice = 1;
+    }
+    __syncthreads();
+    const bool again = *twice != 0;
+    if (again) {   // counts in place of masks
+        __syncthreads();
+        if (tid == 0) {
+            for (int e = 0; e < p.n_exp; ++e) mask[2 * e] = mask[2 * e + 1] = 0;
+            for (int i = 0; i < p.pairs; ++i)
+                if (ids[i] != kNone) ++mask[2 * ids[i]];
+        }
+        __syncthreads();
+    }
+    auto count = [&](int e) -> int { return again ? (int)mask[2 * e] : __popc(mask[2 * e]) + __popc(mask[2 * e + 1]); };
+    if (tid < 32) {
+        // Experts in order, a run of them per lane: running sums of pairs and groups.
+        const int per = (p.n_exp + 31) / 32, e0 = lane * per, e1 = min(e0 + per, p.n_exp);
+        int np = 0, ng = 0;
+        for (int e = e0; e < e1; ++e) {
+            np += count(e);
+            ng += (count(e) + CAP - 1) / CAP;
+        }
+        int ip = np, ig = ng;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, ip, o), b = __shfl_up_sync(0xffffffffu, ig, o);
+            if (lane >= o) {
+                ip += a;
+                ig += b;
             }
-            if (lane == 0) *t.n = __popc(m);
         }
-        return;
+        if (lane == 31) *t.n = ig;
+        ip -= np;
+        ig -= ng;
+        for (int e = e0; e < e1; ++e) {
+            offs[e] = (uint32_t)ip;
+            for (int c = count(e); c > 0; c -= CAP) {
+                t.gexp[ig] = (uint16_t)e;
+                t.gbeg[ig] = (uint16_t)ip;
+                t.gcnt[ig] = (uint16_t)min(c, CAP);
+                ip += min(c, CAP);
+                ++ig;
+            }
+        }
     }
-    int* count = scratch;
-    int* offs = scratch + p.n_exp;
-    for (int e = tid; e < p.n_exp; e += blockDim.x) count[e] = 0;
     __syncthreads();
-    for (int i = tid; i < p.pairs; i += blockDim.x)
-        if (ids[i] != kNone) atomicAdd(&count[ids[i]], 1);
-    __syncthreads();
-    if (tid >= 32) return;
-    // Experts in order, a run of them per lane: running sums of pairs and groups.
-    const int per = (p.n_exp + 31) / 32, e0 = lane * per, e1 = min(e0 + per, p.n_exp);
-    int np = 0, ng = 0;
-    for (int e = e0; e < e1; ++e) {
-        np += count[e];
-        ng += (count[e] + CAP - 1) / CAP;
-    }
-    int ip = np, ig = ng;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, ip, o), b = __shfl_up_sync(0xffffffffu, ig, o);
-        if (lane >= o) {
-            ip += a;
-            ig += b;
+    if (again) {
+        if (tid == 0)
+            for (int i = 0; i < p.pairs; ++i)
+                if (ids[i] != kNone) t.pairs[offs[ids[i]]++] = (uint16_t)i;
+    } else {
+        for (int i = tid; i < p.pairs; i += nt) {
+            const int e = ids[i], tok = i / p.k;
+            if (e == kNone) continue;
+            const uint32_t below = (1u << (tok & 31)) - 1;
+            const int before = tok < 32 ? __popc(mask[2 * e] & below) : __popc(mask[2 * e]) + __popc(mask[2 * e + 1] & below);
+            t.pairs[offs[e] + before] = (uint16_t)i;
         }
-    }
-    if (lane == 31) *t.n = ig;
-    ip -= np;
-    ig -= ng;
-    for (int e = e0; e < e1; ++e) {
-        offs[e] = ip;
-        for (int c = count[e]; c > 0; c -= CAP) {
-            t.gexp[ig] = (uint16_t)e;
-            t.gbeg[ig] = (uint16_t)ip;
-            t.gcnt[ig] = (uint16_t)min(c, CAP);
-            ip += min(c, CAP);
-            ++ig;
-        }
-    }
-    __syncwarp();
-    // Pairs into their expert's run, in order.
-    for (int b = 0; b < p.pairs; b += 32) {
-        const int i = b + lane;
-        const int e = i < p.pairs ? ids[i] : kNone;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        int at = 0;
-        if (e != kNone) {
-            at = offs[e] + __popc(same & ((1u << lane) - 1));
-            t.pairs[at] = (uint16_t)i;
-        }
-        __syncwarp();
-        if (e != kNone && lane == 31 - __clz((int)same)) offs[e] = at + 1;
-        __syncwarp();
     }
 }
 
@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     pdl_wait_prior();   // the ids; x or the sums of `up`
     {
         uint16_t* ids = reinterpret_cast<uint16_t*>(smem + p.off_ring);   // before the first fetch
-        int* scratch = reinterpret_cast<int*>(smem + p.off_ring + 2 * ((p.pairs + 7) & ~7));
+        uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + p.off_ring + 2 * ((p.pairs + 7) & ~7));
+        for (int i = threadIdx.x; i <= 3 * p.n_exp; i += blockDim.x) scratch[i] = 0;
         for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
             const int e = __ldcg(p.ids + i);
             ids[i] = e >= 0 && e < p.n_exp ? (uint16_t)e : kNone;
@@ -230,24 +231,26 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
         make_groups<NT>(p, tb, ids, scratch);
         __syncthreads();
     }
-    // My jobs: index ((group * slices + slice) * jobs + job).
-    const int64_t total = (int64_t)*tb.n * p.slices * p.jobs;
-    const int64_t j0 = total * blockIdx.x / gridDim.x, j1 = total * (blockIdx.x + 1) / gridDim.x;
+    // My jobs: index ((group * slices + slice) * jobs + job), below 2^30.
+    const uint32_t total = (uint32_t)*tb.n * p.slices * p.jobs;
+    const int each = (int)(total / gridDim.x), more = (int)(total % gridDim.x), bx = (int)blockIdx.x;
+    const int j0 = bx * each + min(bx, more), j1 = j0 + each + (bx < more ? 1 : 0);
     if (j0 >= j1) return;
-    const int e0 = (int)(j0 / p.jobs), e1 = (int)((j1 - 1) / p.jobs);   // my (group, slice)s
+    const int e0 = j0 / p.jobs, e1 = (j1 - 1) / p.jobs;   // my (group, slice)s
 
-    // The activations of (group, slice) e into its set: items (unit, pair) from `first` on, every `step`-th two.
+    // The activations of (group, slice) e into its set: every step-th (unit, pair) from `first` on, two at a time.
     auto prepare = [&](int e, int first, int step) {
         const int set = (e - e0) & 1, g = e / p.slices, u0 = (e - g * p.slices) * p.ku, nu = min(p.ku, p.nunits - u0);
         const int n = tb.gcnt[g], beg = tb.gbeg[g];
         uint8_t* xb = xbuf + set * x_set;
         float4* xm = reinterpret_cast<float4*>(xb + x_bytes);
-        for (int i0 = 2 * first; i0 < nu * n; i0 += 2 * step) {
+#pragma unroll 1
+        for (int i0 = first; i0 < nu * n; i0 += 2 * step) {
             float4 a[2], b[2];
             int at[2], un[2];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const int i = min(i0 + m, nu * n - 1);
+                const int i = min(i0 + m * step, nu * n - 1);
                 un[m] = i / n;
                 at[m] = i - un[m] * n;
                 const int pair = tb.pairs[beg + at[m]], u = u0 + un[m];
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m)
-                if (i0 + m < nu * n)
+                if (i0 + m * step < nu * n)
                     dm::put_x<NT, U::kW4, U::kMin && U::kG16>(a[m], b[m], xb + un[m] * (NT * dm::kXRow), xm + un[m] * 8 * NT, at[m], lane);
         }
     };
@@ -291,12 +294,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     chunks.set(rb, lane);
     // A step: one unit of a job.
     struct Step {
-        int64_t job;
-        int u, end;           // unit, and the end of the slice
+        int job, u, end;      // job, unit, and the end of the slice
         int64_t off0, off1;   // byte offsets of the tiles' first rows
     };
     auto enter = [&](Step& s) {   // the first unit of job s.job
-        const int e = (int)(s.job / p.jobs), j = (int)(s.job - (int64_t)e * p.jobs), g = e / p.slices;
+        const int e = s.job / p.jobs, j = s.job - e * p.jobs, g = e / p.slices;
         s.u = (e - g * p.slices) * p.ku;
         s.end = min(s.u + p.ku, p.nunits);
         const int64_t row = (int64_t)tb.gexp[g] * p.rows + (int64_t)j * (DOWN ? 2 * kTileRows : kTileRows);
@@ -305,8 +307,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     };
     auto fetch = [&](const Step& s, int slot) {
         if (s.job < j1) {
-            const int64_t at = (int64_t)s.u * S::kUB;
-            const int bytes = (int)min((int64_t)S::kUB, (int64_t)rb - at);
+            const int at = s.u * S::kUB;
+            const int bytes = min(S::kUB, (int)rb - at);
             chunks.fetch(p.W0 + s.off0 + at, bytes, slots_u32 + slot * (2 * S::kTile), lane, pol);
             chunks.fetch(p.W1 + s.off1 + at, bytes, slots_u32 + slot * (2 * S::kTile) + S::kTile, lane, pol);
         }
@@ -322,14 +324,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     if (cur.job < j1) enter(cur);
     ahead = cur;
     fetch(ahead, 0);
-    // All warps prepare the first two sets, then two of them the others while the rest multiplies.
+    // All warps prepare the first set, then two of them the others while the rest multiplies.  (A set's barriers count
+    // its uses: set 0 is full at first without one.)
     prepare(e0, warp, p.nw + kPrepWarps);
-    if (e0 < e1) prepare(e0 + 1, warp, p.nw + kPrepWarps);
     __syncthreads();
     if (warp >= p.nw) {
-        for (int e = e0 + 2; e <= e1; ++e) {
+        for (int e = e0 + 1; e <= e1; ++e) {
             const int set = (e - e0) & 1, turn = (e - e0) >> 1;
-            if (!mbar_wait_abortable(&xfree[set], (uint32_t)(turn - 1) & 1u, p.status, abort)) return;
+            if (turn > 0 && !mbar_wait_abortable(&xfree[set], (uint32_t)(turn - 1) & 1u, p.status, abort)) return;
             prepare(e, warp - p.nw, kPrepWarps);
             __syncwarp();
             if (lane == 0) mbar_arrive(&xfull[set]);
@@ -345,13 +347,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&xfree[(e - e0) & 1]);
             }
-            const int turn = (e + 1 - e0) >> 1;
-            if (e + 1 <= e1 && turn > 0 && !mbar_wait_abortable(&xfull[(e + 1 - e0) & 1], (uint32_t)(turn - 1) & 1u, p.status, abort))
-                dead = true;
+            const int next = e + 1 - e0, fill = (next >> 1) - (next & 1 ? 0 : 1);   // the set's fill that a barrier counts
+            if (e + 1 <= e1 && next > 0 && !mbar_wait_abortable(&xfull[next & 1], (uint32_t)fill & 1u, p.status, abort)) dead = true;
         }
     };
     while (cur.job < j1 && !dead) {
-        const int me = (int)(cur.job / p.jobs), j = (int)(cur.job - (int64_t)me * p.jobs), g = me / p.slices, u0 = cur.u;
+        const int me = cur.job / p.jobs, j = cur.job - me * p.jobs, g = me / p.slices, u0 = cur.u;
         float2 ya[NT / 4] = {}, yb[NT / 4] = {};
         leave(me);
         if (dead) break;
@@ -458,7 +459,7 @@ inline int plan(Args& a, int type_block_bytes, int type_block_elems, int tile_by
             if (time < best) {
                 best = time;
                 cap_best = cap;
-                const int64_t ring = std::max<int64_t>((int64_t)b.nw * 4 * tile_bytes, 2 * ((a.pairs + 7) & ~7) + 8 * a.n_exp);
+                const int64_t ring = std::max<int64_t>((int64_t)b.nw * 4 * tile_bytes, 2 * ((a.pairs + 7) & ~7) + 12 * a.n_exp + 16);
                 *smem = (uint32_t)(b.off_ring + ring + 16);
                 chosen = b;
             }

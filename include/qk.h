@@ -257,7 +257,7 @@ qk_status qk_gemv_swiglu(int type, const void* Wg, const void* Wu, int64_t rows,
  * A logit that is NaN ranks first and gives NaN gates for its token.
  * Deterministic.
  * n_tok == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also rows or
- * cols below 1 or above 2^18), QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG (scale
+ * cols below 1 or above 2^16), QK_ERR_NULL, QK_ERR_ALIGN, QK_ERR_ARG (scale
  * not finite), QK_ERR_WORKSPACE. */
 size_t qk_moe_workspace(int type, int type_down, int n_exp, int64_t rows, int64_t cols, int k, int64_t n_tok);
 qk_status qk_moe_ffn(int type, const void* Wg, const void* Wu, int type_down, const void* Wd, int n_exp, int64_t rows,

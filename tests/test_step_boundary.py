@@ -123,7 +123,7 @@ MOE = dict(type=qk.Q4_K, Wg=F, Wu=F, type_down=qk.Q6_K, Wd=F, n_exp=8, rows=512,
 @pytest.mark.parametrize("kw,status", [
     (dict(type=0), TYPE), (dict(type_down=9), TYPE), (dict(n_exp=0), SHAPE), (dict(n_exp=513), SHAPE), (dict(k=0), SHAPE),
     (dict(k=9), SHAPE), (dict(n_exp=64, k=17), SHAPE), (dict(rows=0), SHAPE), (dict(rows=500), SHAPE), (dict(cols=300), SHAPE),
-    (dict(cols=0), SHAPE), (dict(rows=(1 << 18) + 256), SHAPE), (dict(cols=(1 << 18) + 256), SHAPE), (dict(n_tok=65), SHAPE),
+    (dict(cols=0), SHAPE), (dict(rows=(1 << 16) + 256), SHAPE), (dict(cols=(1 << 16) + 256), SHAPE), (dict(n_tok=65), SHAPE),
     (dict(n_tok=-1), SHAPE), (dict(scale=float("nan")), ARG), (dict(Wg=None), NULL), (dict(Wu=None), NULL), (dict(Wd=None), NULL),
     (dict(x=None), NULL), (dict(ids=None), NULL), (dict(gate=None), NULL), (dict(out=None), NULL), (dict(ws=None), NULL),
     (dict(Wg=F + 8), ALIGN), (dict(router=F + 4), ALIGN), (dict(x=F + 8), ALIGN), (dict(ws=F + 8), ALIGN), (dict(ids=F + 2), ALIGN),

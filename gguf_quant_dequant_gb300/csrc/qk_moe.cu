@@ -65,13 +65,14 @@ __device__ __forceinline__ void choose(F logit, int n, int k, bool norm, float s
 // experts, a warp per expert (or several, by columns, where there are fewer
 // experts than warps); its logits meet in shared memory and CTA t chooses for
 // token t.  Latency bounds it: the tokens go through shared memory, so that a
-// lane's eight loads of the router are in flight at a time.  In one launch: a
+// lane has four loads of the router in flight at a time (eight would leave room
+// for one CTA on an SM, and 61 tokens in two waves).  In one launch: a
 // first version that left the choice to every CTA of the next kernel added 5 us
 // there for 61 tokens of 128 experts.
 constexpr int kRouteCluster = 8, kRouteWarps = 16, kRouteCols = 2048;   // columns of the tokens in shared memory at a time
 
 template <int TT>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const float* __restrict__ x, const float* __restrict__ router,
+__global__ void __launch_bounds__(kRouteWarps * 32, 2) route_kernel(const float* __restrict__ x, const float* __restrict__ router,
                                                                  int64_t cols, int n_tok, int n_exp, int k, bool norm, float scale,
                                                                  int32_t* __restrict__ ids, float* __restrict__ gate) {
     constexpr int kPer = QK_MOE_MAX_EXP / kRouteCluster;
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const float* __
             for (int t = 0; t < TT; ++t) acc[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             const float* w = router + (int64_t)(e0 + e) * cols + base;
             const int c0 = lane * 4 + part * 128, steps = c0 < n ? (n - 1 - c0) / (128 * share) + 1 : 0;
-#pragma unroll 8
+#pragma unroll 4
             for (int i = 0; i < steps; ++i) {
                 const int c = c0 + i * 128 * share;
                 const float4 r = __ldg(reinterpret_cast<const float4*>(w + c));

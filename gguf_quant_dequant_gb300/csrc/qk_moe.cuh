@@ -9,8 +9,9 @@
 // and multiplied with all its activations (qk_dunits.cuh).
 //   * A job is one group, one slice of K (`ku` units of 256) and two tiles of 16
 //     rows that share the activations: the gate's and the up's rows (up), or 32
-//     rows (down).  Jobs are dealt out in order: a range to every CTA (one per
-//     SM), every nw-th of it to a warp.
+//     rows (down).  Every CTA (one per SM) has a range of jobs, of which its warps
+//     take the next one each (fixed turns left the warps of the schedulers with
+//     one warp more, and with them the launch, 10 % behind).
 //   * A warp streams the packed rows of its jobs into its own two slots of
 //     shared memory (cp.async, one step of 256 columns ahead) and waits for
 //     nobody else's: with one warp filling stages for eight by bulk copies, the
@@ -72,6 +73,21 @@ struct Tables {
 template <int CAP>
 __device__ __forceinline__ void make_groups(const Args& p, const Tables& t, const uint16_t* ids, uint32_t* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, nt = (int)blockDim.x;
+    if (p.n_tok == 1) {   // every pair is a group of its own
+        if (tid < 32) {
+            const bool ok = lane < p.pairs && ids[lane] != kNone;   // at most 16
+            const unsigned m = __ballot_sync(0xffffffffu, ok);
+            const int at = __popc(m & ((1u << lane) - 1));
+            if (ok) {
+                t.pairs[at] = (uint16_t)lane;
+                t.gexp[at] = ids[lane];
+                t.gbeg[at] = (uint16_t)at;
+                t.gcnt[at] = 1;
+            }
+            if (lane == 0) *t.n = __popc(m);
+        }
+        return;
+    }
     uint32_t* mask = scratch;                  // [n_exp][2]: tokens
     uint32_t* offs = scratch + 2 * p.n_exp;    // [n_exp]: first place
     uint32_t* twice = scratch + 3 * p.n_exp;
@@ -203,6 +219,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     tb.gbeg = reinterpret_cast<uint16_t*>(smem + p.off_gbeg);
     tb.gcnt = reinterpret_cast<uint16_t*>(smem + p.off_gcnt);
     tb.n = const_cast<int*>(reinterpret_cast<volatile int*>(xfree + 2)) + 1;
+    int* taken = tb.n + 1;   // jobs that have been handed out
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rb = p.row_bytes;
     // Prepared activations, two sets: B fragments, then block sums.
@@ -215,14 +232,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
             mbar_init(&xfree[b], p.nw);
         }
         *abort = 0;
+        *taken = p.nw;
         fence_barrier_init();
     }
     pdl_launch_dependents();
-    pdl_wait_prior();   // the ids; x or the sums of `up`
     {
         uint16_t* ids = reinterpret_cast<uint16_t*>(smem + p.off_ring);   // before the first fetch
         uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + p.off_ring + 2 * ((p.pairs + 7) & ~7));
-        for (int i = threadIdx.x; i <= 3 * p.n_exp; i += blockDim.x) scratch[i] = 0;
+        if (p.n_tok > 1)
+            for (int i = threadIdx.x; i <= 3 * p.n_exp; i += blockDim.x) scratch[i] = 0;
+        pdl_wait_prior();   // the ids; x or the sums of `up`
         for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
             const int e = __ldcg(p.ids + i);
             ids[i] = e >= 0 && e < p.n_exp ? (uint16_t)e : kNone;
@@ -316,7 +335,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     };
     auto advance = [&](Step& s) {
         if (++s.u < s.end) return;
-        s.job += p.nw;
+        int n = 0;
+        if (lane == 0) n = atomicAdd(taken, 1);
+        s.job = j0 + __shfl_sync(0xffffffffu, n, 0);
         if (s.job < j1) enter(s);
     };
     Step cur, ahead;
@@ -359,7 +380,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
         const uint8_t* xb = xbuf + ((me - e0) & 1) * x_set;
         const float4* xm = reinterpret_cast<const float4*>(xb + x_bytes);
         for (int u = u0; u < cur.end; ++u) {
-            advance(ahead);
+            if (ahead.job < j1) advance(ahead);
             fetch(ahead, slot ^ 1);
             cp_async_wait<1>();
             __syncwarp();   // every lane's chunks of this step have arrived
@@ -422,9 +443,8 @@ inline double groups_of(int n, int k, int n_exp, int cap) {
 }
 
 // The geometry of one product: the size of groups (4 or 8, returned) and the
-// slices of K that are expected to take the least time, in units' times: a
-// round of jobs over the warps costs its units (more with groups of eight) and
-// an overhead.  unit_bytes of shared memory for two steps of a warp.
+// slices of K that are expected to take the least time, in units' times: a job
+// costs its units (more with groups of eight) and an overhead.  unit_bytes of shared memory for two steps of a warp.
 inline int plan(Args& a, int type_block_bytes, int type_block_elems, int tile_bytes, bool down, int sms, uint32_t* smem) {
     a.row_bytes = (uint32_t)(a.cols / type_block_elems * type_block_bytes);
     a.nxb = (int)(a.cols / 32);
@@ -453,9 +473,10 @@ inline int plan(Args& a, int type_block_bytes, int type_block_elems, int tile_by
             // the last words of a row's reads may lie behind it
             b.nw = (int)std::min<int64_t>((kSmemMax - b.off_ring - 16) / (4 * tile_bytes), kMaxWarps);
             if (b.nw < 4) continue;
-            const double rounds = std::ceil(groups * b.slices * b.jobs / sms / b.nw);
-            // the SM's issue slots are shared by its warps
-            const double time = rounds * b.nw * (b.ku * (cap == 4 ? 1.0 : 1.35) + 0.7);
+            // jobs of a warp, and half a job that the last ones to finish take longer
+            const double jobs = groups * b.slices * b.jobs / sms / b.nw, turns = jobs > 1.0 ? jobs + 0.5 : 1.0;
+            // the SM's issue slots are shared by its warps; a dozen of them use what there is
+            const double time = turns * std::max(b.nw, 12) * (b.ku * (cap == 4 ? 1.0 : 1.25) + 0.7);
             if (time < best) {
                 best = time;
                 cap_best = cap;

@@ -727,7 +727,7 @@ qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t 
     const qk_status st = device_state(nullptr, &sms);
     if (st != QK_OK) return st;
     const qk::VerifyArgs a{logits, dtype == QK_OUT_BF16, n_rows, vocab, row_stride, cu, n_req, draft, mask, temp, u_accept,
-                           u_sample, probs, probs_stride, path, path_stride, n_path, tokens};
+                           u_sample, probs, probs_stride, path, path_stride, n_path, tokens, false};
     cudaError_t e = qk::launch_verify_tree(a, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "qk_verify_tree launch");
     g_last_error.clear();

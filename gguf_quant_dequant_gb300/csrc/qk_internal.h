@@ -143,6 +143,7 @@ struct VerifyArgs {
     int32_t* path;
     int64_t path_stride;
     int32_t *n_path, *tokens;
+    bool probs_vec;   // rows of probs on 16-byte boundaries (set by the launcher)
 };
 cudaError_t launch_verify_tree(const VerifyArgs& a, int sms, cudaStream_t s);
 

@@ -10,16 +10,22 @@
 // W_v = max(e_v - tau q_v, 0), tau the sum of the S of the refusals before.
 // (The target's p after refusals is W / S: the usual residual max(p - q, 0),
 // normed, written without norming.)  Where no child is taken the token after
-// the path is the first v with sum_{v' <= v} W_v' > u S.  Only rows on the path
-// are read, which is why the walk is one launch and not a pass over all rows.
+// the path is the first v with sum_{v' <= v} W_v' > u S.
 //
-// One cluster of CTAs walks one request: every CTA has a contiguous part of
-// the vocabulary, every warp a contiguous part of that, so that the warps'
-// sums in order bracket the threshold and one warp looks its part up again.
-// All CTAs hold all warps' sums (written through distributed shared memory)
-// and take every decision alike.
+// Only rows on the path are read, which is why the walk is one launch and not
+// a pass over all rows.  One cluster of CTAs walks one request: every CTA has a
+// contiguous part of the vocabulary, every warp a contiguous part of that, so
+// that the warps' sums in order bracket the threshold and one part is looked
+// through again.  A step is a chain of latencies (the row, its maximum over the
+// cluster, its sum over the cluster), so:
+//   * a thread keeps its logits of the row, then their weights, in registers
+//     (up to kKeep of them; longer parts are read again from L2);
+//   * each warp writes its maximum and its sum to every CTA of the cluster: one
+//     cluster barrier per exchange, and every CTA decides by itself;
+//   * the next row of a chain is asked for (into L2) while the sum is formed.
 #include <algorithm>
 #include <cooperative_groups.h>
+#include <cstdint>
 
 #include "qk_internal.h"
 #include "qk_ptx.cuh"
@@ -30,8 +36,9 @@ namespace qk {
 namespace vt {
 
 constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 constexpr int kNodes = QK_TREE_MAX;
+constexpr int kKeep = 32;             // logits of a row that a thread keeps
 constexpr float kGreedy = 0x1p-20f;   // temperatures below it: the largest logit
 
 template <bool BF16>
@@ -39,51 +46,108 @@ __device__ __forceinline__ float logit(const void* row, int64_t v) {
     return BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(row)[v] << 16) : static_cast<const float*>(row)[v];
 }
 
-// exp((x - top) rate) for the largest logit top of the row; NaN counts as -inf, and of a row with +inf only those count.
+// exp((x - top) rate) for the largest logit top of the row; NaN counts as -inf (the maximum drops it; exp(-200) is 0), and of
+// a row with +inf only those count.
 __device__ __forceinline__ float weight(float x, float top, float rate) {
-    const float d = __fsub_rn(x, top);
-    const float e = expf(__fmul_rn(d, rate));
-    return x == top ? 1.0f : d > -INFINITY ? e : 0.0f;
+    const float e = expf(fmaxf(__fmul_rn(__fsub_rn(x, top), rate), -200.0f));
+    return x == top ? 1.0f : e;
 }
 __device__ __forceinline__ float rest(float e, float tau, float q) { return fmaxf(__fsub_rn(e, __fmul_rn(tau, q)), 0.0f); }
 
-// Sum of fp32 values to about 2^-48: the running sum and the rounding it loses.
+// Sums are whole numbers of 2^-bits (bits = 46 for up to 65,536 tokens, one less for each doubling), so that they are
+// the same in whatever order they are formed: on this GPU a 64-bit floating addition costs a warp sixteen cycles of
+// the whole SM, and two reductions with them took 2.9 us a row.
+struct Fix {
+    float up;      // 2^bits
+    double down;   // 2^-bits
+    __device__ __forceinline__ int64_t of(float v) const { return __float2ll_rn(v * up); }
+};
+// Sum of weights in 0 .. 1 to about 2^-46: the running sum, from 1 on (so that it is the larger one), and the rounding it
+// loses.
 struct Sum {
-    float h = 0.0f, l = 0.0f;
+    float h = 1.0f, l = 0.0f;
     __device__ __forceinline__ void add(float v) {
-        const float s = __fadd_rn(h, v), b = __fsub_rn(s, h);
-        l = __fadd_rn(l, __fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(v, b)));
+        const float s = __fadd_rn(h, v);
+        l = __fadd_rn(l, __fsub_rn(v, __fsub_rn(s, h)));
         h = s;
     }
-    __device__ __forceinline__ double value() const { return (double)h + (double)l; }
+    __device__ __forceinline__ int64_t value(const Fix& f) const { return f.of(__fsub_rn(h, 1.0f)) + f.of(l); }
 };
 
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {   // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+// The largest of the warp's (m, at), the lowest place of equals.
+__device__ __forceinline__ void warp_top(float& m, int& at) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m, o);
+        const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+        if (om > m || (om == m && oa < at)) {
+            m = om;
+            at = oa;
+        }
+    }
+}
 
+constexpr int kNowhere = 0x7fffffff;
 struct Shared {
-    double sums[2][kMaxCluster * kWarps];   // W's sum of every warp of the cluster; by turns
-    double plain[kMaxCluster * kWarps];     // e's, of the current node
-    float top[2][kMaxCluster];              // the largest logit of every CTA's part, and its place; by turns
-    int best[2][kMaxCluster];
-    float wtop[kWarps];
-    int wbest[kWarps];
+    int64_t sums[2][kMaxCluster * kWarps];  // W's sum of every warp of the cluster; by turns
+    int64_t plain[kMaxCluster * kWarps];    // e's, of the last node
+    float top[2][kMaxCluster * kWarps];     // every warp's largest logit and its place; by turns
+    int best[2][kMaxCluster * kWarps];
+    int64_t piece[kWarps];                  // the sampled part's pieces
     int parent[kNodes], token[kNodes];
-    int refused[kNodes];                    // tokens taken out of the current node's W
-    int n_refused, verdict, child, part, usual;
-    double total, before, target;
+    int part, usual, next, again;
+    uint64_t refused;                       // children of the node, without the drafter's probabilities
+    double tau;
+    int64_t target, before;
 };
-enum : int { kNone = 0, kTaken = 1, kRefused = 2 };   // of the children from one on
 
+// Elements of a warp's part: lane-wise vectors of kVec, 32 of them a step.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+struct Lanes {
+    static constexpr int kVec = VEC ? (BF16 ? 8 : 4) : 1, kStep = 32 * kVec;
+    // kVec logits from v on; -inf from v1 on (v < v1).
+    static __device__ __forceinline__ void load(const void* row, int64_t v, int64_t v1, float (&x)[kVec]) {
+        if (VEC && v + kVec <= v1) {
+            if constexpr (BF16) {
+                const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + v);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) x[i] = __uint_as_float(i & 1 ? w[(i >> 1) & 3] & 0xffff0000u : w[(i >> 1) & 3] << 16);
+            } else {
+                const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + v);
+                const float w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) x[i] = w[i & 3];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[i] = v + i < v1 ? logit<BF16>(row, v + i) : -INFINITY;
+        }
+    }
+};
+
+// KEEP: the part of a thread fits its registers.
+template <bool BF16, bool VEC, bool KEEP>
+__global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const VerifyArgs a) {
+    using L = Lanes<BF16, VEC>;
+    constexpr int kVec = L::kVec, kStep = L::kStep, kRegs = KEEP ? kKeep / kVec : 1, kAhead = KEEP ? 1 : 8 / (kVec > 4 ? 2 : 1);
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
-    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank(), parts = C * kWarps;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = rank * kWarps + warp;
     const int64_t r = blockIdx.x / C;
     int64_t row0 = a.cu[r], row1 = a.cu[r + 1];
     row0 = min(max(row0, (int64_t)0), a.n_rows);
@@ -97,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
         if (rank == 0 && tid == 0) a.n_path[r] = 0;
         return;   // the whole cluster
     }
-    const float temp = a.temp[r];
+    const float temp = a.temp[r], u_sample = a.u_sample[r];
     const bool greedy = !(temp >= kGreedy);
     const float rate = greedy ? 1.0f : __frcp_rn(temp);
     const bool drafter = a.probs != nullptr && !greedy;
@@ -105,131 +169,263 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
         // the parent is the nearest ancestor: the highest bit below the node's own
         const uint64_t up = a.mask ? a.mask[row0 + tid] & ((1ull << tid) - 1) : (tid ? 1ull << (tid - 1) : 0ull);
         sh.parent[tid] = up ? 63 - __clzll((long long)up) : -1;
-        sh.token[tid] = a.draft ? a.draft[row0 + tid] : -1;
+        sh.token[tid] = a.draft[row0 + tid];
     }
-    // My part of the vocabulary: v0 .. v1 - 1, a multiple of a warp's step long (but the last).
-    constexpr int kVec = VEC ? (BF16 ? 8 : 4) : 1, kStep = 32 * kVec;
-    const int64_t share = ((a.vocab + (int64_t)C * kWarps - 1) / ((int64_t)C * kWarps) + kStep - 1) / kStep * kStep;
-    const int64_t v0 = min((int64_t)(rank * kWarps + warp) * share, a.vocab), v1 = min(v0 + share, a.vocab);
-    // f(v, x) for the elements of the warp's part, in a lane's order
-    auto walk = [&](const void* row, auto f) {
-        for (int64_t v = v0 + lane * kVec; v < v1; v += kStep) {
-            if (VEC && v + kVec <= v1) {
-                float x[kVec];
-                if constexpr (BF16) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + v);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) x[i] = __uint_as_float(i & 1 ? w[(i >> 1) & 3] & 0xffff0000u : w[(i >> 1) & 3] << 16);
-                } else {
-                    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + v);
-                    const float w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) x[i] = w[i & 3];
-                }
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) f(v + i, x[i]);
-            } else {
-                for (int i = 0; i < kVec && v + i < v1; ++i) f(v + i, logit<BF16>(row, v + i));
-            }
-        }
-    };
+    // My part of the vocabulary: v0 .. v1 - 1, a multiple of a step long (but the last).
+    const int64_t share = ((a.vocab + parts - 1) / parts + kStep - 1) / kStep * kStep;
+    const int64_t v0 = min(me * share, a.vocab), v1 = min(v0 + share, a.vocab);
+    const int bits = min(46, 62 - (32 - __clz((int)a.vocab)));
+    const Fix fix{__uint_as_float((uint32_t)(127 + bits) << 23), __longlong_as_double((int64_t)(1023 - bits) << 52)};
     // An exchange writes one buffer and ends with the cluster's barrier; the buffer is written again two exchanges of its
-    // kind later, after another barrier that every CTA reaches only when it has read it.
+    // kind later, after another barrier that every warp reaches only when it has read it.
     int top_turn = 0, sum_turn = 0;
-    // Every warp's sum to every CTA of the cluster, and their sum in order.
-    auto exchange = [&](double mine, bool plain) {
+    auto exchange = [&](int64_t mine) {   // every warp's sum to every CTA
         sum_turn ^= 1;
-        if (lane < C) cl.map_shared_rank(&sh, lane)->sums[sum_turn][rank * kWarps + warp] = mine;
+        if (lane < C) cl.map_shared_rank(&sh, lane)->sums[sum_turn][me] = mine;
         cl.sync();
-        if (warp == 0) {
-            double s = 0.0;
-            for (int i = lane; i < C * kWarps; i += 32) {
-                const double v = sh.sums[sum_turn][i];
-                if (plain) sh.plain[i] = v;
-                s += v;
-            }
-            s = warp_sum(s);
-            if (lane == 0) sh.total = s;
-        }
-        __syncthreads();
+    };
+    auto total_of = [&]() {   // their sum
+        int64_t s = 0;
+        for (int i = lane; i < parts; i += 32) s += sh.sums[sum_turn][i];
+        return warp_sum(s);
     };
     int cur = 0, length = 1;
     if (rank == 0 && tid == 0) path[0] = 0;
-    cl.sync();   // every CTA of the cluster runs before another writes to its shared memory
+    cl.sync();   // every CTA of the cluster runs (and has its tree) before another writes to its shared memory
     for (;;) {
         const void* row = static_cast<const uint8_t*>(a.logits) + (row0 + cur) * a.row_stride * (BF16 ? 2 : 4);
         const float* q = drafter ? a.probs + (row0 + cur) * a.probs_stride : nullptr;
-        // The row's largest logit and its first place.
-        float m = -INFINITY;
-        int at = 0x7fffffff;
-        walk(row, [&](int64_t v, float x) {
-            if (x > m) {
-                m = x;
-                at = (int)v;
-            }
-        });
+        // The drafter's probabilities of kVec tokens from v on (0 behind the part: the weights there are 0 too).
+        auto load_q = [&](int64_t v, float (&w)[kVec]) {
+            if (kVec >= 4 && a.probs_vec && v + kVec <= v1) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, o);
-            const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-            if (om > m || (om == m && oa < at)) {
-                m = om;
-                at = oa;
-            }
-        }
-        if (lane == 0) {
-            sh.wtop[warp] = m;
-            sh.wbest[warp] = at;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            m = lane < kWarps ? sh.wtop[lane] : -INFINITY;
-            at = lane < kWarps ? sh.wbest[lane] : 0x7fffffff;
+                for (int i = 0; i < kVec; i += 4) {
+                    const float4 u = *reinterpret_cast<const float4*>(q + v + i);
+                    w[i] = u.x;
+                    if (kVec >= 4) w[(i + 1) % kVec] = u.y, w[(i + 2) % kVec] = u.z, w[(i + 3) % kVec] = u.w;
+                }
+            } else {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float om = __shfl_xor_sync(0xffffffffu, m, o);
-                const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-                if (om > m || (om == m && oa < at)) {
-                    m = om;
-                    at = oa;
+                for (int i = 0; i < kVec; ++i) w[i] = v + i < v1 ? q[v + i] : 0.0f;
+            }
+        };
+        // My logits: kept, or passed by; the largest and its first place.
+        float x[kRegs][kVec], m = -INFINITY;
+        int at = kNowhere;
+        auto look = [&](const float (&w)[kVec], int64_t v) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (w[i] > m) {
+                    m = w[i];
+                    at = (int)(v + i);
+                }
+        };
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int k = 0; k < kRegs; ++k) {
+                const int64_t v = v0 + k * kStep + lane * kVec;
+                if (v < v1) {
+                    L::load(row, v, v1, x[k]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) x[k][i] = -INFINITY;
                 }
             }
-            if (lane < C) {
-                Shared* p = cl.map_shared_rank(&sh, lane);
-                p->top[top_turn][rank] = m;
-                p->best[top_turn][rank] = at;
+        }
+        // What the tests of the children will read: lane i of a warp has child i, and i + 32.
+        int kid[2];
+        float kx[2], ku[2], kq[2];
+        unsigned kids[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane + 32 * h;
+            const bool child = i > cur && i < n && sh.parent[i] == cur;
+            kids[h] = __ballot_sync(0xffffffffu, child);
+            kid[h] = child ? sh.token[i] : -1;
+            kx[h] = -INFINITY;
+            ku[h] = 0.0f;
+            kq[h] = 1.0f;
+            if (kid[h] >= 0 && kid[h] < a.vocab) {
+                kx[h] = logit<BF16>(row, kid[h]);
+                ku[h] = a.u_accept[row0 + i];
+                if (drafter) kq[h] = q[kid[h]];
             }
+        }
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int k = 0; k < kRegs; ++k)
+                if (v0 + k * kStep < v1) look(x[k], v0 + k * kStep + lane * kVec);
+        } else {
+            for (int64_t v = v0 + lane * kVec; v < v1; v += kAhead * kStep) {
+                float w[kAhead][kVec];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (v + k * kStep < v1) {
+                        L::load(row, v + k * kStep, v1, w[k]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kVec; ++i) w[k][i] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) look(w[k], v + k * kStep);
+            }
+        }
+        warp_top(m, at);
+        if (lane < C) {
+            Shared* p = cl.map_shared_rank(&sh, lane);
+            p->top[top_turn][me] = m;
+            p->best[top_turn][me] = at;
         }
         cl.sync();
         m = -INFINITY;
-        at = 0x7fffffff;
-        for (int c = 0; c < C; ++c)
-            if (sh.top[top_turn][c] > m) {   // parts in order: the first place stays
-                m = sh.top[top_turn][c];
-                at = sh.best[top_turn][c];
+        at = kNowhere;
+        for (int i = lane; i < parts; i += 32)
+            if (sh.top[top_turn][i] > m) {   // parts in order: the first place stays
+                m = sh.top[top_turn][i];
+                at = sh.best[top_turn][i];
             }
+        warp_top(m, at);
         const float top = m;
-        const int best = at;   // 0x7fffffff: a row with nothing above -inf
+        const int best = at;   // kNowhere: a row with nothing above -inf
         top_turn ^= 1;
+        int next = -1;
         if (greedy) {
-            if (warp == 0) {
-                int next = 0x7fffffff;
-                for (int i = lane; i < n; i += 32)
-                    if (sh.parent[i] == cur && sh.token[i] == best) next = min(next, i);
-                next = __reduce_min_sync(0xffffffffu, next);
-                if (lane == 0) sh.child = next == 0x7fffffff || length >= a.path_stride ? -1 : next;
-            }
-            __syncthreads();
-            const int next = sh.child;
-            __syncthreads();
+            const unsigned b0 = __ballot_sync(0xffffffffu, kid[0] == best), b1 = __ballot_sync(0xffffffffu, kid[1] == best);
+            if (length < a.path_stride && best != kNowhere) next = b0 ? __ffs(b0) - 1 : b1 ? 31 + __ffs(b1) : -1;
             if (next < 0) {
                 if (rank == 0 && tid == 0) {
-                    tokens[length - 1] = best == 0x7fffffff ? -1 : best;
+                    tokens[length - 1] = best == kNowhere ? -1 : best;
                     a.n_path[r] = length;
                 }
                 break;
             }
+        } else {
+            // The first child's row is the next one to be read, if any.
+            if (kids[0] | kids[1]) {
+                const int64_t c = kids[0] ? __ffs(kids[0]) - 1 : 31 + __ffs(kids[1]);
+                const uint8_t* ahead = static_cast<const uint8_t*>(a.logits) + (row0 + c) * a.row_stride * (BF16 ? 2 : 4);
+                for (int64_t b = v0 * (BF16 ? 2 : 4) + lane * 128; b < v1 * (BF16 ? 2 : 4); b += 32 * 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + b));
+            }
+            // The row's sum; kept logits turn into weights.
+            {
+                Sum s;
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int k = 0; k < kRegs; ++k)
+                        if (v0 + k * kStep < v1)
+#pragma unroll
+                            for (int i = 0; i < kVec; ++i) {
+                                x[k][i] = top > -INFINITY ? weight(x[k][i], top, rate) : 0.0f;
+                                s.add(x[k][i]);
+                            }
+                } else if (top > -INFINITY) {
+                    for (int64_t v = v0 + lane * kVec; v < v1; v += kAhead * kStep) {
+                        float w[kAhead][kVec];
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            if (v + k * kStep < v1) {
+                                L::load(row, v + k * kStep, v1, w[k]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < kVec; ++i) w[k][i] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                            for (int i = 0; i < kVec; ++i) s.add(weight(w[k][i], top, rate));
+                    }
+                }
+                exchange(warp_sum(s.value(fix)));
+            }
+            const int plain_turn = sum_turn;
+            // The children, in order: the first warp of every CTA decides, all alike.
+            float kw[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) kw[h] = kid[h] >= 0 && top > -INFINITY ? weight(kx[h], top, rate) : 0.0f;
+            unsigned todo[2] = {kids[0], kids[1]};
+            uint64_t refused = 0;
+            double tau = 0.0;
+            for (;;) {
+                if (warp == 0) {
+                    int64_t total = total_of();
+                    int got = -1;
+                    bool again = false;   // a refusal that changes W everywhere
+                    while (length < a.path_stride && (todo[0] | todo[1]) && !again) {
+                        const int h = todo[0] ? 0 : 1, c = __ffs(todo[h]) - 1;
+                        if (h) todo[1] &= todo[1] - 1;
+                        else todo[0] &= todo[0] - 1;
+                        const int y = __shfl_sync(0xffffffffu, h ? kid[1] : kid[0], c);
+                        float w = __shfl_sync(0xffffffffu, h ? kw[1] : kw[0], c);
+                        const float qy = __shfl_sync(0xffffffffu, h ? kq[1] : kq[0], c), u = __shfl_sync(0xffffffffu, h ? ku[1] : ku[0], c);
+                        if (drafter) {
+                            if (tau > 0.0) w = rest(w, (float)tau, qy);
+                        } else {   // the same token on a child refused before
+                            const bool gone = ((refused >> lane & 1) && kid[0] == y) || ((refused >> (lane + 32) & 1) && kid[1] == y);
+                            if (__any_sync(0xffffffffu, gone)) w = 0.0f;
+                        }
+                        if ((double)u * (double)qy * ((double)total * fix.down) < (double)w) {
+                            got = c + 32 * h;
+                            break;
+                        }
+                        if (drafter) {
+                            again = true;
+                            tau += (double)total * fix.down;
+                        } else if (w > 0.0f) {
+                            refused |= 1ull << (c + 32 * h);
+                            total = max(total - fix.of(w), (int64_t)0);
+                        }
+                    }
+                    if (lane == 0) {
+                        sh.next = got;
+                        sh.again = again;
+                        sh.tau = tau;
+                        sh.refused = refused;
+                    }
+                }
+                __syncthreads();
+                next = sh.next;
+                const bool first = tau == 0.0;
+                tau = sh.tau;
+                if (!sh.again) break;
+                if (first)   // the sums of e, for a row in which nothing will be left
+                    for (int i = tid; i < parts; i += kThreads) sh.plain[i] = sh.sums[plain_turn][i];
+                const float off = (float)tau;
+                Sum s;
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int k = 0; k < kRegs; ++k) {
+                        const int64_t v = v0 + k * kStep + lane * kVec;
+                        if (v < v1) {
+                            float q1[kVec];
+                            load_q(v, q1);
+#pragma unroll
+                            for (int i = 0; i < kVec; ++i) s.add(rest(x[k][i], off, q1[i]));
+                        }
+                    }
+                } else if (top > -INFINITY) {
+                    constexpr int kTwo = kVec == 8 ? 1 : kVec == 4 ? 2 : 4;
+                    for (int64_t v = v0 + lane * kVec; v < v1; v += kTwo * kStep) {
+                        float w2[kTwo][kVec], q2[kTwo][kVec];
+#pragma unroll
+                        for (int k = 0; k < kTwo; ++k)
+                            if (v + k * kStep < v1) {
+                                L::load(row, v + k * kStep, v1, w2[k]);
+                                load_q(v + k * kStep, q2[k]);
+                            }
+#pragma unroll
+                        for (int k = 0; k < kTwo; ++k)
+                            if (v + k * kStep < v1)
+#pragma unroll
+                                for (int i = 0; i < kVec; ++i) s.add(rest(weight(w2[k][i], top, rate), off, q2[k][i]));
+                    }
+                }
+                exchange(warp_sum(s.value(fix)));   // (and all have read the decision)
+            }
+        }
+        if (next >= 0) {
             if (rank == 0 && tid == 0) {
                 tokens[length - 1] = sh.token[next];
                 path[length] = next;
@@ -238,115 +434,33 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
             ++length;
             continue;
         }
-        // The row's sum.
-        {
-            Sum s;
-            if (top > -INFINITY) walk(row, [&](int64_t, float x) { s.add(weight(x, top, rate)); });
-            if (tid == 0) sh.n_refused = 0;
-            exchange(warp_sum(s.value()), true);
-        }
-        // The children, in order: all of them at once, or with the drafter's probabilities one by one, as a refusal
-        // changes every W.
-        int verdict = kNone, first = cur + 1;
-        double tau = 0.0;
-        while (length < a.path_stride) {
-            if (warp == 0) {
-                int got = kNone, which = n;
-                for (int base = first & ~31; base < n && got == kNone; base += 32) {
-                    const int i = base + lane;
-                    const bool child = i >= first && i < n && sh.parent[i] == cur;
-                    const int y = child ? sh.token[i] : -1;
-                    float w = 0.0f, qy = 1.0f, u = 0.0f;
-                    if (y >= 0 && y < a.vocab && top > -INFINITY) {
-                        w = weight(logit<BF16>(row, y), top, rate);
-                        if (drafter) {
-                            qy = q[y];
-                            if (tau > 0.0) w = rest(w, (float)tau, qy);
-                        }
-                        u = a.u_accept[row0 + i];
-                    }
-                    unsigned todo = __ballot_sync(0xffffffffu, child);
-                    while (todo) {
-                        const int c = __ffs(todo) - 1;
-                        todo &= todo - 1;
-                        const int yc = __shfl_sync(0xffffffffu, y, c);
-                        float wc = __shfl_sync(0xffffffffu, w, c);
-                        const float qc = __shfl_sync(0xffffffffu, qy, c), uc = __shfl_sync(0xffffffffu, u, c);
-                        if (!drafter) {
-                            bool gone = false;
-                            for (int k = lane; k < sh.n_refused; k += 32) gone |= sh.refused[k] == yc;
-                            if (__any_sync(0xffffffffu, gone)) wc = 0.0f;
-                        }
-                        const double S = sh.total;
-                        __syncwarp();
-                        which = base + c;
-                        if ((double)uc * (double)qc * S < (double)wc) {
-                            got = kTaken;
-                            break;
-                        }
-                        if (drafter) {
-                            got = kRefused;
-                            break;
-                        }
-                        if (wc > 0.0f && lane == 0) {
-                            sh.refused[sh.n_refused++] = yc;
-                            const int64_t part = yc / share;   // the warp whose part it is
-                            const double v = sh.sums[sum_turn][part], left = v - (double)wc;
-                            sh.sums[sum_turn][part] = left > 1e-13 * v ? left : 0.0;   // what rounding leaves of nothing
-                            sh.total = S - (double)wc;
-                        }
-                        __syncwarp();
-                    }
-                }
-                if (lane == 0) {
-                    sh.verdict = got;
-                    sh.child = which;
-                }
-            }
-            __syncthreads();
-            verdict = sh.verdict;
-            first = sh.child;
-            const double S = sh.total;
-            if (verdict != kRefused) break;
-            ++first;
-            tau += S;
-            Sum s;
-            const float off = (float)tau;
-            if (top > -INFINITY) walk(row, [&](int64_t v, float x) { s.add(rest(weight(x, top, rate), off, q[v])); });
-            exchange(warp_sum(s.value()), false);   // (its barriers also part this round's verdict from the next)
-        }
-        if (verdict == kTaken) {
-            if (rank == 0 && tid == 0) {
-                tokens[length - 1] = sh.token[first];
-                path[length] = first;
-            }
-            cur = first;
-            ++length;
-            continue;
-        }
-        // The token after the path: the warp whose part holds the threshold, then the token in it.
+        // The token after the path.  First the part that holds the threshold.
+        __syncthreads();   // the decision has been read, sh.plain is written
+        const uint64_t refused = sh.refused;
+        const double tau = sh.tau;
         if (warp == 0) {
-            const bool usual = sh.total > 0.0;   // nothing left (by rounding): the row's own weights
-            const double* part = usual ? sh.sums[sum_turn] : sh.plain;
-            const int parts = C * kWarps, each = (parts + 31) / 32;
-            double mine = 0.0;
+            if (lane == 0)
+                for (uint64_t left = refused; left; left &= left - 1) {   // tokens taken out of their parts' sums
+                    const int y = sh.token[__ffsll((long long)left) - 1];
+                    sh.sums[sum_turn][y / share] = max(sh.sums[sum_turn][y / share] - fix.of(weight(logit<BF16>(row, y), top, rate)), (int64_t)0);
+                }
+            __syncwarp();
+            const bool usual = tau == 0.0 || total_of() > 0;   // else nothing is left (by rounding): the row's own weights
+            const int64_t* part = usual ? sh.sums[sum_turn] : sh.plain;
+            const int each = (parts + 31) / 32;
+            int64_t mine = 0;
             for (int k = 0; k < each; ++k)
                 if (lane * each + k < parts) mine += part[lane * each + k];
-            double upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double t = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += t;
-            }
-            const double S = __shfl_sync(0xffffffffu, upto, 31);
-            const double target = (double)a.u_sample[r] * S;
-            double run = upto - mine, before = 0.0;
-            int hit = 0x7fffffff, last = -1;
+            const int64_t upto = warp_scan(mine, lane), S = __shfl_sync(0xffffffffu, upto, 31);
+            // sums above u S: above its whole part (u outside 0 .. 1 or NaN: some token all the same)
+            const int64_t target = (int64_t)fmin(fmax((double)u_sample * (double)S, 0.0), 0x1p62);
+            int64_t run = upto - mine, before = 0;
+            int hit = kNowhere, last = -1;
             for (int k = 0; k < each; ++k) {
                 const int i = lane * each + k;
-                if (i < parts && part[i] > 0.0) {
+                if (i < parts && part[i] > 0) {
                     last = i;
-                    if (hit == 0x7fffffff && run + part[i] > target) {
+                    if (hit == kNowhere && run + part[i] > target) {
                         hit = i;
                         before = run;
                     }
@@ -356,13 +470,13 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
             const int found = __reduce_min_sync(0xffffffffu, hit);
             last = __reduce_max_sync(0xffffffffu, last);
             if (lane == 0) {
-                sh.part = found != 0x7fffffff ? found : last;   // none when rounding puts the threshold at the end: the last token
-                sh.target = found != 0x7fffffff ? target : INFINITY;
-                sh.before = 0.0;
+                sh.part = found != kNowhere ? found : last;   // none when the threshold is the end: the last token
+                sh.target = found != kNowhere ? target : INT64_MAX;
+                sh.before = 0;
                 sh.usual = usual;
             }
             __syncwarp();
-            if (found != 0x7fffffff && hit == found) sh.before = before;
+            if (found != kNowhere && hit == found) sh.before = before;
         }
         __syncthreads();
         const int part = sh.part;
@@ -370,43 +484,77 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
             if (rank == 0 && tid == 0) a.n_path[r] = length;
             break;
         }
-        if (part / kWarps == rank && part % kWarps == warp) {
-            const bool usual = sh.usual != 0;
-            const double target = sh.target;
-            const float off = (float)tau;
-            double run = sh.before;
-            int token = -1, last = -1;
-            for (int64_t b = v0; b < v1 && token < 0; b += kStep) {
-                double w[kVec], mine = 0.0;
+        if (part / kWarps != rank) break;
+        // Then the token: the part's CTA cuts it into pieces of whole steps, a warp each, in order.
+        const bool usual = sh.usual != 0;
+        const int64_t target = sh.target;
+        const float off = usual ? (float)tau : 0.0f;
+        const int64_t p0 = min((int64_t)part * share, a.vocab), p1 = min(p0 + share, a.vocab);
+        const int64_t each = ((share / kStep + kWarps - 1) / kWarps) * kStep;
+        const int64_t w0 = min(p0 + warp * each, p1), w1 = min(w0 + each, p1);
+        auto weights = [&](int64_t v, float (&w)[kVec]) {   // W of kVec tokens from v on
+            if (v >= w1) {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const int64_t v = b + lane * kVec + i;
-                    float e = v < v1 ? weight(logit<BF16>(row, v), top, rate) : 0.0f;
-                    if (usual && drafter && tau > 0.0 && v < v1) e = rest(e, off, q[v]);
-                    if (usual && !drafter)
-                        for (int k = 0; k < sh.n_refused; ++k)
-                            if (sh.refused[k] == v) e = 0.0f;
-                    w[i] = e;
-                    mine += w[i];
-                }
-                double upto = mine;
+                for (int i = 0; i < kVec; ++i) w[i] = 0.0f;
+                return;
+            }
+            L::load(row, v, w1, w);
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double t = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += t;
-                }
-                double at = run + (upto - mine);
-                int hit = 0x7fffffff, some = -1;
+            for (int i = 0; i < kVec; ++i) {
+                w[i] = weight(w[i], top, rate);
+                if (off > 0.0f && v + i < w1) w[i] = rest(w[i], off, q[v + i]);
+            }
+            for (uint64_t left = usual ? refused : 0; left; left &= left - 1) {
+                const int y = sh.token[__ffsll((long long)left) - 1];
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
-                    if (w[i] > 0.0) {
-                        at += w[i];
+                    if (v + i == y) w[i] = 0.0f;
+            }
+        };
+        int64_t mine = 0;
+        for (int64_t b = w0; b < w1; b += kStep) {
+            float w[kVec];
+            weights(b + lane * kVec, w);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) mine += fix.of(w[i]);
+        }
+        mine = warp_sum(mine);
+        if (lane == 0) sh.piece[warp] = mine;
+        __syncthreads();
+        int64_t run = sh.before;
+        int mine_is = -1, last_is = -1;   // the warp whose piece holds the threshold; the last with weight
+        for (int k = 0; k < kWarps; ++k) {
+            const int64_t p = sh.piece[k];
+            if (p > 0) {
+                last_is = k;
+                if (mine_is < 0) {
+                    if (run + p > target) mine_is = k;
+                    else run += p;
+                }
+            }
+        }
+        if (warp == (mine_is >= 0 ? mine_is : last_is < 0 ? 0 : last_is)) {
+            const int64_t goal = mine_is >= 0 ? target : INT64_MAX;
+            int token = -1, last = -1;
+            for (int64_t b = w0; b < w1 && token < 0; b += kStep) {
+                float w[kVec];
+                weights(b + lane * kVec, w);
+                int64_t sum = 0;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) sum += fix.of(w[i]);
+                const int64_t upto = warp_scan(sum, lane);
+                int64_t sofar = run + (upto - sum);
+                int hit = kNowhere, some = -1;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    if (w[i] > 0.0f) {
+                        sofar += fix.of(w[i]);
                         some = (int)(b + lane * kVec + i);
-                        if (hit == 0x7fffffff && at > target) hit = some;
+                        if (hit == kNowhere && sofar > goal) hit = some;
                     }
                 hit = __reduce_min_sync(0xffffffffu, hit);
                 last = max(last, __reduce_max_sync(0xffffffffu, some));
-                if (hit != 0x7fffffff) token = hit;
+                if (hit != kNowhere) token = hit;
                 run += __shfl_sync(0xffffffffu, upto, 31);
             }
             if (lane == 0) {
@@ -418,13 +566,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     }
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16, bool VEC, bool KEEP>
 static cudaError_t go(const VerifyArgs& a, int cluster, cudaStream_t s) {
-    auto kern = verify_kernel<BF16, VEC>;
-    if (cluster > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.n_req * cluster));
     cfg.blockDim = dim3(kThreads);
@@ -435,19 +578,27 @@ static cudaError_t go(const VerifyArgs& a, int cluster, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<BF16, VEC, KEEP>, a);
+}
+
+template <bool BF16, bool VEC>
+static cudaError_t go(const VerifyArgs& a, int cluster, cudaStream_t s) {
+    using L = vt::Lanes<BF16, VEC>;
+    const int64_t parts = (int64_t)cluster * kWarps, share = ((a.vocab + parts - 1) / parts + L::kStep - 1) / L::kStep;
+    return share * L::kVec <= kKeep ? go<BF16, VEC, true>(a, cluster, s) : go<BF16, VEC, false>(a, cluster, s);
 }
 
 }  // namespace vt
 
 cudaError_t launch_verify_tree(const VerifyArgs& a, int sms, cudaStream_t s) {
     // CTAs of a request: as many as leave each some thousand tokens and all of them a place at once.
-    int cluster = 8;
-    while (cluster > 1 && ((int64_t)cluster * a.n_req > 2 * sms || a.vocab / cluster < 1024)) cluster >>= 1;
+    const int cluster = (int)std::max<int64_t>(1, std::min<int64_t>({vt::kMaxCluster, 2 * sms / a.n_req, a.vocab / 1024}));
     const int es = a.bf16 ? 2 : 4;
     const bool vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * es % 16 == 0;
-    if (a.bf16) return vec ? vt::go<true, true>(a, cluster, s) : vt::go<true, false>(a, cluster, s);
-    return vec ? vt::go<false, true>(a, cluster, s) : vt::go<false, false>(a, cluster, s);
+    VerifyArgs b = a;
+    b.probs_vec = reinterpret_cast<uintptr_t>(a.probs) % 16 == 0 && a.probs_stride % 4 == 0;
+    if (a.bf16) return vec ? vt::go<true, true>(b, cluster, s) : vt::go<true, false>(b, cluster, s);
+    return vec ? vt::go<false, true>(b, cluster, s) : vt::go<false, false>(b, cluster, s);
 }
 
 }  // namespace qk

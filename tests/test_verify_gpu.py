@@ -96,7 +96,7 @@ def test_same_tokens_again_and_refusals(gpu, drafter):
     star = [1] + [(1 << i) | 1 for i in range(1, 64)]
     s["mask"] = signed(star * 6)
     s["draft"] = torch.arange(64).remainder(9).to(torch.int32).repeat(6)
-    s["draft"][5], s["draft"][70] = -1, 50
+    s["draft"][5], s["draft"][6], s["draft"][70], s["draft"][71] = -1, -2, 50, 2147483647
     s["u_accept"] = 0.5 + 0.5 * s["u_accept"]
     check(s, run(gpu, s))
 
@@ -152,7 +152,10 @@ def test_rows_without_weight_and_specials(gpu):
     s["draft"][7], s["draft"][10] = 1500, 1999
     s["u_accept"][7] = 0.4
     s["temp"][4] = float("inf")
+    s["draft"][1] = 2147483647
     out = run(gpu, s)
+    greedy = dict(s, temp=torch.zeros(5))
+    check(greedy, run(gpu, greedy))
     check(s, out)
     assert out["n_path"][0] == 1 and out["tokens"][0, 0] == -1
     assert out["tokens"][2, 0] == 1500 and out["tokens"][3, 0] == 1999 and out["n_path"][3] > 1

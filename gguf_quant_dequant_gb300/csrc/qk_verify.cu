@@ -24,6 +24,7 @@
 //     cluster barrier per exchange, and every CTA decides by itself;
 //   * the next row of a chain is asked for (into L2) while the sum is formed.
 #include <algorithm>
+#include <cfloat>
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -46,11 +47,16 @@ __device__ __forceinline__ float logit(const void* row, int64_t v) {
     return BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(row)[v] << 16) : static_cast<const float*>(row)[v];
 }
 
-// exp((x - top) rate) for the largest logit top of the row; NaN counts as -inf (the maximum drops it; exp(-200) is 0), and of
-// a row with +inf only those count.
+// exp((x - top) rate) for the largest logit top of the row, and its parts for
+// two at a time: NaN counts as -inf (the maximum drops it; exp(-200) is 0).  A
+// row with +inf is given top = FLT_MAX and rate 1, which leaves its mass there.
+__device__ __forceinline__ float exponent(float t) { return fminf(fmaxf(t, -200.0f), 0.0f); }
 __device__ __forceinline__ float weight(float x, float top, float rate) {
-    const float e = expf(fmaxf(__fmul_rn(__fsub_rn(x, top), rate), -200.0f));
-    return x == top ? 1.0f : e;
+    return expf(exponent(__fmul_rn(__fsub_rn(x, top), rate)));
+}
+__device__ __forceinline__ float2 weight2(float2 x, float top, float rate) {
+    const float2 t = __fmul2_rn(__fadd2_rn(x, make_float2(-top, -top)), make_float2(rate, rate));
+    return make_float2(expf(exponent(t.x)), expf(exponent(t.y)));
 }
 __device__ __forceinline__ float rest(float e, float tau, float q) { return fmaxf(__fsub_rn(e, __fmul_rn(tau, q)), 0.0f); }
 
@@ -62,17 +68,43 @@ struct Fix {
     double down;   // 2^-bits
     __device__ __forceinline__ int64_t of(float v) const { return __float2ll_rn(v * up); }
 };
-// Sum of weights in 0 .. 1 to about 2^-46: the running sum, from 1 on (so that it is the larger one), and the rounding it
-// loses.
+// Two sums of weights in 0 .. 1 to about 2^-46: the running sums, from 1 on (so
+// that they are the larger ones), and the rounding they lose.
 struct Sum {
-    float h = 1.0f, l = 0.0f;
-    __device__ __forceinline__ void add(float v) {
-        const float s = __fadd_rn(h, v);
-        l = __fadd_rn(l, __fsub_rn(v, __fsub_rn(s, h)));
+    float2 h = {1.0f, 1.0f}, l = {0.0f, 0.0f};
+    __device__ __forceinline__ void add(float2 v) {
+        const float2 s = __fadd2_rn(h, v), d = __fadd2_rn(s, make_float2(-h.x, -h.y));
+        l = __fadd2_rn(l, __fadd2_rn(v, make_float2(-d.x, -d.y)));
         h = s;
     }
-    __device__ __forceinline__ int64_t value(const Fix& f) const { return f.of(__fsub_rn(h, 1.0f)) + f.of(l); }
+    // kVec weights (one alone beside a zero).
+    template <int N>
+    __device__ __forceinline__ void add(const float (&v)[N]) {
+        if constexpr (N == 1) {
+            add(make_float2(v[0], 0.0f));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) add(make_float2(v[i], v[i + 1]));
+        }
+    }
+    __device__ __forceinline__ int64_t value(const Fix& f) const {
+        return f.of(__fsub_rn(h.x, 1.0f)) + f.of(__fsub_rn(h.y, 1.0f)) + f.of(l.x) + f.of(l.y);
+    }
 };
+// Logits to weights.
+template <int N>
+__device__ __forceinline__ void weigh(float (&v)[N], float top, float rate) {
+    if constexpr (N == 1) {
+        v[0] = weight(v[0], top, rate);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 w = weight2(make_float2(v[i], v[i + 1]), top, rate);
+            v[i] = w.x;
+            v[i + 1] = w.y;
+        }
+    }
+}
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -163,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
     }
     const float temp = a.temp[r], u_sample = a.u_sample[r];
     const bool greedy = !(temp >= kGreedy);
-    const float rate = greedy ? 1.0f : __frcp_rn(temp);
+    const float rate_of = greedy ? 1.0f : __frcp_rn(temp);
     const bool drafter = a.probs != nullptr && !greedy;
     if (tid < n) {
         // the parent is the nearest ancestor: the highest bit below the node's own
@@ -286,8 +318,9 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                 at = sh.best[top_turn][i];
             }
         warp_top(m, at);
-        const float top = m;
-        const int best = at;   // kNowhere: a row with nothing above -inf
+        const bool some = m > -INFINITY;   // else a row without weight
+        const float top = fminf(m, FLT_MAX), rate = m == INFINITY ? 1.0f : rate_of;
+        const int best = at;   // kNowhere: nothing above -inf
         top_turn ^= 1;
         int next = -1;
         if (greedy) {
@@ -314,13 +347,11 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                 if constexpr (KEEP) {
 #pragma unroll
                     for (int k = 0; k < kRegs; ++k)
-                        if (v0 + k * kStep < v1)
-#pragma unroll
-                            for (int i = 0; i < kVec; ++i) {
-                                x[k][i] = top > -INFINITY ? weight(x[k][i], top, rate) : 0.0f;
-                                s.add(x[k][i]);
-                            }
-                } else if (top > -INFINITY) {
+                        if (v0 + k * kStep < v1 && some) {
+                            weigh(x[k], top, rate);
+                            s.add(x[k]);
+                        }
+                } else if (some) {
                     for (int64_t v = v0 + lane * kVec; v < v1; v += kAhead * kStep) {
                         float w[kAhead][kVec];
 #pragma unroll
@@ -333,9 +364,10 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                             }
                         }
 #pragma unroll
-                        for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-                            for (int i = 0; i < kVec; ++i) s.add(weight(w[k][i], top, rate));
+                        for (int k = 0; k < kAhead; ++k) {
+                            weigh(w[k], top, rate);
+                            s.add(w[k]);
+                        }
                     }
                 }
                 exchange(warp_sum(s.value(fix)));
@@ -344,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
             // The children, in order: the first warp of every CTA decides, all alike.
             float kw[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) kw[h] = kid[h] >= 0 && top > -INFINITY ? weight(kx[h], top, rate) : 0.0f;
+            for (int h = 0; h < 2; ++h) kw[h] = kid[h] >= 0 && some ? weight(kx[h], top, rate) : 0.0f;
             unsigned todo[2] = {kids[0], kids[1]};
             uint64_t refused = 0;
             double tau = 0.0;
@@ -398,14 +430,15 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
 #pragma unroll
                     for (int k = 0; k < kRegs; ++k) {
                         const int64_t v = v0 + k * kStep + lane * kVec;
-                        if (v < v1) {
+                        if (v < v1 && some) {
                             float q1[kVec];
                             load_q(v, q1);
 #pragma unroll
-                            for (int i = 0; i < kVec; ++i) s.add(rest(x[k][i], off, q1[i]));
+                            for (int i = 0; i < kVec; ++i) q1[i] = rest(x[k][i], off, q1[i]);
+                            s.add(q1);
                         }
                     }
-                } else if (top > -INFINITY) {
+                } else if (some) {
                     constexpr int kTwo = kVec == 8 ? 1 : kVec == 4 ? 2 : 4;
                     for (int64_t v = v0 + lane * kVec; v < v1; v += kTwo * kStep) {
                         float w2[kTwo][kVec], q2[kTwo][kVec];
@@ -417,9 +450,12 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                             }
 #pragma unroll
                         for (int k = 0; k < kTwo; ++k)
-                            if (v + k * kStep < v1)
+                            if (v + k * kStep < v1) {
+                                weigh(w2[k], top, rate);
 #pragma unroll
-                                for (int i = 0; i < kVec; ++i) s.add(rest(weight(w2[k][i], top, rate), off, q2[k][i]));
+                                for (int i = 0; i < kVec; ++i) w2[k][i] = rest(w2[k][i], off, q2[k][i]);
+                                s.add(w2[k]);
+                            }
                     }
                 }
                 exchange(warp_sum(s.value(fix)));   // (and all have read the decision)

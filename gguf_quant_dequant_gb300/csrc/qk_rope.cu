@@ -13,8 +13,17 @@
 // Angles: pos * freq is kept as a whole number of 2^-96 turns, so that a far
 // position loses nothing (fp32 would be a radian off near position 2^24); the
 // cosine and sine come from their power series on an eighth of a turn, in
-// pairs of fp32 (about 2^-40), and are rounded to fp32 once.  They are
-// computed once per token and CTA and shared by its heads.
+// pairs of fp32 (about 2^-40), and are rounded to fp32 once.
+//
+// A warp takes a token and walks over its heads, 32 / (d / 8) rows a step, the
+// next step's loads ahead of this one's arithmetic.  It computes the token's
+// cosines and sines once (they cost some 200 instructions each) and keeps
+// what its lanes need of them in registers for all heads; a CTA per token with
+// the table in shared memory took 337 us for 32,764 tokens of 32 + 2 x 8 heads
+// (d 128, Q4_0 pages), this takes 209.  The instructions bound it (about 150 a
+// step with norm and rotation, 160 more where a step is quantized; the issue
+// slots are 79 % used): the bytes of that call would need 106 us.  Few tokens
+// are bound by latency: 3.5 us for one token of 32 + 8 heads.
 #include <algorithm>
 
 #include "qk_internal.h"
@@ -25,8 +34,10 @@
 namespace qk {
 namespace rope {
 
-constexpr int kThreads = 256;
-constexpr int kTable = 1024;   // (cos, sin) pairs a CTA can hold
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxHalf = 128;   // pairs of a row
+constexpr int kCtas = 3;        // on an SM: 80 registers a thread (2: 32 % slower for 32,764 tokens, 5: 30 %, for what spills)
+constexpr int kShares = 2;      // of the tokens' heads for each warp of the GPU (4: 20 % slower with 61 x 29 tokens)
 
 // ---------------------------------------------------------------- angles --
 // freq / (2 pi) as a fraction of a turn in units of 2^-96, modulo one turn
@@ -135,7 +146,7 @@ struct Args {
     const int32_t* pos;
     const float *q_norm, *k_norm, *freq;
     float eps;
-    bool pairs, q_vec, k_vec, v_vec, qo_vec, ko_vec;
+    bool pairs;
     void *q_out, *k_out;
     int64_t qo_stride, ko_stride;
     // the cache (keys and values go there when there is one)
@@ -143,7 +154,7 @@ struct Args {
     uint8_t *K, *V;
     Pool pool;
     unsigned* status;
-    int tok_per_cta, heads_per_cta;
+    int per;   // steps (32 / lanes rows each) of a warp per token
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -151,12 +162,44 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
     return w;
 }
-template <bool BF16>
-__device__ __forceinline__ void store8(void* base, int64_t at, bool vec, const float (&x)[8]) {
+// Eight elements of a row as they lie in memory (VEC: 16-byte aligned).
+template <bool BF16, bool VEC>
+struct Raw {
+    uint32_t w[BF16 ? 4 : 8];
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        if constexpr (BF16) {
+            const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+            if (VEC) {
+                const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+            }
+        } else {
+            const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+            if (VEC) {
+                const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p)), v = __ldcs(reinterpret_cast<const uint4*>(p + 4));
+                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = p[i];
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float2 (&x)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u))
+                        : make_float2(__uint_as_float(w[(2 * i) % (BF16 ? 4 : 8)]), __uint_as_float(w[(2 * i + 1) % (BF16 ? 4 : 8)]));
+    }
+};
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store8(void* base, int64_t at, const float (&x)[8]) {
     if constexpr (BF16) {
         uint16_t* p = static_cast<uint16_t*>(base) + at;
         const uint4 w = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
-        if (vec) {
+        if (VEC) {
             *reinterpret_cast<uint4*>(p) = w;
         } else {
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -168,7 +211,7 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool vec, const f
         }
     } else {
         float* p = static_cast<float*>(base) + at;
-        if (vec) {
+        if (VEC) {
             *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
         } else {
@@ -178,133 +221,168 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool vec, const f
     }
 }
 
+// Two products, and their sums with others, each rounded by itself. (The sums
+// are not taken in pairs too: a paired product and a paired sum become one
+// fused operation, whatever their roundings say.)
+__device__ __forceinline__ float2 mul_rn(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add_rn(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+
 // T: the cache's block type, or 0 where keys go to rows.
-template <int T, bool IN16, bool OUT16>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
-    __shared__ float2 table[kTable];
-    const int tid = threadIdx.x, lanes = 1 << a.lanes_log2, sub = tid & (lanes - 1);
-    const int heads = a.n_heads + a.n_kv + a.n_v, half = a.rot >> 1;
-    const int64_t t0 = (int64_t)blockIdx.x * a.tok_per_cta;
-    const int h0 = blockIdx.y * a.heads_per_cta;
-    const int n_heads_here = min(a.heads_per_cta, heads - h0);
-    const int n_tok_here = (int)min((int64_t)a.tok_per_cta, a.n_tok - t0);
-    const int rows = n_tok_here * n_heads_here;
-    for (int i = tid; i < n_tok_here * half; i += kThreads) {
-        const int t = i / half, f = i - t * half;
-        table[i] = cos_sin(turns_of(a.freq[f]), a.pos[t0 + t]);
-    }
+template <int T, bool IN16, bool OUT16, bool VEC>
+__global__ void __launch_bounds__(kThreads, kCtas) rope_kernel(const Args a) {
+    __shared__ Turn turns[kMaxHalf];
+    __shared__ float2 tables[kWarps][kMaxHalf];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lanes = 1 << a.lanes_log2, sub = lane & (lanes - 1), half = a.rot >> 1;
+    const int rows = 32 >> a.lanes_log2;   // of a step
+    const int e0 = 8 * sub;                // my elements of a row
+    const int steps_q = (a.n_heads + rows - 1) / rows, steps_k = (a.n_kv + rows - 1) / rows, steps_v = (a.n_v + rows - 1) / rows;
+    const int s0 = blockIdx.y * a.per, s1 = min(s0 + a.per, steps_q + steps_k + steps_v);
+    for (int f = tid; f < half; f += kThreads) turns[f] = turns_of(a.freq[f]);
     __syncthreads();
-    const int e0 = 8 * sub;                   // my elements of a row
-    const int step = kThreads >> a.lanes_log2;
-    const int rounds = (rows + step - 1) / step;
-    for (int it = 0; it < rounds; ++it) {
-        const int row = it * step + (tid >> a.lanes_log2);
-        const bool live = row < rows;
-        const int t = live ? row / n_heads_here : 0;
-        const int head = live ? h0 + row - t * n_heads_here : 0;
-        const int64_t tok = t0 + t;
-        const int kind = !live ? 3 : head < a.n_heads ? 0 : head < a.n_heads + a.n_kv ? 1 : 2;   // query, key, value, none
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        const int g = head - (kind == 1 ? a.n_heads : kind == 2 ? a.n_heads + a.n_kv : 0);
-        int64_t slot = -1;
-        if (T != 0 && (kind == 1 || kind == 2)) {
-            slot = a.slots[tok];
-            if (slot < -1 || (slot >= 0 && (slot >> a.pool.page_log2) >= a.pool.n_pages)) {
-                atomicOr(a.status, STATUS_BAD_PAGE);
-                slot = -1;
+    // The lane's rotation: y = x c + partner s.
+    const bool turn = e0 < a.rot, second = e0 >= half;
+    const int other = lane + (turn ? (second ? -(half >> 3) : half >> 3) : 0);
+    float2* const table = tables[warp];
+    const float inv_d = 1.0f / (float)a.d;   // d is a power of two: exact
+
+    const int64_t tok = (int64_t)blockIdx.x * kWarps + warp;
+    if (tok >= a.n_tok) return;
+    const int pos = half > 0 ? a.pos[tok] : 0;
+    int64_t slot = -1;
+    if (T != 0 && s1 > steps_q) {
+        slot = a.slots[tok];
+        if (slot < -1 || (slot >= 0 && (slot >> a.pool.page_log2) >= a.pool.n_pages)) {
+            if (lane == 0) atomicOr(a.status, STATUS_BAD_PAGE);
+            slot = -1;
+        }
+    }
+    // The token's cosines and sines, by the warp: y = x c + partner s.
+    float2 c[4], sn[4];
+    if (half > 0 && s0 < steps_q + steps_k) {
+        for (int f = lane; f < half; f += 32) table[f] = cos_sin(turns[f], pos);
+        __syncwarp();
+        const float2* r = table + (a.pairs ? e0 >> 1 : second ? e0 - half : e0);
+        if (turn) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 r0 = r[a.pairs ? i : 2 * i], r1 = r[a.pairs ? i : 2 * i + 1];
+                c[i] = make_float2(r0.x, r1.x), sn[i] = make_float2(!a.pairs && second ? r0.y : -r0.y, a.pairs || second ? r1.y : -r1.y);
             }
         }
-        if (kind == 0) kv::load8<IN16>(a.q, tok * a.q_stride + (int64_t)g * a.d + e0, a.q_vec, x);
-        if (kind == 1) kv::load8<IN16>(a.k, tok * a.k_stride + (int64_t)g * a.d + e0, a.k_vec, x);
-        if (kind == 2) kv::load8<IN16>(a.v, tok * a.v_stride + (int64_t)g * a.d + e0, a.v_vec, x);
-        const float* w = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-        if (__any_sync(0xffffffffu, w != nullptr)) {
-            float s[8];
+    }
+    int first = 0;   // of the kind's steps
+#pragma unroll 1
+    for (int kind = 0; kind < (T == 0 ? 2 : 3); ++kind) {   // queries, keys, values
+        const int n = kind == 0 ? a.n_heads : kind == 1 ? a.n_kv : a.n_v;
+        const int last = first + (n + rows - 1) / rows;
+        const int from = max(s0, first) - first, to = min(s1, last) - first;
+        first = last;
+        if (from >= to) continue;
+        const float* norm = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+        float2 w[4];
+        if (norm) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = __fmul_rn(x[i], x[i]);
-            float sum = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])),
-                                  __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
-            for (int o = 1; o < lanes; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-            if (w) {
-                const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.d), a.eps)));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), w[e0 + i]);
-            }
+            for (int i = 0; i < 4; ++i) w[i] = make_float2(norm[e0 + 2 * i], norm[e0 + 2 * i + 1]);
         }
-        if (half > 0 && __any_sync(0xffffffffu, kind < 2)) {
-            const bool turns = kind < 2 && e0 < a.rot;
-            const float2* cs = table + t * half;
-            if (a.pairs) {
-                if (turns) {
+        const int g0 = from * rows + (lane >> a.lanes_log2);   // my head in the first step
+        const int in_step = rows * a.d;
+        const bool rows_out = kind == 0 || T == 0;
+        int64_t in = tok * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + (int64_t)g0 * a.d + e0;
+        const void* base = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+        int64_t out = 0;   // elements, or bytes of the pool
+        void* to_rows = kind == 0 ? a.q_out : a.k_out;
+        uint8_t* pool = kind == 1 ? a.K : a.V;
+        if (rows_out)
+            out = tok * (kind == 0 ? a.qo_stride : a.ko_stride) + (int64_t)g0 * a.d + e0;
+        else if constexpr (T != 0)
+            out = (sub >> 2) * Fmt<T>::BB + pool_row(a.pool, slot >> a.pool.page_log2, g0, (int)(slot & ((1 << a.pool.page_log2) - 1)));
+        const int64_t out_step = rows_out ? in_step : (int64_t)rows * a.pool.row_bytes << a.pool.page_log2;
+        const bool turned = half > 0 && kind < 2;
+        int left = n - g0;   // my head is one while this is above 0
+        Raw<IN16, VEC> next{};
+        if (left > 0) next.load(base, in);
+#pragma unroll 1
+        for (int st = from; st < to; ++st, left -= rows, out += out_step) {
+            float2 x[4];
+            next.get(x);
+            in += in_step;
+            if (st + 1 < to && left > rows) next.load(base, in);
+            if (norm) {
+                float2 q[4];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float2 r = cs[(e0 + i) >> 1];
-                        const float u = x[i], v = x[i + 1];
-                        x[i] = __fadd_rn(__fmul_rn(u, r.x), -__fmul_rn(v, r.y));
-                        x[i + 1] = __fadd_rn(__fmul_rn(v, r.x), __fmul_rn(u, r.y));
-                    }
+                for (int i = 0; i < 4; ++i) q[i] = mul_rn(x[i], x[i]);
+                float sum = __fadd_rn(__fadd_rn(__fadd_rn(q[0].x, q[0].y), __fadd_rn(q[1].x, q[1].y)),
+                                      __fadd_rn(__fadd_rn(q[2].x, q[2].y), __fadd_rn(q[3].x, q[3].y)));
+                sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 1));
+                sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 2));
+                if (lanes > 4) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 4));
+                if (lanes > 8) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 8));
+                if (lanes > 16) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 16));
+                const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, inv_d), a.eps)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = mul_rn(mul_rn(x[i], make_float2(inv, inv)), w[i]);
+            }
+            if (turned) {
+                float2 p[4];
+                if (a.pairs) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = make_float2(x[i].y, x[i].x);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        p[i] = make_float2(__shfl_sync(0xffffffffu, x[i].x, other), __shfl_sync(0xffffffffu, x[i].y, other));
                 }
-            } else {
-                const bool second = e0 >= half;
-                const int other = (tid & 31) + (turns ? (second ? -(half >> 3) : half >> 3) : 0);
-                float p[8];
+                if (turn) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, x[i], other);
-                if (turns) {
-                    cs += second ? e0 - half : e0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 r = cs[i];
-                        const float m = __fmul_rn(p[i], r.y);
-                        x[i] = __fadd_rn(__fmul_rn(x[i], r.x), second ? m : -m);
-                    }
+                    for (int i = 0; i < 4; ++i) x[i] = add_rn(mul_rn(x[i], c[i]), mul_rn(p[i], sn[i]));
                 }
             }
-        }
-        if (kind == 0) store8<OUT16>(a.q_out, tok * a.qo_stride + (int64_t)g * a.d + e0, a.qo_vec, x);
-        if constexpr (T == 0) {
-            if (kind == 1) store8<OUT16>(a.k_out, tok * a.ko_stride + (int64_t)g * a.d + e0, a.ko_vec, x);
-        } else if (__any_sync(0xffffffffu, kind == 1 || kind == 2)) {
-            uint8_t* dst = nullptr;
-            if (slot >= 0)
-                dst = (kind == 1 ? a.K : a.V) + (sub >> 2) * Fmt<T>::BB +
-                      pool_row(a.pool, slot >> a.pool.page_log2, g, (int)(slot & ((1 << a.pool.page_log2) - 1)));
-            kv::append_block<T>(x, dst, sub & 3);
+            const float y[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+            if (rows_out) {
+                if (left > 0) store8<OUT16, VEC>(to_rows, out, y);
+            } else if constexpr (T != 0) {
+                kv::append_block<T>(y, left > 0 && slot >= 0 ? pool + out : nullptr, sub & 3);
+            }
         }
     }
 }
 
 template <int T, bool IN16, bool OUT16>
-static cudaError_t go(const Args& a, dim3 grid, cudaStream_t s) {
-    rope_kernel<T, IN16, OUT16><<<grid, kThreads, 0, s>>>(a);
+static cudaError_t go(const Args& a, bool vec, dim3 grid, cudaStream_t s) {
+    if (vec)
+        rope_kernel<T, IN16, OUT16, true><<<grid, kThreads, 0, s>>>(a);
+    else
+        rope_kernel<T, IN16, OUT16, false><<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 static cudaError_t launch(int type, Args a, bool in16, bool out16, int sms, cudaStream_t s) {
-    const int heads = a.n_heads + a.n_kv + a.n_v, lanes = a.d / 8;
+    const int lanes = a.d / 8;
     a.lanes_log2 = lanes == 4 ? 2 : lanes == 8 ? 3 : lanes == 16 ? 4 : 5;
+    // 16-byte loads and stores, where all rows allow them.
     const int es = in16 ? 2 : 4, eo = out16 ? 2 : 4;
-    auto vec = [](const void* p, int64_t stride, int e) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * e % 16 == 0; };
-    a.q_vec = vec(a.q, a.q_stride, es);
-    a.k_vec = vec(a.k, a.k_stride, es);
-    a.v_vec = vec(a.v, a.v_stride, es);
-    a.qo_vec = vec(a.q_out, a.qo_stride, eo);
-    a.ko_vec = vec(a.k_out, a.ko_stride, eo);
-    const int fit = kThreads / lanes;   // rows of one round
-    if (heads < fit) {                  // several tokens a CTA
-        a.tok_per_cta = std::min(fit / heads, kTable / std::max(a.rot / 2, 1));
-        a.heads_per_cta = heads;
-    } else {                            // a token a CTA, or for few tokens a round of its heads
-        a.tok_per_cta = 1;
-        a.heads_per_cta = a.n_tok >= 2 * sms ? heads : fit;
-    }
-    const dim3 grid((unsigned)((a.n_tok + a.tok_per_cta - 1) / a.tok_per_cta), (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta));
+    auto fits = [](int n, const void* p, int64_t stride, int e) {
+        return n == 0 || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * e % 16 == 0);
+    };
+    const bool vec = fits(a.n_heads, a.q, a.q_stride, es) && fits(a.n_kv, a.k, a.k_stride, es) && fits(a.n_v, a.v, a.v_stride, es) &&
+                     fits(a.n_heads, a.q_out, a.qo_stride, eo) && (type != 0 || fits(a.n_kv, a.k_out, a.ko_stride, eo));
+    // A warp takes a token's steps `per` at a time, so that there are about
+    // kShares shares for each warp the GPU holds; each share computes the
+    // token's cosines and sines again.
+    const int rows = 32 / lanes;
+    const int64_t steps = (a.n_heads + rows - 1) / rows + (a.n_kv + rows - 1) / rows + (a.n_v + rows - 1) / rows;
+    const int64_t warps = (int64_t)sms * kCtas * kWarps;
+    const int64_t per = std::min(steps, std::max<int64_t>(1, a.n_tok * steps / (kShares * warps)));
+    const int64_t parts = (steps + per - 1) / per;
+    a.per = (int)((steps + parts - 1) / parts);
+    const dim3 grid((unsigned)((a.n_tok + kWarps - 1) / kWarps), (unsigned)((steps + a.per - 1) / a.per));
     switch (type) {
-    case 0: return in16 ? (out16 ? go<0, true, true>(a, grid, s) : go<0, true, false>(a, grid, s))
-                        : (out16 ? go<0, false, true>(a, grid, s) : go<0, false, false>(a, grid, s));
-    case T_Q8_0: return in16 ? go<T_Q8_0, true, true>(a, grid, s) : go<T_Q8_0, false, true>(a, grid, s);
-    case T_Q5_0: return in16 ? go<T_Q5_0, true, true>(a, grid, s) : go<T_Q5_0, false, true>(a, grid, s);
-    case T_Q4_0: return in16 ? go<T_Q4_0, true, true>(a, grid, s) : go<T_Q4_0, false, true>(a, grid, s);
+    case 0: return in16 ? (out16 ? go<0, true, true>(a, vec, grid, s) : go<0, true, false>(a, vec, grid, s))
+                        : (out16 ? go<0, false, true>(a, vec, grid, s) : go<0, false, false>(a, vec, grid, s));
+    case T_Q8_0: return in16 ? go<T_Q8_0, true, true>(a, vec, grid, s) : go<T_Q8_0, false, true>(a, vec, grid, s);
+    case T_Q5_0: return in16 ? go<T_Q5_0, true, true>(a, vec, grid, s) : go<T_Q5_0, false, true>(a, vec, grid, s);
+    case T_Q4_0: return in16 ? go<T_Q4_0, true, true>(a, vec, grid, s) : go<T_Q4_0, false, true>(a, vec, grid, s);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -80,7 +80,8 @@ SIGNATURES = {
                             _int, _i64, _i64, _p]),
     "qk_kv_append_rope": (_int, [_int, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _int, _int, _int, _p, _p, _p, ctypes.c_float,
                                  _p, _int, _int, _p, _p, _p, _i64, _int, _p, _i64, _p]),
-    "qk_verify_tree": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p]),
+    "qk_verify_workspace": (_sz, [_i64, _i64, _i64]),
+    "qk_verify_tree": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p, _sz, _p]),
     "qk_moe_workspace": (_sz, [_int, _int, _int, _i64, _i64, _int, _i64]),
     "qk_moe_ffn": (_int, [_int, _p, _p, _int, _p, _int, _i64, _i64, _p, _int, _int, ctypes.c_float, _p, _i64, _p, _p, _p, _p,
                           _sz, _p]),
@@ -619,8 +620,13 @@ def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x
     return out, ids, gate
 
 
+@functools.lru_cache(maxsize=256)
+def verify_workspace(n_rows: int, n_req: int, vocab: int) -> int:
+    return load().qk_verify_workspace(n_rows, n_req, vocab)
+
+
 def verify_tree(logits, cu, draft, mask, temp, u_accept, u_sample, probs=None, max_path: int = TREE_MAX, out=None,
-                stream=None) -> dict:
+                ws=None, stream=None) -> dict:
     """Drafted trees judged against the target's probabilities (qk_verify_tree):
     logits fp32 or bf16 CUDA [n_rows, vocab]; cu int32 [n_req + 1]; draft
     int32, mask int64 (or None: chains), u_accept fp32 [n_rows]; temp, u_sample
@@ -640,11 +646,18 @@ def verify_tree(logits, cu, draft, mask, temp, u_accept, u_sample, probs=None, m
     elif out["path"].dim() != 2:
         raise QKError(2, w, f"path of two dimensions expected, got shape {tuple(out['path'].shape)}")
     P = out["path"].shape[1]
+    need = verify_workspace(n, r, V)
+    if ws is None and need:
+        ws = _empty(need, torch.uint8, logits, stream, kept=False)
+    elif ws is not None and not (ws.is_cuda and ws.is_contiguous()):
+        _on_gpu(ws, w)
+        raise QKError(8, w, f"contiguous ws expected, got strides {ws.stride()}")
     _check(load().qk_verify_tree(
         logits.data_ptr(), _dtype(logits, w), n, V, _rows(logits, w), _of(cu, i32, w, r + 1), r, _of(draft, i32, w, n),
         _of(mask, torch.int64, w, n), _of(temp, f32, w, r), _of(u_accept, f32, w, n), _of(u_sample, f32, w, r), _ptr(probs),
         0 if probs is None else _rows(probs, w), _of(out["path"], i32, w, r * P), P, _of(out["n_path"], i32, w, r),
-        _of(out["tokens"], i32, w, r * P), _stream_on(logits, stream)), "qk_verify_tree")
+        _of(out["tokens"], i32, w, r * P), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_on(logits, stream)),
+        "qk_verify_tree")
     return out
 
 

@@ -704,10 +704,15 @@ qk_status qk_kv_append_rope(int type, const void* q, const void* k, const void* 
     return QK_OK;
 }
 
+size_t qk_verify_workspace(int64_t n_rows, int64_t n_req, int64_t vocab) {
+    if (n_rows < 0 || n_req < 1 || vocab < 1 || !count_ok(n_rows) || !count_ok(vocab) || n_req > (1 << 27)) return 0;
+    return (size_t)qk::verify_ws_bytes(n_rows, n_req, vocab);
+}
+
 qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride, const int32_t* cu,
                          int64_t n_req, const int32_t* draft, const uint64_t* mask, const float* temp, const float* u_accept,
                          const float* u_sample, const float* probs, int64_t probs_stride, int32_t* path, int64_t path_stride,
-                         int32_t* n_path, int32_t* tokens, void* stream) {
+                         int32_t* n_path, int32_t* tokens, void* ws, size_t ws_bytes, void* stream) {
     if (dtype != QK_OUT_F32 && dtype != QK_OUT_BF16) return fail(QK_ERR_ARG, "bad dtype %d", dtype);
     if (!count_ok(n_rows) || !count_ok(vocab) || vocab < 1 || n_req < 0 || n_req > (1 << 27))
         return fail(QK_ERR_SHAPE, "bad n_rows=%lld, vocab=%lld or n_req=%lld", (long long)n_rows, (long long)vocab,
@@ -723,11 +728,17 @@ qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t 
                           (const void*)probs, (const void*)path, (const void*)n_path, (const void*)tokens})
         if (!aligned(p, 4)) return fail(QK_ERR_ALIGN, "the lists and probs must be 4-byte aligned");
     if (!aligned(mask, 8)) return fail(QK_ERR_ALIGN, "mask must be 8-byte aligned");
+    const size_t need = qk_verify_workspace(n_rows, n_req, vocab);
+    if (need) {
+        if (!ws) return fail(QK_ERR_NULL, "ws is NULL");
+        if (ws_bytes < need) return fail(QK_ERR_WORKSPACE, "ws_bytes=%zu, %zu needed", ws_bytes, need);
+        if (!aligned(ws, 16)) return fail(QK_ERR_ALIGN, "ws must be 16-byte aligned");
+    }
     int sms = 0;
     const qk_status st = device_state(nullptr, &sms);
     if (st != QK_OK) return st;
     const qk::VerifyArgs a{logits, dtype == QK_OUT_BF16, n_rows, vocab, row_stride, cu, n_req, draft, mask, temp, u_accept,
-                           u_sample, probs, probs_stride, path, path_stride, n_path, tokens, false};
+                           u_sample, probs, probs_stride, path, path_stride, n_path, tokens, ws, false};
     cudaError_t e = qk::launch_verify_tree(a, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "qk_verify_tree launch");
     g_last_error.clear();

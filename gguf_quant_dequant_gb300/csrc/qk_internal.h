@@ -143,8 +143,10 @@ struct VerifyArgs {
     int32_t* path;
     int64_t path_stride;
     int32_t *n_path, *tokens;
+    void* ws;
     bool probs_vec;   // rows of probs on 16-byte boundaries (set by the launcher)
 };
+int64_t verify_ws_bytes(int64_t n_rows, int64_t n_req, int64_t vocab);
 cudaError_t launch_verify_tree(const VerifyArgs& a, int sms, cudaStream_t s);
 
 // A mixture-of-experts layer (qk_moe.cu); the members are qk_moe_ffn's

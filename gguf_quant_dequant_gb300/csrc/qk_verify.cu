@@ -38,6 +38,7 @@ namespace vt {
 
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
+constexpr int kPieceWarps = 8;
 constexpr int kNodes = QK_TREE_MAX;
 constexpr int kKeep = 32;             // logits of a row that a thread keeps
 constexpr float kGreedy = 0x1p-20f;   // temperatures below it: the largest logit
@@ -141,6 +142,8 @@ struct Shared {
     int64_t piece[kWarps];                  // the sampled part's pieces
     int parent[kNodes], token[kNodes];
     int part, usual, next, again;
+    float node_top[kNodes];                 // of the nodes' rows, where pieces were summed first: the largest logit, its place
+    int node_best[kNodes], taken[kNodes];   // and the child that is taken for sure, or -1
     uint64_t refused;                       // children of the node, without the drafter's probabilities
     double tau;
     int64_t target, before;
@@ -171,9 +174,90 @@ struct Lanes {
     }
 };
 
+// ------------------------------------------------------- rows at once --
+// What is known of 1,024 of a row's logits: their largest and its first place,
+// the sum of their weights relative to it, and the rate they were taken at.
+struct Piece {
+    float top;
+    int best;
+    float sum, rate;
+};
+constexpr int kPiece = 1024;
+// How far the pieces' sum can be off the row's, and more.  Weights count down to
+// exponents of -32 (2^31 of them come to less than 2^-15 of the largest's 1); up
+// to there the fast exponential (2 + 1.2 |t| steps of 2^-23) and two roundings of
+// the exponent (|t| 2^-23) leave less than a part 2^-16.  A child is sure to be
+// taken when it is by this margin.
+constexpr double kSure = 1.0 + 0x1p-13;
+
+// A warp per piece; no warp waits for another.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kPieceWarps * 32) piece_kernel(const VerifyArgs a, Piece* pieces, int per_row) {
+    using L = Lanes<BF16, VEC>;
+    constexpr int kVec = L::kVec, kStep = L::kStep, kRegs = kPiece / kStep;
+    const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    const int item = (int)blockIdx.x * kPieceWarps + (threadIdx.x >> 5), row = item / per_row, part = item - row * per_row;
+    if (row >= a.n_rows) return;
+    const void* p = static_cast<const uint8_t*>(a.logits) + (int64_t)row * a.row_stride * (BF16 ? 2 : 4);
+    const int64_t v0 = (int64_t)part * kPiece, v1 = min(v0 + kPiece, a.vocab);
+    float x[kRegs][kVec];
+#pragma unroll
+    for (int k = 0; k < kRegs; ++k) {
+        const int64_t v = v0 + k * kStep + lane * kVec;
+        if (v < v1) {
+            L::load(p, v, v1, x[k]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[k][i] = -INFINITY;
+        }
+    }
+    // The row's request: the last one that begins at or before it.
+    int64_t r = 0;
+    for (int64_t width = a.n_req; width > 1;) {
+        const int64_t step = (width + 31) / 32, i = r + lane * step;
+        const bool below = lane * step < width && a.cu[i] <= row;
+        const int n = __popc(__ballot_sync(0xffffffffu, below));
+        const int64_t skip = (int64_t)max(n - 1, 0) * step;
+        r += skip;
+        width = min(step, width - skip);
+    }
+    const float temp = a.temp[r];
+    const bool greedy = !(temp >= kGreedy);
+    const float rate = greedy ? 1.0f : __frcp_rn(temp);
+    float m = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kRegs; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) m = fmaxf(m, x[k][i]);
+    int at = kNowhere;
+    if (greedy) {
+#pragma unroll
+        for (int k = kRegs - 1; k >= 0; --k)
+#pragma unroll
+            for (int i = kVec - 1; i >= 0; --i)
+                if (x[k][i] == m && m > -INFINITY) at = (int)(v0 + k * kStep + lane * kVec + i);
+        warp_top(m, at);
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (m > -INFINITY) {
+            float s[4] = {0, 0, 0, 0};   // NaN stays: then nothing is sure
+#pragma unroll
+            for (int k = 0; k < kRegs; ++k)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) s[(k * kVec + i) & 3] += __expf((x[k][i] - m) * rate);
+            total = (s[0] + s[1]) + (s[2] + s[3]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) pieces[item] = Piece{m, at, total, rate};
+}
+
 // KEEP: the part of a thread fits its registers.
 template <bool BF16, bool VEC, bool KEEP>
-__global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const VerifyArgs a, const Piece* pieces, int per_row) {
     using L = Lanes<BF16, VEC>;
     constexpr int kVec = L::kVec, kStep = L::kStep, kRegs = KEEP ? kKeep / kVec : 1, kAhead = KEEP ? 1 : 8 / (kVec > 4 ? 2 : 1);
     __shared__ Shared sh;
@@ -224,7 +308,75 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
     int cur = 0, length = 1;
     if (rank == 0 && tid == 0) path[0] = 0;
     cl.sync();   // every CTA of the cluster runs (and has its tree) before another writes to its shared memory
+    if (pieces) {
+        // A warp a node: its row's largest logit, and the child that is taken for sure once the node is reached, where the
+        // pieces of the row decide by a margin (and no other child is tried before it).
+        pdl_wait_prior();
+        for (int p = warp; p < n; p += kWarps) {
+            const Piece* of = pieces + (row0 + p) * per_row;
+            unsigned kids[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = lane + 32 * h;
+                kids[h] = __ballot_sync(0xffffffffu, i > p && i < n && sh.parent[i] == p);
+            }
+            int c = kids[0] ? __ffs(kids[0]) - 1 : kids[1] ? 31 + __ffs(kids[1]) : -1;
+            const int y = c >= 0 ? sh.token[c] : -1;
+            const bool test = !greedy && y >= 0 && y < a.vocab;
+            float x = 0.0f, qy = 1.0f, u = 0.0f;
+            if (test) {
+                x = logit<BF16>(static_cast<const uint8_t*>(a.logits) + (row0 + p) * a.row_stride * (BF16 ? 2 : 4), y);
+                u = a.u_accept[row0 + c];
+                if (drafter) qy = a.probs[(row0 + p) * a.probs_stride + y];
+            }
+            float m = -INFINITY;
+            int at = kNowhere;
+            bool same = true;
+            for (int i = lane; i < per_row; i += 32) {
+                const Piece one = of[i];
+                same &= one.rate == rate_of;
+                if (one.top > m) {
+                    m = one.top;
+                    at = one.best;
+                }
+            }
+            warp_top(m, at);
+            bool sure = false;
+            if (greedy) {
+#pragma unroll
+                for (int h = 1; h >= 0; --h) {
+                    const int i = lane + 32 * h;
+                    const unsigned hit = __ballot_sync(0xffffffffu, (kids[h] >> lane & 1) && at != kNowhere && sh.token[i] == at);
+                    if (hit) {
+                        c = __ffs(hit) - 1 + 32 * h;
+                        sure = true;
+                    }
+                }
+            } else if (test && fabsf(m) < INFINITY) {
+                double S = 0.0;
+                for (int i = lane; i < per_row; i += 32) S += (double)of[i].sum * (double)weight(of[i].top, m, rate_of);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+                sure = (double)u * (double)qy * S * kSure < (double)weight(x, m, rate_of);
+            }
+            sure = __all_sync(0xffffffffu, same) && sure;
+            if (lane == 0) {
+                sh.node_top[p] = m;
+                sh.node_best[p] = at;
+                sh.taken[p] = sure ? c : -1;
+            }
+        }
+        __syncthreads();
+    }
     for (;;) {
+        while (pieces && length < a.path_stride && sh.taken[cur] >= 0) {
+            cur = sh.taken[cur];
+            if (rank == 0 && tid == 0) {
+                tokens[length - 1] = sh.token[cur];
+                path[length] = cur;
+            }
+            ++length;
+        }
         const void* row = static_cast<const uint8_t*>(a.logits) + (row0 + cur) * a.row_stride * (BF16 ? 2 : 4);
         const float* q = drafter ? a.probs + (row0 + cur) * a.probs_stride : nullptr;
         // The drafter's probabilities of kVec tokens from v on (0 behind the part: the weights there are 0 too).
@@ -283,45 +435,50 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                 if (drafter) kq[h] = q[kid[h]];
             }
         }
-        if constexpr (KEEP) {
-#pragma unroll
-            for (int k = 0; k < kRegs; ++k)
-                if (v0 + k * kStep < v1) look(x[k], v0 + k * kStep + lane * kVec);
+        if (pieces) {
+            m = sh.node_top[cur];
+            at = sh.node_best[cur];
         } else {
-            for (int64_t v = v0 + lane * kVec; v < v1; v += kAhead * kStep) {
-                float w[kAhead][kVec];
+            if constexpr (KEEP) {
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    if (v + k * kStep < v1) {
-                        L::load(row, v + k * kStep, v1, w[k]);
-                    } else {
+                for (int k = 0; k < kRegs; ++k)
+                    if (v0 + k * kStep < v1) look(x[k], v0 + k * kStep + lane * kVec);
+            } else {
+                for (int64_t v = v0 + lane * kVec; v < v1; v += kAhead * kStep) {
+                    float w[kAhead][kVec];
 #pragma unroll
-                        for (int i = 0; i < kVec; ++i) w[k][i] = -INFINITY;
+                    for (int k = 0; k < kAhead; ++k) {
+                        if (v + k * kStep < v1) {
+                            L::load(row, v + k * kStep, v1, w[k]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kVec; ++i) w[k][i] = -INFINITY;
+                        }
                     }
-                }
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) look(w[k], v + k * kStep);
+                    for (int k = 0; k < kAhead; ++k) look(w[k], v + k * kStep);
+                }
             }
-        }
-        warp_top(m, at);
-        if (lane < C) {
-            Shared* p = cl.map_shared_rank(&sh, lane);
-            p->top[top_turn][me] = m;
-            p->best[top_turn][me] = at;
-        }
-        cl.sync();
-        m = -INFINITY;
-        at = kNowhere;
-        for (int i = lane; i < parts; i += 32)
-            if (sh.top[top_turn][i] > m) {   // parts in order: the first place stays
-                m = sh.top[top_turn][i];
-                at = sh.best[top_turn][i];
+            warp_top(m, at);
+            if (lane < C) {
+                Shared* p = cl.map_shared_rank(&sh, lane);
+                p->top[top_turn][me] = m;
+                p->best[top_turn][me] = at;
             }
-        warp_top(m, at);
+            cl.sync();
+            m = -INFINITY;
+            at = kNowhere;
+            for (int i = lane; i < parts; i += 32)
+                if (sh.top[top_turn][i] > m) {   // parts in order: the first place stays
+                    m = sh.top[top_turn][i];
+                    at = sh.best[top_turn][i];
+                }
+            warp_top(m, at);
+            top_turn ^= 1;
+        }
         const bool some = m > -INFINITY;   // else a row without weight
         const float top = fminf(m, FLT_MAX), rate = m == INFINITY ? 1.0f : rate_of;
         const int best = at;   // kNowhere: nothing above -inf
-        top_turn ^= 1;
         int next = -1;
         if (greedy) {
             const unsigned b0 = __ballot_sync(0xffffffffu, kid[0] == best), b1 = __ballot_sync(0xffffffffu, kid[1] == best);
@@ -335,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
             }
         } else {
             // The first child's row is the next one to be read, if any.
-            if (kids[0] | kids[1]) {
+            if (!pieces && (kids[0] | kids[1])) {
                 const int64_t c = kids[0] ? __ffs(kids[0]) - 1 : 31 + __ffs(kids[1]);
                 const uint8_t* ahead = static_cast<const uint8_t*>(a.logits) + (row0 + c) * a.row_stride * (BF16 ? 2 : 4);
                 for (int64_t b = v0 * (BF16 ? 2 : 4) + lane * 128; b < v1 * (BF16 ? 2 : 4); b += 32 * 128)
@@ -603,28 +760,50 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
 }
 
 template <bool BF16, bool VEC, bool KEEP>
-static cudaError_t go(const VerifyArgs& a, int cluster, cudaStream_t s) {
+static cudaError_t go(const VerifyArgs& a, int cluster, int per_row, cudaStream_t s) {
+    Piece* pieces = per_row ? static_cast<Piece*>(a.ws) : nullptr;
+    if (per_row) {
+        const int64_t ctas = (a.n_rows * per_row + kPieceWarps - 1) / kPieceWarps;
+        piece_kernel<BF16, VEC><<<(unsigned)ctas, kPieceWarps * 32, 0, s>>>(a, pieces, per_row);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.n_req * cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<BF16, VEC, KEEP>, a);
+    cfg.numAttrs = per_row ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<BF16, VEC, KEEP>, a, (const Piece*)pieces, per_row);
 }
 
 template <bool BF16, bool VEC>
-static cudaError_t go(const VerifyArgs& a, int cluster, cudaStream_t s) {
+static cudaError_t go(const VerifyArgs& a, int cluster, int per_row, cudaStream_t s) {
     using L = vt::Lanes<BF16, VEC>;
     const int64_t parts = (int64_t)cluster * kWarps, share = ((a.vocab + parts - 1) / parts + L::kStep - 1) / L::kStep;
-    return share * L::kVec <= kKeep ? go<BF16, VEC, true>(a, cluster, s) : go<BF16, VEC, false>(a, cluster, s);
+    return share * L::kVec <= kKeep ? go<BF16, VEC, true>(a, cluster, per_row, s) : go<BF16, VEC, false>(a, cluster, per_row, s);
 }
 
 }  // namespace vt
+
+constexpr int kRowsAtOnce = 16;
+
+// Pieces of a row that are summed first, or 0 where the walk alone is quicker.
+static int pieces_of(int64_t n_rows, int64_t n_req, int64_t vocab) {
+    const int64_t per_row = (vocab + vt::kPiece - 1) / vt::kPiece;
+    if (n_rows <= n_req || n_rows > kRowsAtOnce * n_req || n_rows * per_row > (int64_t)1 << 30) return 0;
+    return (int)per_row;
+}
+
+int64_t verify_ws_bytes(int64_t n_rows, int64_t n_req, int64_t vocab) {
+    return n_rows * pieces_of(n_rows, n_req, vocab) * (int64_t)sizeof(vt::Piece);
+}
 
 cudaError_t launch_verify_tree(const VerifyArgs& a, int sms, cudaStream_t s) {
     // CTAs of a request: as many as leave each some thousand tokens and all of them a place at once.
@@ -633,8 +812,9 @@ cudaError_t launch_verify_tree(const VerifyArgs& a, int sms, cudaStream_t s) {
     const bool vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * es % 16 == 0;
     VerifyArgs b = a;
     b.probs_vec = reinterpret_cast<uintptr_t>(a.probs) % 16 == 0 && a.probs_stride % 4 == 0;
-    if (a.bf16) return vec ? vt::go<true, true>(b, cluster, s) : vt::go<true, false>(b, cluster, s);
-    return vec ? vt::go<false, true>(b, cluster, s) : vt::go<false, false>(b, cluster, s);
+    const int per_row = pieces_of(a.n_rows, a.n_req, a.vocab);
+    if (a.bf16) return vec ? vt::go<true, true>(b, cluster, per_row, s) : vt::go<true, false>(b, cluster, per_row, s);
+    return vec ? vt::go<false, true>(b, cluster, per_row, s) : vt::go<false, false>(b, cluster, per_row, s);
 }
 
 }  // namespace qk

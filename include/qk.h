@@ -631,13 +631,16 @@ qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64
  *          the token after the path; n_path int32 [n_req] of each (0 for a
  *          request without rows); entries behind them are -1.  A path ends at
  *          path_stride nodes (the last one's children are then not tried).
+ *   ws     at least qk_verify_workspace(..) bytes (0 for some sizes: ws may
+ *          then be NULL), 16-byte aligned.
  * Deterministic.  n_req == 0 queues nothing.  n_req is at most 2^27.
  * Errors: QK_ERR_SHAPE (also vocab or path_stride below 1), QK_ERR_NULL,
- * QK_ERR_ALIGN, QK_ERR_ARG. */
+ * QK_ERR_ALIGN, QK_ERR_ARG, QK_ERR_WORKSPACE. */
+size_t qk_verify_workspace(int64_t n_rows, int64_t n_req, int64_t vocab);
 qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t vocab, int64_t row_stride, const int32_t* cu,
                          int64_t n_req, const int32_t* draft, const uint64_t* mask, const float* temp, const float* u_accept,
                          const float* u_sample, const float* probs, int64_t probs_stride, int32_t* path, int64_t path_stride,
-                         int32_t* n_path, int32_t* tokens, void* stream);
+                         int32_t* n_path, int32_t* tokens, void* ws, size_t ws_bytes, void* stream);
 
 /* Test hook: unpack nblocks consecutive blocks into their integer fields.
  *   codes int16 [nblocks * block_elems]: Q4_K 0..15, Q5_K 0..31, Q6_K 0..63,

@@ -61,11 +61,13 @@ def test_nothing_to_do(lib):
     assert call(lib.qk_norm_rope, ROPE, n_tok=0, q=None, pos=None) == 0
     assert call(lib.qk_norm_rope, ROPE, n_heads=0, n_kv=0, q=None, k=None) == 0
     assert call(lib.qk_kv_append_rope, APPEND, n_tok=0, q=None, v=None) == 0
-    assert call(lib.qk_verify_tree, VERIFY, n_req=0, logits=None) == 0
+    assert call(lib.qk_verify_tree, VERIFY, n_req=0, logits=None, ws=None) == 0
+    assert [qk.verify_workspace(*a) for a in ((6, 2, 100), (6, 2, 1025), (2, 2, 100), (0, 1, 9), (-1, 1, 9), (6, 0, 9))] == \
+        [6 * 16, 6 * 2 * 16, 0, 0, 0, 0]
 
 
 VERIFY = dict(logits=F, dtype=0, n_rows=6, vocab=100, row_stride=100, cu=F, n_req=2, draft=F, mask=F, temp=F, u_accept=F, u_sample=F,
-              probs=F, probs_stride=100, path=F, path_stride=8, n_path=F, tokens=F, stream=None)
+              probs=F, probs_stride=100, path=F, path_stride=8, n_path=F, tokens=F, ws=F, ws_bytes=96, stream=None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -73,7 +75,8 @@ VERIFY = dict(logits=F, dtype=0, n_rows=6, vocab=100, row_stride=100, cu=F, n_re
     (dict(n_req=(1 << 27) + 1), SHAPE), (dict(path_stride=0), SHAPE), (dict(row_stride=99), SHAPE), (dict(probs_stride=99), SHAPE),
     (dict(logits=None), NULL), (dict(cu=None), NULL), (dict(draft=None), NULL), (dict(temp=None), NULL), (dict(u_accept=None), NULL),
     (dict(u_sample=None), NULL), (dict(path=None), NULL), (dict(n_path=None), NULL), (dict(tokens=None), NULL),
-    (dict(logits=F + 2), ALIGN), (dict(mask=F + 4), ALIGN), (dict(probs=F + 2), ALIGN), (dict(path=F + 2), ALIGN)])
+    (dict(logits=F + 2), ALIGN), (dict(mask=F + 4), ALIGN), (dict(probs=F + 2), ALIGN), (dict(path=F + 2), ALIGN), (dict(ws=None), NULL),
+    (dict(ws=F + 8), ALIGN), (dict(ws_bytes=95), 5)])
 def test_verify_tree_refusals(lib, kw, status):
     assert call(lib.qk_verify_tree, VERIFY, **kw) == status
     assert lib.qk_last_error()

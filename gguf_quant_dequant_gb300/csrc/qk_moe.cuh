@@ -235,13 +235,18 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
         *taken = p.nw;
         fence_barrier_init();
     }
-    pdl_launch_dependents();
+    if (DOWN) pdl_launch_dependents();
     {
         uint16_t* ids = reinterpret_cast<uint16_t*>(smem + p.off_ring);   // before the first fetch
         uint32_t* scratch = reinterpret_cast<uint32_t*>(smem + p.off_ring + 2 * ((p.pairs + 7) & ~7));
         if (p.n_tok > 1)
             for (int i = threadIdx.x; i <= 3 * p.n_exp; i += blockDim.x) scratch[i] = 0;
-        pdl_wait_prior();   // the ids; x or the sums of `up`
+        // `down` is let go by `up` only when that one has seen the kernel before it to its end, so the ids stand for
+        // both: `down` makes its groups and asks for its first weights while the last CTAs of `up` still work.
+        if (!DOWN) {
+            pdl_wait_prior();
+            pdl_launch_dependents();
+        }
         for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
             const int e = __ldcg(p.ids + i);
             ids[i] = e >= 0 && e < p.n_exp ? (uint16_t)e : kNone;
@@ -254,7 +259,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     const uint32_t total = (uint32_t)*tb.n * p.slices * p.jobs;
     const int each = (int)(total / gridDim.x), more = (int)(total % gridDim.x), bx = (int)blockIdx.x;
     const int j0 = bx * each + min(bx, more), j1 = j0 + each + (bx < more ? 1 : 0);
-    if (j0 >= j1) return;
+    if (j0 >= j1) {
+        if (DOWN) pdl_wait_prior();   // no grid ends before the one that it follows
+        return;
+    }
     const int e0 = j0 / p.jobs, e1 = (j1 - 1) / p.jobs;   // my (group, slice)s
 
     // The activations of (group, slice) e into its set: every step-th (unit, pair) from `first` on, two at a time.
@@ -347,6 +355,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     fetch(ahead, 0);
     // All warps prepare the first set, then two of them the others while the rest multiplies.  (A set's barriers count
     // its uses: set 0 is full at first without one.)
+    if (DOWN) pdl_wait_prior();   // the sums of `up`
     prepare(e0, warp, p.nw + kPrepWarps);
     __syncthreads();
     if (warp >= p.nw) {

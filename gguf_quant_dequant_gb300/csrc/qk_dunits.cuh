@@ -37,13 +37,14 @@ using namespace hm;
 // Prepared x of one unit: NT = 4 [block][row][plane][64 bytes], NT = 8
 // [block][plane][row][64 bytes] (conflict-free for the B loads); the words of a
 // plane in their order, or 0, 4, 1, 5, .. (kW4).  xm [block][row]: the block's
-// sum twice (kHalves: its halves' sums), 2^e twice.
+// sum twice (HALVES: its halves' sums, times -OFF 2^-24 where there is an offset),
+// 2^e twice.
 template <int NT>
 __device__ __forceinline__ uint32_t x_off(int blk, int row, int plane) {
     return NT == 4 ? (uint32_t)(blk * 512 + row * 128 + plane * 64) : (uint32_t)(blk * 1024 + plane * 512 + row * 64);
 }
 constexpr int kXRow = 8 * 128;   // bytes of a row of x in a unit
-template <int NT, bool W4, bool HALVES>
+template <int NT, bool W4, bool HALVES, int OFF>
 __device__ __forceinline__ void put_x(float4 a, float4 b, uint8_t* xb, float4* xm, int row, int lane) {
     const int blk = lane >> 2, q = lane & 3;
     uint32_t hi[4], lo[4];
@@ -60,7 +61,8 @@ __device__ __forceinline__ void put_x(float4 a, float4 b, uint8_t* xb, float4* x
         *reinterpret_cast<uint4*>(h + 16 * q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(l + 16 * q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    if (q == 0) xm[blk * NT + row] = HALVES ? make_float4(m.z, m.w, m.y, m.y) : make_float4(m.x, m.x, m.y, m.y);
+    constexpr float kOff = OFF ? -(float)OFF * 0x1p-24f : 1.0f;
+    if (q == 0) xm[blk * NT + row] = HALVES ? make_float4(kOff * m.z, kOff * m.w, m.y, m.y) : make_float4(m.x, m.x, m.y, m.y);
 }
 
 // Words of a row that starts on an even shared address: aligned words joined
@@ -99,7 +101,7 @@ struct Scale {
 };
 
 // A decoder: UB bytes per row and unit, kW4 (above), kG16 (scaled by
-// sixteens), kMin (has a min), block(pair c, b), Ctx, load(ctx, r0, r1, lane),
+// sixteens), kMin (has a min), kOff (codes less this; 0: the fragments have it off), block(pair c, b), Ctx, load(ctx, r0, r1, lane),
 // pair(ctx, c, lane, A, s): fragments A[b][step] and scales s[b] of the pair's
 // two blocks; pairs are taken in their order.
 template <int T> struct DU;
@@ -136,8 +138,16 @@ __device__ __forceinline__ void frag_raw(uint32_t (&A)[4], uint32_t w0, uint32_t
     A[3] = (w1 >> 8) & M;
 }
 
+// The same of code bytes with nothing beside them.
+__device__ __forceinline__ void frag_bytes(uint32_t (&A)[4], uint32_t w0, uint32_t w1) {
+    A[0] = __byte_perm(w0, 0u, 0x4240u);
+    A[1] = __byte_perm(w1, 0u, 0x4240u);
+    A[2] = __byte_perm(w0, 0u, 0x4341u);
+    A[3] = __byte_perm(w1, 0u, 0x4341u);
+}
+
 template <> struct DU<T_Q4_K> {
-    static constexpr int UB = 144;
+    static constexpr int UB = 144, kOff = 0;
     static constexpr bool kW4 = false, kG16 = false, kMin = true;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
@@ -161,7 +171,7 @@ template <> struct DU<T_Q4_K> {
 };
 
 template <> struct DU<T_Q5_K> {
-    static constexpr int UB = 176;
+    static constexpr int UB = 176, kOff = 0;
     static constexpr bool kW4 = false, kG16 = false, kMin = true;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
@@ -193,20 +203,21 @@ template <> struct DU<T_Q5_K> {
 };
 
 // Pair c: the 32-blocks (th, gl) and (th, gl + 2), th = c / 2, gl = c % 2, of
-// low and high nibbles of the same bytes.
+// low and high nibbles of the same bytes.  Codes 0 .. 63 as they are: their
+// offset, 32, goes into the sums of x.
 template <> struct DU<T_Q6_K> {
-    static constexpr int UB = 210;
+    static constexpr int UB = 210, kOff = 32;
     static constexpr bool kW4 = true, kG16 = true, kMin = false;
     __device__ static __forceinline__ int block(int c, int b) { return 4 * (c >> 1) + (c & 1) + 2 * b; }
     struct Ctx {
-        float f0[4], f1[4];   // d * scale of the thread's own pair: block, half
+        float f0[4], f1[4];   // d * scale * 2^24 of the thread's own pair: block, half
         Even r0, r1;
         uint32_t h0[2], h1[2];   // high bits of the current half
     };
     __device__ static __forceinline__ void own(const uint8_t* r, int t, float (&f)[4]) {
         const int at = 8 * (t >> 1) + 2 * (t & 1);
         const uint32_t u = (ld_u16(r + 192 + at) | (ld_u16(r + 196 + at) << 16)) ^ 0x80808080u;   // + 128
-        const float d = h2f(ld_u16(r + 208));
+        const float d = h2f(ld_u16(r + 208)) * 0x1p24f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) f[k] = d * (ubyte_f(u, k) - 128.0f);   // exact
     }
@@ -217,25 +228,20 @@ template <> struct DU<T_Q6_K> {
         x.r1.set(r1 + 4 * (lane & 3));
     }
     __device__ static __forceinline__ void pair(Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
-        const int src = (lane & 28) | c, th = c >> 1, gl = c & 1, sh = 4 - 2 * gl;
+        const int src = (lane & 28) | c, th = c >> 1, gl = c & 1, sh = 2 * gl;
         if (gl == 0) {
             x.h0[0] = x.r0.word(128 + 32 * th), x.h0[1] = x.r0.word(144 + 32 * th);
             x.h1[0] = x.r1.word(128 + 32 * th), x.h1[1] = x.r1.word(144 + 32 * th);
         }
-        const uint32_t CLO = dup16(0xE420u), CHI = dup16(0xD600u);   // -(1024 + 32), -(64 + 32)
-        auto cv = [](uint32_t lo, uint32_t m1, uint32_t hi, uint32_t m2, uint32_t mg) { return and_or(lo, m1, and_or(hi, m2, mg)); };
+        // four code bytes: a nibble each, and two bits at 4
+        auto code = [](uint32_t low, uint32_t high) { return and_or(low, 0x0F0F0F0Fu, high & 0x30303030u); };
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t q0 = x.r0.word(64 * th + 32 * gl + 16 * j), q1 = x.r1.word(64 * th + 32 * gl + 16 * j);
-            const uint32_t v0 = x.h0[j] << sh, v1 = x.h1[j] << sh, e0 = x.h0[j] >> (8 - sh), e1 = x.h1[j] >> (8 - sh);
-            A[0][j][0] = hadd2(cv(q0, 0x000F000Fu, v0, 0x00300030u, 0x64006400u), CLO);
-            A[0][j][1] = hadd2(cv(q1, 0x000F000Fu, v1, 0x00300030u, 0x64006400u), CLO);
-            A[0][j][2] = hadd2(cv(q0 >> 8, 0x000F000Fu, e0, 0x00300030u, 0x64006400u), CLO);
-            A[0][j][3] = hadd2(cv(q1 >> 8, 0x000F000Fu, e1, 0x00300030u, 0x64006400u), CLO);
-            A[1][j][0] = hadd2(cv(q0, 0x00F000F0u, v0, 0x03000300u, 0x54005400u), CHI);
-            A[1][j][1] = hadd2(cv(q1, 0x00F000F0u, v1, 0x03000300u, 0x54005400u), CHI);
-            A[1][j][2] = hadd2(cv(q0 >> 8, 0x00F000F0u, e0, 0x03000300u, 0x54005400u), CHI);
-            A[1][j][3] = hadd2(cv(q1 >> 8, 0x00F000F0u, e1, 0x03000300u, 0x54005400u), CHI);
+            const uint32_t k0 = code(q0, x.h0[j] << (4 - sh)), k1 = code(q1, x.h1[j] << (4 - sh));
+            const uint32_t n0 = code(q0 >> 4, x.h0[j] >> sh), n1 = code(q1 >> 4, x.h1[j] >> sh);
+            frag_bytes(A[0][j], k0, k1);
+            frag_bytes(A[1][j], n0, n1);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -274,7 +280,7 @@ struct Blocks32 {
 };
 
 template <> struct DU<T_Q8_0> : Blocks32<34> {
-    static constexpr int UB = 8 * 34;
+    static constexpr int UB = 8 * 34, kOff = 0;
     static constexpr bool kW4 = false, kG16 = false, kMin = false;
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const uint32_t C = dup16(0xE480u);   // -(1024 + 128)
@@ -297,7 +303,7 @@ template <> struct DU<T_Q8_0> : Blocks32<34> {
 
 // Word t holds the low nibbles of weights 4t .. and the high ones of 16 + 4t ..
 template <> struct DU<T_Q4_0> : Blocks32<18> {
-    static constexpr int UB = 8 * 18;
+    static constexpr int UB = 8 * 18, kOff = 0;
     static constexpr bool kW4 = true, kG16 = false, kMin = false;
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const uint32_t LO = dup16(0xE408u), HI = dup16(0xD480u);   // -(1024 + 8), -(64 + 8)
@@ -313,7 +319,7 @@ template <> struct DU<T_Q4_0> : Blocks32<18> {
 };
 
 template <> struct DU<T_Q5_0> : Blocks32<22> {
-    static constexpr int UB = 8 * 22;
+    static constexpr int UB = 8 * 22, kOff = 0;
     static constexpr bool kW4 = true, kG16 = false, kMin = false;
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const uint32_t C = dup16(0xE410u);   // -(1024 + 16)
@@ -335,7 +341,7 @@ template <> struct DU<T_Q5_0> : Blocks32<22> {
 // Pair c: blocks 2c, 2c + 1 = half c / 2 of the super-block, code bits 2 j0 ..
 // and 2 j0 + 2 .., j0 = 2 (c % 2); a block's halves are scaled on their own.
 template <> struct DU<T_Q2_K> {
-    static constexpr int UB = 84;
+    static constexpr int UB = 84, kOff = 0;
     static constexpr bool kW4 = true, kG16 = true, kMin = true;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
@@ -377,7 +383,7 @@ template <> struct DU<T_Q2_K> {
 };
 
 template <> struct DU<T_Q3_K> {
-    static constexpr int UB = 110;
+    static constexpr int UB = 110, kOff = 0;
     static constexpr bool kW4 = true, kG16 = true, kMin = false;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
@@ -457,7 +463,7 @@ __device__ __forceinline__ void run_unit(const uint8_t* a0, const uint8_t* a1, c
 #pragma unroll
                 for (int k = 0; k < NT / 4; ++k) {
                     const float4* p = xm + blk * NT + (NT == 4 ? t : 2 * t + k);
-                    if constexpr (D::kMin) {
+                    if constexpr (D::kMin || D::kOff) {
                         m[b][k] = *p;
                     } else {
                         const float2 up = reinterpret_cast<const float2*>(p)[1];
@@ -491,7 +497,10 @@ __device__ __forceinline__ void run_unit(const uint8_t* a0, const uint8_t* a1, c
                         };
                         const float4 x = m[b][k];
                         const float2 up = make_float2(x.z, x.w);
-                        if constexpr (D::kG16) y[k] = __ffma2_rn(up, __ffma2_rn(s[b].f[0], sum(0), __fmul2_rn(s[b].f[1], sum(1))), y[k]);
+                        if constexpr (D::kOff)
+                            y[k] = __ffma2_rn(s[b].f[0], __ffma2_rn(sum(0), up, make_float2(x.x, x.x)),
+                                              __ffma2_rn(s[b].f[1], __ffma2_rn(sum(1), up, make_float2(x.y, x.y)), y[k]));
+                        else if constexpr (D::kG16) y[k] = __ffma2_rn(up, __ffma2_rn(s[b].f[0], sum(0), __fmul2_rn(s[b].f[1], sum(1))), y[k]);
                         else y[k] = __ffma2_rn(s[b].f[0], __fmul2_rn(sum(0), up), y[k]);
                         if constexpr (D::kMin) {
                             if constexpr (D::kG16) {

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
                 if (i0 + m * step < nu * n)
-                    dm::put_x<NT, U::kW4, U::kMin && U::kG16>(a[m], b[m], xb + un[m] * (NT * dm::kXRow), xm + un[m] * 8 * NT, at[m], lane);
+                    dm::put_x<NT, U::kW4, U::kG16 && (U::kMin || U::kOff != 0), U::kOff>(a[m], b[m], xb + un[m] * (NT * dm::kXRow), xm + un[m] * 8 * NT, at[m], lane);
         }
     };
 

@@ -1,8 +1,8 @@
 """The expert layer against the oracle: the router's choice, and the products
 of the chosen experts within a bound that follows from each product's.
 
-A product of a row w = ds q - dm with x is within e = 2^-17 sum (|ds q| + |dm|)
-|x| + 1e-6: x as two fp16 terms is 2^-22 off, the fp32 sums have one rounding
+A product of a row w = ds q - dm (Q6_K: q in 0 .. 63, dm = 32 ds) with x is within
+e = 2^-17 sum (|ds q| + |dm|) |x| + 1e-6: x as two fp16 terms is 2^-22 off, the fp32 sums have one rounding
 (or, inside an MMA, truncation) per 16 weights, block and slice of at most 2^6
 blocks, up to 2^7 of 2^-24 together.  |SiLU'| <= 1.1, so h = SiLU(g) u is within
 eh = 1.1 eg (|u| + eu) + |SiLU(g)| eu + 2^-20 |h|, the down product of h within
@@ -38,6 +38,10 @@ def reference(W, E, rows, cols, up, down, x, ids, gate):
         """Expert e's weights, and |ds q| + |dm| of each."""
         t, b = type_id(name), w.reshape(E, -1)[e]
         v = np.asarray(oracle.dequant(t, b, r, c), np.float64)
+        if name == "Q6_K":
+            _, sc, _, d, _ = oracle.unpack(t, b, r * c // 256)
+            dm = 32 * np.repeat(np.asarray(sc, np.float64).reshape(-1, 16) * np.asarray(d, np.float64).reshape(-1, 1), 16, 1).reshape(r, c)
+            return v, np.abs(v + dm) + np.abs(dm)
         if name not in ("Q4_K", "Q5_K", "Q2_K"):
             return v, np.abs(v)
         _, _, mins, _, dmin = oracle.unpack(t, b, r * c // 256)

@@ -53,6 +53,8 @@ CASES = [  # n, heads, n_kv, d, rot, dtype, out, norm, pairs, gap, far
     (331, 5, 3, 128, 96, "f32", "f32", True, False, 0, 1000000),
     (3, 4, 2, 128, 0, "bf16", "f32", True, False, 0, 10),
     (2, 3, 3, 256, 256, "f32", "bf16", False, False, 1, 10),
+    (6001, 12, 4, 64, 32, "bf16", "f32", True, True, 0, 1 << 24),
+    (9973, 5, 2, 32, 32, "f32", "f32", True, False, 7, 1 << 20),
 ]
 
 
@@ -121,6 +123,8 @@ APPEND = [  # type, n, heads, n_kv, d, rot, dtype, norm, pairs, gap, page
     ("Q4_0", 400, 32, 8, 128, 128, "bf16", False, False, 128, 16),
     ("Q8_0", 65, 0, 1, 32, 32, "bf16", False, True, 0, 256),
     ("Q5_0", 90, 6, 2, 32, 0, "f32", True, False, 3, 128),
+    ("Q8_0", 5003, 8, 4, 128, 64, "f32", True, False, 4, 32),
+    ("Q4_0", 8009, 3, 3, 64, 64, "bf16", True, True, 0, 16),
 ]
 
 

@@ -225,3 +225,69 @@ def test_a_graph_and_two_streams(gpu):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(out[k], want[0][k]) for k in out)
+
+
+@pytest.mark.parametrize("drafter", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_children_near_their_threshold(gpu, drafter, dtype):
+    """u beside W / (q S) by a part of 2^-15, more than the walk's sums are off and less than the pieces' may be."""
+    n, r, V = 9, 8, 5000
+    s = make(19, [n] * r, V, drafter, chain=True, dtype=dtype)
+    x = s["logits"].float().numpy()
+    for i in range(r):
+        for j in range(1, n):
+            up = i * n + j - 1
+            e, y = step_ref.weights(x[up], float(s["temp"][i])), int(s["draft"][up + 1])
+            q = float(s["probs"][up, y]) if drafter else 1.0
+            s["u_accept"][up + 1] = e[y] / (q * e.sum()) * (1 + (2.0**-15 if j > i else -2.0**-15))
+    out = run(gpu, s)
+    check(s, out)
+    assert out["n_path"].tolist() == [i + 1 for i in range(r)]
+
+
+def test_nodes_behind_refusals(gpu):
+    """Walks that leave the line of first children: every first child is refused."""
+    s = make(20, [40, 3, 64, 1], 3000, False)
+    at, first = 0, []
+    for n in (40, 3, 64, 1):
+        par = step_ref.parents(n, [int(v) & (2**64 - 1) for v in s["mask"][at:at + n]])
+        first += [i > 0 and par.index(par[i]) == i for i in range(n)]
+        at += n
+    s["u_accept"] = torch.where(torch.tensor(first), torch.full_like(s["u_accept"], 1e9), 0.3 * s["u_accept"])
+    check(s, run(gpu, s))
+    # two children everywhere: the first is refused, the second has some weight and costs nothing
+    n = 41
+    s = make(23, [n, n], 3000, False, likely=False)
+    bits = [1]
+    for i in range(1, n):
+        bits.append(bits[(i - 1) // 2 * 2] | 1 << i)
+    s["mask"] = signed(bits * 2)
+    s["u_accept"] = torch.tensor([1e9 if i % 2 else 0.0 for i in range(n)] * 2)
+    out = run(gpu, s)
+    check(s, out)
+    assert out["n_path"].tolist() == [n // 2 + 1] * 2 and out["path"][0, :n // 2 + 1].tolist() == list(range(0, n, 2))
+
+
+def test_given_workspaces(gpu):
+    s, z = make(21, [8] * 5, 9000, True, chain=True), make(22, [8] * 5, 9000, True, chain=True)
+    want = run(gpu, s), run(gpu, z)
+    ws = torch.full((qk.verify_workspace(40, 5, 9000),), 255, dtype=torch.uint8, device=gpu)
+    assert ws.numel() == 40 * 9 * 16
+    graph, got = torch.cuda.CUDAGraph(), []
+    d = [{k: None if v is None else v.to(gpu) for k, v in c.items()} for c in (s, z)]
+    with torch.cuda.graph(graph):           # two calls that share it
+        for c in d:
+            got.append(qk.verify_tree(c["logits"], c["cu"], c["draft"], c["mask"], c["temp"], c["u_accept"], c["u_sample"],
+                                      probs=c["probs"], ws=ws))
+    for _ in range(3):
+        ws.random_(0, 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(a[k], b[k]) for k in a)
+    with pytest.raises(qk.QKError) as e:
+        run(gpu, s, ws=ws[:-16])
+    assert e.value.status == 5
+    with pytest.raises(qk.QKError) as e:
+        run(gpu, s, ws=ws[::2])
+    assert e.value.status == 8

@@ -587,6 +587,13 @@ def moe_workspace(t: int, t_down: int, n_exp: int, rows: int, cols: int, k: int,
     return load().qk_moe_workspace(t, t_down, n_exp, rows, cols, k, n_tok)
 
 
+@functools.lru_cache(maxsize=256)
+def _moe_bytes(t: int, t_down: int, n_exp: int, rows: int, cols: int) -> tuple:
+    """Bytes of Wg (or Wu) and of Wd; (0, 0) where there is no such layer."""
+    a, b = row_bytes(t, cols), row_bytes(t_down, rows)
+    return (n_exp * rows * a, n_exp * cols * b) if a and b and n_exp > 0 else (0, 0)
+
+
 def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x, k: int, router=None, norm: bool = True,
             scale: float = 1.0, ids=None, gate=None, out=None, ws=None, stream=None):
     """A mixture-of-experts layer (qk_moe_ffn): packed uint8 Wg, Wu [n_exp,
@@ -596,7 +603,7 @@ def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x
     import torch
     w, i32, f32 = "moe_ffn", torch.int32, torch.float32
     n = x.shape[0]
-    up, down = n_exp * rows * row_bytes(t, cols), n_exp * cols * row_bytes(t_down, rows)
+    up, down = _moe_bytes(t, t_down, n_exp, rows, cols)
     if not (up and down):
         raise QKError(2, w, f"no packed experts of n_exp={n_exp}, rows={rows}, cols={cols} in types {t}, {t_down}")
     if router is None and (ids is None or gate is None):
@@ -640,9 +647,9 @@ def verify_tree(logits, cu, draft, mask, temp, u_accept, u_sample, probs=None, m
     if probs is not None and (probs.dtype is not f32 or probs.shape != logits.shape):
         raise QKError(2, w, "probs must be float32 of the logits' shape")
     if out is None:
-        e = _empty(r * (2 * max_path + 1), i32, logits, stream)
-        a, b, c = e.split((r * max_path, r * max_path, r))
-        out = {"path": a.view(r, max_path), "tokens": b.view(r, max_path), "n_path": c}
+        shape = (r, max_path)   # three tensors: views of one cost the host more
+        out = {"path": _empty(shape, i32, logits, stream), "tokens": _empty(shape, i32, logits, stream),
+               "n_path": _empty(r, i32, logits, stream)}
     elif out["path"].dim() != 2:
         raise QKError(2, w, f"path of two dimensions expected, got shape {tuple(out['path'].shape)}")
     P = out["path"].shape[1]

@@ -3,7 +3,7 @@
 // converted once.
 //
 // Arithmetic: integer codes as exact fp16 A fragments, x as hi + lo fp16 terms
-// after a power of two per 32-block, fp32 sums scaled per block.  The types
+// after a power of two per 32-block, fp32 sums scaled per block.  Most types
 // without a min hold the code less its offset (placed in the mantissa of a
 // magic value and brought down by one exact add, as in qk_hunits.cuh).  The
 // types with a min hold the code itself, as the fp16 subnormal whose bits it is
@@ -11,7 +11,9 @@
 // power of two goes into the scale; w = ds q - dm is then summed as ds sum(q x)
 // - dm sum(x), so the error is a fraction of sum (|ds q| + |dm|) |x|.  (With the
 // nearest code to dm / ds taken off first, as the decode GEMV does, it would be
-// one of sum |w x|, for 45 % more instructions.)
+// one of sum |w x|, for an add per two weights and its bookkeeping.)  Q6_K is
+// summed that way too, dm = 32 ds: 8 % fewer instructions for its product, 4 %
+// less time for a layer with it.
 // In qk_hunits.cuh a warp's four column groups hold four parts of K for one row
 // of x; here all sixteen k of an MMA come from one 32-block and the eight
 // columns are rows of x: four rows by (hi, lo), or eight rows with hi and lo in

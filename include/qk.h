@@ -252,8 +252,9 @@ qk_status qk_gemv_swiglu(int type, const void* Wg, const void* Wu, int64_t rows,
  * Every expert that some token chose is read once per four or eight of its
  * tokens.  Three launches, four with a router.  Accuracy: each product is
  * within 2^-17 * sum_k (|scale code| + |min|) |x_k| + 1e-6 of its exact value
- * (for the types without a min that is sum |w x|; about 2^-22 in practice), the
- * SiLU and the sum over experts are fp32; the router's logits are fp32 sums.
+ * (for the types without a min that is sum |w x|, but Q6_K's codes count as 0 ..
+ * 63 with a min of 32 scales; in practice 2^-22 of the result without and 2^-20
+ * with a min), the SiLU and the sum over experts are fp32; the router's logits are fp32 sums.
  * A logit that is NaN ranks first and gives NaN gates for its token.
  * Deterministic.
  * n_tok == 0 queues nothing.  Errors: QK_ERR_TYPE, QK_ERR_SHAPE (also rows or
@@ -605,8 +606,9 @@ qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64
  * highest bit of its mask below its own (mask NULL: a chain).  Nodes without an
  * ancestor, and nodes past QK_TREE_MAX of a request, are never reached.
  * With e_v = exp((x_v - max x) / temp[r]) for the logits x of the node that the
- * path has reached (fp32; sums and comparisons in 64 bits), its children are
- * tried by rising index; child c with token y = draft[c] is taken when
+ * path has reached (fp32; sums are whole numbers of 2^-46 of the largest
+ * weight, for more than 65,536 tokens of 2^-45 and so on, and comparisons are in
+ * 64 bits), its children are tried by rising index; child c with token y = draft[c] is taken when
  *   u_accept[c] * q_y * sum_v W_v < W_y,
  * probs NULL (drafts picked without probabilities): q = 1, and W = e without
  *   the tokens of the children refused before;

@@ -21,8 +21,8 @@
 // what its lanes need of them in registers for all heads; a CTA per token with
 // the table in shared memory took 337 us for 32,764 tokens of 32 + 2 x 8 heads
 // (d 128, Q4_0 pages), this takes 209.  The instructions bound it (about 150 a
-// step with norm and rotation, 160 more where a step is quantized; the issue
-// slots are 79 % used): the bytes of that call would need 106 us.  Few tokens
+// step with norm and rotation, 150 more where a step is quantized; the issue
+// slots are 68 % used, DRAM 40 %): the bytes of that call would need 106 us.  Few tokens
 // are bound by latency: 3.5 us for one token of 32 + 8 heads.
 #include <algorithm>
 

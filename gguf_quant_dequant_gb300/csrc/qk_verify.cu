@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
         for (int64_t i = tid; i < a.path_stride; i += kThreads) path[i] = tokens[i] = -1;
     if (n == 0) {
         if (rank == 0 && tid == 0) a.n_path[r] = 0;
+        pdl_wait_prior();   // (no launch ends before the one that sums its pieces)
         return;   // the whole cluster
     }
     const float temp = a.temp[r], u_sample = a.u_sample[r];
@@ -339,13 +340,13 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
     int cur = 0, length = 1;
     if (rank == 0 && tid == 0) path[0] = 0;
     cl.sync();   // every CTA of the cluster runs (and has its tree) before another writes to its shared memory
+    pdl_wait_prior();   // the pieces
     uint64_t line = 0;   // the nodes whose rows were summed in pieces
     if (pieces && n > 1) {
         // A warp a node: its row's largest logit, and the child that is taken for sure once the node is reached, where the
         // pieces of the row decide by a margin (and no other child is tried before it).
         line = first_line(lane < n ? sh.parent[lane] : -1, lane + 32 < n ? sh.parent[lane + 32] : -1, n, lane);
         const int nodes = __popcll(line);
-        pdl_wait_prior();
         for (int k = warp; k < nodes; k += kWarps) {
             const int p = node_of(line, k);
             const Piece* of = pieces + (row0 + p) * per_row;

@@ -291,3 +291,16 @@ def test_given_workspaces(gpu):
     with pytest.raises(qk.QKError) as e:
         run(gpu, s, ws=ws[::2])
     assert e.value.status == 8
+
+
+def test_rows_of_no_request(gpu):
+    s = make(24, [1, 4, 1], 2500, False, chain=True)
+    s["cu"] = torch.tensor([2, 3, 3, 5], dtype=torch.int32)       # one row, none, two; the others are nobody's
+    s["temp"][2], s["mask"] = 0.7, None
+    out = run(gpu, s)
+    check(s, out)
+    assert out["n_path"][1] == 0
+    s["cu"] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    out = run(gpu, s)
+    check(s, out)
+    assert out["n_path"].tolist() == [1, 1, 1]

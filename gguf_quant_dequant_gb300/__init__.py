@@ -444,11 +444,12 @@ def kv_compact(t: int, K, V, page: int, n_kv: int, d: int, table, base, path, n_
 
 
 def _like_rows(out, n: int, h: int, d: int, dtype, like, stream, what: str):
+    """out, or a new tensor, and its elements from row to row."""
     if out is None:
-        return _empty((n, h, d), dtype, like, stream)
+        return _empty((n, h, d), dtype, like, stream), h * d
     if out.dtype is not dtype or out.shape != (n, h, d):
         raise QKError(2, what, f"{dtype} of shape {(n, h, d)} expected, got {out.dtype} of {tuple(out.shape)}")
-    return out
+    return out, _rows(out, what)
 
 
 def norm_rope(q, k, pos, freq, q_norm=None, k_norm=None, eps: float = 1e-6, pairs: bool = False, out_dtype=None, q_out=None,
@@ -468,17 +469,18 @@ def norm_rope(q, k, pos, freq, q_norm=None, k_norm=None, eps: float = 1e-6, pair
     if q is not None and k is not None and (k.dtype is not q.dtype or k.shape[0] != n or k.shape[2] != d):
         raise QKError(2, w, "q and k differ in type, tokens or width")
     out_dtype = out_dtype or x.dtype
+    qs = ks = 0
     if q is not None:
-        q_out = _like_rows(q_out, n, hq, d, out_dtype, x, stream, w)
+        q_out, qs = _like_rows(q_out, n, hq, d, out_dtype, x, stream, w)
     if k is not None:
-        k_out = _like_rows(k_out, n, hk, d, out_dtype, x, stream, w)
+        k_out, ks = _like_rows(k_out, n, hk, d, out_dtype, x, stream, w)
     y = q_out if q is not None else k_out
     rot = 0 if freq is None else 2 * freq.shape[0]
     _check(load().qk_norm_rope(
         _ptr(q), _ptr(k), _dtype(x, w), n, 0 if q is None else _rows(q, w), 0 if k is None else _rows(k, w), hq, hk, d,
         _of(pos, torch.int32, w, n) if rot else None, _of(q_norm, f32, w, d), _of(k_norm, f32, w, d), eps, _of(freq, f32, w, rot // 2),
         rot, pairs, None if q is None else q_out.data_ptr(), None if k is None else k_out.data_ptr(), _dtype(y, w),
-        0 if q is None else _rows(q_out, w), 0 if k is None else _rows(k_out, w), _stream_on(x, stream)), "qk_norm_rope")
+        qs, ks, _stream_on(x, stream)), "qk_norm_rope")
     return (q_out if q is not None else None), (k_out if k is not None else None)
 
 
@@ -492,19 +494,19 @@ def kv_append_rope(t: int, q, k, v, pos, freq, slots, K, V, page: int, q_norm=No
     n, n_kv, d = k.shape
     if v.shape != k.shape or v.dtype is not k.dtype:
         raise QKError(2, w, "k and v differ in shape or type")
-    h = 0
+    h = qs = 0
     if q is not None:
         h = q.shape[1]
         if q.dtype is not k.dtype or q.shape[0] != n or q.shape[2] != d:
             raise QKError(2, w, "q and k differ in type, tokens or width")
-        q_out = _like_rows(q_out, n, h, d, torch.bfloat16, k, stream, w)
+        q_out, qs = _like_rows(q_out, n, h, d, torch.bfloat16, k, stream, w)
     pages = _pool_pages(t, K, V, n_kv, d, page, w)
     rot = 0 if freq is None else 2 * freq.shape[0]
     _check(load().qk_kv_append_rope(
         t, _ptr(q), k.data_ptr(), v.data_ptr(), _dtype(k, w), n, _rows(q, w) if h else 0, _rows(k, w), _rows(v, w), h, n_kv, d,
         _of(pos, torch.int32, w, n) if rot else None, _of(q_norm, f32, w, d), _of(k_norm, f32, w, d), eps, _of(freq, f32, w, rot // 2),
         rot, pairs, _of(slots, torch.int64, w, n), K.data_ptr(), V.data_ptr(), pages, page, q_out.data_ptr() if h else None,
-        _rows(q_out, w) if h else 0, _stream_on(k, stream)), "qk_kv_append_rope")
+        qs if h else 0, _stream_on(k, stream)), "qk_kv_append_rope")
     return q_out if q is not None else None
 
 

@@ -368,12 +368,28 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
             float m = -INFINITY;
             int at = kNowhere;
             bool same = true;
-            for (int i = lane; i < per_row; i += 32) {
-                const Piece one = of[i];
-                same &= one.rate == rate_of;
-                if (one.top > m) {
-                    m = one.top;
-                    at = one.best;
+            // four loads of 16 bytes in flight a lane
+            Piece some[4];
+            auto four = [&](int base) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = base + 32 * j + lane;
+                    some[j] = Piece{-INFINITY, kNowhere, 0.0f, rate_of};
+                    if (i < per_row) {
+                        const float4 u = *reinterpret_cast<const float4*>(of + i);
+                        some[j] = Piece{u.x, __float_as_int(u.y), u.z, u.w};
+                    }
+                }
+            };
+            for (int base = 0; base < per_row; base += 128) {
+                four(base);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    same &= some[j].rate == rate_of;
+                    if (some[j].top > m) {
+                        m = some[j].top;
+                        at = some[j].best;
+                    }
                 }
             }
             warp_top(m, at);
@@ -390,7 +406,11 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                 }
             } else if (test && fabsf(m) < INFINITY) {
                 double S = 0.0;
-                for (int i = lane; i < per_row; i += 32) S += (double)of[i].sum * (double)weight(of[i].top, m, rate_of);
+                for (int base = 0; base < per_row; base += 128) {
+                    if (per_row > 128) four(base);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S += (double)some[j].sum * (double)weight(some[j].top, m, rate_of);
+                }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
                 sure = (double)u * (double)qy * S * kSure < (double)weight(x, m, rate_of);
@@ -527,11 +547,14 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                 break;
             }
         } else {
-            // The first child's row is the next one to be read, if any.
+            // What is likely to be read next: the first child's row, or, where the pieces have left the child open, the
+            // drafter's row for what its refusal leaves.
             if (kids[0] | kids[1]) {
-                const int64_t c = kids[0] ? __ffs(kids[0]) - 1 : 31 + __ffs(kids[1]);
-                const uint8_t* ahead = static_cast<const uint8_t*>(a.logits) + (row0 + c) * a.row_stride * (BF16 ? 2 : 4);
-                for (int64_t b = v0 * (BF16 ? 2 : 4) + lane * 128; b < v1 * (BF16 ? 2 : 4); b += 32 * 128)
+                const bool open = drafter && (line >> cur & 1);
+                const int64_t c = kids[0] ? __ffs(kids[0]) - 1 : 31 + __ffs(kids[1]), es = open ? 4 : BF16 ? 2 : 4;
+                const uint8_t* ahead = open ? reinterpret_cast<const uint8_t*>(q)
+                                            : static_cast<const uint8_t*>(a.logits) + (row0 + c) * a.row_stride * es;
+                for (int64_t b = v0 * es + lane * 128; b < v1 * es; b += 32 * 128)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + b));
             }
             // The row's sum; kept logits turn into weights.

@@ -172,6 +172,8 @@ struct Slot {
     static constexpr int kChunks = (kUB + kSkew + 15) / 16;
     static constexpr int kRow = 16 * (kChunks | 1);
     static constexpr int kTile = kTileRows * kRow;
+    // of a warp: two steps of two tiles, and the scales of a step's
+    static constexpr int kWarp = 4 * kTile + (dm::DU<T>::kSc ? 2 * 4 * dm::kScalePitch * 16 : 0);
 };
 
 __device__ __forceinline__ void cp_async16_stream(uint32_t dst, const void* src, uint64_t policy, bool on) {
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
     // ---------------- multiplies ----------------
     const int g8 = lane >> 2, t = lane & 3;
     const uint64_t pol = policy_evict_first();
-    uint8_t* slots = smem + p.off_ring + warp * (4 * S::kTile);   // two steps of two tiles
+    uint8_t* slots = smem + p.off_ring + warp * S::kWarp;
     const uint32_t slots_u32 = smem_u32(slots);
     Chunks<T> chunks;
     chunks.set(rb, lane);
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_kernel(const Args p) {
             const uint8_t* a1 = q + 8 * S::kRow + ((o0 + (g8 + 8) * rb) & 15u);
             const uint8_t* b0 = q + S::kTile + ((o1 + g8 * rb) & 15u);
             const uint8_t* b1 = q + S::kTile + 8 * S::kRow + ((o1 + (g8 + 8) * rb) & 15u);
-            dm::run_unit<T, NT>(a0, a1, b0, b1, xb + (u - u0) * (NT * dm::kXRow), xm + (u - u0) * 8 * NT, lane, min(8, p.nxb - 8 * u),
-                                ya, yb);
+            dm::run_unit<T, NT>(a0, a1, b0, b1, xb + (u - u0) * (NT * dm::kXRow), xm + (u - u0) * 8 * NT,
+                                reinterpret_cast<float4*>(slots + 4 * S::kTile), lane, min(8, p.nxb - 8 * u), ya, yb);
             __syncwarp();   // every lane is done with the slot
             slot ^= 1;
         }
@@ -460,8 +462,8 @@ inline double groups_of(int n, int k, int n_exp, int cap) {
 
 // The geometry of one product: the size of groups (4 or 8, returned) and the
 // slices of K that are expected to take the least time, in units' times: a job
-// costs its units (more with groups of eight) and an overhead.  unit_bytes of shared memory for two steps of a warp.
-inline int plan(Args& a, int type_block_bytes, int type_block_elems, int tile_bytes, bool down, int sms, uint32_t* smem) {
+// costs its units (more with groups of eight) and an overhead.  warp_bytes of shared memory for two steps of a warp.
+inline int plan(Args& a, int type_block_bytes, int type_block_elems, int warp_bytes, bool down, int sms, uint32_t* smem) {
     a.row_bytes = (uint32_t)(a.cols / type_block_elems * type_block_bytes);
     a.nxb = (int)(a.cols / 32);
     a.nunits = (int)((a.cols + kUnitW - 1) / kUnitW);
@@ -487,7 +489,7 @@ inline int plan(Args& a, int type_block_bytes, int type_block_elems, int tile_by
             b.off_x = take(2 * (int64_t)b.ku * cap * (dm::kXRow + 8 * 16));
             b.off_ring = (uint32_t)((take.at + 127) & ~(int64_t)127);
             // the last words of a row's reads may lie behind it
-            b.nw = (int)std::min<int64_t>((kSmemMax - b.off_ring - 16) / (4 * tile_bytes), kMaxWarps);
+            b.nw = (int)std::min<int64_t>((kSmemMax - b.off_ring - 16) / warp_bytes, kMaxWarps);
             if (b.nw < 4) continue;
             // jobs of a warp, and half a job that the last ones to finish take longer
             const double jobs = groups * b.slices * b.jobs / sms / b.nw, turns = jobs > 1.0 ? jobs + 0.5 : 1.0;
@@ -496,7 +498,7 @@ inline int plan(Args& a, int type_block_bytes, int type_block_elems, int tile_by
             if (time < best) {
                 best = time;
                 cap_best = cap;
-                const int64_t ring = std::max<int64_t>((int64_t)b.nw * 4 * tile_bytes, 2 * ((a.pairs + 7) & ~7) + 12 * a.n_exp + 16);
+                const int64_t ring = std::max<int64_t>((int64_t)b.nw * warp_bytes, 2 * ((a.pairs + 7) & ~7) + 12 * a.n_exp + 16);
                 *smem = (uint32_t)(b.off_ring + ring + 16);
                 chosen = b;
             }
@@ -526,7 +528,7 @@ cudaError_t launch_kernel(K kern, const Args& a, int grid, uint32_t smem, cudaSt
 template <int T, int BB, int BE, bool DOWN>
 cudaError_t go(Args& a, int sms, cudaStream_t s, bool launch) {
     uint32_t smem = 0;
-    const int cap = plan(a, BB, BE, Slot<T>::kTile, DOWN, sms, &smem);
+    const int cap = plan(a, BB, BE, Slot<T>::kWarp, DOWN, sms, &smem);
     if (cap == 0) return cudaErrorInvalidValue;
     if (!launch) return cudaSuccess;
     return cap == 4 ? launch_kernel(moe_kernel<T, 4, DOWN>, a, sms, smem, s) : launch_kernel(moe_kernel<T, 8, DOWN>, a, sms, smem, s);

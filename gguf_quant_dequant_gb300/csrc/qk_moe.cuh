@@ -18,19 +18,19 @@
 //     copies (20 to 50 ns each on an SM, whatever their size up to a kilobyte)
 //     and the sums of the stage's warps took longer than the products: 61
 //     tokens, 8 of 128 experts of 2048 x 768, Q4_K and Q6_K: 374 us a layer,
-//     now 172.
+//     now 168.
 //   * Two more warps prepare the activations of the next (group, slice) while
 //     the others work on one: x in `up`, SiLU(g) * u in `down` (the first is
 //     prepared by all).
 //   * Slices of K leave partial sums, added in order by whoever reads them: the
 //     preparation of `down`, and a last kernel that also weighs and adds the
 //     experts.  The result does not depend on timing.
-// Bound by the instructions that convert weights and hand round scales, at half
-// of the issue slots (128 registers a thread leave three or four warps to a
-// scheduler, and their chains of loads, conversions and MMAs are not hidden by
-// one another): 13 tokens, 2 of 8 experts of 4096 x 14336: up 123 us (Q4_K, 529
-// MB, 54 % of the DRAM rate), down 133 (Q6_K, 441 MB, 42 %).  One token: latency,
-// some 8 us a product.
+// What bounds it: 13 tokens, 2 of 8 experts of 4096 x 14336: up 122 us (Q4_K, 529
+// MB, 54 % of the DRAM rate), down 133 (Q6_K, 441 MB, 42 %), issue slots half used,
+// no pipe above two thirds; with the products left out the layer takes 206 us of
+// its 292, with nothing fetched 243, so each side takes the other's place,
+// likely in the load-store unit.  One token: some 8 us a product, of which the
+// weights' bytes are 2.
 #pragma once
 #include <algorithm>
 #include <cmath>

@@ -6,14 +6,20 @@
 // after a power of two per 32-block, fp32 sums scaled per block.  Most types
 // without a min hold the code less its offset (placed in the mantissa of a
 // magic value and brought down by one exact add, as in qk_hunits.cuh).  The
-// types with a min hold the code itself, as the fp16 subnormal whose bits it is
-// (q 2^-24, or 2^k that for a code k bits up): one mask and nothing else, the
-// power of two goes into the scale; w = ds q - dm is then summed as ds sum(q x)
-// - dm sum(x), so the error is a fraction of sum (|ds q| + |dm|) |x|.  (With the
-// nearest code to dm / ds taken off first, as the decode GEMV does, it would be
-// one of sum |w x|, for an add per two weights and its bookkeeping.)  Q6_K is
-// summed that way too, dm = 32 ds: 8 % fewer instructions for its product, 4 %
-// less time for a layer with it.
+// types with a min hold the code itself, as the fp16 subnormal whose bits it is:
+// a shift and a mask and nothing else, the power of two goes into the scale; w =
+// ds q - dm is then summed as ds sum(q x) - dm sum(x), so the error is a fraction
+// of sum (|ds q| + |dm|) |x|.  (With the nearest code to dm / ds taken off first,
+// as the decode GEMV does, it would be one of sum |w x|, for an add per two
+// weights and its bookkeeping.)  Q6_K is summed that way too, dm = 32 ds: 8 %
+// fewer instructions for its product, 4 % less time for a layer with it.
+// The codes lie at bits 4 .. 7 (Q4_K), 3 .. 7, 2 .. 7 or 4 and 6 up, as high as
+// costs little: an MMA adds products to a fixed number of places below the
+// largest exponent, and a subnormal counts with the exponent that it is written
+// with, so codes at the lowest bits lose what stands behind 2^-24 of 1 and not of
+// themselves.  With Q4_K at bits 0 .. 3 and Q2_K at 0, 1, 4 and 5 a layer was 1.5e-6
+// and 3e-6 of its norm off; now it is 2 to 4e-7, as with the other types, for 1 to
+// 2 % more time.
 // In qk_hunits.cuh a warp's four column groups hold four parts of K for one row
 // of x; here all sixteen k of an MMA come from one 32-block and the eight
 // columns are rows of x: four rows by (hi, lo), or eight rows with hi and lo in
@@ -41,7 +47,7 @@ using namespace hm;
 // Prepared x of one unit: NT = 4 [block][row][plane][64 bytes], NT = 8
 // [block][plane][row][64 bytes] (conflict-free for the B loads); the words of a
 // plane in their order, or 0, 4, 1, 5, .. (kW4).  xm [block][row]: the block's
-// sum twice (HALVES: its halves' sums, times -OFF 2^-24 where there is an offset),
+// sum twice (HALVES: its halves' sums, times -OFF 2^-22 where there is an offset),
 // 2^e twice.
 template <int NT>
 __device__ __forceinline__ uint32_t x_off(int blk, int row, int plane) {
@@ -65,7 +71,7 @@ __device__ __forceinline__ void put_x(float4 a, float4 b, uint8_t* xb, float4* x
         *reinterpret_cast<uint4*>(h + 16 * q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(l + 16 * q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    constexpr float kOff = OFF ? -(float)OFF * 0x1p-24f : 1.0f;
+    constexpr float kOff = OFF ? -(float)OFF * 0x1p-22f : 1.0f;
     if (q == 0) xm[blk * NT + row] = HALVES ? make_float4(kOff * m.z, kOff * m.w, m.y, m.y) : make_float4(m.x, m.x, m.y, m.y);
 }
 
@@ -111,12 +117,12 @@ struct Scale {
 // two blocks; pairs are taken in their order.
 template <int T> struct DU;
 
-// Q4_K and Q5_K: d * sc and dmin * m of the thread's own pair of blocks, by 2^24
-// and 2^20 (the codes' places).
+// Q4_K and Q5_K: d * sc and dmin * m of the thread's own pair of blocks, the
+// first by 2^BITS (the codes' place).
 struct RowMin {
     float2 ds, ndm;
 };
-template <bool HIGH>   // the second block's codes are four bits up
+template <int BITS>
 __device__ __forceinline__ RowMin row_min(const uint4& h, int t) {
     const uint32_t f = HU<T_Q4_K>::fields(h, t);
     const float d = h2f(h.x & 0xFFFFu), dmin = h2f(h.x >> 16);
@@ -125,8 +131,8 @@ __device__ __forceinline__ RowMin row_min(const uint4& h, int t) {
         return __fadd2_rn(make_float2(__uint_as_float(__byte_perm(f, 0x4B000000u, s0)), __uint_as_float(__byte_perm(f, 0x4B000000u, s1))),
                           make_float2(-kM, -kM));
     };
-    const float d24 = d * 0x1p24f;
-    return {__fmul2_rn(make_float2(d24, HIGH ? d * 0x1p20f : d24), two(0x7650, 0x7651)),
+    const float up = d * (float)(1 << BITS);
+    return {__fmul2_rn(make_float2(up, up), two(0x7650, 0x7651)),
             __fmul2_rn(make_float2(-dmin, -dmin), two(0x7652, 0x7653))};
 }
 // The scales of a tile's rows in shared memory, [pair][g][2]: ds of both blocks
@@ -144,15 +150,19 @@ __device__ __forceinline__ void scales_min(const float4* sc, int c, Scale (&s)[2
     s[0].n[0] = make_float2(v.x, v.y);
     s[1].n[0] = make_float2(v.z, v.w);
 }
-// Four A registers of raw codes under mask M of each half word.
-__device__ __forceinline__ void frag_raw(uint32_t (&A)[4], uint32_t w0, uint32_t w1, uint32_t M) {
-    A[0] = w0 & M;
-    A[1] = w1 & M;
-    A[2] = (w0 >> 8) & M;
-    A[3] = (w1 >> 8) & M;
+// Four A registers each of the low and the high nibbles, at bits 4 .. 7.
+__device__ __forceinline__ void nibbles(uint32_t (&lo)[4], uint32_t (&hi)[4], uint32_t w0, uint32_t w1) {
+    constexpr uint32_t M = 0x00F000F0u;
+    lo[0] = (w0 << 4) & M;
+    lo[1] = (w1 << 4) & M;
+    lo[2] = (w0 >> 4) & M;
+    lo[3] = (w1 >> 4) & M;
+    hi[0] = w0 & M;
+    hi[1] = w1 & M;
+    hi[2] = (w0 >> 8) & M;
+    hi[3] = (w1 >> 8) & M;
 }
-
-// The same of code bytes with nothing beside them.
+// Four A registers of code bytes.
 __device__ __forceinline__ void frag_bytes(uint32_t (&A)[4], uint32_t w0, uint32_t w1) {
     A[0] = __byte_perm(w0, 0u, 0x4240u);
     A[1] = __byte_perm(w1, 0u, 0x4240u);
@@ -169,17 +179,15 @@ template <> struct DU<T_Q4_K> {
         const uint8_t *r0, *r1;
     };
     __device__ static __forceinline__ void load(Ctx& x, const uint8_t* r0, const uint8_t* r1, int lane, float4* sc) {
-        put_scales(sc, lane, row_min<true>(lds128(r0), lane & 3), row_min<true>(lds128(r1), lane & 3));
+        put_scales(sc, lane, row_min<20>(lds128(r0), lane & 3), row_min<20>(lds128(r1), lane & 3));
         x.sc = sc + 2 * (lane >> 2);
         x.r0 = r0 + 16 + 8 * (lane & 3);
         x.r1 = r1 + 16 + 8 * (lane & 3);
     }
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const uint2 w0 = lds64(x.r0 + 32 * c), w1 = lds64(x.r1 + 32 * c);
-        frag_raw(A[0][0], w0.x, w1.x, 0x000F000Fu);
-        frag_raw(A[0][1], w0.y, w1.y, 0x000F000Fu);
-        frag_raw(A[1][0], w0.x, w1.x, 0x00F000F0u);
-        frag_raw(A[1][1], w0.y, w1.y, 0x00F000F0u);
+        nibbles(A[0][0], A[1][0], w0.x, w1.x);
+        nibbles(A[0][1], A[1][1], w0.y, w1.y);
         scales_min(x.sc, c, s);
     }
 };
@@ -194,23 +202,22 @@ template <> struct DU<T_Q5_K> {
         uint2 v0, v1;   // the fifth bits of the thread's words, four bits up, moved down two bits a pair
     };
     __device__ static __forceinline__ void load(Ctx& x, const uint8_t* r0, const uint8_t* r1, int lane, float4* sc) {
-        put_scales(sc, lane, row_min<false>(lds128(r0), lane & 3), row_min<false>(lds128(r1), lane & 3));
+        put_scales(sc, lane, row_min<21>(lds128(r0), lane & 3), row_min<21>(lds128(r1), lane & 3));
         x.sc = sc + 2 * (lane >> 2);
         x.v0 = lds64(r0 + 16 + 8 * (lane & 3));
         x.v1 = lds64(r1 + 16 + 8 * (lane & 3));
         x.r0 = r0 + 48 + 8 * (lane & 3);
         x.r1 = r1 + 48 + 8 * (lane & 3);
     }
-    // Code bytes of the low and high nibbles with their fifth bits (bits 0 and 1 of v's bytes).
-    __device__ static __forceinline__ uint32_t low(uint32_t w, uint32_t v) { return and_or(w, 0x0F0F0F0Fu, (v << 4) & 0x10101010u); }
-    __device__ static __forceinline__ uint32_t high(uint32_t w, uint32_t v) { return and_or(w >> 4, 0x0F0F0F0Fu, (v << 3) & 0x10101010u); }
+    // Code bytes, at bits 3 .. 7, of the low and high nibbles with their fifth bits (bits 0 and 1 of v's bytes).
+    __device__ static __forceinline__ uint32_t low(uint32_t w, uint32_t v) { return and_or(w << 3, 0x78787878u, (v << 7) & 0x80808080u); }
+    __device__ static __forceinline__ uint32_t high(uint32_t w, uint32_t v) { return and_or(w >> 1, 0x78787878u, (v << 6) & 0x80808080u); }
     __device__ static __forceinline__ void pair(Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const uint2 w0 = lds64(x.r0 + 32 * c), w1 = lds64(x.r1 + 32 * c);
-        constexpr uint32_t M = 0x001F001Fu;
-        frag_raw(A[0][0], low(w0.x, x.v0.x), low(w1.x, x.v1.x), M);
-        frag_raw(A[0][1], low(w0.y, x.v0.y), low(w1.y, x.v1.y), M);
-        frag_raw(A[1][0], high(w0.x, x.v0.x), high(w1.x, x.v1.x), M);
-        frag_raw(A[1][1], high(w0.y, x.v0.y), high(w1.y, x.v1.y), M);
+        frag_bytes(A[0][0], low(w0.x, x.v0.x), low(w1.x, x.v1.x));
+        frag_bytes(A[0][1], low(w0.y, x.v0.y), low(w1.y, x.v1.y));
+        frag_bytes(A[1][0], high(w0.x, x.v0.x), high(w1.x, x.v1.x));
+        frag_bytes(A[1][1], high(w0.y, x.v0.y), high(w1.y, x.v1.y));
         x.v0.x >>= 2, x.v0.y >>= 2, x.v1.x >>= 2, x.v1.y >>= 2;
         scales_min(x.sc, c, s);
     }
@@ -224,14 +231,14 @@ template <> struct DU<T_Q6_K> {
     static constexpr bool kW4 = true, kG16 = true, kMin = false, kSc = false;
     __device__ static __forceinline__ int block(int c, int b) { return 4 * (c >> 1) + (c & 1) + 2 * b; }
     struct Ctx {
-        float f0[4], f1[4];   // d * scale * 2^24 of the thread's own pair: block, half
+        float f0[4], f1[4];   // d * scale * 2^22 of the thread's own pair: block, half
         Even r0, r1;
         uint32_t h0[2], h1[2];   // high bits of the current half
     };
     __device__ static __forceinline__ void own(const uint8_t* r, int t, float (&f)[4]) {
         const int at = 8 * (t >> 1) + 2 * (t & 1);
         const uint32_t u = (ld_u16(r + 192 + at) | (ld_u16(r + 196 + at) << 16)) ^ 0x80808080u;   // + 128
-        const float d = h2f(ld_u16(r + 208)) * 0x1p24f;
+        const float d = h2f(ld_u16(r + 208)) * 0x1p22f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) f[k] = d * (ubyte_f(u, k) - 128.0f);   // exact
     }
@@ -247,13 +254,13 @@ template <> struct DU<T_Q6_K> {
             x.h0[0] = x.r0.word(128 + 32 * th), x.h0[1] = x.r0.word(144 + 32 * th);
             x.h1[0] = x.r1.word(128 + 32 * th), x.h1[1] = x.r1.word(144 + 32 * th);
         }
-        // four code bytes: a nibble each, and two bits at 4
-        auto code = [](uint32_t low, uint32_t high) { return and_or(low, 0x0F0F0F0Fu, high & 0x30303030u); };
+        // four code bytes, at bits 2 .. 7: a nibble each, and two bits
+        auto code = [](uint32_t low, uint32_t high) { return and_or(low, 0x3C3C3C3Cu, high & 0xC0C0C0C0u); };
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t q0 = x.r0.word(64 * th + 32 * gl + 16 * j), q1 = x.r1.word(64 * th + 32 * gl + 16 * j);
-            const uint32_t k0 = code(q0, x.h0[j] << (4 - sh)), k1 = code(q1, x.h1[j] << (4 - sh));
-            const uint32_t n0 = code(q0 >> 4, x.h0[j] >> sh), n1 = code(q1 >> 4, x.h1[j] >> sh);
+            const uint32_t k0 = code(q0 << 2, x.h0[j] << (6 - sh)), k1 = code(q1 << 2, x.h1[j] << (6 - sh));
+            const uint32_t n0 = code(q0 >> 2, x.h0[j] << (2 - sh)), n1 = code(q1 >> 2, x.h1[j] << (2 - sh));
             frag_bytes(A[0][j], k0, k1);
             frag_bytes(A[1][j], n0, n1);
         }
@@ -359,13 +366,13 @@ template <> struct DU<T_Q2_K> {
     static constexpr bool kW4 = true, kG16 = true, kMin = true, kSc = false;
     __device__ static __forceinline__ int block(int c, int b) { return 2 * c + b; }
     struct Ctx {
-        float f0[4], f1[4], n0[4], n1[4];   // of the thread's own pair: block, half; scales by 2^24 less the codes' place
+        float f0[4], f1[4], n0[4], n1[4];   // of the thread's own pair: block, half; scales by 2^20 and 2^18 (the codes' places)
         const uint8_t *r0, *r1;
     };
     __device__ static __forceinline__ void own(const uint8_t* r, int t, float (&f)[4], float (&n)[4]) {
         const uint32_t sm = lds32(r + 4 * t), dd = lds32(r + 80);   // (scale, min) bytes; d, dmin
         const uint32_t sc = sm & 0x0F0F0F0Fu, mn = (sm >> 4) & 0x0F0F0F0Fu;
-        const float d = h2f(dd & 0xFFFFu) * (t & 1 ? 0x1p20f : 0x1p24f), dmin = h2f(dd >> 16);
+        const float d = h2f(dd & 0xFFFFu) * 0x1p20f, dmin = h2f(dd >> 16);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             f[k] = (k < 2 ? d : d * 0.25f) * ubyte_f(sc, k);
@@ -381,14 +388,18 @@ template <> struct DU<T_Q2_K> {
     }
     __device__ static __forceinline__ void pair(const Ctx& x, int c, int lane, uint32_t (&A)[2][2][4], Scale (&s)[2]) {
         const int src = (lane & 28) | c;
-        const uint32_t M0 = c & 1 ? 0x00300030u : 0x00030003u;
+        const int sh = c & 1 ? 0 : 4;   // to bits 4 .. 7
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t w0 = lds32(x.r0 + 32 * (c >> 1) + 16 * j), w1 = lds32(x.r1 + 32 * (c >> 1) + 16 * j);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int k = 2 * b + j;
-                frag_raw(A[b][j], w0, w1, b ? M0 << 2 : M0);
+                const uint32_t M = b ? 0x00C000C0u : 0x00300030u;
+                A[b][j][0] = (w0 << sh) & M;
+                A[b][j][1] = (w1 << sh) & M;
+                A[b][j][2] = (w0 >> (8 - sh)) & M;
+                A[b][j][3] = (w1 >> (8 - sh)) & M;
                 s[b].f[j] = make_float2(from(x.f0[k], src), from(x.f1[k], src));
                 s[b].n[j] = make_float2(from(x.n0[k], src), from(x.n1[k], src));
             }

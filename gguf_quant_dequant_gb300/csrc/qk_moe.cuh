@@ -18,7 +18,7 @@
 //     copies (20 to 50 ns each on an SM, whatever their size up to a kilobyte)
 //     and the sums of the stage's warps took longer than the products: 61
 //     tokens, 8 of 128 experts of 2048 x 768, Q4_K and Q6_K: 374 us a layer,
-//     now 168.
+//     now 169.
 //   * Two more warps prepare the activations of the next (group, slice) while
 //     the others work on one: x in `up`, SiLU(g) * u in `down` (the first is
 //     prepared by all).

@@ -70,35 +70,58 @@ __device__ __forceinline__ float2 weight2(float2 x, float top, float rate) {
 }
 __device__ __forceinline__ float rest(float e, float tau, float q) { return fmaxf(__fsub_rn(e, __fmul_rn(tau, q)), 0.0f); }
 
-// Sums are whole numbers of 2^-bits (bits = 46 for up to 65,536 tokens, one less for each doubling), so that they are
-// the same in whatever order they are formed: on this GPU a 64-bit floating addition costs a warp sixteen cycles of
-// the whole SM, and two reductions with them took 2.9 us a row.
+// Sums are of weights as whole numbers of 2^-bits, each rounded by itself (bits = 46 for up to 65,536 tokens, one less for
+// each doubling), so that they are the same in whatever order and by whatever threads they are formed: a row's sum, its
+// parts' sums and the running sum that finds a token agree to the last bit.  On this GPU a 64-bit floating addition costs a
+// warp sixteen cycles of the whole SM, and two reductions with them took 2.9 us a row.
 struct Fix {
     float up;      // 2^bits
     double down;   // 2^-bits
+    float magic;   // 1.5 2^(23 - bits): added to a number below 2^-24, its last place is 2^-bits
+    int high;      // bits - 23
+    static __device__ __forceinline__ Fix unit(int bits) {
+        return {__uint_as_float((uint32_t)(127 + bits) << 23), __longlong_as_double((int64_t)(1023 - bits) << 52),
+                __uint_as_float(((uint32_t)(150 - bits) << 23) | 0x400000u), bits - 23};
+    }
     __device__ __forceinline__ int64_t of(float v) const { return __float2ll_rn(v * up); }
 };
-// Two sums of weights in 0 .. 1 to about 2^-46: the running sums, from 1 on (so
-// that they are the larger ones), and the rounding they lose.
+// Running sum of `of` of weights in 0 .. 1 without a conversion each: v + 1 rounds v to 23 bits, which stand in the sum's
+// mantissa as a whole number; what that leaves out, added to `magic`, does the same for the bits below.  (A tie is one of the
+// low part alone, and both parts' offsets are even, so it falls as in `of`.)  Both mantissas are added as 32-bit words,
+// offsets and all, which holds for 511 weights; two integer additions more for two weights than compensated fp32 sums.
 struct Sum {
-    float2 h = {1.0f, 1.0f}, l = {0.0f, 0.0f};
-    __device__ __forceinline__ void add(float2 v) {
-        const float2 s = __fadd2_rn(h, v), d = __fadd2_rn(s, make_float2(-h.x, -h.y));
-        l = __fadd2_rn(l, __fadd2_rn(v, make_float2(-d.x, -d.y)));
-        h = s;
+    uint32_t h = 0, l = 0;
+    int n = 0;   // weights in them
+    int64_t all = 0;
+    __device__ __forceinline__ void add(float2 v, const Fix& f) {
+        const float2 t = __fadd2_rn(v, make_float2(1.0f, 1.0f)), d = __fadd2_rn(t, make_float2(-1.0f, -1.0f));
+        const float2 r = __fadd2_rn(__fadd2_rn(v, make_float2(-d.x, -d.y)), make_float2(f.magic, f.magic));
+        h += __float_as_uint(t.x) + __float_as_uint(t.y);
+        l += __float_as_uint(r.x) + __float_as_uint(r.y);
     }
     // kVec weights (one alone beside a zero).
     template <int N>
-    __device__ __forceinline__ void add(const float (&v)[N]) {
+    __device__ __forceinline__ void add(const float (&v)[N], const Fix& f) {
         if constexpr (N == 1) {
-            add(make_float2(v[0], 0.0f));
+            add(make_float2(v[0], 0.0f), f);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 2) add(make_float2(v[i], v[i + 1]));
+            for (int i = 0; i < N; i += 2) add(make_float2(v[i], v[i + 1]), f);
         }
+        n += N == 1 ? 2 : N;
     }
-    __device__ __forceinline__ int64_t value(const Fix& f) const {
-        return f.of(__fsub_rn(h.x, 1.0f)) + f.of(__fsub_rn(h.y, 1.0f)) + f.of(l.x) + f.of(l.y);
+    __device__ __forceinline__ void flush(const Fix& f) {
+        all += ((int64_t)(h - (uint32_t)n * 0x3f800000u) << f.high) + (int32_t)(l - (uint32_t)n * __float_as_uint(f.magic));
+        h = l = 0;
+        n = 0;
+    }
+    // Before up to 64 weights more.
+    __device__ __forceinline__ void room(const Fix& f) {
+        if (n > 511 - 64) flush(f);
+    }
+    __device__ __forceinline__ int64_t value(const Fix& f) {
+        flush(f);
+        return all;
     }
 };
 // Logits to weights.
@@ -195,9 +218,11 @@ constexpr int kPiece = 1024;
 // How far the pieces' sum can be off the row's, and more.  Weights count down to
 // exponents of -32 (2^31 of them come to less than 2^-15 of the largest's 1); up
 // to there the fast exponential (2 + 1.2 |t| steps of 2^-23) and two roundings of
-// the exponent (|t| 2^-23) leave less than a part 2^-16.  A child is sure to be
-// taken when it is by this margin.
+// the exponent (|t| 2^-23) leave less than a part 2^-16.  The row's own sum has
+// every weight rounded to a whole number of its unit, at most 2^-15 of it in all
+// up to kPieceVocab tokens.  A child is sure to be taken when it is by this margin.
 constexpr double kSure = 1.0 + 0x1p-13;
+constexpr int64_t kPieceVocab = 1 << 24;
 
 // The parent of a request's node i (row `row` of the mask), or -1.
 __device__ __forceinline__ int parent_of(const uint64_t* mask, int64_t row, int i) {
@@ -322,8 +347,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
     // My part of the vocabulary: v0 .. v1 - 1, a multiple of a step long (but the last).
     const int64_t share = ((a.vocab + parts - 1) / parts + kStep - 1) / kStep * kStep;
     const int64_t v0 = min(me * share, a.vocab), v1 = min(v0 + share, a.vocab);
-    const int bits = min(46, 62 - (32 - __clz((int)a.vocab)));
-    const Fix fix{__uint_as_float((uint32_t)(127 + bits) << 23), __longlong_as_double((int64_t)(1023 - bits) << 52)};
+    const Fix fix = Fix::unit(min(46, 62 - (32 - __clz((int)a.vocab - 1))));
     // An exchange writes one buffer and ends with the cluster's barrier; the buffer is written again two exchanges of its
     // kind later, after another barrier that every warp reaches only when it has read it.
     int top_turn = 0, sum_turn = 0;
@@ -565,10 +589,11 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                     for (int k = 0; k < kRegs; ++k)
                         if (v0 + k * kStep < v1 && some) {
                             weigh(x[k], top, rate);
-                            s.add(x[k]);
+                            s.add(x[k], fix);
                         }
                 } else if (some) {
                     for (int64_t v = v0 + lane * kVec; v < v1; v += kAhead * kStep) {
+                        s.room(fix);
                         float w[kAhead][kVec];
 #pragma unroll
                         for (int k = 0; k < kAhead; ++k) {
@@ -582,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
 #pragma unroll
                         for (int k = 0; k < kAhead; ++k) {
                             weigh(w[k], top, rate);
-                            s.add(w[k]);
+                            s.add(w[k], fix);
                         }
                     }
                 }
@@ -651,12 +676,13 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                             load_q(v, q1);
 #pragma unroll
                             for (int i = 0; i < kVec; ++i) q1[i] = rest(x[k][i], off, q1[i]);
-                            s.add(q1);
+                            s.add(q1, fix);
                         }
                     }
                 } else if (some) {
                     constexpr int kTwo = kVec == 8 ? 1 : kVec == 4 ? 2 : 4;
                     for (int64_t v = v0 + lane * kVec; v < v1; v += kTwo * kStep) {
+                        s.room(fix);
                         float w2[kTwo][kVec], q2[kTwo][kVec];
 #pragma unroll
                         for (int k = 0; k < kTwo; ++k)
@@ -670,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                                 weigh(w2[k], top, rate);
 #pragma unroll
                                 for (int i = 0; i < kVec; ++i) w2[k][i] = rest(w2[k][i], off, q2[k][i]);
-                                s.add(w2[k]);
+                                s.add(w2[k], fix);
                             }
                     }
                 }
@@ -855,10 +881,11 @@ static cudaError_t go(const VerifyArgs& a, int cluster, int per_row, int sms, cu
 }  // namespace vt
 
 // Pieces of a row that are summed first, or 0: where no request can have a
-// child, and where they would take more than 256 MiB.
+// child, where a row has too many tokens for their margin, and where they would
+// take more than 256 MiB.
 static int pieces_of(int64_t n_rows, int64_t n_req, int64_t vocab) {
     const int64_t per_row = (vocab + vt::kPiece - 1) / vt::kPiece;
-    return n_rows <= n_req || n_rows * per_row > 1 << 24 ? 0 : (int)per_row;
+    return n_rows <= n_req || vocab > vt::kPieceVocab || n_rows * per_row > 1 << 24 ? 0 : (int)per_row;
 }
 
 int64_t verify_ws_bytes(int64_t n_rows, int64_t n_req, int64_t vocab) {

@@ -607,9 +607,10 @@ qk_status qk_logits_process(const void* logits, int dtype, int64_t n_rows, int64
  * highest bit of its mask below its own (mask NULL: a chain).  Nodes without an
  * ancestor, and nodes past QK_TREE_MAX of a request, are never reached.
  * With e_v = exp((x_v - max x) / temp[r]) for the logits x of the node that the
- * path has reached (fp32; sums are whole numbers of 2^-46 of the largest
- * weight, for more than 65,536 tokens of 2^-45 and so on, and comparisons are in
- * 64 bits), its children are tried by rising index; child c with token y = draft[c] is taken when
+ * path has reached (fp32; in sums each weight counts as a whole number of 2^-46
+ * of the largest, for more than 65,536 tokens of 2^-45 and so on, so that they
+ * depend on the row alone; comparisons are in 64 bits), its children are tried by
+ * rising index; child c with token y = draft[c] is taken when
  *   u_accept[c] * q_y * sum_v W_v < W_y,
  * probs NULL (drafts picked without probabilities): q = 1, and W = e without
  *   the tokens of the children refused before;

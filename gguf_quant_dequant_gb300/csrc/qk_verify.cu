@@ -622,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
             uint64_t refused = 0;
             double tau = 0.0;
             for (;;) {
+                const bool first = tau == 0.0;   // (before the first warp adds to it)
                 if (warp == 0) {
                     int64_t total = total_of();
                     int got = -1;
@@ -660,7 +661,6 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
                 }
                 __syncthreads();
                 next = sh.next;
-                const bool first = tau == 0.0;
                 tau = sh.tau;
                 if (!sh.again) break;
                 if (first)   // the sums of e, for a row in which nothing will be left

@@ -168,7 +168,7 @@ __device__ __forceinline__ void warp_top(float& m, int& at) {
 constexpr int kNowhere = 0x7fffffff;
 struct Shared {
     int64_t sums[2][kMaxCluster * kWarps];  // W's sum of every warp of the cluster; by turns
-    int64_t plain[kMaxCluster * kWarps];    // e's, of the last node
+    int64_t plain[kMaxCluster * kWarps];    // e's, of the last node, where a child was refused
     float top[2][kMaxCluster * kWarps];     // every warp's largest logit and its place; by turns
     int best[2][kMaxCluster * kWarps];
     int64_t piece[kWarps];                  // the sampled part's pieces
@@ -717,13 +717,16 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) verify_kernel(const Ve
         const uint64_t refused = sh.refused;
         const double tau = sh.tau;
         if (warp == 0) {
+            if (refused)
+                for (int i = lane; i < parts; i += 32) sh.plain[i] = sh.sums[sum_turn][i];
+            __syncwarp();
             if (lane == 0)
                 for (uint64_t left = refused; left; left &= left - 1) {   // tokens taken out of their parts' sums
                     const int y = sh.token[__ffsll((long long)left) - 1];
                     sh.sums[sum_turn][y / share] = max(sh.sums[sum_turn][y / share] - fix.of(weight(logit<BF16>(row, y), top, rate)), (int64_t)0);
                 }
             __syncwarp();
-            const bool usual = tau == 0.0 || total_of() > 0;   // else nothing is left (by rounding): the row's own weights
+            const bool usual = (tau == 0.0 && !refused) || total_of() > 0;   // else nothing is left: the row's own weights
             const int64_t* part = usual ? sh.sums[sum_turn] : sh.plain;
             const int each = (parts + 31) / 32;
             int64_t mine = 0;

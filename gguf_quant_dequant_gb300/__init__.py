@@ -584,9 +584,12 @@ def logits_process(logits, cu, hist, hist_len, rep, pres, freq, draft=None, mask
     return out
 
 
-@functools.lru_cache(maxsize=256)
 def moe_workspace(t: int, t_down: int, n_exp: int, rows: int, cols: int, k: int, n_tok: int) -> int:
+    """Bytes for the current device (they follow from its number of SMs)."""
     return load().qk_moe_workspace(t, t_down, n_exp, rows, cols, k, n_tok)
+
+
+_moe_need: dict = {}   # workspaces by device and sizes, of calls that went through
 
 
 @functools.lru_cache(maxsize=256)
@@ -616,8 +619,11 @@ def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x
         gate = _empty((n, k), f32, x, stream)
     if out is None:
         out = _empty((n, cols), f32, x, stream)
+    sizes = need = None
     if ws is None:
-        ws = _empty(max(moe_workspace(t, t_down, n_exp, rows, cols, k, n), 16), torch.uint8, x, stream, kept=False)
+        sizes = (x.device.index, t, t_down, n_exp, rows, cols, k, n)
+        need = _moe_need.get(sizes) or moe_workspace(*sizes[1:])
+        ws = _empty(max(need, 16), torch.uint8, x, stream, kept=False)
     elif not (ws.is_cuda and ws.is_contiguous()):
         _on_gpu(ws, w)
         raise QKError(8, w, f"contiguous ws expected, got strides {ws.stride()}")
@@ -626,6 +632,10 @@ def moe_ffn(t: int, Wg, Wu, t_down: int, Wd, n_exp: int, rows: int, cols: int, x
                              _of(router, f32, w, n_exp * cols), k, norm, scale, _of(x, f32, w, n * cols), n, _of(ids, i32, w, n * k),
                              _of(gate, f32, w, n * k), _of(out, f32, w, n * cols), ws.data_ptr(), ws.numel() * ws.element_size(),
                              _stream_on(x, stream)), "qk_moe_ffn")
+    if sizes is not None and sizes not in _moe_need:
+        if len(_moe_need) >= 256:
+            _moe_need.clear()
+        _moe_need[sizes] = need
     return out, ids, gate
 
 

@@ -85,6 +85,7 @@ SIGNATURES = {
     "qk_moe_workspace": (_sz, [_int, _int, _int, _i64, _i64, _int, _i64]),
     "qk_moe_ffn": (_int, [_int, _p, _p, _int, _p, _int, _i64, _i64, _p, _int, _int, ctypes.c_float, _p, _i64, _p, _p, _p, _p,
                           _sz, _p]),
+    "qk_test_moe_group": (_int, [_int, _int, _int, _i64, _i64, _int, _i64, _int, _int]),
     "qk_unpack": (_int, [_int, _p, _i64, _p, _p, _p, _p, _p, _p]),
     "qk_device_status": (_int, [_p]),
     "qk_test_stalled_wait": (_int, [ctypes.c_uint32, _p]),

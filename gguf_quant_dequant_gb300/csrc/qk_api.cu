@@ -769,6 +769,12 @@ size_t qk_moe_workspace(int type, int type_down, int n_exp, int64_t rows, int64_
     return (size_t)qk::moe_ws_bytes(moe_args(type, type_down, n_exp, rows, cols, k, n_tok), sm_count_or_default());
 }
 
+int qk_test_moe_group(int type, int type_down, int n_exp, int64_t rows, int64_t cols, int k, int64_t n_tok, int down, int sms) {
+    if (!known_type(type) || !known_type(type_down) || !moe_shape_ok(type, type_down, n_tok, k, n_exp, rows, cols) || n_tok == 0)
+        return 0;
+    return qk::moe_group(moe_args(type, type_down, n_exp, rows, cols, k, n_tok), down != 0, sms > 0 ? sms : sm_count_or_default());
+}
+
 qk_status qk_moe_ffn(int type, const void* Wg, const void* Wu, int type_down, const void* Wd, int n_exp, int64_t rows,
                      int64_t cols, const float* router, int k, int norm, float scale, const float* x, int64_t n_tok,
                      int32_t* ids, float* gate, float* out, void* ws, size_t ws_bytes, void* stream) {

@@ -169,6 +169,7 @@ struct MoeArgs {
     void* ws;
 };
 int64_t moe_ws_bytes(const MoeArgs& m, int sms);   // types, sizes and n_tok only
+int moe_group(const MoeArgs& m, bool down_product, int sms);   // most pairs of a group; the same members
 cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStream_t s);
 
 // One thread waiting on an mbarrier nothing arrives on (bounded by limit_ns).

@@ -229,6 +229,12 @@ int64_t moe_ws_bytes(const MoeArgs& m, int sms) {
     return set_up(m, sms, up, down, bytes) == cudaSuccess ? bytes[0] + bytes[1] : 0;
 }
 
+int moe_group(const MoeArgs& m, bool down_product, int sms) {
+    moe::Args up, down;
+    int64_t bytes[2];
+    return set_up(m, sms, up, down, bytes) == cudaSuccess ? (down_product ? down.cap : up.cap) : 0;
+}
+
 cudaError_t launch_moe_ffn(const MoeArgs& m, unsigned* status, int sms, cudaStream_t s) {
     moe::Args up, down;
     int64_t bytes[2];

@@ -63,6 +63,7 @@ struct Args {
     int jobs;                   // of a (group, slice)
     int nw;                     // warps that multiply
     int gmax;                   // groups the tables hold
+    int cap;                    // most pairs of a group (4 or 8)
     uint32_t off_pairs, off_gexp, off_gbeg, off_gcnt, off_bar, off_x, off_ring;
     unsigned* status;
 };
@@ -460,17 +461,17 @@ inline double groups_of(int n, int k, int n_exp, int cap) {
     return n_exp * sum;
 }
 
-// The geometry of one product: the size of groups (4 or 8, returned) and the
+// The geometry of one product: the size of groups (cap: 4 or 8; 0 where nothing fits) and the
 // slices of K that are expected to take the least time, in units' times: a job
 // costs its units (more with groups of eight) and an overhead.  warp_bytes of shared memory for two steps of a warp.
-inline int plan(Args& a, int type_block_bytes, int type_block_elems, int warp_bytes, bool down, int sms, uint32_t* smem) {
+inline void plan(Args& a, int type_block_bytes, int type_block_elems, int warp_bytes, bool down, int sms, uint32_t* smem) {
     a.row_bytes = (uint32_t)(a.cols / type_block_elems * type_block_bytes);
     a.nxb = (int)(a.cols / 32);
     a.nunits = (int)((a.cols + kUnitW - 1) / kUnitW);
     a.jobs = (int)(a.rows / (down ? 2 * kTileRows : kTileRows));
     double best = 1e300;
-    int cap_best = 0;
     Args chosen = a;
+    chosen.cap = 0;
     for (const int cap : {4, 8}) {
         if (cap == 8 && a.n_tok <= 4) continue;
         const double groups = groups_of(a.n_tok, a.k, a.n_exp, cap);
@@ -497,15 +498,14 @@ inline int plan(Args& a, int type_block_bytes, int type_block_elems, int warp_by
             const double time = turns * std::max(b.nw, 12) * (b.ku * (cap == 4 ? 1.0 : 1.25) + 0.7);
             if (time < best) {
                 best = time;
-                cap_best = cap;
                 const int64_t ring = std::max<int64_t>((int64_t)b.nw * warp_bytes, 2 * ((a.pairs + 7) & ~7) + 12 * a.n_exp + 16);
                 *smem = (uint32_t)(b.off_ring + ring + 16);
                 chosen = b;
+                chosen.cap = cap;
             }
         }
     }
     a = chosen;
-    return cap_best;
 }
 
 template <class K>
@@ -528,10 +528,10 @@ cudaError_t launch_kernel(K kern, const Args& a, int grid, uint32_t smem, cudaSt
 template <int T, int BB, int BE, bool DOWN>
 cudaError_t go(Args& a, int sms, cudaStream_t s, bool launch) {
     uint32_t smem = 0;
-    const int cap = plan(a, BB, BE, Slot<T>::kWarp, DOWN, sms, &smem);
-    if (cap == 0) return cudaErrorInvalidValue;
+    plan(a, BB, BE, Slot<T>::kWarp, DOWN, sms, &smem);
+    if (a.cap == 0) return cudaErrorInvalidValue;
     if (!launch) return cudaSuccess;
-    return cap == 4 ? launch_kernel(moe_kernel<T, 4, DOWN>, a, sms, smem, s) : launch_kernel(moe_kernel<T, 8, DOWN>, a, sms, smem, s);
+    return a.cap == 4 ? launch_kernel(moe_kernel<T, 4, DOWN>, a, sms, smem, s) : launch_kernel(moe_kernel<T, 8, DOWN>, a, sms, smem, s);
 }
 
 template <bool DOWN>

@@ -660,6 +660,12 @@ qk_status qk_verify_tree(const void* logits, int dtype, int64_t n_rows, int64_t 
 qk_status qk_unpack(int type, const void* W, int64_t nblocks, int16_t* codes,
                     int16_t* sc, uint8_t* mins, float* d, float* dmin, void* stream);
 
+/* Test hook: the most (token, expert) pairs, 4 or 8, that qk_moe_ffn multiplies
+ * an expert's weights with at a time, in its gate and up products (down == 0) or
+ * its down product, for these sizes on a GPU of `sms` SMs (0: the current
+ * device's).  0 for sizes that the call refuses, and for no tokens. */
+int qk_test_moe_group(int type, int type_down, int n_exp, int64_t rows, int64_t cols, int k, int64_t n_tok, int down, int sms);
+
 /* Diagnostic of the failure-detection path; the pages have no counterpart.
  * Every mbarrier wait inside the library's kernels is bounded (2 s): when it
  * runs out the kernel records a timeout in the device status word, drains

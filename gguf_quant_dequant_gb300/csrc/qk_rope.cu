@@ -10,10 +10,12 @@
 // distance 1, 2, 4 ..), so that a value, and the byte it is quantized to, does
 // not depend on where or how it is computed.
 //
-// Angles: pos * freq is kept as a whole number of 2^-96 turns, so that a far
-// position loses nothing (fp32 would be a radian off near position 2^24); the
-// cosine and sine come from their power series on an eighth of a turn, in
-// pairs of fp32 (about 2^-40), and are rounded to fp32 once.
+// Angles: freq is kept as a whole number of 2^-96 turns, so that a far position
+// loses nothing (fp32 would be a radian off near position 2^24); what is left of
+// the angle, within an eighth of a turn, is held as two fp32 (2^-89 turns at
+// worst, which only sines of angles below 2^-46 notice); the cosine and sine come
+// from their power series there, in pairs of fp32 (about 2^-40), and are rounded
+// to fp32 once.
 //
 // A warp takes a token and walks over its heads, 32 / (d / 8) rows a step, the
 // next step's loads ahead of this one's arithmetic.  It computes the token's

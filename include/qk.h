@@ -474,9 +474,10 @@ qk_status qk_kv_append(int type, const void* k, const void* v, int dtype, int64_
  * Every square, sum, quotient, root and product above is rounded to fp32 by
  * itself, the squares are added by neighbours (x0^2 + x1^2, .., then those
  * sums by neighbours), and cos and sin are the fp32 nearest to their exact
- * values, up to one value in some ten thousand that is the next one: angles are
- * kept to 2^-96 of a turn, so far positions lose nothing.  Results are then
- * rounded once to out_dtype.
+ * values, up to one value in some ten thousand that is the next one: the angle of
+ * a position is kept to 2^-96 of a turn, so far positions lose nothing.  (A cos
+ * or sin that is nearly zero, as at frequencies below 2^-46, is within half a step
+ * of fp32 and 2^-84 + |pos| 2^-93.)  Results are then rounded once to out_dtype.
  * n_tok == 0, or no heads, queues nothing.  Errors: QK_ERR_SHAPE, QK_ERR_NULL,
  * QK_ERR_ALIGN, QK_ERR_ARG (dtype, eps). */
 qk_status qk_norm_rope(const void* q, const void* k, int dtype, int64_t n_tok, int64_t q_stride, int64_t k_stride, int n_heads,

@@ -18,7 +18,7 @@
 // largest exponent, and a subnormal counts with the exponent that it is written
 // with, so codes at the lowest bits lose what stands behind 2^-24 of 1 and not of
 // themselves.  With Q4_K at bits 0 .. 3 and Q2_K at 0, 1, 4 and 5 a layer was 1.5e-6
-// and 3e-6 of its norm off; now it is 2 to 4e-7, as with the other types, for 1 to
+// and 3e-6 of its norm off; now it is 2 to 5e-7, as with the other types, for 1 to
 // 2 % more time.
 // In qk_hunits.cuh a warp's four column groups hold four parts of K for one row
 // of x; here all sixteen k of an MMA come from one 32-block and the eight

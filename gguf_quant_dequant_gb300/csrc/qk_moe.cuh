@@ -26,11 +26,11 @@
 //     preparation of `down`, and a last kernel that also weighs and adds the
 //     experts.  The result does not depend on timing.
 // What bounds it: 13 tokens, 2 of 8 experts of 4096 x 14336: up 122 us (Q4_K, 529
-// MB, 54 % of the DRAM rate), down 133 (Q6_K, 441 MB, 42 %), issue slots half used,
-// no pipe above two thirds; with the products left out the layer takes 206 us of
-// its 292, with nothing fetched 243, so each side takes the other's place,
-// likely in the load-store unit.  One token: some 8 us a product, of which the
-// weights' bytes are 2.
+// MB, 55 % of the DRAM rate), down 135 (Q6_K, 441 MB, 42 %), issue slots half used,
+// no pipe above 70 %; with the products left out the layer takes 202 us of its
+// 297, with nothing fetched 248, so each side takes the other's place, likely in
+// the load-store unit.  One token: some 8 us a product, of which the weights'
+// bytes are 2.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -63,9 +63,9 @@ struct Args {
     int jobs;                   // of a (group, slice)
     int nw;                     // warps that multiply
     int gmax;                   // groups the tables hold
-    int cap;                    // most pairs of a group (4 or 8)
     uint32_t off_pairs, off_gexp, off_gbeg, off_gcnt, off_bar, off_x, off_ring;
     unsigned* status;
+    int cap;                    // most pairs of a group (4 or 8)
 };
 
 struct Tables {
@@ -463,7 +463,20 @@ inline double groups_of(int n, int k, int n_exp, int cap) {
 
 // The geometry of one product: the size of groups (cap: 4 or 8; 0 where nothing fits) and the
 // slices of K that are expected to take the least time, in units' times: a job
-// costs its units (more with groups of eight) and an overhead.  warp_bytes of shared memory for two steps of a warp.
+// costs its units (1.25 each with groups of eight, for their second B loads and
+// MMAs) and 0.7 for its sums and their way out.  warp_bytes of shared memory for
+// two steps of a warp.
+// The four numbers in it are fitted to times; both sides of each choice, with one
+// product's geometry forced (the layer, us; narrow: 8 of 128 experts of 2048 x 768,
+// wide: 2 of 8 of 4096 x 14336, Q4_K and Q6_K):
+//   groups of 4 / 8: 13 tokens narrow 94 / 101 (up), 94 / 102 (down), wide 289 / 299
+//     (up), 289 / 289 (down); 61 narrow 169 / 170, 168 / 171; 64 wide 852 / 738, 858 / 737;
+//   units of a slice of up, 1 / 2 / 4 / 8: 61 narrow 187 / 171 / 169 / 170, 13 wide
+//     346 / 312 / 291 / 289, 64 wide 876 / 780 / 737 / 852 (fours again);
+//   of down, 1 / 2 / 3 / 4 / 6: 13 wide 311 / 290 / 285 / 289 / 300, 64 wide 801 / 738 /
+//     729 / 727 / 879.  (The planned 2 there makes 28 slices, whose partial sums,
+//     59 MB, are not counted: 1.5 %.)
+// One token: 28 and 69, the best of all 28 and 68.
 inline void plan(Args& a, int type_block_bytes, int type_block_elems, int warp_bytes, bool down, int sms, uint32_t* smem) {
     a.row_bytes = (uint32_t)(a.cols / type_block_elems * type_block_bytes);
     a.nxb = (int)(a.cols / 32);

@@ -23,9 +23,9 @@
 //     taken by a margin above what such a sum can be off is passed over without
 //     going through its parent's row; everything else is decided by the walk's
 //     exact sums, so the answer is the same with and without the pieces.  48
-//     chains of 8 rows of 128,256 fp32: 123 us without, 72 us with them (38 us
-//     of it the pieces', at 5.2 TB/s); one chain of 64 rows of 32,000: 121 and
-//     39 us; trees of 64 nodes: 35 and 36 us;
+//     chains of 8 rows of 128,256 fp32: 128 us without, 72 us with them (39 us
+//     of it the pieces', at 5.1 TB/s); one chain of 6 rows of 32,000: 21 and 13
+//     us, of 64: 69 and 37; trees of 64 nodes: 35 either way;
 //   * a thread keeps its logits of the row, then their weights, in registers
 //     (up to kKeep of them; longer parts are read again from L2; kept in shared
 //     memory they cost 15 % more than either);

@@ -253,7 +253,7 @@ qk_status qk_gemv_swiglu(int type, const void* Wg, const void* Wu, int64_t rows,
  * tokens.  Three launches, four with a router.  Accuracy: each product is
  * within 2^-17 * sum_k (|scale code| + |min|) |x_k| + 1e-6 of its exact value
  * (for the types without a min that is sum |w x|, but Q6_K's codes count as 0 ..
- * 63 with a min of 32 scales); in practice the layer is 2 to 4e-7 of its norm
+ * 63 with a min of 32 scales); in practice the layer is 2 to 5e-7 of its norm
  * off.  The SiLU and the sum over experts are fp32; the router's logits are fp32
  * sums.
  * A logit that is NaN ranks first and gives NaN gates for its token.
